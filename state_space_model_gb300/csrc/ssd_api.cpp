@@ -3,119 +3,24 @@
 // stream.  Every check runs before the first launch; nothing here allocates,
 // frees or synchronises.
 #include "ssd.h"
+#include "ssd_checks.h"
 #include "ssd_decode.h"
 #include "ssd_internal.h"
 #include "ssd_mixer.h"
 #include "ssd_tc.cuh"
 
-#include <cstdarg>
 #include <cstdio>
 #include <cstring>
-#include <initializer_list>
 #include <string>
 
 namespace {
 
-thread_local std::string g_detail;
+using namespace ssd::checks;
 
-ssd_status fail(ssd_status st, const char *fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    g_detail = buf;
-    return st;
-}
-
-ssd_status ok() {
-    g_detail.clear();
-    return SSD_OK;
-}
-
-size_t elem_size(int dt) { return dt == SSD_BF16 ? 2 : 4; }
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 bool supported_dim(int64_t v) { return v == 16 || v == 32 || v == 64 || v == 128; }
 bool supported_chunk(int64_t q) { return q == 64 || q == 128 || q == 256; }
-
-// Address range [lo, hi) a tensor touches; empty when any extent is 0.
-struct Range {
-    uintptr_t lo = 0, hi = 0;
-};
-Range range_of(const ssd_tensor *t) {
-    Range r;
-    if (!t || !t->data) return r;
-    int64_t last = 0;
-    for (int i = 0; i < t->ndim; ++i) {
-        if (t->shape[i] == 0) return r;
-        last += (t->shape[i] - 1) * t->stride[i];
-    }
-    r.lo = reinterpret_cast<uintptr_t>(t->data);
-    r.hi = r.lo + size_t(last + 1) * elem_size(t->dtype);
-    return r;
-}
-Range range_raw(const void *p, size_t bytes) {
-    Range r;
-    if (p && bytes) {
-        r.lo = reinterpret_cast<uintptr_t>(p);
-        r.hi = r.lo + bytes;
-    }
-    return r;
-}
-bool overlap(Range a, Range b) {
-    return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi;
-}
-
-// Checks one tensor's rank, dtype, shape, unit inner stride and alignment.
-// dtype < 0 accepts f32 or bf16 (int32 only where asked for by name).
-// contiguous demands packed row-major strides.
-ssd_status check_tensor(const ssd_tensor *t, const char *name, int ndim,
-                        const int64_t *shape, int dtype, bool contiguous,
-                        bool align_strides16) {
-    if (!t) return fail(SSD_ERR_INVALID_ARG, "%s: null tensor descriptor", name);
-    if (t->ndim != ndim)
-        return fail(SSD_ERR_INVALID_ARG, "%s: ndim %d, expected %d", name, t->ndim, ndim);
-    auto dname = [](int d) { return d == SSD_F32 ? "f32" : d == SSD_BF16 ? "bf16" : "i32"; };
-    if (t->dtype != SSD_F32 && t->dtype != SSD_BF16 && t->dtype != SSD_I32)
-        return fail(SSD_ERR_INVALID_ARG, "%s: unknown dtype code %d", name, t->dtype);
-    if ((dtype >= 0 && t->dtype != dtype) || (dtype < 0 && t->dtype == SSD_I32))
-        return fail(SSD_ERR_INVALID_ARG, "%s: dtype %s, expected %s", name, dname(t->dtype),
-                    dtype >= 0 ? dname(dtype) : "f32 or bf16");
-    int64_t numel = 1;
-    for (int i = 0; i < ndim; ++i) {
-        if (t->shape[i] != shape[i])
-            return fail(SSD_ERR_INVALID_ARG, "%s: shape[%d] = %lld, expected %lld", name, i,
-                        (long long)t->shape[i], (long long)shape[i]);
-        numel *= shape[i];
-    }
-    if (numel > 0 && !t->data) return fail(SSD_ERR_INVALID_ARG, "%s: null data pointer", name);
-    if (t->stride[ndim - 1] != 1 && shape[ndim - 1] > 1)
-        return fail(SSD_ERR_INVALID_ARG, "%s: innermost stride %lld, must be 1", name,
-                    (long long)t->stride[ndim - 1]);
-    if (contiguous) {
-        int64_t want = 1;
-        for (int i = ndim - 1; i >= 0; --i) {
-            if (shape[i] > 1 && t->stride[i] != want)
-                return fail(SSD_ERR_INVALID_ARG, "%s: must be contiguous (stride[%d] = %lld, "
-                            "expected %lld)", name, i, (long long)t->stride[i], (long long)want);
-            want *= shape[i];
-        }
-    }
-    for (int i = 0; i < ndim - 1; ++i)
-        if (t->stride[i] < 0)
-            return fail(SSD_ERR_INVALID_ARG, "%s: negative stride", name);
-    const size_t es = elem_size(t->dtype);
-    if (numel > 0 && (reinterpret_cast<uintptr_t>(t->data) % (align_strides16 ? 16 : es)))
-        return fail(SSD_ERR_ALIGNMENT, "%s: base pointer %p not %zu-byte aligned", name, t->data,
-                    align_strides16 ? size_t(16) : es);
-    if (align_strides16)
-        for (int i = 0; i < ndim - 1; ++i)
-            if (shape[i] > 1 && (t->stride[i] * int64_t(es)) % 16)
-                return fail(SSD_ERR_ALIGNMENT, "%s: stride[%d] = %lld elements is not a multiple "
-                            "of 16 bytes", name, i, (long long)t->stride[i]);
-    return SSD_OK;
-}
 
 ssd_status check_geometry(int64_t B, int64_t L, int64_t H, int64_t P, int64_t N, int64_t G,
                           int64_t Q) {
@@ -187,42 +92,6 @@ Plan plan_workspace(const ssd::Dims &d, int xdt) {
     return p;
 }
 
-// Every data pointer must be device (or managed) memory of the current
-// device: a host pointer handed to a kernel would fault it.  Runs after all
-// pure-host checks, so argument errors are reported without touching CUDA.
-struct NamedPtr {
-    const void *p;
-    const char *name;
-};
-ssd_status check_device_ptrs(std::initializer_list<NamedPtr> ptrs) {
-    int dev = -1;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return fail(SSD_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
-    for (const NamedPtr &np : ptrs) {
-        if (!np.p) continue;
-        cudaPointerAttributes at{};
-        e = cudaPointerGetAttributes(&at, np.p);
-        if (e != cudaSuccess) {
-            cudaGetLastError();
-            return fail(SSD_ERR_INVALID_ARG, "%s: pointer %p is not CUDA memory (%s)", np.name,
-                        np.p, cudaGetErrorString(e));
-        }
-        if (at.type == cudaMemoryTypeManaged) continue;
-        if (at.type != cudaMemoryTypeDevice)
-            return fail(SSD_ERR_INVALID_ARG, "%s: pointer %p is host memory; device memory is "
-                        "required", np.name, np.p);
-        if (at.device != dev)
-            return fail(SSD_ERR_INVALID_ARG, "%s: pointer on device %d, current device is %d",
-                        np.name, at.device, dev);
-    }
-    return SSD_OK;
-}
-
-ssd_status cuda_status(cudaError_t e, const char *what) {
-    if (e == cudaSuccess) return SSD_OK;
-    return fail(SSD_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
 void fill_x(ssd::Args &a, const ssd_tensor *x) {
     a.x = x->data;
     a.x_sb = x->stride[0];
@@ -257,17 +126,6 @@ void fill_y(ssd::Args &a, ssd_tensor *y) {
 
 }  // namespace
 
-namespace ssd {
-void set_error_detail(const char *fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    g_detail = buf;
-}
-}  // namespace ssd
-
 extern "C" {
 
 const char *ssd_status_string(ssd_status s) {
@@ -284,7 +142,7 @@ const char *ssd_status_string(ssd_status s) {
     return "SSD_UNKNOWN_STATUS";
 }
 
-const char *ssd_last_error_detail(void) { return g_detail.c_str(); }
+const char *ssd_last_error_detail(void) { return error_detail().c_str(); }
 
 const char *ssd_describe_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
                               int64_t dstate, int64_t ngroups, int64_t chunk_size,
@@ -294,10 +152,10 @@ const char *ssd_describe_plan(int64_t batch, int64_t seqlen, int64_t nheads, int
         text = "rejected: unknown dtype code";
         return text.c_str();
     }
-    const std::string saved = g_detail;
+    const std::string saved = error_detail();
     if (check_geometry(batch, seqlen, nheads, headdim, dstate, ngroups, chunk_size) != SSD_OK) {
-        text = "rejected: " + g_detail;
-        g_detail = saved;
+        text = "rejected: " + error_detail();
+        error_detail() = saved;
         return text.c_str();
     }
     ssd::Dims d{batch, seqlen, nheads, headdim, dstate, ngroups, chunk_size,
