@@ -74,9 +74,12 @@ typedef enum {
                                  build only: libssd_gb300_debug.so)          */
 } ssd_status;
 
-/* SSD_I32 only for the parent and state-slot indices of ssd_state_update_tokens
- * and the conv-state slot indices of ssd_mixer_prologue. */
-typedef enum { SSD_F32 = 0, SSD_BF16 = 1, SSD_I32 = 2 } ssd_dtype;
+/* SSD_I32 only for the parent and state-slot indices of ssd_state_update_tokens,
+ * the conv-state slot indices of ssd_mixer_prologue and the slots, positions,
+ * page tables and lengths of the key/value cache; SSD_F8E4M3 (8 bits: sign, 4
+ * exponent, 3 mantissa bits, no infinities, largest value 448) only for that
+ * cache's pools. */
+typedef enum { SSD_F32 = 0, SSD_BF16 = 1, SSD_I32 = 2, SSD_F8E4M3 = 3 } ssd_dtype;
 
 typedef struct {
     void *data;          /* device pointer                                   */
@@ -396,6 +399,102 @@ ssd_status ssd_mixer_prologue(const ssd_tensor *xBC, const ssd_tensor *conv_weig
                               const ssd_tensor *dt, const ssd_tensor *dt_bias,
                               int32_t dt_softplus, int64_t ngroups, ssd_tensor *x,
                               ssd_tensor *B, ssd_tensor *C, ssd_tensor *dt_out, void *stream);
+
+/* ---- attention layers: the paged key/value cache --------------------------------
+ * Hybrid models interleave state-space layers with attention layers.  These
+ * entry points serve the latter next to ssd_mixer_prologue and
+ * ssd_state_update_tokens: the write into the cache, the read back, and the
+ * attention of new tokens over it.  Conventions as at the top of this file
+ * (device pointers, checks before any launch, no allocation, deterministic).
+ *
+ * The cache is two pools of pages, one of keys and one of values, each
+ * [pages, Hkv, ps, D] (ps tokens a page) with free page, head and token
+ * strides, the same for both pools (so [pages, ps, Hkv, D] memory is passed
+ * as a transposed view).  A pool holds the dtype of the layer (bf16 or f32),
+ * or SSD_F8E4M3 with one f32 scale for each token and head, [pages, Hkv, ps]
+ * (innermost stride 1, the same strides for both): a held element stands for
+ * code * scale.  Slot s of a pool is token s % ps of page s / ps; a page
+ * table [B, M] names the pages of each sequence in order, so that position n
+ * of sequence b lies in page table[b, n / ps].  D is 64 or 128; ps any
+ * positive size; Hq (query heads) a multiple of Hkv, query head h reads
+ * key/value head h / (Hq / Hkv).  Pools and the query / key / value tensors
+ * have 16-byte aligned bases and outer strides; pages * ps < 2^31.
+ * Indices live on the device and cannot be checked here: every index is safe
+ * to pass, and what one out of range means is said at each call. */
+
+/* For each of T tokens, in one pass: RMS norm of each query and key head
+ * (q_weight / k_weight [D] f32, NULL = no norm), rotation by position (cos,
+ * sin [S, R/2] f32, NULL = none), and the write of key and value to slot
+ * slots[t]:
+ *
+ *   u = x * w / sqrt(mean(x^2) + eps)
+ *   (a, b) -> (a cos - b sin, b cos + a sin)  for the R/2 pairs of the first R
+ *       places: (i, i + R/2), or (2i, 2i + 1) if interleaved != 0, with row
+ *       positions[t] of cos and sin; places R.. stay
+ *   q_out[t] = u rounded once;  key and value rounded once to the pools' dtype,
+ *   or with scales: scale = max(amax, 2^-96) / 448 over the head's row, code =
+ *   u / scale rounded to nearest even (a row that holds an infinity or NaN
+ *   reads back as NaN)
+ *
+ * q, q_out [T, Hq, D], k, v [T, Hkv, D], bf16 or f32 (views of one projection
+ * do); slots [T], positions [T] SSD_I32 contiguous; R a multiple of 16, R <= D;
+ * k_scale, v_scale with SSD_F8E4M3 pools only.  A token whose slot lies outside
+ * [0, pages * ps) or whose position lies outside [0, S) is padding: nothing is
+ * read or written for it, its q_out rows included.  Tokens must name distinct
+ * slots (not checked: two on one slot race).  One launch. */
+ssd_status ssd_kv_append(const ssd_tensor *q, const ssd_tensor *k, const ssd_tensor *v,
+                         const ssd_tensor *slots, const ssd_tensor *positions,
+                         const ssd_tensor *cos, const ssd_tensor *sin,
+                         const ssd_tensor *q_weight, const ssd_tensor *k_weight, float eps,
+                         int32_t interleaved, ssd_tensor *k_cache, ssd_tensor *v_cache,
+                         ssd_tensor *k_scale, ssd_tensor *v_scale, ssd_tensor *q_out,
+                         void *stream);
+
+/* Cached keys and values as contiguous rows: with cu_lens [B + 1] (SSD_I32,
+ * not decreasing) row i belongs to the sequence b with cu_lens[b] <= i <
+ * cu_lens[b + 1] and is its position starts[b] + i - cu_lens[b] (starts [B]
+ * SSD_I32 or NULL = 0).  k, v [T, Hkv, D] f32 or bf16: the dtype of the pools,
+ * or code * scale rounded once.  page_table [B, M] SSD_I32, innermost stride 1.
+ * Rows of no sequence, and positions outside the table or in a page outside
+ * [0, pages), are written as zeros.  One launch. */
+ssd_status ssd_kv_read(const ssd_tensor *k_cache, const ssd_tensor *v_cache,
+                       const ssd_tensor *k_scale, const ssd_tensor *v_scale,
+                       const ssd_tensor *page_table, const ssd_tensor *cu_lens,
+                       const ssd_tensor *starts, ssd_tensor *k, ssd_tensor *v, void *stream);
+
+/* Bytes of workspace ssd_paged_attention needs for this problem (written to
+ * *bytes): the partial results of sequences that several CTAs share.
+ * cache_dtype is the ssd_dtype of the pools.  The answer depends on the SM
+ * count of the current device. */
+ssd_status ssd_paged_attention_workspace_size(int64_t batch, int64_t tokens, int64_t q_heads,
+                                              int64_t kv_heads, int64_t headdim,
+                                              int32_t cache_dtype, size_t *bytes);
+
+/* Attention of T new tokens of each sequence (T = 1: plain decoding; T > 1:
+ * draft tokens checked together, or a piece of a prompt) over the cache, the
+ * new tokens' own keys and values included.  With n = lens[b], row t stands at
+ * position e = n - T + t and sees positions j <= e, with window > 0 also j > e -
+ * window:
+ *
+ *   out[b, t, h] = sum_j p_j v_j,  p = softmax_j(scale * q[b, t, h] . k_j)
+ *   lse[b, t, h] = log sum_j exp(scale * q[b, t, h] . k_j)
+ *
+ * A row that sees nothing (n = 0, e < 0) gives out = 0 and lse = -inf.
+ * Positions outside the table (n above M * ps) or in a page outside [0, pages)
+ * are not there: no row sees them.  What lies in slots that a row does not see
+ * (NaN included) does not reach it.
+ * q, out [B, T, Hq, D] (f32 with f32 pools, else bf16); page_table [B, M]
+ * SSD_I32, innermost stride 1; lens [B] SSD_I32; lse [B, T, Hq] f32
+ * contiguous, may be NULL; workspace as above, 256-byte aligned, contents
+ * ignored.  Two launches; scores, sums and partial results in f32, the
+ * probabilities rounded to 16 bits for the product with bf16 values or 8-bit
+ * codes. */
+ssd_status ssd_paged_attention(const ssd_tensor *q, const ssd_tensor *k_cache,
+                               const ssd_tensor *v_cache, const ssd_tensor *k_scale,
+                               const ssd_tensor *v_scale, const ssd_tensor *page_table,
+                               const ssd_tensor *lens, float scale, int64_t window,
+                               ssd_tensor *out, ssd_tensor *lse, void *workspace,
+                               size_t workspace_bytes, void *stream);
 
 /* ---- stage entry points (the four steps of ssd_chunked_fwd, one call each;
  *      same conventions; used to check each step on its own) ---------------- */

@@ -15,7 +15,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libssd_gb300_debug.so" if os.environ.get("SSD_DEBUG_BOUNDS") == "1"
                         else "libssd_gb300.so")
 
-SSD_F32, SSD_BF16, SSD_I32 = 0, 1, 2
+SSD_F32, SSD_BF16, SSD_I32, SSD_F8E4M3 = 0, 1, 2, 3
 STATUS = {0: "SSD_OK", 1: "SSD_ERR_INVALID_ARG", 2: "SSD_ERR_UNSUPPORTED",
           3: "SSD_ERR_ALIGNMENT", 4: "SSD_ERR_WORKSPACE", 5: "SSD_ERR_CUDA",
           6: "SSD_ERR_TIMEOUT", 7: "SSD_ERR_DEVICE_BOUNDS"}
@@ -40,6 +40,7 @@ _lock = threading.Lock()
 
 _T = ctypes.POINTER(SsdTensor)
 _VP, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+_F32 = ctypes.c_float
 
 # name -> argtypes; every entry point returns an ssd_status (int)
 SIGNATURES = {
@@ -58,6 +59,11 @@ SIGNATURES = {
     "ssd_state_update_tokens": [_T, _T, _T, _T, _T, _T, _T, _T, _T, _I32, _I64, _T, _T, _T, _T,
                                 _I32, _VP],
     "ssd_mixer_prologue": [_T, _T, _T, _T, _T, _T, _T, _T, _I32, _I64, _T, _T, _T, _T, _VP],
+    # descriptors passed by address (attn.py packs them itself)
+    "ssd_kv_append": [_VP] * 9 + [_F32, _I32] + [_VP] * 6,
+    "ssd_kv_read": [_VP] * 10,
+    "ssd_paged_attention_workspace_size": [_I64] * 5 + [_I32, ctypes.POINTER(ctypes.c_size_t)],
+    "ssd_paged_attention": [_VP] * 7 + [_F32, _I64] + [_VP] * 3 + [_SZ, _VP],
     "ssd_stage_chunk_cumsum": [_T, _T, _I64, _T, _VP],
     "ssd_stage_chunk_state": [_T, _T, _T, _T, _I64, _I64, _T, _VP],
     "ssd_stage_state_passing": [_T, _T, _T, _I64, _T, _T, _VP],

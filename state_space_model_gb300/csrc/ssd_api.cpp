@@ -226,12 +226,13 @@ ssd_status ssd_device_status(void *stream) {
             return st;
         if (v[0] & 4u) {
             static const char *const files[] = {"?", "ssd_fused.cu", "ssd_pair.cu", "ssd_tc.cu",
-                                                "ssd_simt.cu", "ssd_selftest.cu", "ssd_tc_f32.cu"};
+                                                "ssd_simt.cu", "ssd_selftest.cu", "ssd_tc_f32.cu",
+                                                "ssd_kv.cu", "ssd_attn.cu"};
             const unsigned f = v[1] >> 16;
             return fail(SSD_ERR_DEVICE_BOUNDS,
                         "a device bounds check failed (flags 0x%x), first at %s line %u; the "
                         "access was skipped and outputs since the last check are not valid",
-                        v[0], f < 7 ? files[f] : "?", v[1] & 0xffffu);
+                        v[0], f < 9 ? files[f] : "?", v[1] & 0xffffu);
         }
         return fail(SSD_ERR_TIMEOUT, "a kernel gave up a bounded wait (flags 0x%x); outputs of "
                     "the calls since the last check are not valid", v[0]);

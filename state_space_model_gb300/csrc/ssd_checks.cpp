@@ -31,7 +31,8 @@ ssd_status ok() {
     return SSD_OK;
 }
 
-size_t elem_size(int dt) { return dt == SSD_BF16 ? 2 : 4; }
+size_t elem_size(int dt) { return dt == SSD_BF16 ? 2 : dt == SSD_F8E4M3 ? 1 : 4; }
+
 Range range_of(const ssd_tensor *t) {
     Range r;
     if (!t || !t->data) return r;
@@ -62,10 +63,12 @@ ssd_status check_tensor(const ssd_tensor *t, const char *name, int ndim,
     if (!t) return fail(SSD_ERR_INVALID_ARG, "%s: null tensor descriptor", name);
     if (t->ndim != ndim)
         return fail(SSD_ERR_INVALID_ARG, "%s: ndim %d, expected %d", name, t->ndim, ndim);
-    auto dname = [](int d) { return d == SSD_F32 ? "f32" : d == SSD_BF16 ? "bf16" : "i32"; };
-    if (t->dtype != SSD_F32 && t->dtype != SSD_BF16 && t->dtype != SSD_I32)
+    auto dname = [](int d) {
+        return d == SSD_F32 ? "f32" : d == SSD_BF16 ? "bf16" : d == SSD_I32 ? "i32" : "f8e4m3";
+    };
+    if (t->dtype < SSD_F32 || t->dtype > SSD_F8E4M3)
         return fail(SSD_ERR_INVALID_ARG, "%s: unknown dtype code %d", name, t->dtype);
-    if ((dtype >= 0 && t->dtype != dtype) || (dtype < 0 && t->dtype == SSD_I32))
+    if ((dtype >= 0 && t->dtype != dtype) || (dtype < 0 && t->dtype != SSD_F32 && t->dtype != SSD_BF16))
         return fail(SSD_ERR_INVALID_ARG, "%s: dtype %s, expected %s", name, dname(t->dtype),
                     dtype >= 0 ? dname(dtype) : "f32 or bf16");
     int64_t numel = 1;
@@ -100,6 +103,27 @@ ssd_status check_tensor(const ssd_tensor *t, const char *name, int ndim,
             if (shape[i] > 1 && (t->stride[i] * int64_t(es)) % 16)
                 return fail(SSD_ERR_ALIGNMENT, "%s: stride[%d] = %lld elements is not a multiple "
                             "of 16 bytes", name, i, (long long)t->stride[i]);
+    return SSD_OK;
+}
+
+ssd_status check_distinct(const ssd_tensor *t, const char *name) {
+    // dimensions by stride, each at least as wide as all below it together
+    int64_t reach = 1, below = -1;
+    for (int k = 0; k < t->ndim; ++k) {
+        int at = -1;
+        for (int i = 0; i < t->ndim; ++i) {
+            if (t->shape[i] <= 1) continue;
+            const int64_t key = t->stride[i] * t->ndim + (t->ndim - 1 - i);
+            if (key > below && (at < 0 || key < t->stride[at] * t->ndim + (t->ndim - 1 - at)))
+                at = i;
+        }
+        if (at < 0) break;
+        if (t->stride[at] < reach)
+            return fail(SSD_ERR_INVALID_ARG, "%s: stride[%d] = %lld makes elements share memory",
+                        name, at, (long long)t->stride[at]);
+        reach = t->stride[at] * (t->shape[at] - 1) + reach;
+        below = t->stride[at] * t->ndim + (t->ndim - 1 - at);
+    }
     return SSD_OK;
 }
 

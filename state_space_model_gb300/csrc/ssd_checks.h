@@ -35,6 +35,10 @@ bool overlap(Range a, Range b);
 ssd_status check_tensor(const ssd_tensor *t, const char *name, int ndim, const int64_t *shape,
                         int dtype, bool contiguous, bool align_strides16);
 
+// An output's strides must keep its elements apart (a broadcast view, with a
+// stride of 0, would be written by several threads at once).
+ssd_status check_distinct(const ssd_tensor *t, const char *name);
+
 // Every data pointer must be device (or managed) memory of the current
 // device: a host pointer handed to a kernel would fault it.  Runs after all
 // pure-host checks, so argument errors are reported without touching CUDA.
