@@ -12,6 +12,9 @@ namespace {
 using namespace ssd::checks;
 
 constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
+// Positions leave room below 2^31 for a tile and for the new tokens, so that
+// the kernels count them in 32 bits.
+constexpr int64_t kMaxPos = kMaxInt - (1 << 17);
 
 int64_t extent(const ssd_tensor *t) {
     int64_t last = 0;
@@ -95,9 +98,9 @@ ssd_status check_table(const ssd_tensor *t, int64_t B, int64_t ps) {
     const int64_t shape[2] = {B, t->shape[1]};
     ssd_status st;
     if ((st = check_tensor(t, "page_table", 2, shape, SSD_I32, false, false))) return st;
-    if (t->shape[1] < 0 || t->shape[1] > kMaxInt || t->shape[1] * ps > kMaxInt)
+    if (t->shape[1] < 0 || t->shape[1] > kMaxInt || t->shape[1] * ps > kMaxPos)
         return fail(SSD_ERR_UNSUPPORTED, "page_table: %lld pages of %lld tokens, more than "
-                    "2^31 - 1 positions", (long long)t->shape[1], (long long)ps);
+                    "2^31 - 2^17 positions", (long long)t->shape[1], (long long)ps);
     return SSD_OK;
 }
 
@@ -366,7 +369,7 @@ ssd_status ssd_paged_attention(const ssd_tensor *q, const ssd_tensor *k_cache,
                                  {need ? workspace : nullptr, "workspace"}})))
         return st;
     a.scale = scale;
-    a.window = window;
+    a.window = window > kMaxPos ? 0 : window;   // such a window hides nothing
     a.q = q->data;
     a.q_sb = q->stride[0];
     a.q_st = q->stride[1];
