@@ -59,7 +59,7 @@ SIGNATURES = {
     "ssd_state_update_tokens": [_T, _T, _T, _T, _T, _T, _T, _T, _T, _I32, _I64, _T, _T, _T, _T,
                                 _I32, _VP],
     "ssd_mixer_prologue": [_T, _T, _T, _T, _T, _T, _T, _T, _I32, _I64, _T, _T, _T, _T, _VP],
-    # descriptors passed by address (attn.py packs them itself)
+    # descriptors passed by address (the compiled binding makes them)
     "ssd_kv_append": [_VP] * 9 + [_F32, _I32] + [_VP] * 6,
     "ssd_kv_read": [_VP] * 10,
     "ssd_paged_attention_workspace_size": [_I64] * 5 + [_I32, ctypes.POINTER(ctypes.c_size_t)],

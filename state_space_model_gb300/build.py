@@ -5,6 +5,10 @@ Each translation unit under ``csrc/`` is compiled in parallel into
 loads on a machine without a GPU driver (nothing touches the driver until
 the first CUDA call).  Usage: ``python -m state_space_model_gb300.build``.
 
+The compiled Python binding of the attention entry points
+(``binding/attn_ext.cpp`` -> ``_attn_ext.so``) is built beside it with the host
+compiler against the installed torch.
+
 ``--debug-bounds`` builds ``libssd_gb300_debug.so`` instead (objects in
 ``_build_debug/``), compiled with ``-DSSD_DEBUG_BOUNDS``: the kernels check
 every index, shared-memory offset and tensor-memory column range they compute
@@ -19,6 +23,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -27,6 +32,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libssd_gb300.so")
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libssd_gb300_debug.so")
+BINDING_SRC = os.path.join(PKG, "binding", "attn_ext.cpp")
+BINDING = os.path.join(PKG, "_attn_ext.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -67,11 +74,46 @@ def up_to_date(debug_bounds: bool = False) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING):
+        return False
+    t = os.path.getmtime(BINDING)
+    return all(os.path.getmtime(p) <= t for p in (
+        BINDING_SRC, os.path.join(ROOT, "include", "ssd.h"), os.path.abspath(__file__)))
+
+
+def build_binding() -> str:
+    """Compiles ``_attn_ext.so``.  It links the torch that is installed and calls the
+    library through addresses that ``attn`` gives it."""
+    import torch
+    troot = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", BINDING_SRC, "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-I", os.path.join(troot, "include"),
+           "-I", os.path.join(troot, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           "-L", os.path.join(troot, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-Wl,-rpath," + os.path.join(troot, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on attn_ext.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose_ptxas: bool | None = None,
           debug_bounds: bool = False) -> str:
     lib = LIB_DEBUG if debug_bounds else LIB
     out_dir = BUILD_DEBUG if debug_bounds else BUILD
+    if force or not _binding_up_to_date():
+        binding = cf.ThreadPoolExecutor(max_workers=1).submit(build_binding)
+    else:
+        binding = None
     if not force and up_to_date(debug_bounds):
+        if binding:
+            binding.result()
         return lib
     if verbose_ptxas is None:
         verbose_ptxas = os.environ.get("SSD_PTXAS_VERBOSE", "0") == "1"
@@ -98,6 +140,8 @@ def build(force: bool = False, verbose_ptxas: bool | None = None,
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
+    if binding:
+        binding.result()
     return lib
 
 
