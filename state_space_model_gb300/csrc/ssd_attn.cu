@@ -10,12 +10,15 @@
 // What bounds it is the cache: each key and value is read once, 2 D elements
 // for 4 D flops a query row, and the G = Hq / Hkv query heads of a key/value
 // head (times the T new tokens) are the only rows that share them.  So the
-// kernels are built to keep reads in flight, not for matrix rate: the two
-// products run on mma.sync with 16 rows a warp.  (tcgen05 takes its operands
-// from shared or tensor memory, 128 rows at least one way round; here the
-// 8-bit keys are widened and the probabilities are made in registers, where
-// mma.sync takes them, and at 16 rows it needs about a third of the time that
-// the reads take.)
+// kernels are built to keep reads in flight, not for matrix rate.  The two
+// products are turned round, S^T = K Q^T and O^T = V^T P^T, with positions and
+// places as the 16 rows of mma.sync and eight queries as its columns: the
+// usual 4 or 8 query heads fill a tile, which with queries as rows would be
+// half empty, and scores, probabilities and output take half the registers
+// and instructions.  (tcgen05 would take 128 positions as rows with as few
+// columns, but its operands come from shared and tensor memory: 8-bit codes
+// would have to be widened there and back, and probabilities stored.  At 8 to
+// 16 queries mma.sync needs a fifth to a third of the time of the reads.)
 #include "ssd_attn.h"
 #include "ssd_debug.cuh"
 #include "ssd_tc.cuh"
@@ -40,13 +43,18 @@ constexpr int kStages = 3;
 
 // ---- the schedule -----------------------------------------------------------------
 //
-// An item is a (sequence, key/value head, block of rows); its work is its
-// tiles of KS positions.  All items' tiles, in that order, form one line that
-// is cut into nc equal parts, one to a CTA, wherever the cuts fall: sequences
-// of any lengths fill the GPU evenly, and lengths are needed on the device
-// only.  An item that a cut falls into is finished by the join kernel from the
-// parts that its CTAs leave in the workspace.  An item without positions has
-// one (masked) tile, so that somebody writes its rows.
+// An item is a (sequence, key/value head, block of rows).  Its cost is its
+// tiles of KS positions, and kItemCost more for what an item takes whatever
+// its length (its queries, the join of the warps, the write).  All items, in
+// that order, form one line of cost units that is cut into nc equal parts, one
+// to a CTA, wherever the cuts fall: sequences of any lengths fill the GPU
+// evenly, and lengths are needed on the device only.  (Without the constant, a
+// CTA whose part is 40 one-tile items took as long as 120 tiles of one item:
+// 96 sequences of 17 to 16384 positions in 8 bits, 160 us.)  An item that a
+// cut falls into is finished by the join kernel from the parts that its CTAs
+// leave in the workspace.  An item without positions has one (masked) tile,
+// so that somebody writes its rows.
+constexpr int kItemCost = 2;
 
 struct Shape {            // of the schedule: what both kernels derive alike
     int KS;               // positions of a tile
@@ -59,29 +67,35 @@ struct Shape {            // of the schedule: what both kernels derive alike
 struct Item {
     int b, hk, rb;
     int len;              // positions of the sequence, new ones included
+    int emin, emax;       // the places of the block's first and last row
     int lo, hi;           // what some row of the block sees (may be empty)
     int first;            // lo rounded down to a tile
     int ntiles;
 };
 
+// (What follows runs once for an item or a CTA; kept out of line, so that the loop
+// over tiles stays small: with all of it inlined the kernel was 120 KB of code, and a
+// fifth of the loop's time was spent waiting for instructions.)
 __device__ __forceinline__ void item_range(const PagedArgs &a, const Shape &s, Item &it) {
     const int rows = a.T * s.G;
     const int r0 = it.rb * s.RB, r1 = min(r0 + s.RB, rows) - 1;
-    const int e0 = it.len - a.T + r0 / s.G, e1 = it.len - a.T + r1 / s.G;   // rows' own places
+    it.emin = it.len - a.T + r0 / s.G;
+    it.emax = it.len - a.T + r1 / s.G;
     const int cap = a.M * a.c.ps;
-    it.hi = min(e1 + 1, cap);
-    it.lo = a.window > 0 ? min(max(0, e0 + 1 - int(a.window)), cap) : 0;
+    it.hi = min(it.emax + 1, cap);
+    it.lo = a.window > 0 ? min(max(0, it.emin + 1 - int(a.window)), cap) : 0;
     it.first = it.lo / s.KS * s.KS;
     it.ntiles = max(1, (it.hi - it.first + s.KS - 1) / s.KS);
 }
 
-__device__ __forceinline__ int64_t seq_tiles(const PagedArgs &a, const Shape &s, int b) {
+__device__ __noinline__ int64_t seq_cost(const PagedArgs &a, const Shape &s, int b) {
     Item it;
     it.len = max(a.lens[b], 0);
     int64_t n = 0;
+#pragma unroll 1
     for (it.rb = 0; it.rb < s.nrb; ++it.rb) {
         item_range(a, s, it);
-        n += it.ntiles;
+        n += it.ntiles + kItemCost;
     }
     return n * a.c.Hkv;
 }
@@ -111,7 +125,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t w, int64_t *sums, int64_t 
 struct Line {
     int64_t total;
     int nc;
-    __device__ __forceinline__ int64_t start(int c) const { return total * c / nc; }
+    __device__ __noinline__ int64_t start(int c) const { return total * c / nc; }
 };
 
 // Where a position of the line lies; all 128 threads call it and get the same.
@@ -120,19 +134,27 @@ struct Finder {
     int b;
     int64_t off;
 
-    // The line's length (every sequence's tiles added up).
-    __device__ int64_t total(const PagedArgs &a, const Shape &s) {
+    // The line's length (every sequence's cost added up).
+    __device__ __noinline__ int64_t total(const PagedArgs &a, const Shape &s) {
         int64_t w = 0, t;
-        for (int i = threadIdx.x; i < a.B; i += 128) w += seq_tiles(a, s, i);
+#pragma unroll 1
+        for (int i = threadIdx.x; i < a.B; i += 128) w += seq_cost(a, s, i);
         block_scan(w, sums, t);
         return t;
     }
-    // The item that holds tile `at` of the line, and the tile's number in it.
-    __device__ int find(const PagedArgs &a, const Shape &s, int64_t at, Item &it) {
+    // The item that holds unit `at` of the line, and the unit's number in it.
+    struct Found {
+        Item it;
+        int unit;
+    };
+    __device__ __noinline__ Found find(const PagedArgs &a, const Shape &s, int64_t at) {
+        Found f;
+        Item &it = f.it;
         int64_t run = 0;
+#pragma unroll 1
         for (int base = 0; base < a.B && run <= at; base += 128) {
             const int i = base + threadIdx.x;
-            const int64_t w = i < a.B ? seq_tiles(a, s, i) : 0;
+            const int64_t w = i < a.B ? seq_cost(a, s, i) : 0;
             int64_t sum;
             const int64_t upto = run + block_scan(w, sums, sum);
             if (at < upto && at >= upto - w) {
@@ -144,13 +166,15 @@ struct Finder {
         __syncthreads();
         it.b = b;
         it.len = max(a.lens[it.b], 0);
-        const int64_t per = seq_tiles(a, s, it.b) / a.c.Hkv;
+        const int64_t per = seq_cost(a, s, it.b) / a.c.Hkv;
         it.hk = int(off / per);
         int64_t left = off - it.hk * per;
+#pragma unroll 1
         for (it.rb = 0;; ++it.rb) {
             item_range(a, s, it);
-            if (left < it.ntiles) return int(left);
-            left -= it.ntiles;
+            f.unit = int(left);
+            if (left < it.ntiles + kItemCost) return f;
+            left -= it.ntiles + kItemCost;
         }
     }
 };
@@ -159,16 +183,18 @@ __device__ __forceinline__ Line make_line(int64_t total, int ncta) {
     return Line{total, int(total < ncta ? total : ncta)};
 }
 
-__device__ __forceinline__ void next_item(const PagedArgs &a, const Shape &s, Item &it) {
+// len: the length of the next sequence
+__device__ __noinline__ Item next_item(const PagedArgs &a, const Shape &s, Item it, int len) {
     if (++it.rb == s.nrb) {
         it.rb = 0;
         if (++it.hk == a.c.Hkv) {
             it.hk = 0;
             ++it.b;
-            if (it.b < a.B) it.len = max(a.lens[it.b], 0);
+            it.len = max(len, 0);
         }
     }
-    if (it.b < a.B) item_range(a, s, it);
+    item_range(a, s, it);
+    return it;
 }
 
 // Partial results of the workspace: part 2 c is the first item of CTA c's
@@ -242,11 +268,14 @@ __device__ __forceinline__ float exp2_(float x) {   // 2 ulp, subnormal results 
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// two codes -> two fp16 values (exact)
-__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
-    const __half2_raw h =
-        __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(codes & 0xffffu), __NV_E4M3);
-    return uint32_t(h.x) | (uint32_t(h.y) << 16);
+// four codes -> two pairs of fp16 values (exact)
+__device__ __forceinline__ void widen4(uint32_t codes, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -255,6 +284,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
+}
+// The 8 x 8 matrix of 16-bit values that the warp holds (two to a lane), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 // Waits until the kernel before this one on the stream has finished (for a
 // launch that may start early) / lets the next one start early.
@@ -267,15 +302,16 @@ __device__ __forceinline__ void let_next_start() {
 
 // ---- the tensor-core kernel -----------------------------------------------------------
 //
-// Four warps, as WK groups of WR: the WR warps of a group take 16 query rows
+// Four warps, as WK groups of WR: the WR warps of a group take 8 NQ query rows
 // each and share the group's positions, the groups take different positions.
 // Each warp copies KW positions of a tile itself (its lanes look the pages
 // up), kStages - 1 tiles ahead, so with WR = 1 the warps run without waiting
 // for one another until an item ends.
-template <int D_, bool F8_, int WR_>
+template <int D_, bool F8_, int NQ_, int WR_>
 struct Cfg {
-    static constexpr int D = D_, WR = WR_, WK = kWarps / WR_;
+    static constexpr int D = D_, NQ = NQ_, WR = WR_, WK = kWarps / WR_;
     static constexpr bool F8 = F8_;
+    static constexpr int RB = 8 * NQ * WR;                  // rows of a row block
     static constexpr int KW = (F8 || D == 64) ? 32 : 16;    // positions a warp copies a tile
     static constexpr int KS = KW * kWarps;                  // positions of a CTA tile
     static constexpr int ROW = D * (F8 ? 1 : 2);            // bytes of a cached row
@@ -283,7 +319,7 @@ struct Cfg {
     static constexpr int STAGE = 2 * PART * kWarps;
     static constexpr int SCALES = F8 ? 2 * KW * 4 : 0;      // bytes of a warp's scales
     static constexpr int AUX = kWarps * (SCALES + 4);       // a stage's scales and mask words
-    static constexpr int XCH = (WK > 1 ? 16 * D + 32 * WR : 0) * 4;   // exchange of the groups
+    static constexpr int XCH = (WK > 1 ? 8 * NQ * D + 16 * NQ * WR : 0) * 4;   // of the groups
     static constexpr int SMEM = kStages * (STAGE + AUX) + XCH;
 };
 
@@ -296,8 +332,8 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return r * ROW + ((c ^ (r & 7)) << 4);
 }
 
-// With codes, which of a group of 16 positions stands in column n of score
-// tile j (0 or 1).  Any order does, as long as keys and values follow the same
+// With codes, which of a group of 16 positions stands in row 8 j + n of a
+// score tile.  Any order does, as long as keys and values follow the same
 // one; this one keeps both kinds of reads free of bank conflicts.
 template <int ROW>
 __device__ __forceinline__ int code_pos(int j, int n) {
@@ -309,13 +345,13 @@ __device__ __forceinline__ int code_pos(int j, int n) {
     return j + (odd ? 8 + ((2 * c) ^ 4) : 2 * c);
 }
 
-template <int D, bool F8, int WR>
+template <int D, bool F8, int NQ, int WR>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
-k_paged_mma(const PagedArgs a, const Shape s) {
-    using C = Cfg<D, F8, WR>;
-    constexpr int KW = C::KW, KS = C::KS, ROW = C::ROW, WK = C::WK;
-    constexpr int NT = KW / 8;            // score tiles of a warp's positions
-    constexpr int ND = D / 8;             // output tiles
+k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
+    using C = Cfg<D, F8, NQ, WR>;
+    constexpr int KW = C::KW, KS = C::KS, ROW = C::ROW, WK = C::WK, RB = C::RB;
+    constexpr int KT = KW / 16;           // score tiles of a warp's positions
+    constexpr int MT = D / 16;            // output tiles
     constexpr int LPR = ROW / 16;         // lanes that copy a row
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Finder finder;
@@ -328,11 +364,18 @@ k_paged_mma(const PagedArgs a, const Shape s) {
     const Line line = make_line(finder.total(a, s), s.ncta);
     if (int(blockIdx.x) >= line.nc) return;
     const int64_t beg = line.start(blockIdx.x), end = line.start(blockIdx.x + 1);
-    const int cnt = int(end - beg);
-    Item it;
-    int tile = finder.find(a, s, beg, it);
-    Item ld = it;                                 // runs ahead: the tile to be copied next
-    int ld_tile = tile, issued = 0;
+    const Finder::Found found = finder.find(a, s, beg);
+    // A cursor: an item, a tile of it, and the units left; the tiles of an item come
+    // after its constant.
+    Item it = found.it;
+    int tile = max(0, found.unit - kItemCost);
+    int64_t left = end - beg - max(0, kItemCost - found.unit);
+    // the second cursor runs ahead: the tile to be copied next
+    Item ld = it;
+    int ld_tile = tile;
+    int64_t ld_left = left;
+    auto len_after = [&](const Item &i) { return a.lens[min(i.b + 1, a.B - 1)]; };
+    int ld_len = len_after(ld);
 
     unsigned char *aux = smem + kStages * C::STAGE;
     float *xch = reinterpret_cast<float *>(aux + kStages * C::AUX);
@@ -344,41 +387,61 @@ k_paged_mma(const PagedArgs a, const Shape s) {
         return reinterpret_cast<uint32_t *>(aux + st * C::AUX + kWarps * C::SCALES) + w;
     };
 
-    // the page of this lane's position of the tile at ld (looked up a tile early)
-    int pos = 0, page = -1;
+    // Where this lane's position of the tile at ld lies, looked up a tile early.
+    const int shift = (a.c.ps & (a.c.ps - 1)) ? -1 : __ffs(a.c.ps) - 1;
+    int page = -1, at = 0;
     auto look_up = [&]() {
         page = -1;
-        if (issued >= cnt) return;
-        pos = ld.first + ld_tile * KS + warp * KW + lane;
-        if (lane < KW && pos >= ld.lo && pos < ld.hi) page = a.table[ld.b * a.tb + pos / a.c.ps];
+        const int pos = ld.first + ld_tile * KS + warp * KW + lane;
+        const int i = shift >= 0 ? pos >> shift : pos / a.c.ps;
+        at = pos - i * a.c.ps;
+        if (ld_left > 0 && lane < KW && pos >= ld.lo && pos < ld.hi) page = a.table[ld.b * a.tb + i];
     };
+    // A warp's KW rows of the pool are one run of memory where a page holds whole runs
+    // of KW positions, one after another.
+    const bool runs = a.c.ps % KW == 0 && a.c.st == D;
+    constexpr int ES = F8 ? 1 : 2, RPI = 32 / LPR;      // bytes of an element, rows a copy
+    const int lrow = lane / LPR, lch = lane % LPR;
     auto issue = [&](int st) {
-        if (issued < cnt) {
+        if (ld_left > 0) {
             const bool ok = page >= 0 && page < a.c.pages;
             const uint32_t mask = __ballot_sync(~0u, ok);
-            const int at = pos % a.c.ps;
             const int64_t off = ok ? page * a.c.sp + ld.hk * a.c.sh + at * a.c.st : 0;
             const uint32_t kdst = stage_at(st, warp), vdst = kdst + C::PART;
+            if (__all_sync(~0u, runs && mask == 0xffffffffu >> (32 - KW))) {
+                const int64_t mine = __shfl_sync(~0u, off, 0) * ES + lrow * ROW + lch * 16;
+                const char *kp = static_cast<const char *>(a.c.k) + mine;
+                const char *vp = static_cast<const char *>(a.c.v) + mine;
+#pragma unroll
+                for (int i = 0; i < KW / RPI; ++i) {
+                    const uint32_t d = chunk_at<ROW>(i * RPI + lrow, lch);
+                    const bool in = SSD_IDX_OK(a.err, mine + i * RPI * ROW + 15, a.c.n * ES);
+                    copy16(kdst + d, kp + i * RPI * ROW, in);
+                    copy16(vdst + d, vp + i * RPI * ROW, in);
+                }
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < KW / RPI; ++i) {
+                    const int r = i * RPI + lrow;
+                    const int64_t o = __shfl_sync(~0u, off, r) * ES + lch * 16;
+                    const bool in = (mask >> r) & 1 && SSD_IDX_OK(a.err, o + 15, a.c.n * ES);
+                    copy16(kdst + chunk_at<ROW>(r, lch), static_cast<const char *>(a.c.k) + o, in);
+                    copy16(vdst + chunk_at<ROW>(r, lch), static_cast<const char *>(a.c.v) + o, in);
+                }
+            }
             if constexpr (F8) {
                 const int64_t so = ok ? page * a.c.ssp + ld.hk * a.c.ssh + at : 0;
                 const uint32_t sd = smem_addr(scale_at(st, warp)) + lane * 4;
                 copy4(sd, a.c.ks + so, ok);
                 copy4(sd + KW * 4, a.c.vs + so, ok);
             }
-#pragma unroll
-            for (int i = 0; i < KW * LPR / 32; ++i) {
-                const int r = i * (32 / LPR) + lane / LPR, ch = lane % LPR;
-                const int64_t o = (__shfl_sync(~0u, off, r)) * (F8 ? 1 : 2) + ch * 16;
-                const bool rok = (mask >> r) & 1 &&
-                                 SSD_IDX_OK(a.err, o + 15, a.c.n * (F8 ? 1 : 2));
-                copy16(kdst + chunk_at<ROW>(r, ch), static_cast<const char *>(a.c.k) + o, rok);
-                copy16(vdst + chunk_at<ROW>(r, ch), static_cast<const char *>(a.c.v) + o, rok);
-            }
             if (lane == 0) *mask_at(st, warp) = mask;
-            ++issued;
+            --ld_left;
             if (++ld_tile == ld.ntiles) {
                 ld_tile = 0;
-                next_item(a, s, ld);
+                ld_left -= kItemCost;
+                ld = next_item(a, s, ld, ld_len);
+                ld_len = len_after(ld);
             }
             look_up();
         }
@@ -391,40 +454,41 @@ k_paged_mma(const PagedArgs a, const Shape s) {
     };
 
     look_up();
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) issue(i);
 
-    // Per item: the query fragments, the running maximum and sum of the rows
-    // g and g + 8 (the sum over this thread's columns), and the output.
-    uint32_t qf[D / 16][4];
-    float o[ND][4], m[2], l[2], qs[2];
+    // Per item: the query fragments (row 8 n + g of the warp's), and for the queries
+    // 8 n + 2 c + p, which this thread's columns hold, the running maximum, the sum
+    // over this thread's positions, and the output.  Scores stay as the product leaves
+    // them (times the key's scale): a row's factor qs >= 0 (scale log2(e), the sign of
+    // the scale being in the queries) enters with the exponential, p = 2^(qs s - qs m).
+    uint32_t qf[NQ][D / 16][2];
+    float o[MT][NQ][4], m[NQ][2], l[NQ][2], qs[NQ][2];
+    int e[NQ][2];                         // the rows' own places
+    const float qscale = fabsf(a.scale) * kLog2e;
+    const uint32_t qsign = a.scale < 0.f ? 0x80008000u : 0u;
     float xs = 0.f, xmax = 0.f;           // codes: the values' common factor (a power of two)
-    int e[2];                             // the rows' own places
     bool fresh = true;
     const int tile_first = tile;          // of the first item; later ones begin at 0
     bool first_item = true;
 
-    for (int n = 0, st = 0; n < cnt; ++n, st = st + 1 == kStages ? 0 : st + 1) {
+    for (int st = 0; left > 0; st = st + 1 == kStages ? 0 : st + 1) {
+        const int rows = a.T * s.G;
+        const int row0 = it.rb * RB + wr * 8 * NQ;
         if (fresh) {
             fresh = false;
-            const int rows = a.T * s.G;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = it.rb * s.RB + wr * 16 + g + 8 * i;
-                const int t = min(r, rows - 1) / s.G;
-                e[i] = it.len - a.T + t;
-                m[i] = -INFINITY;
-                l[i] = 0.f;
-                const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) +
-                                         it.b * a.q_sb + t * a.q_st +
-                                         (it.hk * s.G + min(r, rows - 1) - t * s.G) * a.q_sh;
+            for (int b = 0; b < NQ; ++b) {
+                const int r = min(row0 + 8 * b + g, rows - 1), t = r / s.G;
+                const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + it.b * a.q_sb +
+                                         t * a.q_st + (it.hk * s.G + r - t * s.G) * a.q_sh;
+                float factor = qscale;
                 if constexpr (!F8) {
-                    qs[i] = a.scale * kLog2e;
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        qf[k][i] = *reinterpret_cast<const uint32_t *>(q + 16 * k + 2 * c);
-                        qf[k][i + 2] = *reinterpret_cast<const uint32_t *>(q + 16 * k + 8 + 2 * c);
-                    }
+                    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            qf[b][k][i] = *reinterpret_cast<const uint32_t *>(q + 16 * k + 8 * i + 2 * c) ^ qsign;
                 } else {
                     // fp16 for the product with widened codes: the row is scaled by a
                     // power of two that brings its largest value to [1, 2), so all but
@@ -447,18 +511,28 @@ k_paged_mma(const PagedArgs a, const Shape s) {
                     uint32_t ex = __float_as_uint(top) & 0x7f800000u;
                     ex = ex == 0 || ex > 0x7e800000u ? 0x3f800000u : ex;
                     const float down = __uint_as_float(0x7f000000u - ex);
-                    qs[i] = a.scale * kLog2e * __uint_as_float(ex);
+                    factor *= __uint_as_float(ex);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        qf[k][i] = pack_f16(__uint_as_float(raw[k].x << 16) * down,
-                                            __uint_as_float(raw[k].x & 0xffff0000u) * down);
-                        qf[k][i + 2] = pack_f16(__uint_as_float(raw[k].y << 16) * down,
-                                                __uint_as_float(raw[k].y & 0xffff0000u) * down);
-                    }
+                    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t u = i ? raw[k].y : raw[k].x;
+                            qf[b][k][i] = pack_f16(__uint_as_float(u << 16) * down,
+                                                   __uint_as_float(u & 0xffff0000u) * down) ^ qsign;
+                        }
+                }
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    qs[b][p] = F8 ? __shfl_sync(~0u, factor, (2 * c + p) * 4) : qscale;
+                    e[b][p] = it.len - a.T + min(row0 + 8 * b + 2 * c + p, rows - 1) / s.G;
+                    m[b][p] = -INFINITY;
+                    l[b][p] = 0.f;
                 }
             }
 #pragma unroll
-            for (int j = 0; j < ND; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int b = 0; b < NQ; ++b) o[j][b][0] = o[j][b][1] = o[j][b][2] = o[j][b][3] = 0.f;
             if constexpr (F8) xs = xmax = 0.f;
         }
         copy_wait<kStages - 2>();
@@ -466,81 +540,108 @@ k_paged_mma(const PagedArgs a, const Shape s) {
         issue(st == 0 ? kStages - 1 : st - 1);
 
         const int kbase = it.first + tile * KS + kg * WR * KW;
-        const int rows = a.T * s.G;
-        const int emin = it.len - a.T + (it.rb * s.RB) / s.G;
-        const int emax = it.len - a.T + (min(it.rb * s.RB + s.RB, rows) - 1) / s.G;
 #pragma unroll 1
         for (int sub = 0; sub < WR; ++sub) {
             const int w = kg * WR + sub;
             const uint32_t mask = *mask_at(st, w);
-            if (mask == 0) continue;
             const int k0 = kbase + sub * KW;
+            // (votes, so that the compiler knows these for the same in all lanes)
+            if (!__any_sync(~0u, mask != 0)) continue;
+            const bool partial = __any_sync(~0u, k0 + KW - 1 > it.emin ||
+                                                     (a.window > 0 && k0 <= it.emax - int(a.window)));
+            const bool all = __all_sync(~0u, !partial && mask == 0xffffffffu >> (32 - KW));
             const uint32_t ksm = stage_at(st, w), vsm = ksm + C::PART;
             const float *ksc = scale_at(st, w), *vsc = ksc + KW;
+            // row g + 8 i of score tile j is position pos_of(j, i) of this warp's
+            auto pos_of = [&](int j, int i) {
+                return 16 * j + (F8 ? code_pos<ROW>(i, g) : g + 8 * i);
+            };
 
-            // scores: 16 rows x KW positions
-            float sc[NT][4];
+            // scores: KW positions x 8 NQ queries
+            float sc[KT][NQ][4];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+            for (int j = 0; j < KT; ++j)
+#pragma unroll
+                for (int b = 0; b < NQ; ++b)
+                    sc[j][b][0] = sc[j][b][1] = sc[j][b][2] = sc[j][b][3] = 0.f;
             if constexpr (!F8) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-                    for (int j = 0; j < NT; j += 2) {
-                        uint32_t b[4];
-                        ldsm4(b, ksm + chunk_at<ROW>(8 * j + (lane >> 4) * 8 + (lane & 7),
-                                                     2 * k + ((lane >> 3) & 1)));
-                        mma<false>(sc[j], qf[k], b[0], b[1]);
-                        mma<false>(sc[j + 1], qf[k], b[2], b[3]);
+                    for (int j = 0; j < KT; ++j) {
+                        uint32_t f[4];
+                        ldsm4(f, ksm + chunk_at<ROW>(16 * j + (lane & 15), 2 * k + (lane >> 4)));
+#pragma unroll
+                        for (int b = 0; b < NQ; ++b)
+                            mma<false>(sc[j][b], f, qf[b][k][0], qf[b][k][1]);
                     }
             } else {
 #pragma unroll
                 for (int h = 0; h < D / 64; ++h)
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        const int r = (j / 2) * 16 + code_pos<ROW>(j & 1, g);
-                        const uint4 u = lds16(ksm + chunk_at<ROW>(r, 4 * h + c));
-                        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+                    for (int j = 0; j < KT; ++j) {
+                        // 16 places of two positions: four steps of the product
+                        const uint4 u = lds16(ksm + chunk_at<ROW>(pos_of(j, 0), 4 * h + c));
+                        const uint4 v = lds16(ksm + chunk_at<ROW>(pos_of(j, 1), 4 * h + c));
+                        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma<true>(sc[j], qf[4 * h + k], widen2(v[k]), widen2(v[k] >> 16));
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t f[4];
+                            widen4(uu[k], f[0], f[2]);
+                            widen4(vv[k], f[1], f[3]);
+#pragma unroll
+                            for (int b = 0; b < NQ; ++b)
+                                mma<true>(sc[j][b], f, qf[b][4 * h + k][0], qf[b][4 * h + k][1]);
+                        }
                     }
-            }
-
-            // scale, mask, running maximum.  vis[i]: bit 2 j + p, row i sees
-            // position p of tile j's pair
-            const bool partial = k0 + KW - 1 > emin || (a.window > 0 && k0 <= emax - int(a.window));
-            float mn[2] = {m[0], m[1]};
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const int x = F8 ? (j / 2) * 16 + code_pos<ROW>(j & 1, 2 * c + p) : 8 * j + 2 * c + p;
-                    const float f = F8 ? ksc[x] : 1.f;
-                    const bool there = (mask >> x) & 1;
+                for (int j = 0; j < KT; ++j)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        bool see = there;
-                        if (partial) {
-                            see = see && k0 + x <= e[i];
-                            if (a.window > 0) see = see && k0 + x > e[i] - int(a.window);
-                        }
-                        float &v = sc[j][2 * i + p];
-                        v = see ? v * (F8 ? qs[i] * f : qs[i]) : -INFINITY;
-                        mn[i] = fmaxf(mn[i], v);
-                    }
-                }
-            float cor[2];
+                        const float f = ksc[pos_of(j, i)];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                mn[i] = fmaxf(mn[i], __shfl_xor_sync(~0u, mn[i], 1));
-                mn[i] = fmaxf(mn[i], __shfl_xor_sync(~0u, mn[i], 2));
+                        for (int b = 0; b < NQ; ++b) {
+                            sc[j][b][2 * i] *= f;
+                            sc[j][b][2 * i + 1] *= f;
+                        }
+                    }
             }
-            bool moved = mn[0] != m[0] || mn[1] != m[1];
+            // Masks, where some position is missing or not every row sees every one: a bit
+            // of vis for each of this thread's scores, in their order.
+            uint32_t vis = 0;
+            if (!all) {
+#pragma unroll
+                for (int j = 0; j < KT; ++j)
+#pragma unroll
+                    for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int x = pos_of(j, i >> 1), own = e[b][i & 1];
+                            bool see = (mask >> x) & 1 && k0 + x <= own;
+                            if (a.window > 0) see = see && k0 + x > own - int(a.window);
+                            vis |= uint32_t(see) << ((j * NQ + b) * 4 + i);
+                            if (!see) sc[j][b][i] = -INFINITY;
+                        }
+            }
+            float mn[NQ][2];
+            bool moved = false;
+#pragma unroll
+            for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    float v = m[b][p];
+#pragma unroll
+                    for (int j = 0; j < KT; ++j) v = fmaxf(v, fmaxf(sc[j][b][p], sc[j][b][2 + p]));
+                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
+                    mn[b][p] = v;
+                    moved = moved || v != m[b][p];
+                }
             float grow = 1.f;
             if constexpr (F8) {
                 // the values' factor must cover this tile's largest finite scale
-                const float vs = lane < KW && (mask >> lane) & 1 ? vsc[lane] : 0.f;
+                const float vs = (mask >> lane) & 1 ? vsc[lane] : 0.f;
                 const bool more = vs > xmax && vs < INFINITY;
                 if (__any_sync(~0u, more)) {
                     float top = more ? vs : 0.f;
@@ -552,100 +653,146 @@ k_paged_mma(const PagedArgs a, const Shape s) {
                     const float was = xmax;
                     xmax = __uint_as_float(ex);
                     // probability times scale goes to fp16 as p vs 2^14 / xmax <= 2^14
-                    xs = __uint_as_float(0x7f000000u - ex);
-                    grow = was * xs;      // 0 on the first tile, where o is 0
+                    const float down = __uint_as_float(0x7f000000u - ex);
+                    xs = down * 16384.f;
+                    grow = was * down;    // 0 on the first tile, where o is 0
                     moved = true;
                 }
             }
-            float base[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                base[i] = mn[i] == -INFINITY ? 0.f : mn[i];
-                cor[i] = exp2_(m[i] - base[i]);
-                m[i] = mn[i];
-            }
             if (__any_sync(~0u, moved)) {
-                l[0] *= cor[0];
-                l[1] *= cor[1];
-                const float c0 = cor[0] * grow, c1 = cor[1] * grow;
 #pragma unroll
-                for (int j = 0; j < ND; ++j) {
-                    o[j][0] *= c0;
-                    o[j][1] *= c0;
-                    o[j][2] *= c1;
-                    o[j][3] *= c1;
+                for (int b = 0; b < NQ; ++b) {
+                    float f[2];
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        f[p] = m[b][p] == -INFINITY ? 0.f : exp2_((m[b][p] - mn[b][p]) * qs[b][p]);
+                        m[b][p] = mn[b][p];
+                        l[b][p] *= f[p];
+                        f[p] *= grow;
+                    }
+#pragma unroll
+                    for (int j = 0; j < MT; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[j][b][i] *= f[i & 1];
                 }
             }
             // probabilities (unnormalised, at most 1), summed in fp32 and rounded to
-            // 16 bits as the left operand of the second product
-            uint32_t pf[NT / 2][4];
+            // 16 bits as the right operand of the second product
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+            for (int b = 0; b < NQ; ++b) {
+                const float base[2] = {m[b][0] == -INFINITY ? 0.f : m[b][0] * qs[b][0],
+                                       m[b][1] == -INFINITY ? 0.f : m[b][1] * qs[b][1]};
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float p0 = exp2_(sc[j][2 * i] - base[i]), p1 = exp2_(sc[j][2 * i + 1] - base[i]);
-                    l[i] += p0 + p1;
-                    if constexpr (F8) {
-                        const int x0 = (j / 2) * 16 + code_pos<ROW>(j & 1, 2 * c);
-                        const int x1 = (j / 2) * 16 + code_pos<ROW>(j & 1, 2 * c + 1);
-                        // what the row does not see stays 0 whatever its scale is
-                        p0 = p0 == 0.f ? 0.f : p0 * (vsc[x0] * xs * 16384.f);
-                        p1 = p1 == 0.f ? 0.f : p1 * (vsc[x1] * xs * 16384.f);
-                        pf[j / 2][(j & 1) * 2 + i] = pack_f16(p0, p1);
-                    } else {
-                        pf[j / 2][(j & 1) * 2 + i] = pack_bf16(p0, p1);
-                    }
+                for (int j = 0; j < KT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sc[j][b][i] = exp2_(fmaf(sc[j][b][i], qs[b][i & 1], -base[i & 1]));
+            }
+            auto blank = [&]() {      // what a row does not see
+#pragma unroll
+                for (int j = 0; j < KT; ++j)
+#pragma unroll
+                    for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!((vis >> ((j * NQ + b) * 4 + i)) & 1)) sc[j][b][i] = 0.f;
+            };
+            if (!all) blank();
+#pragma unroll
+            for (int j = 0; j < KT; ++j)
+#pragma unroll
+                for (int b = 0; b < NQ; ++b) {
+                    l[b][0] += sc[j][b][0] + sc[j][b][2];
+                    l[b][1] += sc[j][b][1] + sc[j][b][3];
                 }
+            if constexpr (F8) {
+#pragma unroll
+                for (int j = 0; j < KT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float f = vsc[pos_of(j, i)] * xs;
+#pragma unroll
+                        for (int b = 0; b < NQ; ++b) {
+                            sc[j][b][2 * i] *= f;
+                            sc[j][b][2 * i + 1] *= f;
+                        }
+                    }
+                if (!all) blank();    // (whatever its scale is)
+            }
+            uint32_t pf[KT][NQ][2];   // transposed: query g, positions 2 c and 2 c + 1
+#pragma unroll
+            for (int j = 0; j < KT; ++j)
+#pragma unroll
+                for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        pf[j][b][i] = transpose8(F8 ? pack_f16(sc[j][b][2 * i], sc[j][b][2 * i + 1])
+                                                    : pack_bf16(sc[j][b][2 * i], sc[j][b][2 * i + 1]));
 
-            // Values.  pv(no, 0): all rows at once.  pv(yes, r): row r alone, with the
-            // values that it does not see taken out.
+            // Values.  pv(no, 0): all queries at once.  pv(yes, r): query r alone, with
+            // the values that it does not see taken out.
             auto pv = [&](auto by_row, int row) {
                 constexpr bool kByRow = decltype(by_row)::value;
-                const int re = kByRow ? __shfl_sync(~0u, row < 8 ? e[0] : e[1], (row & 7) * 4) : 0;
-                auto keep = [&](int x) {     // position x: all bits where the row sees it
+                int re = 0;
+                if constexpr (kByRow) {
+#pragma unroll
+                    for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            const int v = __shfl_sync(~0u, e[b][p], (row & 7) >> 1);
+                            if (8 * b + p == (row & ~6)) re = v;
+                        }
+                }
+                auto keep = [&](int x) {     // all bits where the row sees position x
                     const bool see = k0 + x <= re && (a.window == 0 || k0 + x > re - int(a.window));
                     return see ? 0xffffu : 0u;
                 };
 #pragma unroll
-                for (int k = 0; k < NT / 2; ++k) {
-                    uint32_t pr[4], keep0 = 0, keep1 = 0;
+                for (int j = 0; j < KT; ++j) {
+                    uint32_t keep0 = 0, keep1 = 0;
                     if constexpr (kByRow) {
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            pr[x] = g + 8 * (x & 1) == row ? pf[k][x] : 0u;
-                        const int y = 16 * k;
-                        auto at = [&](int j, int n) { return y + (F8 ? code_pos<ROW>(j, n) : 8 * j + n); };
+                        auto at = [&](int i, int x) {
+                            return 16 * j + (F8 ? code_pos<ROW>(i, x) : 8 * i + x);
+                        };
                         keep0 = keep(at(0, 2 * c)) | keep(at(0, 2 * c + 1)) << 16;
                         keep1 = keep(at(1, 2 * c)) | keep(at(1, 2 * c + 1)) << 16;
                     }
-                    auto add = [&](float (&d)[4], uint32_t b0, uint32_t b1) {
+                    auto add = [&](int mt, uint32_t (&f)[4]) {
                         if constexpr (kByRow) {
-                            float t[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma<F8>(t, pr, b0 & keep0, b1 & keep1);
-                            if (g == (row & 7)) {
-                                if (row < 8) d[0] += t[0], d[1] += t[1];
-                                else d[2] += t[2], d[3] += t[3];
+                            f[0] &= keep0;
+                            f[1] &= keep0;
+                            f[2] &= keep1;
+                            f[3] &= keep1;
+#pragma unroll
+                            for (int b = 0; b < NQ; ++b) {
+                                const bool mine = 8 * b + g == row;
+                                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma<F8>(t, f, mine ? pf[j][b][0] : 0u, mine ? pf[j][b][1] : 0u);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (8 * b + 2 * c + (i & 1) == row) o[mt][b][i] += t[i];
                             }
                         } else {
-                            mma<F8>(d, pf[k], b0, b1);
+#pragma unroll
+                            for (int b = 0; b < NQ; ++b) mma<F8>(o[mt][b], f, pf[j][b][0], pf[j][b][1]);
                         }
                     };
                     if constexpr (!F8) {
 #pragma unroll
-                        for (int j = 0; j < ND; j += 2) {
-                            uint32_t b[4];
-                            ldsm4_trans(b, vsm + chunk_at<ROW>(16 * k + (lane & 15), j + (lane >> 4)));
-                            add(o[j], b[0], b[1]);
-                            add(o[j + 1], b[2], b[3]);
+                        for (int mt = 0; mt < MT; ++mt) {
+                            uint32_t f[4];
+                            ldsm4_trans(f, vsm + chunk_at<ROW>(16 * j + (lane & 7) + ((lane >> 4) << 3),
+                                                               2 * mt + ((lane >> 3) & 1)));
+                            add(mt, f);
                         }
                     } else {
                         // four positions' codes for the D / 8 places from (D / 8) g on;
-                        // place j of them is column g of output tile j
+                        // places 2 t and 2 t + 1 of them are rows g and g + 8 of output tile t
                         constexpr int NW = D / 32;     // words of a position
                         uint32_t v[4][NW];
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const int r = 16 * k + code_pos<ROW>(x >> 1, 2 * c + (x & 1));
+                            const int r = 16 * j + code_pos<ROW>(x >> 1, 2 * c + (x & 1));
                             if constexpr (D == 128) {
                                 const uint4 u = lds16(vsm + chunk_at<ROW>(r, g));
                                 v[x][0] = u.x, v[x][1] = u.y, v[x][2] = u.z, v[x][3] = u.w;
@@ -655,17 +802,16 @@ k_paged_mma(const PagedArgs a, const Shape s) {
                             }
                         }
 #pragma unroll
-                        for (int q = 0; q < NW; ++q) {
-                            // bytes of two positions side by side, place by place
-                            const uint32_t a0 = __byte_perm(v[0][q], v[1][q], 0x5140);
-                            const uint32_t a1 = __byte_perm(v[0][q], v[1][q], 0x7362);
-                            const uint32_t b0 = __byte_perm(v[2][q], v[3][q], 0x5140);
-                            const uint32_t b1 = __byte_perm(v[2][q], v[3][q], 0x7362);
-                            add(o[4 * q], widen2(a0), widen2(b0));
-                            add(o[4 * q + 1], widen2(a0 >> 16), widen2(b0 >> 16));
-                            add(o[4 * q + 2], widen2(a1), widen2(b1));
-                            add(o[4 * q + 3], widen2(a1 >> 16), widen2(b1 >> 16));
-                        }
+                        for (int q = 0; q < NW; ++q)
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                // bytes of two positions side by side, place by place
+                                const uint32_t sel = z ? 0x7362 : 0x5140;
+                                uint32_t f[4];
+                                widen4(__byte_perm(v[0][q], v[1][q], sel), f[0], f[1]);
+                                widen4(__byte_perm(v[2][q], v[3][q], sel), f[2], f[3]);
+                                add(2 * q + z, f);
+                            }
                     }
                 }
             };
@@ -686,142 +832,172 @@ k_paged_mma(const PagedArgs a, const Shape s) {
             }
             if (__any_sync(~0u, foul)) {
 #pragma unroll 1
-                for (int row = 0; row < 16; ++row) pv(std::true_type{}, row);
+                for (int row = 0; row < 8 * NQ; ++row) pv(std::true_type{}, row);
             } else {
                 pv(std::false_type{}, 0);
             }
         }
 
         // the item's last tile, or the stretch's: join the groups, write
-        if (tile + 1 == it.ntiles || n + 1 == cnt) {
+        if (tile + 1 == it.ntiles || left == 1) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                l[i] += __shfl_xor_sync(~0u, l[i], 1);
-                l[i] += __shfl_xor_sync(~0u, l[i], 2);
-            }
+            for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int q = 4; q < 32; q <<= 1) l[b][p] += __shfl_xor_sync(~0u, l[b][p], q);
             if constexpr (F8) {
                 const float back = xmax * (1.f / 16384.f);
 #pragma unroll
-                for (int j = 0; j < ND; ++j)
+                for (int j = 0; j < MT; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[j][i] *= back;
+                    for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[j][b][i] *= back;
             }
             if constexpr (WK > 1) {
-                // the groups' results one after another (in a fixed order), 16 D
-                // floats at a time, a lane's values 32 floats apart
-                float *ml = xch + 16 * D;
-#pragma unroll
+                // the groups' results one after another (in a fixed order), a WR-th of
+                // the places at a time, a lane's values 32 floats apart
+                constexpr int MP = MT / WR;
+                float *buf = xch + wr * (8 * NQ * D / WR), *ml = xch + 8 * NQ * D + wr * 16 * NQ;
+#pragma unroll 1
                 for (int src = 1; src < WK; ++src) {
-                    float f0[2], f1[2];
+                    float f0[NQ][2], f1[NQ][2];
 #pragma unroll
                     for (int part = 0; part < WR; ++part) {
-                        constexpr int NP = ND / WR;
-                        float *buf = xch + wr * (16 * D / WR);
                         __syncthreads();
                         if (kg == src) {
 #pragma unroll
-                            for (int j = 0; j < NP; ++j)
+                            for (int j = 0; j < MP; ++j)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    buf[(j * 4 + i) * 32 + lane] = o[part * NP + j][i];
-                            if (part == 0 && c == 0) {
-                                ml[wr * 32 + g] = m[0];
-                                ml[wr * 32 + g + 8] = m[1];
-                                ml[wr * 32 + 16 + g] = l[0];
-                                ml[wr * 32 + 24 + g] = l[1];
+                                for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        buf[((j * NQ + b) * 4 + i) * 32 + lane] = o[part * MP + j][b][i];
+                            if (part == 0 && g == 0) {
+#pragma unroll
+                                for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                                    for (int p = 0; p < 2; ++p) {
+                                        ml[8 * b + 2 * c + p] = m[b][p];
+                                        ml[8 * NQ + 8 * b + 2 * c + p] = l[b][p];
+                                    }
                             }
                         }
                         __syncthreads();
                         if (kg == 0) {
                             if (part == 0) {
 #pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    const float m1 = ml[wr * 32 + g + 8 * i];
-                                    const float mt = fmaxf(m[i], m1);
-                                    const float bs = mt == -INFINITY ? 0.f : mt;
-                                    f0[i] = exp2_(m[i] - bs);
-                                    f1[i] = exp2_(m1 - bs);
-                                    m[i] = mt;
-                                    l[i] = l[i] * f0[i] + ml[wr * 32 + 16 + g + 8 * i] * f1[i];
-                                }
+                                for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                                    for (int p = 0; p < 2; ++p) {
+                                        const float m0 = m[b][p], m1 = ml[8 * b + 2 * c + p];
+                                        const float mt = fmaxf(m0, m1);
+                                        f0[b][p] = m0 == -INFINITY ? 0.f : exp2_((m0 - mt) * qs[b][p]);
+                                        f1[b][p] = m1 == -INFINITY ? 0.f : exp2_((m1 - mt) * qs[b][p]);
+                                        m[b][p] = mt;
+                                        l[b][p] = l[b][p] * f0[b][p] +
+                                                  ml[8 * NQ + 8 * b + 2 * c + p] * f1[b][p];
+                                    }
                             }
 #pragma unroll
-                            for (int j = 0; j < NP; ++j)
+                            for (int j = 0; j < MP; ++j)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    float &v = o[part * NP + j][i];
-                                    v = v * f0[i >> 1] + buf[(j * 4 + i) * 32 + lane] * f1[i >> 1];
-                                }
+                                for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        float &v = o[part * MP + j][b][i];
+                                        v = v * f0[b][i & 1] +
+                                            buf[((j * NQ + b) * 4 + i) * 32 + lane] * f1[b][i & 1];
+                                    }
                         }
                     }
                 }
             }
             if (kg == 0) {
                 const bool whole = tile + 1 == it.ntiles && (first_item ? tile_first == 0 : true);
-                float *part = reinterpret_cast<float *>(a.ws) +
-                              size_t(2 * blockIdx.x + (first_item ? 0 : 1)) * part_floats(s.RB, D);
+                if (!whole) {
+                    float *part = reinterpret_cast<float *>(a.ws) +
+                                  size_t(2 * blockIdx.x + (first_item ? 0 : 1)) * part_floats(RB, D);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int rr = wr * 16 + g + 8 * i, r = it.rb * s.RB + rr;
-                    if (r >= rows) continue;
-                    // this thread's places: pairs 8 j + 2 c, or with codes the D / 4
-                    // places from (D / 4) c on
-                    if (!whole) {
-                        float *dst = part + rr * D;
-                        if constexpr (!F8) {
+                    for (int b = 0; b < NQ; ++b)
 #pragma unroll
-                            for (int j = 0; j < ND; ++j)
-                                *reinterpret_cast<float2 *>(dst + 8 * j + 2 * c) =
-                                    make_float2(o[j][2 * i], o[j][2 * i + 1]);
-                        } else {
+                        for (int p = 0; p < 2; ++p) {
+                            const int rr = wr * 8 * NQ + 8 * b + 2 * c + p;
+                            if (it.rb * RB + rr >= rows) continue;
+                            float *dst = part + rr * D;
+                            if constexpr (!F8) {
 #pragma unroll
-                            for (int p = 0; p < 2; ++p)
+                                for (int j = 0; j < MT; ++j)
 #pragma unroll
-                                for (int j = 0; j < ND; j += 4)
-                                    *reinterpret_cast<float4 *>(dst + ND * (2 * c + p) + j) =
-                                        make_float4(o[j][2 * i + p], o[j + 1][2 * i + p],
-                                                    o[j + 2][2 * i + p], o[j + 3][2 * i + p]);
-                        }
-                        if (c == 0) {
-                            part[s.RB * D + rr] = m[i];
-                            part[s.RB * (D + 1) + rr] = l[i];
-                        }
-                        continue;
-                    }
-                    const int t = r / s.G, h = it.hk * s.G + r - t * s.G;
-                    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-                    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + it.b * a.o_sb +
-                                         t * a.o_st + h * a.o_sh;
-                    if constexpr (!F8) {
+                                    for (int i = 0; i < 2; ++i) dst[16 * j + 8 * i + g] = o[j][b][2 * i + p];
+                            } else {
 #pragma unroll
-                        for (int j = 0; j < ND; ++j)
-                            *reinterpret_cast<uint32_t *>(dst + 8 * j + 2 * c) =
-                                pack_bf16(o[j][2 * i] * inv, o[j][2 * i + 1] * inv);
-                    } else {
-#pragma unroll
-                        for (int p = 0; p < 2; ++p)
-#pragma unroll
-                            for (int j = 0; j < ND; j += 8) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    w[q] = pack_bf16(o[j + 2 * q][2 * i + p] * inv,
-                                                     o[j + 2 * q + 1][2 * i + p] * inv);
-                                *reinterpret_cast<uint4 *>(dst + ND * (2 * c + p) + j) =
-                                    make_uint4(w[0], w[1], w[2], w[3]);
+                                for (int j = 0; j < MT; j += 2)
+                                    *reinterpret_cast<float4 *>(dst + (D / 8) * g + 2 * j) =
+                                        make_float4(o[j][b][p], o[j][b][2 + p], o[j + 1][b][p],
+                                                    o[j + 1][b][2 + p]);
                             }
+                            if (g == 0) {
+                                part[RB * D + rr] = m[b][p] == -INFINITY ? m[b][p] : m[b][p] * qs[b][p];
+                                part[RB * (D + 1) + rr] = l[b][p];
+                            }
+                        }
+                } else {
+                    auto out_row = [&](int r) {
+                        const int t = r / s.G;
+                        return static_cast<__nv_bfloat16 *>(a.out) + it.b * a.o_sb + t * a.o_st +
+                               (it.hk * s.G + r - t * s.G) * a.o_sh;
+                    };
+#pragma unroll
+                    for (int b = 0; b < NQ; ++b) {
+                        float inv[2];
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            inv[p] = l[b][p] == 0.f ? 0.f : 1.f / l[b][p];
+                            const int r = row0 + 8 * b + 2 * c + p;
+                            if (r >= rows) continue;
+                            if constexpr (F8) {
+                                __nv_bfloat16 *dst = out_row(r) + (D / 8) * g;
+#pragma unroll
+                                for (int j = 0; j < MT; j += 4) {
+                                    uint32_t w[4];
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q)
+                                        w[q] = pack_bf16(o[j + q][b][p] * inv[p], o[j + q][b][2 + p] * inv[p]);
+                                    *reinterpret_cast<uint4 *>(dst + 2 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+                                }
+                            }
+                            if (a.lse && g == 0) {
+                                const int t = r / s.G;
+                                a.lse[(int64_t(it.b) * a.T + t) * a.Hq + it.hk * s.G + r - t * s.G] =
+                                    l[b][p] == 0.f ? -INFINITY : (m[b][p] * qs[b][p] + log2f(l[b][p])) * kLn2;
+                            }
+                        }
+                        if constexpr (!F8) {
+                            const int r = row0 + 8 * b + g;     // transposed: a quad writes a row's eight places
+                            __nv_bfloat16 *dst = out_row(min(r, rows - 1));
+#pragma unroll
+                            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const uint32_t v = transpose8(pack_bf16(o[j][b][2 * i] * inv[0],
+                                                                            o[j][b][2 * i + 1] * inv[1]));
+                                    if (r < rows)
+                                        *reinterpret_cast<uint32_t *>(dst + 16 * j + 8 * i + 2 * c) = v;
+                                }
+                        }
                     }
-                    if (a.lse && c == 0)
-                        a.lse[(int64_t(it.b) * a.T + t) * a.Hq + h] =
-                            l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
                 }
             }
         }
+        --left;
         if (++tile == it.ntiles) {
             tile = 0;
+            left -= kItemCost;
             first_item = false;
             fresh = true;
-            next_item(a, s, it);
+            it = next_item(a, s, it, len_after(it));
         }
     }
     copy_wait<0>();
@@ -832,16 +1008,18 @@ k_paged_mma(const PagedArgs a, const Shape s) {
 // CTA (x, y): rows 4 y.. of the item that the cut between CTAs x and x + 1
 // falls into, if it is that item's first cut; a warp a row.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) k_paged_join(const PagedArgs a, const Shape s) {
+__global__ void __launch_bounds__(128) k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
     __shared__ Finder finder;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int x = blockIdx.x;
     const Line line = make_line(finder.total(a, s), s.ncta);
     if (x + 1 >= line.nc) return;
     const int64_t cut = line.start(x + 1);
-    Item it;
-    const int64_t t0 = cut - finder.find(a, s, cut, it), t1 = t0 + it.ntiles;
-    if (t0 == cut || line.start(x) > t0) return;     // no item is cut here, or not first
+    const Finder::Found found = finder.find(a, s, cut);
+    const Item it = found.it;
+    const int64_t t0 = cut - found.unit, tiles = t0 + kItemCost, t1 = tiles + it.ntiles;
+    // no tiles of one item on both sides of the cut, or not its first such cut
+    if (cut <= tiles || line.start(x) > tiles) return;
     const int rr = blockIdx.y * 4 + warp, r = it.rb * s.RB + rr;
     if (rr >= s.RB || r >= a.T * s.G) return;
 
@@ -965,14 +1143,14 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t> (&done)[4]) {
     return e;
 }
 
-template <int D, bool F8, int WR>
+template <int D, bool F8, int NQ, int WR>
 cudaError_t launch_mma(const PagedArgs &a, Shape s, cudaStream_t stream) {
-    using C = Cfg<D, F8, WR>;
+    using C = Cfg<D, F8, NQ, WR>;
     static std::atomic<uint64_t> done[4];
     s.KS = C::KS;
-    cudaError_t e = allow_smem(k_paged_mma<D, F8, WR>, C::SMEM, done);
+    cudaError_t e = allow_smem(k_paged_mma<D, F8, NQ, WR>, C::SMEM, done);
     if (e != cudaSuccess) return e;
-    k_paged_mma<D, F8, WR><<<s.ncta, kWarps * 32, C::SMEM, stream>>>(a, s);
+    k_paged_mma<D, F8, NQ, WR><<<s.ncta, kWarps * 32, C::SMEM, stream>>>(a, s);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // The join may start while the last parts are being computed; it waits for
     // them before it reads any.
@@ -988,16 +1166,14 @@ cudaError_t launch_mma(const PagedArgs &a, Shape s, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, k_paged_join<__nv_bfloat16, D>, a, s);
 }
 
-// Warps along the rows of a key/value head: 16 rows each, the rest of the
-// four along the positions.  More rows than 64 are several row blocks, each of
-// which reads the cache.
-int row_warps(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
-
+// Rows of a block: 8 or 16 to a warp, then up to four warps along the rows (and
+// the rest of the four along the positions).  More rows than 64 are several row
+// blocks, each of which reads the cache.
 Shape make_shape(const PagedArgs &a) {
     Shape s{};
     s.G = a.Hq / a.c.Hkv;
     const int64_t rows = int64_t(a.T) * s.G;
-    s.RB = 16 * row_warps(rows);
+    s.RB = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     s.nrb = int((rows + s.RB - 1) / s.RB);
     s.ncta = device_sm_count() * kCtasPerSm;
     return s;
@@ -1007,9 +1183,10 @@ template <int D, bool F8>
 cudaError_t launch_rows(const PagedArgs &a, cudaStream_t stream) {
     const Shape s = make_shape(a);
     switch (s.RB) {
-    case 16: return launch_mma<D, F8, 1>(a, s, stream);
-    case 32: return launch_mma<D, F8, 2>(a, s, stream);
-    default: return launch_mma<D, F8, 4>(a, s, stream);
+    case 8: return launch_mma<D, F8, 1, 1>(a, s, stream);
+    case 16: return launch_mma<D, F8, 2, 1>(a, s, stream);
+    case 32: return launch_mma<D, F8, 2, 2>(a, s, stream);
+    default: return launch_mma<D, F8, 2, 4>(a, s, stream);
     }
 }
 
