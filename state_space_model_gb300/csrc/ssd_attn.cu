@@ -38,8 +38,13 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 4;                 // of a CTA of the tensor-core kernel
-constexpr int kCtasPerSm = 2;
-constexpr int kStages = 3;
+#ifndef X_CTAS
+#define X_CTAS 2
+#define X_STAGES 3
+#endif
+// CTAs an SM, and tiles of copies a warp has room for, by the queries of a warp (NQ)
+constexpr int ctas_per_sm(int nq) { return nq == 1 ? X_CTAS : 2; }
+constexpr int stages(int nq) { return nq == 1 ? X_STAGES : 3; }
 
 // ---- the schedule -----------------------------------------------------------------
 //
@@ -122,66 +127,74 @@ __device__ __forceinline__ int64_t block_scan(int64_t w, int64_t *sums, int64_t 
     return w + before;
 }
 
-struct Line {
-    int64_t total;
-    int nc;
-    __device__ __noinline__ int64_t start(int c) const { return total * c / nc; }
+__device__ __noinline__ int64_t divide(int64_t x, int64_t y) {   // both >= 0; mostly short
+    return ((x | y) >> 32) == 0 ? int64_t(uint32_t(x) / uint32_t(y)) : x / y;
+}
+
+// A stretch of the line: CTA c takes units [c part, (c + 1) part) of total.
+struct Stretch {
+    Item it;              // the item that holds its first unit
+    int unit;             // that unit's number in the item
+    int64_t beg, left;    // the first unit, how many
+    int64_t part;
 };
 
-// Where a position of the line lies; all 128 threads call it and get the same.
+// All 128 threads call it, and get the same; left <= 0: there is none.
 struct Finder {
     int64_t sums[4];
     int b;
     int64_t off;
 
-    // The line's length (every sequence's cost added up).
-    __device__ __noinline__ int64_t total(const PagedArgs &a, const Shape &s) {
-        int64_t w = 0, t;
+    __device__ __noinline__ Stretch find(const PagedArgs &a, const Shape &s, int cta) {
+        Stretch f;
+        int64_t total = 0, w = 0, upto = 0;
 #pragma unroll 1
-        for (int i = threadIdx.x; i < a.B; i += 128) w += seq_cost(a, s, i);
-        block_scan(w, sums, t);
-        return t;
-    }
-    // The item that holds unit `at` of the line, and the unit's number in it.
-    struct Found {
-        Item it;
-        int unit;
-    };
-    __device__ __noinline__ Found find(const PagedArgs &a, const Shape &s, int64_t at) {
-        Found f;
-        Item &it = f.it;
+        for (int base = 0; base < a.B; base += 128) {
+            const int i = base + threadIdx.x;
+            int64_t sum;
+            w = i < a.B ? seq_cost(a, s, i) : 0;
+            upto = total + block_scan(w, sums, sum);
+            total += sum;
+        }
+        f.part = divide(total + s.ncta - 1, s.ncta);
+        f.beg = cta * f.part;
+        f.left = min(f.part, total - f.beg);
+        if (f.left <= 0) return f;
         int64_t run = 0;
 #pragma unroll 1
-        for (int base = 0; base < a.B && run <= at; base += 128) {
+        for (int base = 0; base < a.B && run <= f.beg; base += 128) {
             const int i = base + threadIdx.x;
-            const int64_t w = i < a.B ? seq_cost(a, s, i) : 0;
-            int64_t sum;
-            const int64_t upto = run + block_scan(w, sums, sum);
-            if (at < upto && at >= upto - w) {
-                b = i;
-                off = at - (upto - w);
+            if (a.B > 128) {      // else w and upto are still there
+                int64_t sum;
+                w = i < a.B ? seq_cost(a, s, i) : 0;
+                upto = run + block_scan(w, sums, sum);
+                run += sum;
             }
-            run += sum;
+            if (f.beg < upto && f.beg >= upto - w) {
+                b = i;
+                off = f.beg - (upto - w);
+            }
         }
         __syncthreads();
+        Item &it = f.it;
         it.b = b;
         it.len = max(a.lens[it.b], 0);
-        const int64_t per = seq_cost(a, s, it.b) / a.c.Hkv;
-        it.hk = int(off / per);
-        int64_t left = off - it.hk * per;
+        it.hk = 0;
+        int64_t rest = off;
+        if (a.c.Hkv > 1) {
+            const int64_t per = divide(seq_cost(a, s, it.b), a.c.Hkv);
+            it.hk = int(divide(off, per));
+            rest = off - it.hk * per;
+        }
 #pragma unroll 1
         for (it.rb = 0;; ++it.rb) {
             item_range(a, s, it);
-            f.unit = int(left);
-            if (left < it.ntiles + kItemCost) return f;
-            left -= it.ntiles + kItemCost;
+            f.unit = int(rest);
+            if (rest < it.ntiles + kItemCost) return f;
+            rest -= it.ntiles + kItemCost;
         }
     }
 };
-
-__device__ __forceinline__ Line make_line(int64_t total, int ncta) {
-    return Line{total, int(total < ncta ? total : ncta)};
-}
 
 // len: the length of the next sequence
 __device__ __noinline__ Item next_item(const PagedArgs &a, const Shape &s, Item it, int len) {
@@ -197,10 +210,22 @@ __device__ __noinline__ Item next_item(const PagedArgs &a, const Shape &s, Item 
     return it;
 }
 
-// Partial results of the workspace: part 2 c is the first item of CTA c's
-// stretch, part 2 c + 1 its last (if that is another).
+// The workspace: a Cut for each CTA, then the partial results, output rows and
+// their maxima (in log2 units) and sums.  Part 2 c is the first item of CTA
+// c's stretch, part 2 c + 1 its last (if that is another).  The CTA that has an
+// item's first tiles, but not all, says in its Cut who has the others.
+struct __align__(16) Cut {
+    int parts;            // CTAs that share the item, from this one on; 0: none
+    int first;            // this one's part, 0 or 1 (the others' is 0)
+    int b, hk, rb;
+    int pad[3];
+};
 __host__ __device__ __forceinline__ size_t part_floats(int RB, int D) {
     return size_t(RB) * (D + 2);
+}
+__device__ __forceinline__ float *part_at(const PagedArgs &a, const Shape &s, int i) {
+    return reinterpret_cast<float *>(a.ws + s.ncta * sizeof(Cut)) +
+           size_t(i) * part_floats(s.RB, a.c.D);
 }
 
 // ---- PTX ---------------------------------------------------------------------------
@@ -305,12 +330,13 @@ __device__ __forceinline__ void let_next_start() {
 // Four warps, as WK groups of WR: the WR warps of a group take 8 NQ query rows
 // each and share the group's positions, the groups take different positions.
 // Each warp copies KW positions of a tile itself (its lanes look the pages
-// up), kStages - 1 tiles ahead, so with WR = 1 the warps run without waiting
+// up), STAGES - 1 tiles ahead, so with WR = 1 the warps run without waiting
 // for one another until an item ends.
 template <int D_, bool F8_, int NQ_, int WR_>
 struct Cfg {
     static constexpr int D = D_, NQ = NQ_, WR = WR_, WK = kWarps / WR_;
     static constexpr bool F8 = F8_;
+    static constexpr int STAGES = stages(NQ);
     static constexpr int RB = 8 * NQ * WR;                  // rows of a row block
     static constexpr int KW = (F8 || D == 64) ? 32 : 16;    // positions a warp copies a tile
     static constexpr int KS = KW * kWarps;                  // positions of a CTA tile
@@ -320,7 +346,7 @@ struct Cfg {
     static constexpr int SCALES = F8 ? 2 * KW * 4 : 0;      // bytes of a warp's scales
     static constexpr int AUX = kWarps * (SCALES + 4);       // a stage's scales and mask words
     static constexpr int XCH = (WK > 1 ? 8 * NQ * D + 16 * NQ * WR : 0) * 4;   // of the groups
-    static constexpr int SMEM = kStages * (STAGE + AUX) + XCH;
+    static constexpr int SMEM = STAGES * (STAGE + AUX) + XCH;
 };
 
 // Byte offset of 16-byte chunk c of row r: chunks are exchanged so that the
@@ -346,9 +372,10 @@ __device__ __forceinline__ int code_pos(int j, int n) {
 }
 
 template <int D, bool F8, int NQ, int WR>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
+__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NQ))
 k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
     using C = Cfg<D, F8, NQ, WR>;
+    constexpr int kStages = C::STAGES;
     constexpr int KW = C::KW, KS = C::KS, ROW = C::ROW, WK = C::WK, RB = C::RB;
     constexpr int KT = KW / 16;           // score tiles of a warp's positions
     constexpr int MT = D / 16;            // output tiles
@@ -361,15 +388,14 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     const int kg = warp / WR, wr = warp % WR;     // key group, row warp
     const int g = lane >> 2, c = lane & 3;        // fragment row and column pair
 
-    const Line line = make_line(finder.total(a, s), s.ncta);
-    if (int(blockIdx.x) >= line.nc) return;
-    const int64_t beg = line.start(blockIdx.x), end = line.start(blockIdx.x + 1);
-    const Finder::Found found = finder.find(a, s, beg);
+    const Stretch span = finder.find(a, s, blockIdx.x);
+    if (threadIdx.x == 0) reinterpret_cast<Cut *>(a.ws)[blockIdx.x].parts = 0;
     // A cursor: an item, a tile of it, and the units left; the tiles of an item come
     // after its constant.
-    Item it = found.it;
-    int tile = max(0, found.unit - kItemCost);
-    int64_t left = end - beg - max(0, kItemCost - found.unit);
+    Item it = span.it;
+    int tile = max(0, span.unit - kItemCost);
+    int64_t left = span.left - max(0, kItemCost - span.unit);
+    if (span.left <= 0 || left <= 0) return;
     // the second cursor runs ahead: the tile to be copied next
     Item ld = it;
     int ld_tile = tile;
@@ -917,8 +943,18 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             if (kg == 0) {
                 const bool whole = tile + 1 == it.ntiles && (first_item ? tile_first == 0 : true);
                 if (!whole) {
-                    float *part = reinterpret_cast<float *>(a.ws) +
-                                  size_t(2 * blockIdx.x + (first_item ? 0 : 1)) * part_floats(RB, D);
+                    float *part = part_at(a, s, 2 * blockIdx.x + (first_item ? 0 : 1));
+                    if (threadIdx.x == 0 && !(first_item && tile_first > 0)) {
+                        // its first tiles, the first of them `tile` + 1 units (and so many tiles) ago
+                        const int64_t t1 = span.beg + span.left + it.ntiles - tile - 1;
+                        Cut cut;
+                        cut.parts = int(divide(t1 + span.part - 1, span.part)) - int(blockIdx.x);
+                        cut.first = first_item ? 0 : 1;
+                        cut.b = it.b;
+                        cut.hk = it.hk;
+                        cut.rb = it.rb;
+                        reinterpret_cast<Cut *>(a.ws)[blockIdx.x] = cut;
+                    }
 #pragma unroll
                     for (int b = 0; b < NQ; ++b)
 #pragma unroll
@@ -1005,67 +1041,76 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
 
 // ---- the join -------------------------------------------------------------------------
 //
-// CTA (x, y): rows 4 y.. of the item that the cut between CTAs x and x + 1
-// falls into, if it is that item's first cut; a warp a row.
+// CTA (x, y): row y of the item whose first part CTA x left; its four warps take
+// every fourth part each.
+constexpr int kJoinAhead = 8;     // parts that a warp loads at once
 template <typename T, int D>
-__global__ void __launch_bounds__(128) k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
-    __shared__ Finder finder;
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int x = blockIdx.x;
-    const Line line = make_line(finder.total(a, s), s.ncta);
-    if (x + 1 >= line.nc) return;
-    const int64_t cut = line.start(x + 1);
-    const Finder::Found found = finder.find(a, s, cut);
-    const Item it = found.it;
-    const int64_t t0 = cut - found.unit, tiles = t0 + kItemCost, t1 = tiles + it.ntiles;
-    // no tiles of one item on both sides of the cut, or not its first such cut
-    if (cut <= tiles || line.start(x) > tiles) return;
-    const int rr = blockIdx.y * 4 + warp, r = it.rb * s.RB + rr;
-    if (rr >= s.RB || r >= a.T * s.G) return;
-
+__global__ void __launch_bounds__(128)
+k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
     constexpr int E = D / 32;
+    __shared__ float sm_m[4], sm_l[4], sm_o[4][D];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, x = blockIdx.x, rr = blockIdx.y;
     wait_for_previous();
-    const float *parts = reinterpret_cast<const float *>(a.ws);
+    const Cut it = reinterpret_cast<const Cut *>(a.ws)[x];
+    const int r = it.rb * s.RB + rr;
+    if (it.parts == 0 || r >= a.T * s.G) return;
+
     float m = -INFINITY, l = 0.f, o[E] = {};
-    for (int c0 = x; c0 < line.nc && line.start(c0) < t1; c0 += 32) {
-        // up to 32 parts: lane i weighs part c0 + i
-        const int n = min(32, line.nc - c0), cc = c0 + lane;
-        float pm = -INFINITY, pl = 0.f;
-        const bool there = lane < n && line.start(cc) < t1;
-        const float *part = parts + size_t(2 * cc + (line.start(cc) < t0 ? 1 : 0)) * part_floats(s.RB, D);
-        if (there) {
-            pm = part[s.RB * D + rr];
-            pl = part[s.RB * (D + 1) + rr];
+#pragma unroll 1
+    for (int c0 = warp; c0 < it.parts; c0 += 4 * kJoinAhead) {
+        float v[kJoinAhead][E], pm[kJoinAhead], pl[kJoinAhead];
+#pragma unroll
+        for (int u = 0; u < kJoinAhead; ++u) {
+            const int c = c0 + 4 * u;
+            pm[u] = -INFINITY;
+            pl[u] = 0.f;
+            if (c < it.parts) {
+                const float *part = part_at(a, s, 2 * (x + c) + (c == 0 ? it.first : 0));
+                pm[u] = part[s.RB * D + rr];
+                pl[u] = part[s.RB * (D + 1) + rr];
+#pragma unroll
+                for (int j = 0; j < E; ++j) v[u][j] = part[rr * D + lane * E + j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < E; ++j) v[u][j] = 0.f;
+            }
         }
-        float mt = fmaxf(m, pm);
+        float mt = m;
 #pragma unroll
-        for (int w = 16; w; w >>= 1) mt = fmaxf(mt, __shfl_xor_sync(~0u, mt, w));
-        const float base = mt == -INFINITY ? 0.f : mt;
-        const float f = exp2_(pm - base), old = exp2_(m - base);
+        for (int u = 0; u < kJoinAhead; ++u) mt = fmaxf(mt, pm[u]);
+        const float base = mt == -INFINITY ? 0.f : mt, old = exp2_(m - base);
         m = mt;
-        float sum = pl * f;
+        l *= old;
 #pragma unroll
-        for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(~0u, sum, w);
-        l = l * old + sum;
+        for (int j = 0; j < E; ++j) o[j] *= old;
 #pragma unroll
-        for (int i = 0; i < E; ++i) o[i] *= old;
-        const int k = __popc(__ballot_sync(~0u, there));
-#pragma unroll 4
-        for (int i = 0; i < k; ++i) {
-            const float w = __shfl_sync(~0u, f, i);
-            const float *src = parts + size_t(2 * (c0 + i) + (line.start(c0 + i) < t0 ? 1 : 0)) *
-                                           part_floats(s.RB, D) + rr * D + lane * E;
+        for (int u = 0; u < kJoinAhead; ++u) {
+            const float f = exp2_(pm[u] - base);
+            l = fmaf(pl[u], f, l);
 #pragma unroll
-            for (int j = 0; j < E; ++j) o[j] = fmaf(src[j], w, o[j]);
+            for (int j = 0; j < E; ++j) o[j] = fmaf(v[u][j], f, o[j]);
         }
     }
-    const int t = r / s.G, h = it.hk * s.G + r - t * s.G;
-    T *dst = static_cast<T *>(a.out) + it.b * a.o_sb + t * a.o_st + h * a.o_sh + lane * E;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (lane == 0) sm_m[warp] = m, sm_l[warp] = l;
 #pragma unroll
-    for (int j = 0; j < E; ++j) dst[j] = T(o[j] * inv);
-    if (a.lse && lane == 0)
-        a.lse[(int64_t(it.b) * a.T + t) * a.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    for (int j = 0; j < E; ++j) sm_o[warp][lane * E + j] = o[j];
+    __syncthreads();
+    const float mt = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
+    const float base = mt == -INFINITY ? 0.f : mt;
+    l = 0.f;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float f = exp2_(sm_m[w] - base);
+        l = fmaf(sm_l[w], f, l);
+        if (threadIdx.x < D) v = fmaf(sm_o[w][threadIdx.x], f, v);
+    }
+    const int t = r / s.G, h = it.hk * s.G + r - t * s.G;
+    if (threadIdx.x < D)
+        static_cast<T *>(a.out)[it.b * a.o_sb + t * a.o_st + h * a.o_sh + threadIdx.x] =
+            T(l == 0.f ? 0.f : v / l);
+    if (a.lse && threadIdx.x == 0)
+        a.lse[(int64_t(it.b) * a.T + t) * a.Hq + h] = l == 0.f ? -INFINITY : (mt + log2f(l)) * kLn2;
 }
 
 // ---- fp32 -------------------------------------------------------------------------------
@@ -1158,7 +1203,7 @@ cudaError_t launch_mma(const PagedArgs &a, Shape s, cudaStream_t stream) {
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(unsigned(s.ncta - 1), unsigned((min(s.RB, a.T * s.G) + 3) / 4));
+    cfg.gridDim = dim3(unsigned(s.ncta), unsigned(min(s.RB, a.T * s.G)));
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cfg.attrs = &at;
@@ -1175,7 +1220,7 @@ Shape make_shape(const PagedArgs &a) {
     const int64_t rows = int64_t(a.T) * s.G;
     s.RB = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     s.nrb = int((rows + s.RB - 1) / s.RB);
-    s.ncta = device_sm_count() * kCtasPerSm;
+    s.ncta = device_sm_count() * ctas_per_sm(s.RB == 8 ? 1 : 2);
     return s;
 }
 
@@ -1204,7 +1249,7 @@ cudaError_t launch_d(const PagedArgs &a, cudaStream_t stream) {
 size_t paged_workspace(const PagedArgs &a) {
     if (a.c.dt == DT_F32) return 0;
     const Shape s = make_shape(a);
-    return size_t(2) * s.ncta * part_floats(s.RB, a.c.D) * sizeof(float);
+    return s.ncta * (sizeof(Cut) + 2 * part_floats(s.RB, a.c.D) * sizeof(float));
 }
 
 cudaError_t launch_paged(const PagedArgs &in, cudaStream_t s) {
