@@ -19,7 +19,9 @@
 // columns, but its operands come from shared and tensor memory: 8-bit codes
 // would have to be widened there and back, and probabilities stored.  At 8 to
 // 16 queries mma.sync needs a fifth to a third of the time of the reads.)
+#include "ptx_sm100.cuh"
 #include "ssd_attn.h"
+#include "ssd_block_math.cuh"
 #include "ssd_debug.cuh"
 #include "ssd_tc.cuh"
 
@@ -36,15 +38,12 @@
 namespace ssd {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kWarps = 4;                 // of a CTA of the tensor-core kernel
-#ifndef X_CTAS
-#define X_CTAS 2
-#define X_STAGES 3
-#endif
-// CTAs an SM, and tiles of copies a warp has room for, by the queries of a warp (NQ)
-constexpr int ctas_per_sm(int nq) { return nq == 1 ? X_CTAS : 2; }
-constexpr int stages(int nq) { return nq == 1 ? X_STAGES : 3; }
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kWarps = 4;                 // of a CTA that compute
+constexpr int kCopyWarps = 2;             // and that copy
+constexpr int kThreads = 32 * (kWarps + kCopyWarps);
+constexpr int kCtasPerSm = 2;
+constexpr int kStages = 3;                // tiles that a CTA has room for
 
 // ---- the schedule -----------------------------------------------------------------
 //
@@ -105,8 +104,7 @@ __device__ __noinline__ int64_t seq_cost(const PagedArgs &a, const Shape &s, int
     return n * a.c.Hkv;
 }
 
-// Block-wide (128 threads): the inclusive prefix of w over the threads, and
-// the block's sum.
+// Block-wide: the inclusive prefix of w over the threads, and the block's sum.
 __device__ __forceinline__ int64_t block_scan(int64_t w, int64_t *sums, int64_t &total) {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
 #pragma unroll
@@ -120,7 +118,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t w, int64_t *sums, int64_t 
     int64_t before = 0;
     total = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kThreads / 32; ++i) {
         if (i < warp) before += sums[i];
         total += sums[i];
     }
@@ -139,9 +137,9 @@ struct Stretch {
     int64_t part;
 };
 
-// All 128 threads call it, and get the same; left <= 0: there is none.
+// All threads of a CTA call it, and get the same; left <= 0: there is none.
 struct Finder {
-    int64_t sums[4];
+    int64_t sums[kThreads / 32];
     int b;
     int64_t off;
 
@@ -149,7 +147,7 @@ struct Finder {
         Stretch f;
         int64_t total = 0, w = 0, upto = 0;
 #pragma unroll 1
-        for (int base = 0; base < a.B; base += 128) {
+        for (int base = 0; base < a.B; base += kThreads) {
             const int i = base + threadIdx.x;
             int64_t sum;
             w = i < a.B ? seq_cost(a, s, i) : 0;
@@ -162,9 +160,9 @@ struct Finder {
         if (f.left <= 0) return f;
         int64_t run = 0;
 #pragma unroll 1
-        for (int base = 0; base < a.B && run <= f.beg; base += 128) {
+        for (int base = 0; base < a.B && run <= f.beg; base += kThreads) {
             const int i = base + threadIdx.x;
-            if (a.B > 128) {      // else w and upto are still there
+            if (a.B > kThreads) {      // else w and upto are still there
                 int64_t sum;
                 w = i < a.B ? seq_cost(a, s, i) : 0;
                 upto = run + block_scan(w, sums, sum);
@@ -244,12 +242,14 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool ok) {
                  "l"(__cvta_generic_to_global(src)), "r"(ok ? 4 : 0)
                  : "memory");
 }
-__device__ __forceinline__ void copy_commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
+// An arrival at bar once this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
 }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// The computing warps of a CTA wait for one another.
+__device__ __forceinline__ void warps_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -266,6 +266,16 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(at));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds1(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds2(uint32_t at) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
     return v;
 }
 __device__ __forceinline__ uint2 lds8(uint32_t at) {
@@ -288,11 +298,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float exp2_(float x) {   // 2 ulp, subnormal results flushed
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 // four codes -> two pairs of fp16 values (exact)
 __device__ __forceinline__ void widen4(uint32_t codes, uint32_t &lo, uint32_t &hi) {
     asm("{\n\t.reg .b16 a, b;\n\t"
@@ -301,10 +306,6 @@ __device__ __forceinline__ void widen4(uint32_t codes, uint32_t &lo, uint32_t &h
         "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
         : "=r"(lo), "=r"(hi)
         : "r"(codes));
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -327,26 +328,24 @@ __device__ __forceinline__ void let_next_start() {
 
 // ---- the tensor-core kernel -----------------------------------------------------------
 //
-// Four warps, as WK groups of WR: the WR warps of a group take 8 NQ query rows
-// each and share the group's positions, the groups take different positions.
-// Each warp copies KW positions of a tile itself (its lanes look the pages
-// up), STAGES - 1 tiles ahead, so with WR = 1 the warps run without waiting
-// for one another until an item ends.
+// Four warps compute, as WK groups of WR: the WR warps of a group take 8 NQ
+// query rows each and share the group's positions, the groups take different
+// positions.  Two more warps copy, up to kStages tiles ahead, across items:
+// looking up pages and making addresses took a third of the computing warps'
+// instructions when each copied its own, and one warp cannot keep up.  Two CTAs fill an SM, so 128 KB of
+// copies are under way while two tiles are worked on.
 template <int D_, bool F8_, int NQ_, int WR_>
 struct Cfg {
     static constexpr int D = D_, NQ = NQ_, WR = WR_, WK = kWarps / WR_;
     static constexpr bool F8 = F8_;
-    static constexpr int STAGES = stages(NQ);
     static constexpr int RB = 8 * NQ * WR;                  // rows of a row block
-    static constexpr int KW = (F8 || D == 64) ? 32 : 16;    // positions a warp copies a tile
-    static constexpr int KS = KW * kWarps;                  // positions of a CTA tile
+    static constexpr int KW = (F8 || D == 64) ? 32 : 16;    // positions of a warp's part of a tile
+    static constexpr int KS = KW * kWarps;                  // positions of a tile
     static constexpr int ROW = D * (F8 ? 1 : 2);            // bytes of a cached row
-    static constexpr int PART = KW * ROW;                   // bytes of a warp's keys (or values)
-    static constexpr int STAGE = 2 * PART * kWarps;
-    static constexpr int SCALES = F8 ? 2 * KW * 4 : 0;      // bytes of a warp's scales
-    static constexpr int AUX = kWarps * (SCALES + 4);       // a stage's scales and mask words
+    static constexpr int STAGE = 2 * KS * ROW;              // keys, then values
+    static constexpr int AUX = (F8 ? 2 * KS * 4 : 0) + 16;  // key and value scales, mask words
     static constexpr int XCH = (WK > 1 ? 8 * NQ * D + 16 * NQ * WR : 0) * 4;   // of the groups
-    static constexpr int SMEM = STAGES * (STAGE + AUX) + XCH;
+    static constexpr int SMEM = kStages * (STAGE + AUX) + XCH;
 };
 
 // Byte offset of 16-byte chunk c of row r: chunks are exchanged so that the
@@ -371,23 +370,199 @@ __device__ __forceinline__ int code_pos(int j, int n) {
     return j + (odd ? 8 + ((2 * c) ^ 4) : 2 * c);
 }
 
+// Position r of a tile: its row of the keys (or values), see chunk_at.
+template <typename C>
+struct Room {
+    unsigned char *smem;
+    __device__ __forceinline__ uint32_t keys(int st) const { return smem_addr(smem) + st * C::STAGE; }
+    __device__ __forceinline__ uint32_t values(int st) const { return keys(st) + C::KS * C::ROW; }
+    __device__ __forceinline__ unsigned char *aux(int st) const {
+        return smem + kStages * C::STAGE + st * C::AUX;
+    }
+    // the key scales of a tile, then its value scales
+    __device__ __forceinline__ float *scales(int st) const { return reinterpret_cast<float *>(aux(st)); }
+    // bit r % 32 of word r / 32: position r is there
+    __device__ __forceinline__ uint32_t *masks(int st) const {
+        return reinterpret_cast<uint32_t *>(aux(st) + C::AUX - 16);
+    }
+    __device__ __forceinline__ float *exchange() const {
+        return reinterpret_cast<float *>(aux(kStages));
+    }
+};
+
+// The left operand of the second product from the values at vsm: output tile by
+// output tile for the 16 positions of score tile j, use(tile, fragment).
+template <typename C, typename Use>
+__device__ __forceinline__ void value_tiles(uint32_t vsm, int j, Use &&use) {
+    constexpr int ROW = C::ROW, D = C::D;
+    const int lane = threadIdx.x % 32, g = lane >> 2, c = lane & 3;
+    if constexpr (!C::F8) {
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) {
+            uint32_t f[4];
+            ldsm4_trans(f, vsm + chunk_at<ROW>(16 * j + (lane & 7) + ((lane >> 4) << 3),
+                                               2 * mt + ((lane >> 3) & 1)));
+            use(mt, f);
+        }
+    } else {
+        // four positions' codes for the D / 8 places from (D / 8) g on;
+        // places 2 t and 2 t + 1 of them are rows g and g + 8 of output tile t
+        constexpr int NW = D / 32;     // words of a position
+        uint32_t v[4][NW];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int r = 16 * j + code_pos<ROW>(x >> 1, 2 * c + (x & 1));
+            if constexpr (D == 128) {
+                const uint4 u = lds16(vsm + chunk_at<ROW>(r, g));
+                v[x][0] = u.x, v[x][1] = u.y, v[x][2] = u.z, v[x][3] = u.w;
+            } else {
+                const uint2 u = lds8(vsm + chunk_at<ROW>(r, g >> 1) + (g & 1) * 8);
+                v[x][0] = u.x, v[x][1] = u.y;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < NW; ++q)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                // bytes of two positions side by side, place by place
+                const uint32_t sel = z ? 0x7362 : 0x5140;
+                uint32_t f[4];
+                widen4(__byte_perm(v[0][q], v[1][q], sel), f[0], f[1]);
+                widen4(__byte_perm(v[2][q], v[3][q], sel), f[2], f[3]);
+                use(2 * q + z, f);
+            }
+    }
+}
+
+// Infinities and NaN of a pair of 16-bit values, replaced by 0.
+template <bool F16>
+__device__ __forceinline__ uint32_t finite2(uint32_t v) {
+    const uint32_t top = F16 ? 0x7c00u : 0x7f80u;
+    if ((v & top) == top) v &= 0xffff0000u;
+    if ((v & (top << 16)) == top << 16) v &= 0xffffu;
+    return v;
+}
+
+// Waits for a phase of bar (bounded: false after two seconds); the wait itself is out
+// of line.
+__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity) {
+    return ptx::mbar_wait(bar, parity);
+}
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
+    return __all_sync(~0u, ptx::mbar_try_wait(bar, parity)) ||
+           __all_sync(~0u, wait_long(bar, parity));
+}
+
+// A copying warp: fills its part of the stages with the stretch's tiles, one after
+// another.  full[st] is arrived at by each lane's copies as they land and by lane 0
+// for the masks, empty[st] by each computing warp.
+template <typename C>
+__device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, const Room<C> room,
+                                           uint64_t *full, uint64_t *empty, Item it, int tile,
+                                           int64_t left, int first) {
+    constexpr int KS = C::KS, ROW = C::ROW, D = C::D, ES = C::F8 ? 1 : 2;
+    constexpr int N = KS / 32 / kCopyWarps;                 // runs of 32 positions: first.. of a tile
+    constexpr int LPR = ROW / 16, RPI = 32 / LPR;           // lanes a row, rows a copy
+    constexpr int RUN = 16;
+    const int lane = threadIdx.x % 32;
+    const int lrow = lane / LPR, lch = lane % LPR;
+    const int shift = (a.c.ps & (a.c.ps - 1)) ? -1 : __ffs(a.c.ps) - 1;
+    // RUN positions of one page after another in memory
+    const bool runs = a.c.ps % RUN == 0 && a.c.st == D;
+    const char *const kpool = static_cast<const char *>(a.c.k);
+    const char *const vpool = static_cast<const char *>(a.c.v);
+
+    // Where this lane's positions of the next tile lie (lane + 32 i), looked up a tile
+    // early, and the length of the next sequence.
+    int page[N], at[N];
+    int len = a.lens[min(it.b + 1, a.B - 1)];
+    auto look_up = [&]() {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            page[i] = -1;
+            const int pos = it.first + tile * KS + 32 * (first + i) + lane;
+            const int p = shift >= 0 ? pos >> shift : pos / a.c.ps;
+            at[i] = pos - p * a.c.ps;
+            if (left > 0 && pos >= it.lo && pos < it.hi) page[i] = a.table[it.b * a.tb + p];
+        }
+    };
+    look_up();
+    for (int n = 0, st = 0; left > 0; ++n, st = st + 1 == kStages ? 0 : st + 1) {
+        if (n >= kStages && !wait_for(&empty[st], (n / kStages - 1) & 1))
+            return false;
+        uint32_t mask[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const bool ok = page[i] >= 0 && page[i] < a.c.pages;
+            mask[i] = __ballot_sync(~0u, ok);
+            const int64_t off = ok ? page[i] * a.c.sp + it.hk * a.c.sh + at[i] * a.c.st : 0;
+            const uint32_t kdst = room.keys(st) + 32 * (first + i) * ROW;
+            const uint32_t vdst = room.values(st) + 32 * (first + i) * ROW;
+            if (__all_sync(~0u, runs && mask[i] == ~0u)) {
+#pragma unroll
+                for (int h = 0; h < 32 / RUN; ++h) {
+                    const int64_t mine = __shfl_sync(~0u, off, h * RUN) * ES + lrow * ROW + lch * 16;
+#pragma unroll
+                    for (int j = 0; j < RUN / RPI; ++j) {
+                        const uint32_t d = chunk_at<ROW>(h * RUN + j * RPI + lrow, lch);
+                        const bool in = SSD_IDX_OK(a.err, mine + j * RPI * ROW + 15, a.c.n * ES);
+                        copy16(kdst + d, kpool + mine + j * RPI * ROW, in);
+                        copy16(vdst + d, vpool + mine + j * RPI * ROW, in);
+                    }
+                }
+            } else if (__any_sync(~0u, mask[i] != 0)) {
+#pragma unroll 1
+                for (int j = 0; j < LPR; ++j) {
+                    const int r = j * RPI + lrow;
+                    const int64_t o = __shfl_sync(~0u, off, r) * ES + lch * 16;
+                    const bool in = (mask[i] >> r) & 1 && SSD_IDX_OK(a.err, o + 15, a.c.n * ES);
+                    copy16(kdst + chunk_at<ROW>(r, lch), kpool + o, in);
+                    copy16(vdst + chunk_at<ROW>(r, lch), vpool + o, in);
+                }
+            }
+            if constexpr (C::F8) {
+                const int64_t so = ok ? page[i] * a.c.ssp + it.hk * a.c.ssh + at[i] : 0;
+                const uint32_t d = smem_addr(room.scales(st)) + (32 * (first + i) + lane) * 4;
+                copy4(d, a.c.ks + so, ok);
+                copy4(d + KS * 4, a.c.vs + so, ok);
+            }
+        }
+        copies_arrive(&full[st]);
+        if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) room.masks(st)[first + i] = mask[i];
+            ptx::mbar_arrive(&full[st]);
+        }
+        --left;
+        if (++tile == it.ntiles) {
+            tile = 0;
+            left -= kItemCost;
+            it = next_item(a, s, it, len);
+            len = a.lens[min(it.b + 1, a.B - 1)];
+        }
+        look_up();
+    }
+    return true;
+}
+
 template <int D, bool F8, int NQ, int WR>
-__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(NQ))
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
 k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
     using C = Cfg<D, F8, NQ, WR>;
-    constexpr int kStages = C::STAGES;
     constexpr int KW = C::KW, KS = C::KS, ROW = C::ROW, WK = C::WK, RB = C::RB;
     constexpr int KT = KW / 16;           // score tiles of a warp's positions
     constexpr int MT = D / 16;            // output tiles
-    constexpr int LPR = ROW / 16;         // lanes that copy a row
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Finder finder;
+    __shared__ uint64_t full[kStages], empty[kStages];
 
     let_next_start();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int kg = warp / WR, wr = warp % WR;     // key group, row warp
-    const int g = lane >> 2, c = lane & 3;        // fragment row and column pair
-
+    if (threadIdx.x < kStages) {
+        ptx::mbar_init(&full[threadIdx.x], kCopyWarps * (32 + 1));
+        ptx::mbar_init(&empty[threadIdx.x], kWarps);
+    }
+    // (its barriers also make the initialised ones visible)
     const Stretch span = finder.find(a, s, blockIdx.x);
     if (threadIdx.x == 0) reinterpret_cast<Cut *>(a.ws)[blockIdx.x].parts = 0;
     // A cursor: an item, a tile of it, and the units left; the tiles of an item come
@@ -396,92 +571,16 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     int tile = max(0, span.unit - kItemCost);
     int64_t left = span.left - max(0, kItemCost - span.unit);
     if (span.left <= 0 || left <= 0) return;
-    // the second cursor runs ahead: the tile to be copied next
-    Item ld = it;
-    int ld_tile = tile;
-    int64_t ld_left = left;
-    auto len_after = [&](const Item &i) { return a.lens[min(i.b + 1, a.B - 1)]; };
-    int ld_len = len_after(ld);
-
-    unsigned char *aux = smem + kStages * C::STAGE;
-    float *xch = reinterpret_cast<float *>(aux + kStages * C::AUX);
-    auto stage_at = [&](int st, int w) { return smem_addr(smem) + st * C::STAGE + w * 2 * C::PART; };
-    auto scale_at = [&](int st, int w) {
-        return reinterpret_cast<float *>(aux + st * C::AUX + w * C::SCALES);
-    };
-    auto mask_at = [&](int st, int w) {
-        return reinterpret_cast<uint32_t *>(aux + st * C::AUX + kWarps * C::SCALES) + w;
-    };
-
-    // Where this lane's position of the tile at ld lies, looked up a tile early.
-    const int shift = (a.c.ps & (a.c.ps - 1)) ? -1 : __ffs(a.c.ps) - 1;
-    int page = -1, at = 0;
-    auto look_up = [&]() {
-        page = -1;
-        const int pos = ld.first + ld_tile * KS + warp * KW + lane;
-        const int i = shift >= 0 ? pos >> shift : pos / a.c.ps;
-        at = pos - i * a.c.ps;
-        if (ld_left > 0 && lane < KW && pos >= ld.lo && pos < ld.hi) page = a.table[ld.b * a.tb + i];
-    };
-    // A warp's KW rows of the pool are one run of memory where a page holds whole runs
-    // of KW positions, one after another.
-    const bool runs = a.c.ps % KW == 0 && a.c.st == D;
-    constexpr int ES = F8 ? 1 : 2, RPI = 32 / LPR;      // bytes of an element, rows a copy
-    const int lrow = lane / LPR, lch = lane % LPR;
-    auto issue = [&](int st) {
-        if (ld_left > 0) {
-            const bool ok = page >= 0 && page < a.c.pages;
-            const uint32_t mask = __ballot_sync(~0u, ok);
-            const int64_t off = ok ? page * a.c.sp + ld.hk * a.c.sh + at * a.c.st : 0;
-            const uint32_t kdst = stage_at(st, warp), vdst = kdst + C::PART;
-            if (__all_sync(~0u, runs && mask == 0xffffffffu >> (32 - KW))) {
-                const int64_t mine = __shfl_sync(~0u, off, 0) * ES + lrow * ROW + lch * 16;
-                const char *kp = static_cast<const char *>(a.c.k) + mine;
-                const char *vp = static_cast<const char *>(a.c.v) + mine;
-#pragma unroll
-                for (int i = 0; i < KW / RPI; ++i) {
-                    const uint32_t d = chunk_at<ROW>(i * RPI + lrow, lch);
-                    const bool in = SSD_IDX_OK(a.err, mine + i * RPI * ROW + 15, a.c.n * ES);
-                    copy16(kdst + d, kp + i * RPI * ROW, in);
-                    copy16(vdst + d, vp + i * RPI * ROW, in);
-                }
-            } else {
-#pragma unroll 1
-                for (int i = 0; i < KW / RPI; ++i) {
-                    const int r = i * RPI + lrow;
-                    const int64_t o = __shfl_sync(~0u, off, r) * ES + lch * 16;
-                    const bool in = (mask >> r) & 1 && SSD_IDX_OK(a.err, o + 15, a.c.n * ES);
-                    copy16(kdst + chunk_at<ROW>(r, lch), static_cast<const char *>(a.c.k) + o, in);
-                    copy16(vdst + chunk_at<ROW>(r, lch), static_cast<const char *>(a.c.v) + o, in);
-                }
-            }
-            if constexpr (F8) {
-                const int64_t so = ok ? page * a.c.ssp + ld.hk * a.c.ssh + at : 0;
-                const uint32_t sd = smem_addr(scale_at(st, warp)) + lane * 4;
-                copy4(sd, a.c.ks + so, ok);
-                copy4(sd + KW * 4, a.c.vs + so, ok);
-            }
-            if (lane == 0) *mask_at(st, warp) = mask;
-            --ld_left;
-            if (++ld_tile == ld.ntiles) {
-                ld_tile = 0;
-                ld_left -= kItemCost;
-                ld = next_item(a, s, ld, ld_len);
-                ld_len = len_after(ld);
-            }
-            look_up();
-        }
-        copy_commit();       // an empty group where nothing is left, so that the count goes on
-    };
-    auto group_sync = [&]() {
-        if constexpr (WR == 1) __syncwarp();
-        else if constexpr (WR == kWarps) __syncthreads();
-        else asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(32 * WR) : "memory");
-    };
-
-    look_up();
-#pragma unroll 1
-    for (int i = 0; i < kStages - 1; ++i) issue(i);
+    const Room<C> room{smem};
+    if (warp >= kWarps) {
+        if (!copy_tiles<C>(a, s, room, full, empty, it, tile, left,
+                           (warp - kWarps) * (KS / 32 / kCopyWarps)) && lane == 0)
+            atomicOr(a.err, kErrTimeout);
+        return;
+    }
+    const int kg = warp / WR, wr = warp % WR;     // key group, row warp
+    const int g = lane >> 2, c = lane & 3;        // fragment row and column pair
+    float *xch = room.exchange();
 
     // Per item: the query fragments (row 8 n + g of the warp's), and for the queries
     // 8 n + 2 c + p, which this thread's columns hold, the running maximum, the sum
@@ -498,7 +597,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     const int tile_first = tile;          // of the first item; later ones begin at 0
     bool first_item = true;
 
-    for (int st = 0; left > 0; st = st + 1 == kStages ? 0 : st + 1) {
+    for (int n = 0, st = 0; left > 0; ++n, st = st + 1 == kStages ? 0 : st + 1) {
         const int rows = a.T * s.G;
         const int row0 = it.rb * RB + wr * 8 * NQ;
         if (fresh) {
@@ -561,23 +660,22 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                 for (int b = 0; b < NQ; ++b) o[j][b][0] = o[j][b][1] = o[j][b][2] = o[j][b][3] = 0.f;
             if constexpr (F8) xs = xmax = 0.f;
         }
-        copy_wait<kStages - 2>();
-        group_sync();        // the group's copies are there, and its last tile is done with
-        issue(st == 0 ? kStages - 1 : st - 1);
-
+        if (!wait_for(&full[st], (n / kStages) & 1)) {
+            if (lane == 0) atomicOr(a.err, kErrTimeout);
+            return;      // all four warps wait for the same copies, so none is left at a barrier
+        }
         const int kbase = it.first + tile * KS + kg * WR * KW;
 #pragma unroll 1
         for (int sub = 0; sub < WR; ++sub) {
-            const int w = kg * WR + sub;
-            const uint32_t mask = *mask_at(st, w);
-            const int k0 = kbase + sub * KW;
+            const int w = kg * WR + sub, k0 = kbase + sub * KW;
+            const uint32_t mask = (room.masks(st)[w * KW / 32] >> (w * KW % 32)) & (0xffffffffu >> (32 - KW));
             // (votes, so that the compiler knows these for the same in all lanes)
             if (!__any_sync(~0u, mask != 0)) continue;
             const bool partial = __any_sync(~0u, k0 + KW - 1 > it.emin ||
                                                      (a.window > 0 && k0 <= it.emax - int(a.window)));
             const bool all = __all_sync(~0u, !partial && mask == 0xffffffffu >> (32 - KW));
-            const uint32_t ksm = stage_at(st, w), vsm = ksm + C::PART;
-            const float *ksc = scale_at(st, w), *vsc = ksc + KW;
+            const uint32_t ksm = room.keys(st) + w * KW * ROW, vsm = room.values(st) + w * KW * ROW;
+            const float *ksc = room.scales(st) + w * KW, *vsc = ksc + KS;
             // row g + 8 i of score tile j is position pos_of(j, i) of this warp's
             auto pos_of = [&](int j, int i) {
                 return 16 * j + (F8 ? code_pos<ROW>(i, g) : g + 8 * i);
@@ -691,7 +789,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                     float f[2];
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
-                        f[p] = m[b][p] == -INFINITY ? 0.f : exp2_((m[b][p] - mn[b][p]) * qs[b][p]);
+                        f[p] = m[b][p] == -INFINITY ? 0.f : ex2((m[b][p] - mn[b][p]) * qs[b][p]);
                         m[b][p] = mn[b][p];
                         l[b][p] *= f[p];
                         f[p] *= grow;
@@ -712,7 +810,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                 for (int j = 0; j < KT; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        sc[j][b][i] = exp2_(fmaf(sc[j][b][i], qs[b][i & 1], -base[i & 1]));
+                        sc[j][b][i] = ex2(fmaf(sc[j][b][i], qs[b][i & 1], -base[i & 1]));
             }
             auto blank = [&]() {      // what a row does not see
 #pragma unroll
@@ -755,99 +853,15 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                         pf[j][b][i] = transpose8(F8 ? pack_f16(sc[j][b][2 * i], sc[j][b][2 * i + 1])
                                                     : pack_bf16(sc[j][b][2 * i], sc[j][b][2 * i + 1]));
 
-            // Values.  pv(no, 0): all queries at once.  pv(yes, r): query r alone, with
-            // the values that it does not see taken out.
-            auto pv = [&](auto by_row, int row) {
-                constexpr bool kByRow = decltype(by_row)::value;
-                int re = 0;
-                if constexpr (kByRow) {
-#pragma unroll
-                    for (int b = 0; b < NQ; ++b)
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            const int v = __shfl_sync(~0u, e[b][p], (row & 7) >> 1);
-                            if (8 * b + p == (row & ~6)) re = v;
-                        }
-                }
-                auto keep = [&](int x) {     // all bits where the row sees position x
-                    const bool see = k0 + x <= re && (a.window == 0 || k0 + x > re - int(a.window));
-                    return see ? 0xffffu : 0u;
-                };
-#pragma unroll
-                for (int j = 0; j < KT; ++j) {
-                    uint32_t keep0 = 0, keep1 = 0;
-                    if constexpr (kByRow) {
-                        auto at = [&](int i, int x) {
-                            return 16 * j + (F8 ? code_pos<ROW>(i, x) : 8 * i + x);
-                        };
-                        keep0 = keep(at(0, 2 * c)) | keep(at(0, 2 * c + 1)) << 16;
-                        keep1 = keep(at(1, 2 * c)) | keep(at(1, 2 * c + 1)) << 16;
-                    }
-                    auto add = [&](int mt, uint32_t (&f)[4]) {
-                        if constexpr (kByRow) {
-                            f[0] &= keep0;
-                            f[1] &= keep0;
-                            f[2] &= keep1;
-                            f[3] &= keep1;
-#pragma unroll
-                            for (int b = 0; b < NQ; ++b) {
-                                const bool mine = 8 * b + g == row;
-                                float t[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma<F8>(t, f, mine ? pf[j][b][0] : 0u, mine ? pf[j][b][1] : 0u);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    if (8 * b + 2 * c + (i & 1) == row) o[mt][b][i] += t[i];
-                            }
-                        } else {
-#pragma unroll
-                            for (int b = 0; b < NQ; ++b) mma<F8>(o[mt][b], f, pf[j][b][0], pf[j][b][1]);
-                        }
-                    };
-                    if constexpr (!F8) {
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            uint32_t f[4];
-                            ldsm4_trans(f, vsm + chunk_at<ROW>(16 * j + (lane & 7) + ((lane >> 4) << 3),
-                                                               2 * mt + ((lane >> 3) & 1)));
-                            add(mt, f);
-                        }
-                    } else {
-                        // four positions' codes for the D / 8 places from (D / 8) g on;
-                        // places 2 t and 2 t + 1 of them are rows g and g + 8 of output tile t
-                        constexpr int NW = D / 32;     // words of a position
-                        uint32_t v[4][NW];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int r = 16 * j + code_pos<ROW>(x >> 1, 2 * c + (x & 1));
-                            if constexpr (D == 128) {
-                                const uint4 u = lds16(vsm + chunk_at<ROW>(r, g));
-                                v[x][0] = u.x, v[x][1] = u.y, v[x][2] = u.z, v[x][3] = u.w;
-                            } else {
-                                const uint2 u = lds8(vsm + chunk_at<ROW>(r, g >> 1) + (g & 1) * 8);
-                                v[x][0] = u.x, v[x][1] = u.y;
-                            }
-                        }
-#pragma unroll
-                        for (int q = 0; q < NW; ++q)
-#pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                // bytes of two positions side by side, place by place
-                                const uint32_t sel = z ? 0x7362 : 0x5140;
-                                uint32_t f[4];
-                                widen4(__byte_perm(v[0][q], v[1][q], sel), f[0], f[1]);
-                                widen4(__byte_perm(v[2][q], v[3][q], sel), f[2], f[3]);
-                                add(2 * q + z, f);
-                            }
-                    }
-                }
-            };
             // Where rows of one warp see different positions, an infinity or NaN that one
-            // row does not see must not meet its zero probability in the product: such a
-            // tile (the values are looked through first) is taken row by row.
+            // row does not see must not meet its zero probability in the product.  A tile
+            // that holds one (the values are looked through first) goes into the product
+            // with zeros in their place, after they were added to the rows that see them
+            // (a probability makes no difference to an infinity or NaN).
             bool foul = false;
             if (partial) {
-#pragma unroll
-                for (int x = 0; x < C::PART / 512; ++x) {
+#pragma unroll 1
+                for (int x = 0; x < KW * ROW / 512; ++x) {
                     const uint4 u = lds16(vsm + (x * 32 + lane) * 16);
                     const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -855,14 +869,55 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                         foul |= F8 ? (((v[y] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0
                                    : (v[y] & 0x7f80u) == 0x7f80u || (v[y] & 0x7f800000u) == 0x7f800000u;
                 }
+                foul = __any_sync(~0u, foul);
             }
-            if (__any_sync(~0u, foul)) {
-#pragma unroll 1
-                for (int row = 0; row < 8 * NQ; ++row) pv(std::true_type{}, row);
+            if (!foul) {
+#pragma unroll
+                for (int j = 0; j < KT; ++j)
+                    value_tiles<C>(vsm, j, [&](int mt, uint32_t (&f)[4]) {
+#pragma unroll
+                        for (int b = 0; b < NQ; ++b) mma<F8>(o[mt][b], f, pf[j][b][0], pf[j][b][1]);
+                    });
             } else {
-                pv(std::false_type{}, 0);
+#pragma unroll 1
+                for (int y = 0; y < KW * (D / 32); ++y) {
+                    const int x = y / (D / 32), mine = 32 * (y % (D / 32)) + lane;   // position, place
+                    const uint32_t at = vsm + chunk_at<ROW>(x, mine * (F8 ? 1 : 2) / 16) +
+                                        mine * (F8 ? 1 : 2) % 16;
+                    float v;
+                    if constexpr (F8) v = (lds1(at) & 0x7f) == 0x7f ? NAN : 0.f;
+                    else v = __uint_as_float(lds2(at) << 16);
+                    for (uint32_t bad = __ballot_sync(~0u, !isfinite(v)); bad; bad &= bad - 1) {
+                        const int from = __ffs(bad) - 1, d = 32 * (y % (D / 32)) + from;
+                        const float add = __shfl_sync(~0u, v, from);
+                        // place d is row dr of output tile dt, in the lanes of group dg
+                        const int dg = F8 ? d / (D / 8) : d % 8;
+                        const int half = F8 ? d % 2 : d / 8 % 2, dt = F8 ? d % (D / 8) / 2 : d / 16;
+#pragma unroll
+                        for (int j = 0; j < MT; ++j)
+#pragma unroll
+                            for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const int own = e[b][i & 1];
+                                    const bool see = k0 + x <= own &&
+                                                     (a.window == 0 || k0 + x > own - int(a.window));
+                                    if (j == dt && g == dg && i >> 1 == half && see) o[j][b][i] += add;
+                                }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < KT; ++j)
+                    value_tiles<C>(vsm, j, [&](int mt, uint32_t (&f)[4]) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[i] = finite2<F8>(f[i]);
+#pragma unroll
+                        for (int b = 0; b < NQ; ++b) mma<F8>(o[mt][b], f, pf[j][b][0], pf[j][b][1]);
+                    });
             }
         }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&empty[st]);
 
         // the item's last tile, or the stretch's: join the groups, write
         if (tile + 1 == it.ntiles || left == 1) {
@@ -891,7 +946,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                     float f0[NQ][2], f1[NQ][2];
 #pragma unroll
                     for (int part = 0; part < WR; ++part) {
-                        __syncthreads();
+                        warps_sync();
                         if (kg == src) {
 #pragma unroll
                             for (int j = 0; j < MP; ++j)
@@ -910,7 +965,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                                     }
                             }
                         }
-                        __syncthreads();
+                        warps_sync();
                         if (kg == 0) {
                             if (part == 0) {
 #pragma unroll
@@ -919,8 +974,8 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                                     for (int p = 0; p < 2; ++p) {
                                         const float m0 = m[b][p], m1 = ml[8 * b + 2 * c + p];
                                         const float mt = fmaxf(m0, m1);
-                                        f0[b][p] = m0 == -INFINITY ? 0.f : exp2_((m0 - mt) * qs[b][p]);
-                                        f1[b][p] = m1 == -INFINITY ? 0.f : exp2_((m1 - mt) * qs[b][p]);
+                                        f0[b][p] = m0 == -INFINITY ? 0.f : ex2((m0 - mt) * qs[b][p]);
+                                        f1[b][p] = m1 == -INFINITY ? 0.f : ex2((m1 - mt) * qs[b][p]);
                                         m[b][p] = mt;
                                         l[b][p] = l[b][p] * f0[b][p] +
                                                   ml[8 * NQ + 8 * b + 2 * c + p] * f1[b][p];
@@ -1033,10 +1088,9 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             left -= kItemCost;
             first_item = false;
             fresh = true;
-            it = next_item(a, s, it, len_after(it));
+            it = next_item(a, s, it, a.lens[min(it.b + 1, a.B - 1)]);
         }
     }
-    copy_wait<0>();
 }
 
 // ---- the join -------------------------------------------------------------------------
@@ -1078,14 +1132,14 @@ k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape 
         float mt = m;
 #pragma unroll
         for (int u = 0; u < kJoinAhead; ++u) mt = fmaxf(mt, pm[u]);
-        const float base = mt == -INFINITY ? 0.f : mt, old = exp2_(m - base);
+        const float base = mt == -INFINITY ? 0.f : mt, old = ex2(m - base);
         m = mt;
         l *= old;
 #pragma unroll
         for (int j = 0; j < E; ++j) o[j] *= old;
 #pragma unroll
         for (int u = 0; u < kJoinAhead; ++u) {
-            const float f = exp2_(pm[u] - base);
+            const float f = ex2(pm[u] - base);
             l = fmaf(pl[u], f, l);
 #pragma unroll
             for (int j = 0; j < E; ++j) o[j] = fmaf(v[u][j], f, o[j]);
@@ -1101,7 +1155,7 @@ k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape 
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-        const float f = exp2_(sm_m[w] - base);
+        const float f = ex2(sm_m[w] - base);
         l = fmaf(sm_l[w], f, l);
         if (threadIdx.x < D) v = fmaf(sm_o[w][threadIdx.x], f, v);
     }
@@ -1195,7 +1249,7 @@ cudaError_t launch_mma(const PagedArgs &a, Shape s, cudaStream_t stream) {
     s.KS = C::KS;
     cudaError_t e = allow_smem(k_paged_mma<D, F8, NQ, WR>, C::SMEM, done);
     if (e != cudaSuccess) return e;
-    k_paged_mma<D, F8, NQ, WR><<<s.ncta, kWarps * 32, C::SMEM, stream>>>(a, s);
+    k_paged_mma<D, F8, NQ, WR><<<s.ncta, kThreads, C::SMEM, stream>>>(a, s);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // The join may start while the last parts are being computed; it waits for
     // them before it reads any.
@@ -1220,7 +1274,7 @@ Shape make_shape(const PagedArgs &a) {
     const int64_t rows = int64_t(a.T) * s.G;
     s.RB = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     s.nrb = int((rows + s.RB - 1) / s.RB);
-    s.ncta = device_sm_count() * ctas_per_sm(s.RB == 8 ? 1 : 2);
+    s.ncta = device_sm_count() * kCtasPerSm;
     return s;
 }
 
