@@ -58,7 +58,7 @@ constexpr int kStages = 3;                // tiles that a CTA has room for
 // cut falls into is finished by the join kernel from the parts that its CTAs
 // leave in the workspace.  An item without positions has one (masked) tile,
 // so that somebody writes its rows.
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 3;
 
 struct Shape {            // of the schedule: what both kernels derive alike
     int KS;               // positions of a tile
@@ -344,8 +344,9 @@ struct Cfg {
     static constexpr int ROW = D * (F8 ? 1 : 2);            // bytes of a cached row
     static constexpr int STAGE = 2 * KS * ROW;              // keys, then values
     static constexpr int AUX = (F8 ? 2 * KS * 4 : 0) + 16;  // key and value scales, mask words
-    static constexpr int XCH = (WK > 1 ? 8 * NQ * D + 16 * NQ * WR : 0) * 4;   // of the groups
-    static constexpr int SMEM = kStages * (STAGE + AUX) + XCH;
+    static constexpr int SMEM = kStages * (STAGE + AUX);
+    // at an item's end the warps' outputs (f32) meet in the stage of its last tile
+    static_assert(kWarps * 8 * NQ * D * 4 <= STAGE, "the outputs fit a stage");
 };
 
 // Byte offset of 16-byte chunk c of row r: chunks are exchanged so that the
@@ -384,9 +385,6 @@ struct Room {
     // bit r % 32 of word r / 32: position r is there
     __device__ __forceinline__ uint32_t *masks(int st) const {
         return reinterpret_cast<uint32_t *>(aux(st) + C::AUX - 16);
-    }
-    __device__ __forceinline__ float *exchange() const {
-        return reinterpret_cast<float *>(aux(kStages));
     }
 };
 
@@ -555,6 +553,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Finder finder;
     __shared__ uint64_t full[kStages], empty[kStages];
+    __shared__ float top_of[kWarps][8 * NQ], sum_of[kWarps][8 * NQ];
 
     let_next_start();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -580,7 +579,6 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     }
     const int kg = warp / WR, wr = warp % WR;     // key group, row warp
     const int g = lane >> 2, c = lane & 3;        // fragment row and column pair
-    float *xch = room.exchange();
 
     // Per item: the query fragments (row 8 n + g of the warp's), and for the queries
     // 8 n + 2 c + p, which this thread's columns hold, the running maximum, the sum
@@ -593,44 +591,53 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     const float qscale = fabsf(a.scale) * kLog2e;
     const uint32_t qsign = a.scale < 0.f ? 0x80008000u : 0u;
     float xs = 0.f, xmax = 0.f;           // codes: the values' common factor (a power of two)
+    const int rows = a.T * s.G;
+    auto load_queries = [&]() {           // of the item at `it`, used once `fresh` is seen
+#pragma unroll
+        for (int b = 0; b < NQ; ++b) {
+            const int r = min(it.rb * RB + wr * 8 * NQ + 8 * b + g, rows - 1), t = r / s.G;
+            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + it.b * a.q_sb +
+                                     t * a.q_st + (it.hk * s.G + r - t * s.G) * a.q_sh;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                if constexpr (F8) {       // places 64 h + 16 c + 4 (k % 4)
+                    const uint2 u = *reinterpret_cast<const uint2 *>(q + (k / 4) * 64 + 16 * c + 4 * (k % 4));
+                    qf[b][k][0] = u.x;
+                    qf[b][k][1] = u.y;
+                } else {
+                    qf[b][k][0] = *reinterpret_cast<const uint32_t *>(q + 16 * k + 2 * c);
+                    qf[b][k][1] = *reinterpret_cast<const uint32_t *>(q + 16 * k + 8 + 2 * c);
+                }
+            }
+        }
+    };
+    load_queries();
     bool fresh = true;
     const int tile_first = tile;          // of the first item; later ones begin at 0
     bool first_item = true;
 
     for (int n = 0, st = 0; left > 0; ++n, st = st + 1 == kStages ? 0 : st + 1) {
-        const int rows = a.T * s.G;
-        const int row0 = it.rb * RB + wr * 8 * NQ;
         if (fresh) {
             fresh = false;
 #pragma unroll
             for (int b = 0; b < NQ; ++b) {
-                const int r = min(row0 + 8 * b + g, rows - 1), t = r / s.G;
-                const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + it.b * a.q_sb +
-                                         t * a.q_st + (it.hk * s.G + r - t * s.G) * a.q_sh;
                 float factor = qscale;
                 if constexpr (!F8) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            qf[b][k][i] = *reinterpret_cast<const uint32_t *>(q + 16 * k + 8 * i + 2 * c) ^ qsign;
+                        for (int i = 0; i < 2; ++i) qf[b][k][i] ^= qsign;
                 } else {
                     // fp16 for the product with widened codes: the row is scaled by a
                     // power of two that brings its largest value to [1, 2), so all but
                     // values 2^-14 times as large stay exact
                     float top = 0.f;
-                    uint2 raw[D / 16];
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {   // places 64 h + 16 c + 4 (k % 4)
-                        raw[k] = *reinterpret_cast<const uint2 *>(q + (k / 4) * 64 + 16 * c +
-                                                                  4 * (k % 4));
+                    for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-                        for (int w = 0; w < 2; ++w) {
-                            const uint32_t u = w ? raw[k].y : raw[k].x;
-                            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u << 16)),
-                                                   fabsf(__uint_as_float(u & 0xffff0000u))));
-                        }
-                    }
+                        for (int i = 0; i < 2; ++i)
+                            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[b][k][i] << 16)),
+                                                   fabsf(__uint_as_float(qf[b][k][i] & 0xffff0000u))));
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
                     uint32_t ex = __float_as_uint(top) & 0x7f800000u;
@@ -640,16 +647,16 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint32_t u = i ? raw[k].y : raw[k].x;
-                            qf[b][k][i] = pack_f16(__uint_as_float(u << 16) * down,
-                                                   __uint_as_float(u & 0xffff0000u) * down) ^ qsign;
-                        }
+                        for (int i = 0; i < 2; ++i)
+                            qf[b][k][i] = pack_f16(__uint_as_float(qf[b][k][i] << 16) * down,
+                                                   __uint_as_float(qf[b][k][i] & 0xffff0000u) * down) ^
+                                          qsign;
                 }
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
+                    const int row = it.rb * RB + wr * 8 * NQ + 8 * b + 2 * c + p;
                     qs[b][p] = F8 ? __shfl_sync(~0u, factor, (2 * c + p) * 4) : qscale;
-                    e[b][p] = it.len - a.T + min(row0 + 8 * b + 2 * c + p, rows - 1) / s.G;
+                    e[b][p] = it.len - a.T + min(row, rows - 1) / s.G;
                     m[b][p] = -INFINITY;
                     l[b][p] = 0.f;
                 }
@@ -916,180 +923,108 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                     });
             }
         }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&empty[st]);
-
-        // the item's last tile, or the stretch's: join the groups, write
-        if (tile + 1 == it.ntiles || left == 1) {
-#pragma unroll
-            for (int b = 0; b < NQ; ++b)
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-#pragma unroll
-                    for (int q = 4; q < 32; q <<= 1) l[b][p] += __shfl_xor_sync(~0u, l[b][p], q);
-            if constexpr (F8) {
-                const float back = xmax * (1.f / 16384.f);
-#pragma unroll
-                for (int j = 0; j < MT; ++j)
-#pragma unroll
-                    for (int b = 0; b < NQ; ++b)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[j][b][i] *= back;
-            }
-            if constexpr (WK > 1) {
-                // the groups' results one after another (in a fixed order), a WR-th of
-                // the places at a time, a lane's values 32 floats apart
-                constexpr int MP = MT / WR;
-                float *buf = xch + wr * (8 * NQ * D / WR), *ml = xch + 8 * NQ * D + wr * 16 * NQ;
-#pragma unroll 1
-                for (int src = 1; src < WK; ++src) {
-                    float f0[NQ][2], f1[NQ][2];
-#pragma unroll
-                    for (int part = 0; part < WR; ++part) {
-                        warps_sync();
-                        if (kg == src) {
-#pragma unroll
-                            for (int j = 0; j < MP; ++j)
-#pragma unroll
-                                for (int b = 0; b < NQ; ++b)
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i)
-                                        buf[((j * NQ + b) * 4 + i) * 32 + lane] = o[part * MP + j][b][i];
-                            if (part == 0 && g == 0) {
-#pragma unroll
-                                for (int b = 0; b < NQ; ++b)
-#pragma unroll
-                                    for (int p = 0; p < 2; ++p) {
-                                        ml[8 * b + 2 * c + p] = m[b][p];
-                                        ml[8 * NQ + 8 * b + 2 * c + p] = l[b][p];
-                                    }
-                            }
-                        }
-                        warps_sync();
-                        if (kg == 0) {
-                            if (part == 0) {
-#pragma unroll
-                                for (int b = 0; b < NQ; ++b)
-#pragma unroll
-                                    for (int p = 0; p < 2; ++p) {
-                                        const float m0 = m[b][p], m1 = ml[8 * b + 2 * c + p];
-                                        const float mt = fmaxf(m0, m1);
-                                        f0[b][p] = m0 == -INFINITY ? 0.f : ex2((m0 - mt) * qs[b][p]);
-                                        f1[b][p] = m1 == -INFINITY ? 0.f : ex2((m1 - mt) * qs[b][p]);
-                                        m[b][p] = mt;
-                                        l[b][p] = l[b][p] * f0[b][p] +
-                                                  ml[8 * NQ + 8 * b + 2 * c + p] * f1[b][p];
-                                    }
-                            }
-#pragma unroll
-                            for (int j = 0; j < MP; ++j)
-#pragma unroll
-                                for (int b = 0; b < NQ; ++b)
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        float &v = o[part * MP + j][b][i];
-                                        v = v * f0[b][i & 1] +
-                                            buf[((j * NQ + b) * 4 + i) * 32 + lane] * f1[b][i & 1];
-                                    }
-                        }
-                    }
-                }
-            }
-            if (kg == 0) {
-                const bool whole = tile + 1 == it.ntiles && (first_item ? tile_first == 0 : true);
-                if (!whole) {
-                    float *part = part_at(a, s, 2 * blockIdx.x + (first_item ? 0 : 1));
-                    if (threadIdx.x == 0 && !(first_item && tile_first > 0)) {
-                        // its first tiles, the first of them `tile` + 1 units (and so many tiles) ago
-                        const int64_t t1 = span.beg + span.left + it.ntiles - tile - 1;
-                        Cut cut;
-                        cut.parts = int(divide(t1 + span.part - 1, span.part)) - int(blockIdx.x);
-                        cut.first = first_item ? 0 : 1;
-                        cut.b = it.b;
-                        cut.hk = it.hk;
-                        cut.rb = it.rb;
-                        reinterpret_cast<Cut *>(a.ws)[blockIdx.x] = cut;
-                    }
-#pragma unroll
-                    for (int b = 0; b < NQ; ++b)
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            const int rr = wr * 8 * NQ + 8 * b + 2 * c + p;
-                            if (it.rb * RB + rr >= rows) continue;
-                            float *dst = part + rr * D;
-                            if constexpr (!F8) {
-#pragma unroll
-                                for (int j = 0; j < MT; ++j)
-#pragma unroll
-                                    for (int i = 0; i < 2; ++i) dst[16 * j + 8 * i + g] = o[j][b][2 * i + p];
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < MT; j += 2)
-                                    *reinterpret_cast<float4 *>(dst + (D / 8) * g + 2 * j) =
-                                        make_float4(o[j][b][p], o[j][b][2 + p], o[j + 1][b][p],
-                                                    o[j + 1][b][2 + p]);
-                            }
-                            if (g == 0) {
-                                part[RB * D + rr] = m[b][p] == -INFINITY ? m[b][p] : m[b][p] * qs[b][p];
-                                part[RB * (D + 1) + rr] = l[b][p];
-                            }
-                        }
-                } else {
-                    auto out_row = [&](int r) {
-                        const int t = r / s.G;
-                        return static_cast<__nv_bfloat16 *>(a.out) + it.b * a.o_sb + t * a.o_st +
-                               (it.hk * s.G + r - t * s.G) * a.o_sh;
-                    };
-#pragma unroll
-                    for (int b = 0; b < NQ; ++b) {
-                        float inv[2];
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            inv[p] = l[b][p] == 0.f ? 0.f : 1.f / l[b][p];
-                            const int r = row0 + 8 * b + 2 * c + p;
-                            if (r >= rows) continue;
-                            if constexpr (F8) {
-                                __nv_bfloat16 *dst = out_row(r) + (D / 8) * g;
-#pragma unroll
-                                for (int j = 0; j < MT; j += 4) {
-                                    uint32_t w[4];
-#pragma unroll
-                                    for (int q = 0; q < 4; ++q)
-                                        w[q] = pack_bf16(o[j + q][b][p] * inv[p], o[j + q][b][2 + p] * inv[p]);
-                                    *reinterpret_cast<uint4 *>(dst + 2 * j) = make_uint4(w[0], w[1], w[2], w[3]);
-                                }
-                            }
-                            if (a.lse && g == 0) {
-                                const int t = r / s.G;
-                                a.lse[(int64_t(it.b) * a.T + t) * a.Hq + it.hk * s.G + r - t * s.G] =
-                                    l[b][p] == 0.f ? -INFINITY : (m[b][p] * qs[b][p] + log2f(l[b][p])) * kLn2;
-                            }
-                        }
-                        if constexpr (!F8) {
-                            const int r = row0 + 8 * b + g;     // transposed: a quad writes a row's eight places
-                            __nv_bfloat16 *dst = out_row(min(r, rows - 1));
-#pragma unroll
-                            for (int j = 0; j < MT; ++j)
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    const uint32_t v = transpose8(pack_bf16(o[j][b][2 * i] * inv[0],
-                                                                            o[j][b][2 * i + 1] * inv[1]));
-                                    if (r < rows)
-                                        *reinterpret_cast<uint32_t *>(dst + 16 * j + 8 * i + 2 * c) = v;
-                                }
-                        }
-                    }
-                }
-            }
-        }
         --left;
-        if (++tile == it.ntiles) {
+        const bool item_end = ++tile == it.ntiles;
+        if (!item_end && left > 0) {
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&empty[st]);
+            continue;
+        }
+
+        // The item's last tile, or the stretch's.  The next item's queries are loaded
+        // while this one is joined: each warp puts its output, maxima (in log2 units) and
+        // sums into this tile's stage, and takes every fourth row from there.
+        const Item done = it;
+        const int tiles_left = it.ntiles - tile;
+        if (item_end) {
             tile = 0;
             left -= kItemCost;
-            first_item = false;
             fresh = true;
             it = next_item(a, s, it, a.lens[min(it.b + 1, a.B - 1)]);
+            if (left > 0) load_queries();
         }
+        warps_sync();
+        const float back = F8 ? xmax * (1.f / 16384.f) : 1.f;
+        // place d of row r: turned by 4 r places, so that neither side meets in one bank
+        float *const outs = reinterpret_cast<float *>(smem + st * C::STAGE);
+        auto spot = [&](int w, int r, int d) { return (w * 8 * NQ + r) * D + ((d + 4 * r) & (D - 1)); };
+#pragma unroll
+        for (int b = 0; b < NQ; ++b)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int r = 8 * b + 2 * c + p;
+#pragma unroll
+                for (int q = 4; q < 32; q <<= 1) l[b][p] += __shfl_xor_sync(~0u, l[b][p], q);
+                if (g == 0) {
+                    top_of[warp][r] = m[b][p] == -INFINITY ? m[b][p] : m[b][p] * qs[b][p];
+                    sum_of[warp][r] = l[b][p];
+                }
+                if constexpr (F8) {      // places (D / 8) g + 2 j + i
+#pragma unroll
+                    for (int j = 0; j < MT; j += 2)
+                        *reinterpret_cast<float4 *>(outs + spot(warp, r, (D / 8) * g + 2 * j)) =
+                            make_float4(o[j][b][p] * back, o[j][b][2 + p] * back, o[j + 1][b][p] * back,
+                                        o[j + 1][b][2 + p] * back);
+                } else {                 // places 16 j + 8 i + g
+#pragma unroll
+                    for (int j = 0; j < MT; ++j)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            outs[spot(warp, r, 16 * j + 8 * i + g)] = o[j][b][2 * i + p];
+                }
+            }
+        warps_sync();
+        const bool whole = item_end && (first_item ? tile_first == 0 : true);
+        float *const part = part_at(a, s, 2 * blockIdx.x + (first_item ? 0 : 1));
+        if (threadIdx.x == 0 && !whole && !(first_item && tile_first > 0)) {
+            // this CTA has the item's first tiles, others the last
+            const int64_t t1 = span.beg + span.left + tiles_left;
+            Cut cut;
+            cut.parts = int(divide(t1 + span.part - 1, span.part)) - int(blockIdx.x);
+            cut.first = first_item ? 0 : 1;
+            cut.b = done.b;
+            cut.hk = done.hk;
+            cut.rb = done.rb;
+            reinterpret_cast<Cut *>(a.ws)[blockIdx.x] = cut;
+        }
+#pragma unroll 1
+        for (int rr = warp; rr < RB && done.rb * RB + rr < rows; rr += kWarps) {
+            constexpr int E = D / 32;
+            const int w0 = rr / (8 * NQ), r = rr % (8 * NQ);    // the row's warp of the first group
+            float mt = -INFINITY, lt = 0.f, v[E] = {};
+#pragma unroll
+            for (int k = 0; k < WK; ++k) mt = fmaxf(mt, top_of[k * WR + w0][r]);
+            const float base = mt == -INFINITY ? 0.f : mt;
+#pragma unroll
+            for (int k = 0; k < WK; ++k) {
+                const float f = ex2(top_of[k * WR + w0][r] - base);
+                const float *src = outs + spot(k * WR + w0, r, E * lane);
+                lt = fmaf(sum_of[k * WR + w0][r], f, lt);
+#pragma unroll
+                for (int i = 0; i < E; ++i) v[i] = fmaf(src[i], f, v[i]);
+            }
+            if (whole) {
+                const int row = done.rb * RB + rr, t = row / s.G, h = done.hk * s.G + row - t * s.G;
+                const float inv = lt == 0.f ? 0.f : 1.f / lt;
+                uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + done.b * a.o_sb +
+                                                             t * a.o_st + h * a.o_sh + E * lane);
+#pragma unroll
+                for (int i = 0; i < E; i += 2) dst[i / 2] = pack_bf16(v[i] * inv, v[i + 1] * inv);
+                if (a.lse && lane == 0)
+                    a.lse[(int64_t(done.b) * a.T + t) * a.Hq + h] =
+                        lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
+            } else {
+#pragma unroll
+                for (int i = 0; i < E; ++i) part[rr * D + E * lane + i] = v[i];
+                if (lane == 0) {
+                    part[RB * D + rr] = mt;
+                    part[RB * (D + 1) + rr] = lt;
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&empty[st]);
+        if (item_end) first_item = false;
     }
 }
 
