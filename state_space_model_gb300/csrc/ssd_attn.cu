@@ -140,8 +140,8 @@ struct Stretch {
 // All threads of a CTA call it, and get the same; left <= 0: there is none.
 struct Finder {
     int64_t sums[kThreads / 32];
-    int b;
-    int64_t off;
+    Item it;
+    int unit;
 
     __device__ __noinline__ Stretch find(const PagedArgs &a, const Shape &s, int cta) {
         Stretch f;
@@ -169,28 +169,28 @@ struct Finder {
                 run += sum;
             }
             if (f.beg < upto && f.beg >= upto - w) {
-                b = i;
-                off = f.beg - (upto - w);
+                it.b = i;
+                it.len = max(a.lens[i], 0);
+                int64_t rest = f.beg - (upto - w);
+                it.hk = 0;
+                if (a.c.Hkv > 1) {
+                    const int64_t per = divide(w, a.c.Hkv);
+                    it.hk = int(divide(rest, per));
+                    rest -= it.hk * per;
+                }
+#pragma unroll 1
+                for (it.rb = 0;; ++it.rb) {
+                    item_range(a, s, it);
+                    if (rest < it.ntiles + kItemCost) break;
+                    rest -= it.ntiles + kItemCost;
+                }
+                unit = int(rest);
             }
         }
         __syncthreads();
-        Item &it = f.it;
-        it.b = b;
-        it.len = max(a.lens[it.b], 0);
-        it.hk = 0;
-        int64_t rest = off;
-        if (a.c.Hkv > 1) {
-            const int64_t per = divide(seq_cost(a, s, it.b), a.c.Hkv);
-            it.hk = int(divide(off, per));
-            rest = off - it.hk * per;
-        }
-#pragma unroll 1
-        for (it.rb = 0;; ++it.rb) {
-            item_range(a, s, it);
-            f.unit = int(rest);
-            if (rest < it.ntiles + kItemCost) return f;
-            rest -= it.ntiles + kItemCost;
-        }
+        f.it = it;
+        f.unit = unit;
+        return f;
     }
 };
 
@@ -548,7 +548,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
     using C = Cfg<D, F8, NQ, WR>;
     constexpr int KW = C::KW, KS = C::KS, ROW = C::ROW, WK = C::WK, RB = C::RB;
-    constexpr int KT = KW / 16;           // score tiles of a warp's positions
+    constexpr int KP = KW * WR < 32 ? KW * WR : 32;     // positions of a pass over a group's part
+    constexpr int KT = KP / 16;           // its score tiles
     constexpr int MT = D / 16;            // output tiles
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Finder finder;
@@ -673,22 +674,22 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
         }
         const int kbase = it.first + tile * KS + kg * WR * KW;
 #pragma unroll 1
-        for (int sub = 0; sub < WR; ++sub) {
-            const int w = kg * WR + sub, k0 = kbase + sub * KW;
-            const uint32_t mask = (room.masks(st)[w * KW / 32] >> (w * KW % 32)) & (0xffffffffu >> (32 - KW));
+        for (int sub = 0; sub < KW * WR / KP; ++sub) {
+            const int x0 = kg * WR * KW + sub * KP, k0 = kbase + sub * KP;   // the pass's first position
+            const uint32_t mask = (room.masks(st)[x0 / 32] >> (x0 % 32)) & (0xffffffffu >> (32 - KP));
             // (votes, so that the compiler knows these for the same in all lanes)
             if (!__any_sync(~0u, mask != 0)) continue;
-            const bool partial = __any_sync(~0u, k0 + KW - 1 > it.emin ||
+            const bool partial = __any_sync(~0u, k0 + KP - 1 > it.emin ||
                                                      (a.window > 0 && k0 <= it.emax - int(a.window)));
-            const bool all = __all_sync(~0u, !partial && mask == 0xffffffffu >> (32 - KW));
-            const uint32_t ksm = room.keys(st) + w * KW * ROW, vsm = room.values(st) + w * KW * ROW;
-            const float *ksc = room.scales(st) + w * KW, *vsc = ksc + KS;
-            // row g + 8 i of score tile j is position pos_of(j, i) of this warp's
+            const bool all = __all_sync(~0u, !partial && mask == 0xffffffffu >> (32 - KP));
+            const uint32_t ksm = room.keys(st) + x0 * ROW, vsm = room.values(st) + x0 * ROW;
+            const float *ksc = room.scales(st) + x0, *vsc = ksc + KS;
+            // row g + 8 i of score tile j is position pos_of(j, i) of the pass
             auto pos_of = [&](int j, int i) {
                 return 16 * j + (F8 ? code_pos<ROW>(i, g) : g + 8 * i);
             };
 
-            // scores: KW positions x 8 NQ queries
+            // scores: KP positions x 8 NQ queries
             float sc[KT][NQ][4];
 #pragma unroll
             for (int j = 0; j < KT; ++j)
@@ -868,7 +869,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             bool foul = false;
             if (partial) {
 #pragma unroll 1
-                for (int x = 0; x < KW * ROW / 512; ++x) {
+                for (int x = 0; x < KP * ROW / 512; ++x) {
                     const uint4 u = lds16(vsm + (x * 32 + lane) * 16);
                     const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -887,7 +888,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                     });
             } else {
 #pragma unroll 1
-                for (int y = 0; y < KW * (D / 32); ++y) {
+                for (int y = 0; y < KP * (D / 32); ++y) {
                     const int x = y / (D / 32), mine = 32 * (y % (D / 32)) + lane;   // position, place
                     const uint32_t at = vsm + chunk_at<ROW>(x, mine * (F8 ? 1 : 2) / 16) +
                                         mine * (F8 ? 1 : 2) % 16;
@@ -988,7 +989,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             reinterpret_cast<Cut *>(a.ws)[blockIdx.x] = cut;
         }
 #pragma unroll 1
-        for (int rr = warp; rr < RB && done.rb * RB + rr < rows; rr += kWarps) {
+        for (int rr = warp; rr < min(RB, rows - done.rb * RB); rr += kWarps) {
             constexpr int E = D / 32;
             const int w0 = rr / (8 * NQ), r = rr % (8 * NQ);    // the row's warp of the first group
             float mt = -INFINITY, lt = 0.f, v[E] = {};
@@ -1030,76 +1031,85 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
 
 // ---- the join -------------------------------------------------------------------------
 //
-// CTA (x, y): row y of the item whose first part CTA x left; its four warps take
-// every fourth part each.
+// CTA (x, y): rows of the item whose first part CTA x left, `per` of the CTA's four
+// warps to a row (each every per-th part), 4 / per rows at a time, gridDim.y of
+// them apart.  A CTA for every row of a wide block would mostly be CTAs that find
+// nothing to do (32 rows: 9 us in place of 4).
 constexpr int kJoinAhead = 8;     // parts that a warp loads at once
 template <typename T, int D>
 __global__ void __launch_bounds__(128)
-k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
+k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s, int per) {
     constexpr int E = D / 32;
     __shared__ float sm_m[4], sm_l[4], sm_o[4][D];
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, x = blockIdx.x, rr = blockIdx.y;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, x = blockIdx.x;
     wait_for_previous();
     const Cut it = reinterpret_cast<const Cut *>(a.ws)[x];
-    const int r = it.rb * s.RB + rr;
-    if (it.parts == 0 || r >= a.T * s.G) return;
-
-    float m = -INFINITY, l = 0.f, o[E] = {};
+    if (it.parts == 0) return;
+    const int rows = min(s.RB, a.T * s.G - it.rb * s.RB);
+    for (int r0 = blockIdx.y * (4 / per); r0 < rows; r0 += gridDim.y * (4 / per)) {
+        const int rr = min(r0 + warp / per, rows - 1);
+        float m = -INFINITY, l = 0.f, o[E] = {};
 #pragma unroll 1
-    for (int c0 = warp; c0 < it.parts; c0 += 4 * kJoinAhead) {
-        float v[kJoinAhead][E], pm[kJoinAhead], pl[kJoinAhead];
+        for (int c0 = warp % per; c0 < it.parts; c0 += per * kJoinAhead) {
+            float v[kJoinAhead][E], pm[kJoinAhead], pl[kJoinAhead];
 #pragma unroll
-        for (int u = 0; u < kJoinAhead; ++u) {
-            const int c = c0 + 4 * u;
-            pm[u] = -INFINITY;
-            pl[u] = 0.f;
-            if (c < it.parts) {
-                const float *part = part_at(a, s, 2 * (x + c) + (c == 0 ? it.first : 0));
-                pm[u] = part[s.RB * D + rr];
-                pl[u] = part[s.RB * (D + 1) + rr];
+            for (int u = 0; u < kJoinAhead; ++u) {
+                const int c = c0 + per * u;
+                pm[u] = -INFINITY;
+                pl[u] = 0.f;
+                if (c < it.parts) {
+                    const float *part = part_at(a, s, 2 * (x + c) + (c == 0 ? it.first : 0));
+                    pm[u] = part[s.RB * D + rr];
+                    pl[u] = part[s.RB * (D + 1) + rr];
 #pragma unroll
-                for (int j = 0; j < E; ++j) v[u][j] = part[rr * D + lane * E + j];
-            } else {
+                    for (int j = 0; j < E; ++j) v[u][j] = part[rr * D + lane * E + j];
+                } else {
 #pragma unroll
-                for (int j = 0; j < E; ++j) v[u][j] = 0.f;
+                    for (int j = 0; j < E; ++j) v[u][j] = 0.f;
+                }
+            }
+            float mt = m;
+#pragma unroll
+            for (int u = 0; u < kJoinAhead; ++u) mt = fmaxf(mt, pm[u]);
+            const float base = mt == -INFINITY ? 0.f : mt, old = ex2(m - base);
+            m = mt;
+            l *= old;
+#pragma unroll
+            for (int j = 0; j < E; ++j) o[j] *= old;
+#pragma unroll
+            for (int u = 0; u < kJoinAhead; ++u) {
+                const float f = ex2(pm[u] - base);
+                l = fmaf(pl[u], f, l);
+#pragma unroll
+                for (int j = 0; j < E; ++j) o[j] = fmaf(v[u][j], f, o[j]);
             }
         }
+        __syncthreads();          // the rows before have been read
+        if (lane == 0) sm_m[warp] = m, sm_l[warp] = l;
+#pragma unroll
+        for (int j = 0; j < E; ++j) sm_o[warp][lane * E + j] = o[j];
+        __syncthreads();
+        if (warp % per || r0 + warp / per >= rows) continue;
         float mt = m;
+        for (int w = 1; w < per; ++w) mt = fmaxf(mt, sm_m[warp + w]);
+        const float base = mt == -INFINITY ? 0.f : mt;
+        l = 0.f;
 #pragma unroll
-        for (int u = 0; u < kJoinAhead; ++u) mt = fmaxf(mt, pm[u]);
-        const float base = mt == -INFINITY ? 0.f : mt, old = ex2(m - base);
-        m = mt;
-        l *= old;
+        for (int j = 0; j < E; ++j) o[j] = 0.f;
+        for (int w = 0; w < per; ++w) {
+            const float f = ex2(sm_m[warp + w] - base);
+            l = fmaf(sm_l[warp + w], f, l);
 #pragma unroll
-        for (int j = 0; j < E; ++j) o[j] *= old;
-#pragma unroll
-        for (int u = 0; u < kJoinAhead; ++u) {
-            const float f = ex2(pm[u] - base);
-            l = fmaf(pl[u], f, l);
-#pragma unroll
-            for (int j = 0; j < E; ++j) o[j] = fmaf(v[u][j], f, o[j]);
+            for (int j = 0; j < E; ++j) o[j] = fmaf(sm_o[warp + w][lane * E + j], f, o[j]);
         }
-    }
-    if (lane == 0) sm_m[warp] = m, sm_l[warp] = l;
+        const int r = it.rb * s.RB + rr, t = r / s.G, h = it.hk * s.G + r - t * s.G;
+        T *dst = static_cast<T *>(a.out) + it.b * a.o_sb + t * a.o_st + h * a.o_sh + lane * E;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-    for (int j = 0; j < E; ++j) sm_o[warp][lane * E + j] = o[j];
-    __syncthreads();
-    const float mt = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
-    const float base = mt == -INFINITY ? 0.f : mt;
-    l = 0.f;
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const float f = ex2(sm_m[w] - base);
-        l = fmaf(sm_l[w], f, l);
-        if (threadIdx.x < D) v = fmaf(sm_o[w][threadIdx.x], f, v);
+        for (int j = 0; j < E; ++j) dst[j] = T(o[j] * inv);
+        if (a.lse && lane == 0)
+            a.lse[(int64_t(it.b) * a.T + t) * a.Hq + h] = l == 0.f ? -INFINITY : (mt + log2f(l)) * kLn2;
     }
-    const int t = r / s.G, h = it.hk * s.G + r - t * s.G;
-    if (threadIdx.x < D)
-        static_cast<T *>(a.out)[it.b * a.o_sb + t * a.o_st + h * a.o_sh + threadIdx.x] =
-            T(l == 0.f ? 0.f : v / l);
-    if (a.lse && threadIdx.x == 0)
-        a.lse[(int64_t(it.b) * a.T + t) * a.Hq + h] = l == 0.f ? -INFINITY : (mt + log2f(l)) * kLn2;
 }
 
 // ---- fp32 -------------------------------------------------------------------------------
@@ -1192,12 +1202,14 @@ cudaError_t launch_mma(const PagedArgs &a, Shape s, cudaStream_t stream) {
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(unsigned(s.ncta), unsigned(min(s.RB, a.T * s.G)));
+    // about 8 CTAs for an item: one wave of them all
+    const int per = s.RB <= 8 ? 4 : s.RB <= 16 ? 2 : 1, at_once = 4 / per;
+    cfg.gridDim = dim3(unsigned(s.ncta), unsigned(min(8, (min(s.RB, a.T * s.G) + at_once - 1) / at_once)));
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_paged_join<__nv_bfloat16, D>, a, s);
+    return cudaLaunchKernelEx(&cfg, k_paged_join<__nv_bfloat16, D>, a, s, per);
 }
 
 // Rows of a block: 8 or 16 to a warp, then up to four warps along the rows (and
