@@ -13,11 +13,13 @@ namespace ssd {
 namespace {
 
 constexpr float kCodeMax = 448.f;          // largest e4m3 value
-constexpr int kFillRows = 152 * 16;        // warps that fill the GPU
+constexpr int kFillWarps = 152 * 16;       // warps that fill the GPU
 constexpr float kAmaxFloor = 0x1p-96f;     // keeps the scale and its inverse normal numbers
 
 // Eight consecutive elements of a row as they lie in memory (held like that while
 // loads are under way: a kernel's registers decide how many can be), and in fp32.
+// Everything is read and written once, with streaming hints (32768 cached tokens read
+// back: 38.9 us without, 36.9 with).
 template <typename T>
 struct Raw8;
 template <>
@@ -26,6 +28,11 @@ struct Raw8<float> {
     __device__ __forceinline__ void load(const float *p) {
         a = reinterpret_cast<const float4 *>(p)[0];
         b = reinterpret_cast<const float4 *>(p)[1];
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void store(float *p) const {
+        reinterpret_cast<float4 *>(p)[0] = a;
+        reinterpret_cast<float4 *>(p)[1] = b;
     }
     __device__ __forceinline__ void get(float (&v)[8]) const {
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
@@ -36,8 +43,10 @@ template <>
 struct Raw8<__nv_bfloat16> {
     uint4 u;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
-        u = *reinterpret_cast<const uint4 *>(p);
+        u = __ldcs(reinterpret_cast<const uint4 *>(p));
     }
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { __stcs(reinterpret_cast<uint4 *>(p), u); }
     __device__ __forceinline__ void get(float (&v)[8]) const {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -50,7 +59,8 @@ struct Raw8<__nv_bfloat16> {
 template <>
 struct Raw8<uint8_t> {       // e4m3 codes
     uint2 u;
-    __device__ __forceinline__ void load(const uint8_t *p) { u = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void load(const uint8_t *p) { u = __ldcs(reinterpret_cast<const uint2 *>(p)); }
+    __device__ __forceinline__ void zero() { u = make_uint2(0, 0); }
     __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -84,7 +94,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
         w[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
 }
 // Codes: v already divided by the row's scale (rounded to nearest even; above
 // 448 saturated, which only the rounding of the division can reach).
@@ -108,46 +118,92 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// A token has Hq query, Hkv key and Hkv value rows; D/16 lanes take a row, two
-// vectors of eight elements a lane, and a warp U times 512 / D rows of one token.
-// The two vectors of a lane hold partners of the rotation (i and i + R/2) where
-// they lie in the first R places, so neither pairing needs another lane's values;
-// the norm and the largest magnitude are sums and maxima over the row's lanes.
-// HBM-bound: every row is read once and written once, and all U loads of a warp go
-// out before its token's slot, position and angles (which the rows share) are
-// known.  8192 tokens of 32 + 2 x 8 heads of 128 with the four-byte angles of a token
-// read again by each row took 53 us.
+// Two fp32 numbers in one register pair and operations on both (one instruction
+// each; the norm and the rotation are a third of a row's instructions without).
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 parts(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ void pairs(const float (&v)[8], F2 (&r)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = f2(v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ void unpair(const F2 (&r)[4], float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = parts(r[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
+// A token's query, key and value rows are taken in passes of 512 / D rows of one kind,
+// D / 16 lanes to a row, two vectors of eight elements a lane; a warp takes U passes
+// of one token.  The two vectors of a lane hold partners of the rotation (i and
+// i + R/2) where they lie in the first R places, so neither pairing needs another
+// lane's values; the norm and the largest magnitude are sums and maxima over the row's
+// lanes.  HBM-bound: every row is read once and written once, and all U loads of a
+// warp go out before its token's slot, position and angles (which the passes share)
+// are known.
 constexpr int kAppendWarps = 4;
 template <typename T, int D, bool kCodes, int U>
-__global__ void __launch_bounds__(32 * kAppendWarps) k_kv_append(const KvAppendArgs a, int warps) {
+__global__ void __launch_bounds__(32 * kAppendWarps, 6)
+k_kv_append(const __grid_constant__ KvAppendArgs a, int warps) {
     constexpr int LR = D / 16, RPP = 32 / LR;
     const int64_t id = int64_t(blockIdx.x) * kAppendWarps + threadIdx.x / 32;
-    const int t = int(id / warps);
+    const int t = __shfl_sync(~0u, int(id / warps), 0);
     if (t >= a.T) return;
-    const int lane = threadIdx.x % 32, l = lane % LR;
-    const int j0 = int(id - int64_t(t) * warps) * (U * RPP) + lane / LR;    // this lane's first row
-    const int rows = a.Hq + 2 * a.c.Hkv;
+    const int lane = threadIdx.x % 32, l = lane % LR, row = lane / LR;
+    const int p0 = __shfl_sync(~0u, int(id - int64_t(t) * warps) * U, 0);
+    const int qp = (a.Hq + RPP - 1) / RPP, kp = (a.c.Hkv + RPP - 1) / RPP;   // passes of a kind
     const int half = a.R / 16;
     const int v0 = l < half ? l : 2 * l, v1 = l < half ? l + half : 2 * l + 1;
 
     const int slot = a.slots[t], pos = a.cos ? a.positions[t] : 0;
+    // pass u: its kind (0 query, 1 key, 2 value), and this lane's head of it
+    auto kind_of = [&](int p) { return p < qp ? 0 : p < qp + kp ? 1 : 2; };
+    auto head_of = [&](int p) { return (p < qp ? p : p < qp + kp ? p - qp : p - qp - kp) * RPP + row; };
     Raw8<T> x[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int j = min(j0 + u * RPP, rows - 1);
-        const T *src = j < a.Hq ? static_cast<const T *>(a.q) + t * a.q_st + j * a.q_sh
-                       : j < a.Hq + a.c.Hkv
-                           ? static_cast<const T *>(a.k) + t * a.k_st + (j - a.Hq) * a.k_sh
-                           : static_cast<const T *>(a.v) + t * a.v_st + (j - a.Hq - a.c.Hkv) * a.v_sh;
-        x[u][0].load(src + 8 * v0);
-        x[u][1].load(src + 8 * v1);
+        const int p = p0 + u, kind = kind_of(p), h = head_of(p);
+        if (h < (kind == 0 ? a.Hq : a.c.Hkv)) {
+            const T *src = kind == 0   ? static_cast<const T *>(a.q) + t * a.q_st + h * a.q_sh
+                           : kind == 1 ? static_cast<const T *>(a.k) + t * a.k_st + h * a.k_sh
+                                       : static_cast<const T *>(a.v) + t * a.v_st + h * a.v_sh;
+            x[u][0].load(src + 8 * v0);
+            x[u][1].load(src + 8 * v1);
+        } else {
+            x[u][0].zero();
+            x[u][1].zero();
+        }
     }
     // padding: the whole warp leaves
     if (slot < 0 || slot >= a.c.pages * a.c.ps || (a.cos && (pos < 0 || pos >= a.S))) return;
     const int page = slot / a.c.ps, at = slot - page * a.c.ps;
 
-    float cs[8] = {}, sn[8] = {};       // interleaved: four for each vector
-    if (a.cos && l < half) {
+    float cs[8], sn[8];       // interleaved: four for each vector
+    const bool turn = a.cos && l < half;
+    if (turn) {
         const float *cp = a.cos + pos * a.cs_st, *sp = a.sin + pos * a.sn_st;
         if (a.interleaved) {
 #pragma unroll
@@ -161,108 +217,149 @@ __global__ void __launch_bounds__(32 * kAppendWarps) k_kv_append(const KvAppendA
             load8(cp + 8 * l, cs);
             load8(sp + 8 * l, sn);
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
     }
+    const int64_t place = page * a.c.sp + at * a.c.st;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int j = j0 + u * RPP;
-        const bool is_q = j < a.Hq, is_v = j >= a.Hq + a.c.Hkv, live = j < rows;
-        const int h = is_q ? j : (is_v ? j - a.Hq - a.c.Hkv : j - a.Hq);
-        float x0[8], x1[8];
-        x[u][0].get(x0);
-        x[u][1].get(x1);
-        const float *w = is_v ? nullptr : (is_q ? a.qw : a.kw);
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x0[i], x0[i], fmaf(x1[i], x1[i], ss));
-#pragma unroll
-        for (int o = LR / 2; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-        if (w) {
-            const float r = rsqrtf(ss * (1.f / D) + a.eps);
-            float w0[8], w1[8];
-            load8(w + 8 * v0, w0);
-            load8(w + 8 * v1, w1);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x0[i] *= r * w0[i];
-                x1[i] *= r * w1[i];
+        const int p = p0 + u, kind = kind_of(p), h = head_of(p);
+        if (p >= qp + 2 * kp) break;
+        const bool live = h < (kind == 0 ? a.Hq : a.c.Hkv);
+        if (!kCodes && kind == 2) {              // values as they are
+            const int64_t off = place + h * a.c.sh;
+            if (live && SSD_IDX_OK(a.err, off + 8 * v1 + 7, a.c.n)) {
+                x[u][0].store(static_cast<T *>(a.c.v) + off + 8 * v0);
+                x[u][1].store(static_cast<T *>(a.c.v) + off + 8 * v1);
             }
+            continue;
         }
-        if (a.cos && !is_v && l < half) {
-            if (a.interleaved) {   // pairs (2i, 2i + 1) inside each vector
+        float y0[8], y1[8];
+        x[u][0].get(y0);
+        x[u][1].get(y1);
+        if (kind < 2) {
+            F2 x0[4], x1[4];
+            pairs(y0, x0);
+            pairs(y1, x1);
+            const float *w = kind == 0 ? a.qw : a.kw;
+            if (w) {
+                F2 sq = f2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sq = fma(x0[i], x0[i], fma(x1[i], x1[i], sq));
+                float ss = parts(sq).x + parts(sq).y;
+#pragma unroll
+                for (int o = LR / 2; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+                const float r = rsqrtf(ss * (1.f / D) + a.eps);
+                float w0[8], w1[8];
+                F2 w0p[4], w1p[4];
+                load8(w + 8 * v0, w0);
+                load8(w + 8 * v1, w1);
+                pairs(w0, w0p);
+                pairs(w1, w1p);
+                const F2 rr = f2(r, r);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float p0 = x0[2 * i], q0 = x0[2 * i + 1], p1 = x1[2 * i], q1 = x1[2 * i + 1];
-                    x0[2 * i] = p0 * cs[i] - q0 * sn[i];
-                    x0[2 * i + 1] = q0 * cs[i] + p0 * sn[i];
-                    x1[2 * i] = p1 * cs[4 + i] - q1 * sn[4 + i];
-                    x1[2 * i + 1] = q1 * cs[4 + i] + p1 * sn[4 + i];
+                    x0[i] = mul(x0[i], mul(w0p[i], rr));
+                    x1[i] = mul(x1[i], mul(w1p[i], rr));
                 }
-            } else {               // x0 holds places i, x1 their partners i + R/2
+            }
+            if (!a.interleaved) {    // x0 holds places i, x1 their partners i + R/2
+                F2 c[4], n[4];
+                pairs(cs, c);
+                pairs(sn, n);
+                const F2 minus = f2(-1.f, -1.f);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float p = x0[i], q = x1[i];
-                    x0[i] = p * cs[i] - q * sn[i];
-                    x1[i] = q * cs[i] + p * sn[i];
+                for (int i = 0; i < 4; ++i) {
+                    const F2 p = x0[i], q = x1[i];
+                    x0[i] = fma(p, c[i], mul(mul(q, n[i]), minus));
+                    x1[i] = fma(q, c[i], mul(p, n[i]));
+                }
+                unpair(x0, y0);
+                unpair(x1, y1);
+            } else {                 // pairs (2i, 2i + 1) inside each vector
+                unpair(x0, y0);
+                unpair(x1, y1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float p0 = y0[2 * i], q0 = y0[2 * i + 1], p1 = y1[2 * i], q1 = y1[2 * i + 1];
+                    if (turn) {
+                        y0[2 * i] = p0 * cs[i] - q0 * sn[i];
+                        y0[2 * i + 1] = q0 * cs[i] + p0 * sn[i];
+                        y1[2 * i] = p1 * cs[4 + i] - q1 * sn[4 + i];
+                        y1[2 * i + 1] = q1 * cs[4 + i] + p1 * sn[4 + i];
+                    }
                 }
             }
         }
-        float amax = kAmaxFloor;
+        if (kind == 0) {
+            if (live) {
+                T *o = static_cast<T *>(a.out) + t * a.o_st + h * a.o_sh;
+                store8(o + 8 * v0, y0);
+                store8(o + 8 * v1, y1);
+            }
+            continue;
+        }
+        const int64_t off = place + h * a.c.sh;
+        const bool in = live && SSD_IDX_OK(a.err, off + 8 * v1 + 7, a.c.n);
         if constexpr (kCodes) {
             // the largest magnitude over the row's lanes; a NaN or an infinity
             // ends in a scale that makes the whole row NaN when it is read
+            float amax = kAmaxFloor;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) amax = max_nan(amax, max_nan(fabsf(x0[i]), fabsf(x1[i])));
+            for (int i = 0; i < 8; ++i) amax = max_nan(amax, max_nan(fabsf(y0[i]), fabsf(y1[i])));
 #pragma unroll
             for (int o = LR / 2; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(~0u, amax, o));
-        }
-        if (!live) continue;
-        if (is_q) {
-            T *o = static_cast<T *>(a.out) + t * a.o_st + h * a.o_sh;
-            store8(o + 8 * v0, x0);
-            store8(o + 8 * v1, x1);
-            continue;
-        }
-        const int64_t off = page * a.c.sp + h * a.c.sh + at * a.c.st;
-        if (!SSD_IDX_OK(a.err, off + 8 * v1 + 7, a.c.n)) continue;
-        if constexpr (kCodes) {
             const float inv = kCodeMax / amax;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                x0[i] *= inv;
-                x1[i] *= inv;
+                y0[i] *= inv;
+                y1[i] *= inv;
             }
-            uint8_t *o = static_cast<uint8_t *>(is_v ? a.c.v : a.c.k) + off;
-            store8_codes(o + 8 * v0, x0);
-            store8_codes(o + 8 * v1, x1);
-            const int64_t soff = page * a.c.ssp + h * a.c.ssh + at;
-            if (l == 0 && SSD_IDX_OK(a.err, soff, a.c.ns))
-                (is_v ? a.c.vs : a.c.ks)[soff] = amax * (1.f / kCodeMax);
-        } else {
-            T *o = static_cast<T *>(is_v ? a.c.v : a.c.k) + off;
-            store8(o + 8 * v0, x0);
-            store8(o + 8 * v1, x1);
+            if (in) {
+                uint8_t *o = static_cast<uint8_t *>(kind == 2 ? a.c.v : a.c.k) + off;
+                store8_codes(o + 8 * v0, y0);
+                store8_codes(o + 8 * v1, y1);
+                const int64_t soff = page * a.c.ssp + h * a.c.ssh + at;
+                if (l == 0 && SSD_IDX_OK(a.err, soff, a.c.ns))
+                    (kind == 2 ? a.c.vs : a.c.ks)[soff] = amax * (1.f / kCodeMax);
+            }
+        } else if (in) {
+            T *o = static_cast<T *>(a.c.k) + off;
+            store8(o + 8 * v0, y0);
+            store8(o + 8 * v1, y1);
         }
     }
 }
 
 template <typename T, int D, bool kCodes, int U>
 cudaError_t append_u(const KvAppendArgs &a, cudaStream_t s) {
-    constexpr int per = U * 512 / D;          // rows of a warp
-    const int warps = (a.Hq + 2 * a.c.Hkv + per - 1) / per;
+    constexpr int RPP = 512 / D;
+    const int passes = (a.Hq + RPP - 1) / RPP + 2 * ((a.c.Hkv + RPP - 1) / RPP);
+    const int warps = (passes + U - 1) / U;
     const int64_t blocks = (a.T * warps + kAppendWarps - 1) / kAppendWarps;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     k_kv_append<T, D, kCodes, U><<<unsigned(blocks), 32 * kAppendWarps, 0, s>>>(a, warps);
     return cudaGetLastError();
 }
 
-// Four times 512 / D rows to a warp where that still fills the GPU with warps (one
-// load of the angles for them, four rows' loads in flight); else one, so that a few
-// tokens spread over as many SMs as they can.
+// As few warps a token as take at most four passes each (fp32: two, for their
+// registers), the passes spread evenly over them, where that still fills the GPU with
+// warps: one load of the angles for a warp's passes, all their loads in flight.  Else a
+// warp a pass, so that a few tokens spread over as many SMs as they can.
 template <typename T, int D, bool kCodes>
 cudaError_t append_t(const KvAppendArgs &a, cudaStream_t s) {
-    const int64_t rows = a.T * (a.Hq + 2 * a.c.Hkv);
-    return rows * D >= int64_t(kFillRows) * 512 * 4 ? append_u<T, D, kCodes, 4>(a, s)
-                                                    : append_u<T, D, kCodes, 1>(a, s);
+    constexpr int RPP = 512 / D, kMost = sizeof(T) == 4 ? 2 : 4;
+    const int passes = (a.Hq + RPP - 1) / RPP + 2 * ((a.c.Hkv + RPP - 1) / RPP);
+    const int warps = (passes + kMost - 1) / kMost;
+    if (a.T * warps < kFillWarps) return append_u<T, D, kCodes, 1>(a, s);
+    switch ((passes + warps - 1) / warps) {
+    case 4:
+        if constexpr (kMost == 4) return append_u<T, D, kCodes, 4>(a, s);
+    case 3:
+        if constexpr (kMost == 4) return append_u<T, D, kCodes, 3>(a, s);
+    default: return append_u<T, D, kCodes, 2>(a, s);
+    }
 }
 
 template <int D>
@@ -280,24 +377,33 @@ cudaError_t append_d(const KvAppendArgs &a, cudaStream_t s) {
 // HBM-bound.  With every vector looking up its own token (three dependent loads each),
 // 32768 tokens of 8 heads of 128 in 8 bits took 47 us.
 constexpr int kReadTokens = 32;      // most tokens of a CTA
+constexpr int kNearLens = 512;       // sequences whose cu_lens a CTA keeps near
 template <typename T, typename P, int D>
-__global__ void __launch_bounds__(256) k_kv_read(const KvReadArgs a, int TB) {
+__global__ void __launch_bounds__(256, 4) k_kv_read(const __grid_constant__ KvReadArgs a, int TB) {
     constexpr int NV = D / 8;
     constexpr int kReadAhead = sizeof(P) == 4 ? 2 : 4;
     __shared__ int64_t off_of[kReadTokens], soff_of[kReadTokens];
+    __shared__ int32_t near_cu[kNearLens];
     const int64_t i0 = int64_t(blockIdx.x) * TB;
     const int n = int(min(int64_t(TB), a.T - i0));
+    // the bisection's loads depend on one another: from shared memory where they fit
+    const int32_t *cu = a.cu;
+    if (a.B < kNearLens) {
+        for (int i = threadIdx.x; i <= a.B; i += 256) near_cu[i] = a.cu[i];
+        __syncthreads();
+        cu = near_cu;
+    }
     if (threadIdx.x < n) {
         const int64_t i = i0 + threadIdx.x;
         // the sequence of row i: the last b with cu[b] <= i
         int lo = -1, hi = a.B;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (a.cu[mid] <= i) lo = mid; else hi = mid;
+            if (cu[mid] <= i) lo = mid; else hi = mid;
         }
         int64_t off = -1, soff = 0;
-        if (lo >= 0 && i < a.cu[lo + 1]) {
-            const int64_t pos = (a.starts ? a.starts[lo] : 0) + (i - a.cu[lo]);
+        if (lo >= 0 && i < cu[lo + 1]) {
+            const int64_t pos = (a.starts ? a.starts[lo] : 0) + (i - cu[lo]);
             if (pos >= 0 && pos < int64_t(a.M) * a.c.ps) {
                 const int pi = int(pos) / a.c.ps, at = int(pos) - pi * a.c.ps;
                 const int page = a.table[lo * a.tb + pi];
@@ -311,46 +417,55 @@ __global__ void __launch_bounds__(256) k_kv_read(const KvReadArgs a, int TB) {
         soff_of[threadIdx.x] = soff;
     }
     __syncthreads();
-    const int per = a.c.Hkv * NV, all = n * per;      // vectors of a token, of the CTA
-    for (int r0 = threadIdx.x; r0 < all; r0 += 256 * kReadAhead) {
-        Raw8<P> kx[kReadAhead], vx[kReadAhead];
-        float ks[kReadAhead], vs[kReadAhead];
-        bool there[kReadAhead];
+    // A thread keeps its place in a token (head, vector) and takes every `apart`-th token;
+    // where a token has more vectors than the CTA threads, one place after another.
+    const int per = a.c.Hkv * NV, apart = per < 256 ? 256 / per : 1;
+    const int tok0 = threadIdx.x / per;
+    for (int place = threadIdx.x - tok0 * per; tok0 < apart && place < per; place += 256) {
+        const int h = place / NV, vec = place % NV;
+        const int64_t in = h * a.c.sh + 8 * vec, sin = h * a.c.ssh;
+        T *ko = static_cast<T *>(a.k) + i0 * a.k_st + h * a.k_sh + 8 * vec;
+        T *vo = static_cast<T *>(a.v) + i0 * a.v_st + h * a.v_sh + 8 * vec;
+        for (int tok = tok0; tok < n; tok += apart * kReadAhead) {
+            Raw8<P> kx[kReadAhead], vx[kReadAhead];
+            float ks[kReadAhead], vs[kReadAhead];
 #pragma unroll
-        for (int u = 0; u < kReadAhead; ++u) {
-            const int r = min(r0 + 256 * u, all - 1), tok = r / per;
-            const int h = (r - tok * per) / NV, vec = r % NV;     // per is a multiple of NV
-            const int64_t off = off_of[tok] + h * a.c.sh + 8 * vec;
-            there[u] = off_of[tok] >= 0 && SSD_IDX_OK(a.err, off + 7, a.c.n);
-            if (there[u]) {
-                kx[u].load(static_cast<const P *>(a.c.k) + off);
-                vx[u].load(static_cast<const P *>(a.c.v) + off);
-                if constexpr (sizeof(P) == 1) {
-                    const int64_t so = soff_of[tok] + h * a.c.ssh;
-                    ks[u] = a.c.ks[so];
-                    vs[u] = a.c.vs[so];
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kReadAhead; ++u) {
-            const int r = r0 + 256 * u;
-            if (r >= all) break;
-            const int tok = r / per, h = (r - tok * per) / NV, vec = r % NV;
-            float k[8] = {}, v[8] = {};
-            if (there[u]) {
-                kx[u].get(k);
-                vx[u].get(v);
-                if constexpr (sizeof(P) == 1) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        k[i] *= ks[u];
-                        v[i] *= vs[u];
+            for (int u = 0; u < kReadAhead; ++u) {
+                const int i = min(tok + u * apart, n - 1);
+                const int64_t off = off_of[i] + in;
+                ks[u] = vs[u] = 0.f;
+                if (off_of[i] >= 0 && SSD_IDX_OK(a.err, off + 7, a.c.n)) {
+                    kx[u].load(static_cast<const P *>(a.c.k) + off);
+                    vx[u].load(static_cast<const P *>(a.c.v) + off);
+                    if constexpr (sizeof(P) == 1) {
+                        ks[u] = a.c.ks[soff_of[i] + sin];
+                        vs[u] = a.c.vs[soff_of[i] + sin];
                     }
+                } else {
+                    kx[u].zero();
+                    vx[u].zero();
                 }
             }
-            store8(static_cast<T *>(a.k) + (i0 + tok) * a.k_st + h * a.k_sh + 8 * vec, k);
-            store8(static_cast<T *>(a.v) + (i0 + tok) * a.v_st + h * a.v_sh + 8 * vec, v);
+#pragma unroll
+            for (int u = 0; u < kReadAhead; ++u) {
+                const int i = tok + u * apart;
+                if (i >= n) break;
+                if constexpr (sizeof(P) == 1) {
+                    float k[8], v[8];
+                    kx[u].get(k);
+                    vx[u].get(v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        k[j] *= ks[u];
+                        v[j] *= vs[u];
+                    }
+                    store8(ko + i * a.k_st, k);
+                    store8(vo + i * a.v_st, v);
+                } else {
+                    kx[u].store(ko + i * a.k_st);
+                    vx[u].store(vo + i * a.v_st);
+                }
+            }
         }
     }
 }
