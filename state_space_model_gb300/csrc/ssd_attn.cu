@@ -1114,61 +1114,198 @@ k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape 
 
 // ---- fp32 -------------------------------------------------------------------------------
 //
-// grid (Hq, T, B): one row to a CTA of four warps, each warp every fourth
-// position, each lane D / 32 places of the head.
-template <int D>
-__global__ void __launch_bounds__(128) k_paged_rows(const PagedArgs a) {
-    constexpr int E = D / 32;
-    __shared__ float sm_m[4], sm_l[4], sm_o[4][D];
-    const int h = blockIdx.x, t = blockIdx.y, b = blockIdx.z;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int hk = h / (a.Hq / a.c.Hkv);
-    const float *q = static_cast<const float *>(a.q) + b * a.q_sb + t * a.q_st + h * a.q_sh + lane * E;
-    float qv[E], o[E] = {}, m = -INFINITY, l = 0.f;
+// The same line, cuts and join, with products on the CUDA cores (tensor cores would
+// round the operands).  Six warps of a CTA take eight positions of a tile each, four
+// lanes a position: a lane holds a quarter of the places, in float4 steps of 16, of
+// its position's key and value, loaded straight into registers a tile ahead, and
+// of the outputs of NR rows.  Each quad of lanes keeps maxima and sums of its own, so
+// nothing but the quarter scores crosses lanes until an item ends.
+constexpr int kF32Warps = kThreads / 32;
+template <int D, int NR>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
+    constexpr int V = D / 16;                    // float4 of a lane's quarter
+    __shared__ Finder finder;
+    __shared__ float qsm[NR][D];                 // queries times scale log2(e)
+    __shared__ float outs[kF32Warps][NR][D], top_of[kF32Warps][NR], sum_of[kF32Warps][NR];
+    let_next_start();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int quad = lane / 4, part4 = lane % 4;
+    const Stretch span = finder.find(a, s, blockIdx.x);
+    if (threadIdx.x == 0) reinterpret_cast<Cut *>(a.ws)[blockIdx.x].parts = 0;
+    Item it = span.it;
+    int tile = max(0, span.unit - kItemCost);
+    int64_t left = span.left - max(0, kItemCost - span.unit);
+    if (span.left <= 0 || left <= 0) return;
+    const int rows = a.T * s.G;
+
+    // the second cursor: the tile whose page is looked up, then loaded
+    Item ld = it;
+    int ld_tile = tile, page = -1, at = 0;
+    int64_t ld_left = left;
+    auto look_up = [&]() {
+        page = -1;
+        const int pos = ld.first + ld_tile * s.KS + warp * 8 + quad;
+        const int p = pos / a.c.ps;
+        at = pos - p * a.c.ps;
+        if (ld_left > 0 && pos >= ld.lo && pos < ld.hi) page = a.table[ld.b * a.tb + p];
+    };
+    float4 nk[V], nv[V];
+    bool nthere = false;
+    auto load = [&]() {
+        const int64_t off = page * a.c.sp + ld.hk * a.c.sh + at * a.c.st;
+        nthere = page >= 0 && page < a.c.pages && SSD_IDX_OK(a.err, off + D - 1, a.c.n);
 #pragma unroll
-    for (int i = 0; i < E; ++i) qv[i] = q[i] * (a.scale * kLog2e);
-    int64_t end = int64_t(a.lens[b]) - a.T + t + 1;
-    const int64_t lo = a.window > 0 && end > a.window ? end - a.window : 0;
-    if (end > int64_t(a.M) * a.c.ps) end = int64_t(a.M) * a.c.ps;
-    for (int64_t j = lo + warp; j < end; j += 4) {
-        const int pi = int(j / a.c.ps), at = int(j - int64_t(pi) * a.c.ps);
-        const int page = a.table[b * a.tb + pi];
-        if (page < 0 || page >= a.c.pages) continue;
-        const int64_t off = page * a.c.sp + hk * a.c.sh + at * a.c.st + lane * E;
-        if (!SSD_IDX_OK(a.err, off + E - 1, a.c.n)) continue;
-        const float *k = static_cast<const float *>(a.c.k) + off, *v = static_cast<const float *>(a.c.v) + off;
-        float s = 0.f;
+        for (int i = 0; i < V; ++i) {
+            nk[i] = nv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (nthere) {
+                const int64_t o = off + 16 * i + 4 * part4;
+                nk[i] = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(a.c.k) + o));
+                nv[i] = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(a.c.v) + o));
+            }
+        }
+        --ld_left;
+        if (++ld_tile == ld.ntiles) {
+            ld_tile = 0;
+            ld_left -= kItemCost;
+            ld = next_item(a, s, ld, a.lens[min(ld.b + 1, a.B - 1)]);
+        }
+        look_up();
+    };
+    look_up();
+    load();
+
+    float4 o[NR][V];
+    float m[NR], l[NR];
+    int e[NR];
+    bool fresh = true, first_item = true;
+    const int tile_first = tile;
+    while (left > 0) {
+        if (fresh) {
+            fresh = false;
+            __syncthreads();
+            for (int i = threadIdx.x; i < NR * D; i += kThreads) {
+                const int r = min(it.rb * NR + i / D, rows - 1), t = r / s.G;
+                qsm[i / D][i % D] = static_cast<const float *>(a.q)[it.b * a.q_sb + t * a.q_st +
+                                                                    (it.hk * s.G + r - t * s.G) * a.q_sh + i % D] *
+                                    (a.scale * kLog2e);
+            }
+            __syncthreads();
 #pragma unroll
-        for (int i = 0; i < E; ++i) s = fmaf(qv[i], k[i], s);
+            for (int r = 0; r < NR; ++r) {
+                e[r] = it.len - a.T + min(it.rb * NR + r, rows - 1) / s.G;
+                m[r] = -INFINITY;
+                l[r] = 0.f;
 #pragma unroll
-        for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(~0u, s, w);
-        const float m2 = fmaxf(m, s);
-        const float base = m2 == -INFINITY ? 0.f : m2;
-        const float f = exp2f(m - base), p = exp2f(s - base);
-        m = m2;
-        l = l * f + p;
+                for (int i = 0; i < V; ++i) o[r][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+        float4 k[V], v[V];
+        const bool there = nthere;
 #pragma unroll
-        for (int i = 0; i < E; ++i) o[i] = fmaf(o[i], f, p * v[i]);
+        for (int i = 0; i < V; ++i) k[i] = nk[i], v[i] = nv[i];
+        const int pos = it.first + tile * s.KS + warp * 8 + quad;
+        if (left > 1) load();
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            float sc = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float4 q = *reinterpret_cast<const float4 *>(&qsm[r][16 * i + 4 * part4]);
+                sc = fmaf(q.x, k[i].x, fmaf(q.y, k[i].y, fmaf(q.z, k[i].z, fmaf(q.w, k[i].w, sc))));
+            }
+            sc += __shfl_xor_sync(~0u, sc, 1);
+            sc += __shfl_xor_sync(~0u, sc, 2);
+            if (there && pos <= e[r] && (a.window == 0 || pos > e[r] - int(a.window))) {
+                const float mt = fmaxf(m[r], sc), base = mt == -INFINITY ? 0.f : mt;
+                const float f = ex2(m[r] - base), p = ex2(sc - base);
+                m[r] = mt;
+                l[r] = fmaf(l[r], f, p);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    o[r][i].x = fmaf(o[r][i].x, f, p * v[i].x);
+                    o[r][i].y = fmaf(o[r][i].y, f, p * v[i].y);
+                    o[r][i].z = fmaf(o[r][i].z, f, p * v[i].z);
+                    o[r][i].w = fmaf(o[r][i].w, f, p * v[i].w);
+                }
+            }
+        }
+        --left;
+        const bool item_end = ++tile == it.ntiles;
+        if (!item_end && left > 0) continue;
+
+        // join the quads of each warp, then the warps
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            float mt = m[r];
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) mt = fmaxf(mt, __shfl_xor_sync(~0u, mt, w));
+            const float f = m[r] == -INFINITY ? 0.f : ex2(m[r] - mt);
+            l[r] *= f;
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) l[r] += __shfl_xor_sync(~0u, l[r], w);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float x[4] = {o[r][i].x * f, o[r][i].y * f, o[r][i].z * f, o[r][i].w * f};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int w = 4; w < 32; w <<= 1) x[j] += __shfl_xor_sync(~0u, x[j], w);
+                if (quad == 0)
+                    *reinterpret_cast<float4 *>(&outs[warp][r][16 * i + 4 * part4]) =
+                        make_float4(x[0], x[1], x[2], x[3]);
+            }
+            if (lane == 0) top_of[warp][r] = mt, sum_of[warp][r] = l[r];
+        }
+        __syncthreads();
+        const bool whole = item_end && (first_item ? tile_first == 0 : true);
+        float *const part = part_at(a, s, 2 * blockIdx.x + (first_item ? 0 : 1));
+        if (threadIdx.x == 0 && !whole && !(first_item && tile_first > 0)) {
+            const int64_t t1 = span.beg + span.left + it.ntiles - tile;
+            Cut cut;
+            cut.parts = int(divide(t1 + span.part - 1, span.part)) - int(blockIdx.x);
+            cut.first = first_item ? 0 : 1;
+            cut.b = it.b;
+            cut.hk = it.hk;
+            cut.rb = it.rb;
+            reinterpret_cast<Cut *>(a.ws)[blockIdx.x] = cut;
+        }
+        for (int i = threadIdx.x; i < NR * D; i += kThreads) {
+            const int rr = i / D, d = i % D, row = it.rb * NR + rr;
+            if (row >= rows) break;
+            float mt = -INFINITY, lt = 0.f, x = 0.f;
+#pragma unroll
+            for (int w = 0; w < kF32Warps; ++w) mt = fmaxf(mt, top_of[w][rr]);
+            const float base = mt == -INFINITY ? 0.f : mt;
+#pragma unroll
+            for (int w = 0; w < kF32Warps; ++w) {
+                const float f = ex2(top_of[w][rr] - base);
+                lt = fmaf(sum_of[w][rr], f, lt);
+                x = fmaf(outs[w][rr][d], f, x);
+            }
+            if (whole) {
+                const int t = row / s.G, h = it.hk * s.G + row - t * s.G;
+                static_cast<float *>(a.out)[it.b * a.o_sb + t * a.o_st + h * a.o_sh + d] =
+                    lt == 0.f ? 0.f : x / lt;
+                if (a.lse && d == 0)
+                    a.lse[(int64_t(it.b) * a.T + t) * a.Hq + h] =
+                        lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
+            } else {
+                part[rr * D + d] = x;
+                if (d == 0) {
+                    part[NR * D + rr] = mt;
+                    part[NR * (D + 1) + rr] = lt;
+                }
+            }
+        }
+        if (item_end) {
+            tile = 0;
+            left -= kItemCost;
+            fresh = true;
+            first_item = false;
+            it = next_item(a, s, it, a.lens[min(it.b + 1, a.B - 1)]);
+        }
     }
-    if (lane == 0) sm_m[warp] = m, sm_l[warp] = l;
-#pragma unroll
-    for (int i = 0; i < E; ++i) sm_o[warp][lane * E + i] = o[i];
-    __syncthreads();
-    if (warp) return;
-    float mt = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3])), lt = 0.f, ot[E] = {};
-    for (int w = 0; w < 4; ++w) {
-        const float f = exp2f(sm_m[w] - (mt == -INFINITY ? 0.f : mt));
-        lt = fmaf(sm_l[w], f, lt);
-#pragma unroll
-        for (int i = 0; i < E; ++i) ot[i] = fmaf(sm_o[w][lane * E + i], f, ot[i]);
-    }
-    float *out = static_cast<float *>(a.out) + b * a.o_sb + t * a.o_st + h * a.o_sh + lane * E;
-    const float inv = lt == 0.f ? 0.f : 1.f / lt;
-#pragma unroll
-    for (int i = 0; i < E; ++i) out[i] = ot[i] * inv;
-    if (a.lse && lane == 0)
-        a.lse[(int64_t(b) * a.T + t) * a.Hq + h] =
-            lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
 }
 
 // ---- launches -----------------------------------------------------------------------------
@@ -1187,17 +1324,10 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t> (&done)[4]) {
     return e;
 }
 
-template <int D, bool F8, int NQ, int WR>
-cudaError_t launch_mma(const PagedArgs &a, Shape s, cudaStream_t stream) {
-    using C = Cfg<D, F8, NQ, WR>;
-    static std::atomic<uint64_t> done[4];
-    s.KS = C::KS;
-    cudaError_t e = allow_smem(k_paged_mma<D, F8, NQ, WR>, C::SMEM, done);
-    if (e != cudaSuccess) return e;
-    k_paged_mma<D, F8, NQ, WR><<<s.ncta, kThreads, C::SMEM, stream>>>(a, s);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    // The join may start while the last parts are being computed; it waits for
-    // them before it reads any.
+// The join may start while the last parts are being computed; it waits for them before
+// it reads any.
+template <typename T, int D>
+cudaError_t launch_join(const PagedArgs &a, const Shape &s, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1209,7 +1339,27 @@ cudaError_t launch_mma(const PagedArgs &a, Shape s, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_paged_join<__nv_bfloat16, D>, a, s, per);
+    return cudaLaunchKernelEx(&cfg, k_paged_join<T, D>, a, s, per);
+}
+
+template <int D, bool F8, int NQ, int WR>
+cudaError_t launch_mma(const PagedArgs &a, Shape s, cudaStream_t stream) {
+    using C = Cfg<D, F8, NQ, WR>;
+    static std::atomic<uint64_t> done[4];
+    s.KS = C::KS;
+    cudaError_t e = allow_smem(k_paged_mma<D, F8, NQ, WR>, C::SMEM, done);
+    if (e != cudaSuccess) return e;
+    k_paged_mma<D, F8, NQ, WR><<<s.ncta, kThreads, C::SMEM, stream>>>(a, s);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return launch_join<__nv_bfloat16, D>(a, s, stream);
+}
+
+template <int D, int NR>
+cudaError_t launch_f32(const PagedArgs &a, Shape s, cudaStream_t stream) {
+    s.KS = 8 * kF32Warps;
+    k_paged_f32<D, NR><<<s.ncta, kThreads, 0, stream>>>(a, s);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_join<float, D>(a, s, stream);
 }
 
 // Rows of a block: 8 or 16 to a warp, then up to four warps along the rows (and
@@ -1219,7 +1369,10 @@ Shape make_shape(const PagedArgs &a) {
     Shape s{};
     s.G = a.Hq / a.c.Hkv;
     const int64_t rows = int64_t(a.T) * s.G;
-    s.RB = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    if (a.c.dt == DT_F32)      // (the outputs of NR rows are NR D / 4 registers)
+        s.RB = rows == 1 ? 1 : rows == 2 || a.c.D == 128 ? 2 : 4;
+    else
+        s.RB = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     s.nrb = int((rows + s.RB - 1) / s.RB);
     s.ncta = device_sm_count() * kCtasPerSm;
     return s;
@@ -1239,8 +1392,10 @@ cudaError_t launch_rows(const PagedArgs &a, cudaStream_t stream) {
 template <int D>
 cudaError_t launch_d(const PagedArgs &a, cudaStream_t stream) {
     if (a.c.dt == DT_F32) {
-        k_paged_rows<D><<<dim3(unsigned(a.Hq), unsigned(a.T), unsigned(a.B)), 128, 0, stream>>>(a);
-        return cudaGetLastError();
+        const Shape s = make_shape(a);
+        if (s.RB == 1) return launch_f32<D, 1>(a, s, stream);
+        if (s.RB == 2) return launch_f32<D, 2>(a, s, stream);
+        return launch_f32<D, D == 64 ? 4 : 2>(a, s, stream);
     }
     return a.c.dt == DT_BF16 ? launch_rows<D, false>(a, stream) : launch_rows<D, true>(a, stream);
 }
@@ -1248,7 +1403,6 @@ cudaError_t launch_d(const PagedArgs &a, cudaStream_t stream) {
 }  // namespace
 
 size_t paged_workspace(const PagedArgs &a) {
-    if (a.c.dt == DT_F32) return 0;
     const Shape s = make_shape(a);
     return s.ncta * (sizeof(Cut) + 2 * part_floats(s.RB, a.c.D) * sizeof(float));
 }
