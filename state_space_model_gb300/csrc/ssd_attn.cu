@@ -60,8 +60,13 @@ constexpr int kStages = 3;                // tiles that a CTA has room for
 // so that somebody writes its rows.
 constexpr int kItemCost = 3;
 
-struct Shape {            // of the schedule: what both kernels derive alike
-    int KS;               // positions of a tile
+// What both kernels derive the schedule from (by value, so that functions out of line
+// have it in registers).
+struct Shape {
+    const int32_t *lens;
+    int B, T, Hkv;
+    int cap;              // positions that the page table has room for
+    int window;
     int RB;               // rows of a row block (the rows of a sequence and head: T G)
     int nrb;              // row blocks
     int G;                // query heads to a key/value head
@@ -77,41 +82,51 @@ struct Item {
     int ntiles;
 };
 
-// (What follows runs once for an item or a CTA; kept out of line, so that the loop
+// (What runs once for an item or a CTA is kept small or out of line, so that the loop
 // over tiles stays small: with all of it inlined the kernel was 120 KB of code, and a
 // fifth of the loop's time was spent waiting for instructions.)
-__device__ __forceinline__ void item_range(const PagedArgs &a, const Shape &s, Item &it) {
-    const int rows = a.T * s.G;
-    const int r0 = it.rb * s.RB, r1 = min(r0 + s.RB, rows) - 1;
-    it.emin = it.len - a.T + r0 / s.G;
-    it.emax = it.len - a.T + r1 / s.G;
-    const int cap = a.M * a.c.ps;
-    it.hi = min(it.emax + 1, cap);
-    it.lo = a.window > 0 ? min(max(0, it.emin + 1 - int(a.window)), cap) : 0;
-    it.first = it.lo / s.KS * s.KS;
-    it.ntiles = max(1, (it.hi - it.first + s.KS - 1) / s.KS);
+template <int KS>
+__device__ __forceinline__ void item_range(const Shape &s, Item &it) {
+    it.emin = it.len - s.T;
+    it.emax = it.len - 1;
+    if (s.nrb > 1) {
+        const int r0 = it.rb * s.RB, r1 = min(r0 + s.RB, s.T * s.G) - 1;
+        it.emin = it.len - s.T + r0 / s.G;
+        it.emax = it.len - s.T + r1 / s.G;
+    }
+    it.hi = min(it.emax + 1, s.cap);
+    it.lo = s.window > 0 ? min(max(0, it.emin + 1 - s.window), s.cap) : 0;
+    it.first = it.lo / KS * KS;
+    it.ntiles = max(1, (it.hi - it.first + KS - 1) / KS);
 }
 
-__device__ __noinline__ int64_t seq_cost(const PagedArgs &a, const Shape &s, int b) {
+// The cost of one key/value head of a sequence.
+template <int KS>
+__device__ __forceinline__ int64_t head_cost(const Shape &s, int len) {
     Item it;
-    it.len = max(a.lens[b], 0);
+    it.len = len;
     int64_t n = 0;
 #pragma unroll 1
     for (it.rb = 0; it.rb < s.nrb; ++it.rb) {
-        item_range(a, s, it);
+        item_range<KS>(s, it);
         n += it.ntiles + kItemCost;
     }
-    return n * a.c.Hkv;
+    return n;
 }
 
-// Block-wide: the inclusive prefix of w over the threads, and the block's sum.
-__device__ __forceinline__ int64_t block_scan(int64_t w, int64_t *sums, int64_t &total) {
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+// The inclusive prefix of w over the lanes of a warp.
+__device__ __forceinline__ int64_t warp_scan(int64_t w) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t v = __shfl_up_sync(~0u, w, o);
-        if (lane >= o) w += v;
+        if (int(threadIdx.x % 32) >= o) w += v;
     }
+    return w;
+}
+// The same over the threads of a CTA, and the sum of all.
+__device__ __forceinline__ int64_t block_scan(int64_t w, int64_t *sums, int64_t &total) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    w = warp_scan(w);
     __syncthreads();
     if (lane == 31) sums[warp] = w;
     __syncthreads();
@@ -125,11 +140,12 @@ __device__ __forceinline__ int64_t block_scan(int64_t w, int64_t *sums, int64_t 
     return w + before;
 }
 
-__device__ __noinline__ int64_t divide(int64_t x, int64_t y) {   // both >= 0; mostly short
-    return ((x | y) >> 32) == 0 ? int64_t(uint32_t(x) / uint32_t(y)) : x / y;
+__device__ __noinline__ int64_t divide_long(int64_t x, int64_t y) { return x / y; }
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {   // both >= 0; mostly short
+    return ((x | y) >> 32) == 0 ? int64_t(uint32_t(x) / uint32_t(y)) : divide_long(x, y);
 }
 
-// A stretch of the line: CTA c takes units [c part, (c + 1) part) of total.
+// A stretch of the line: CTA c takes units [c part, (c + 1) part) of the total.
 struct Stretch {
     Item it;              // the item that holds its first unit
     int unit;             // that unit's number in the item
@@ -137,74 +153,100 @@ struct Stretch {
     int64_t part;
 };
 
-// All threads of a CTA call it, and get the same; left <= 0: there is none.
-struct Finder {
-    int64_t sums[kThreads / 32];
-    Item it;
-    int unit;
-
-    __device__ __noinline__ Stretch find(const PagedArgs &a, const Shape &s, int cta) {
-        Stretch f;
-        int64_t total = 0, w = 0, upto = 0;
+// The place in a sequence's items of the unit `rest` from its first.
+template <int KS>
+__device__ __forceinline__ void place(const Shape &s, int64_t rest, int64_t per, Stretch &f) {
+    f.it.hk = s.Hkv > 1 ? int(divide(rest, per)) : 0;
+    rest -= f.it.hk * per;
 #pragma unroll 1
-        for (int base = 0; base < a.B; base += kThreads) {
-            const int i = base + threadIdx.x;
-            int64_t sum;
-            w = i < a.B ? seq_cost(a, s, i) : 0;
-            upto = total + block_scan(w, sums, sum);
-            total += sum;
-        }
-        f.part = divide(total + s.ncta - 1, s.ncta);
-        f.beg = cta * f.part;
-        f.left = min(f.part, total - f.beg);
-        if (f.left <= 0) return f;
-        int64_t run = 0;
-#pragma unroll 1
-        for (int base = 0; base < a.B && run <= f.beg; base += kThreads) {
-            const int i = base + threadIdx.x;
-            if (a.B > kThreads) {      // else w and upto are still there
-                int64_t sum;
-                w = i < a.B ? seq_cost(a, s, i) : 0;
-                upto = run + block_scan(w, sums, sum);
-                run += sum;
-            }
-            if (f.beg < upto && f.beg >= upto - w) {
-                it.b = i;
-                it.len = max(a.lens[i], 0);
-                int64_t rest = f.beg - (upto - w);
-                it.hk = 0;
-                if (a.c.Hkv > 1) {
-                    const int64_t per = divide(w, a.c.Hkv);
-                    it.hk = int(divide(rest, per));
-                    rest -= it.hk * per;
-                }
-#pragma unroll 1
-                for (it.rb = 0;; ++it.rb) {
-                    item_range(a, s, it);
-                    if (rest < it.ntiles + kItemCost) break;
-                    rest -= it.ntiles + kItemCost;
-                }
-                unit = int(rest);
-            }
-        }
-        __syncthreads();
-        f.it = it;
-        f.unit = unit;
-        return f;
+    for (f.it.rb = 0;; ++f.it.rb) {
+        item_range<KS>(s, f.it);
+        if (rest < f.it.ntiles + kItemCost) break;
+        rest -= f.it.ntiles + kItemCost;
     }
+    f.unit = int(rest);
+}
+
+struct FinderRoom {
+    int64_t sums[kThreads / 32], rest, per;
+    int b, len;
 };
 
+// Stretch number cta; left <= 0: there is none.  All threads of a CTA call it and get
+// the same.  Up to 32 sequences each warp finds for itself, a lane a sequence (with
+// barriers between the warps, more divisions and parameters read through memory this
+// took half of a short call: 2.6 us); more go a thread a sequence, twice over.
+template <int KS>
+__device__ __forceinline__ Stretch find_few(const Shape &s, int cta) {
+    Stretch f;
+    const int lane = threadIdx.x % 32;
+    const int len = lane < s.B ? max(s.lens[lane], 0) : 0;
+    const int64_t per = head_cost<KS>(s, len), w = lane < s.B ? per * s.Hkv : 0;
+    const int64_t upto = warp_scan(w), total = __shfl_sync(~0u, upto, 31);
+    f.part = divide(total + s.ncta - 1, s.ncta);
+    f.beg = cta * f.part;
+    f.left = min(f.part, total - f.beg);
+    if (f.left <= 0) return f;
+    const int who = __ffs(__ballot_sync(~0u, f.beg < upto && f.beg >= upto - w)) - 1;
+    f.it.b = who;
+    f.it.len = __shfl_sync(~0u, len, who);
+    place<KS>(s, f.beg - __shfl_sync(~0u, upto - w, who), __shfl_sync(~0u, per, who), f);
+    return f;
+}
+template <int KS>
+__device__ __noinline__ Stretch find_many(const Shape s, int cta, FinderRoom *room) {
+    Stretch f;
+    int64_t total = 0;
+#pragma unroll 1
+    for (int base = 0; base < s.B; base += kThreads) {
+        const int i = base + threadIdx.x;
+        int64_t sum;
+        block_scan(i < s.B ? head_cost<KS>(s, max(s.lens[i], 0)) * s.Hkv : 0, room->sums, sum);
+        total += sum;
+    }
+    f.part = divide(total + s.ncta - 1, s.ncta);
+    f.beg = cta * f.part;
+    f.left = min(f.part, total - f.beg);
+    if (f.left <= 0) return f;
+    int64_t run = 0;
+#pragma unroll 1
+    for (int base = 0; base < s.B && run <= f.beg; base += kThreads) {
+        const int i = base + threadIdx.x;
+        const int len = i < s.B ? max(s.lens[i], 0) : 0;
+        const int64_t per = head_cost<KS>(s, len), w = i < s.B ? per * s.Hkv : 0;
+        int64_t sum;
+        const int64_t upto = run + block_scan(w, room->sums, sum);
+        run += sum;
+        if (f.beg < upto && f.beg >= upto - w) {
+            room->b = i;
+            room->len = len;
+            room->per = per;
+            room->rest = f.beg - (upto - w);
+        }
+    }
+    __syncthreads();
+    f.it.b = room->b;
+    f.it.len = room->len;
+    place<KS>(s, room->rest, room->per, f);
+    return f;
+}
+template <int KS>
+__device__ __forceinline__ Stretch find(const Shape &s, int cta, FinderRoom *room) {
+    return s.B <= 32 ? find_few<KS>(s, cta) : find_many<KS>(s, cta, room);
+}
+
 // len: the length of the next sequence
-__device__ __noinline__ Item next_item(const PagedArgs &a, const Shape &s, Item it, int len) {
+template <int KS>
+__device__ __noinline__ Item next_item(const Shape s, Item it, int len) {
     if (++it.rb == s.nrb) {
         it.rb = 0;
-        if (++it.hk == a.c.Hkv) {
+        if (++it.hk == s.Hkv) {
             it.hk = 0;
             ++it.b;
             it.len = max(len, 0);
         }
     }
-    item_range(a, s, it);
+    item_range<KS>(s, it);
     return it;
 }
 
@@ -535,7 +577,7 @@ __device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, c
         if (++tile == it.ntiles) {
             tile = 0;
             left -= kItemCost;
-            it = next_item(a, s, it, len);
+            it = next_item<KS>(s, it, len);
             len = a.lens[min(it.b + 1, a.B - 1)];
         }
         look_up();
@@ -552,7 +594,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     constexpr int KT = KP / 16;           // its score tiles
     constexpr int MT = D / 16;            // output tiles
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ Finder finder;
+    __shared__ FinderRoom finder;
     __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ float top_of[kWarps][8 * NQ], sum_of[kWarps][8 * NQ];
 
@@ -562,8 +604,8 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
         ptx::mbar_init(&full[threadIdx.x], kCopyWarps * (32 + 1));
         ptx::mbar_init(&empty[threadIdx.x], kWarps);
     }
-    // (its barriers also make the initialised ones visible)
-    const Stretch span = finder.find(a, s, blockIdx.x);
+    __syncthreads();
+    const Stretch span = find<KS>(s, blockIdx.x, &finder);
     if (threadIdx.x == 0) reinterpret_cast<Cut *>(a.ws)[blockIdx.x].parts = 0;
     // A cursor: an item, a tile of it, and the units left; the tiles of an item come
     // after its constant.
@@ -941,7 +983,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             tile = 0;
             left -= kItemCost;
             fresh = true;
-            it = next_item(a, s, it, a.lens[min(it.b + 1, a.B - 1)]);
+            it = next_item<KS>(s, it, a.lens[min(it.b + 1, a.B - 1)]);
             if (left > 0) load_queries();
         }
         warps_sync();
@@ -1125,13 +1167,15 @@ template <int D, int NR>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
     constexpr int V = D / 16;                    // float4 of a lane's quarter
-    __shared__ Finder finder;
-    __shared__ float qsm[NR][D];                 // queries times scale log2(e)
-    __shared__ float outs[kF32Warps][NR][D], top_of[kF32Warps][NR], sum_of[kF32Warps][NR];
+    __shared__ FinderRoom finder;
+    __shared__ __align__(16) float qsm[NR][D];   // queries times scale log2(e)
+    __shared__ __align__(16) float outs[kF32Warps][NR][D];
+    __shared__ float top_of[kF32Warps][NR], sum_of[kF32Warps][NR];
     let_next_start();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int quad = lane / 4, part4 = lane % 4;
-    const Stretch span = finder.find(a, s, blockIdx.x);
+    constexpr int KS = 8 * kF32Warps;
+    const Stretch span = find<KS>(s, blockIdx.x, &finder);
     if (threadIdx.x == 0) reinterpret_cast<Cut *>(a.ws)[blockIdx.x].parts = 0;
     Item it = span.it;
     int tile = max(0, span.unit - kItemCost);
@@ -1145,7 +1189,7 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     int64_t ld_left = left;
     auto look_up = [&]() {
         page = -1;
-        const int pos = ld.first + ld_tile * s.KS + warp * 8 + quad;
+        const int pos = ld.first + ld_tile * KS + warp * 8 + quad;
         const int p = pos / a.c.ps;
         at = pos - p * a.c.ps;
         if (ld_left > 0 && pos >= ld.lo && pos < ld.hi) page = a.table[ld.b * a.tb + p];
@@ -1168,7 +1212,7 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
         if (++ld_tile == ld.ntiles) {
             ld_tile = 0;
             ld_left -= kItemCost;
-            ld = next_item(a, s, ld, a.lens[min(ld.b + 1, a.B - 1)]);
+            ld = next_item<KS>(s, ld, a.lens[min(ld.b + 1, a.B - 1)]);
         }
         look_up();
     };
@@ -1204,7 +1248,7 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
         const bool there = nthere;
 #pragma unroll
         for (int i = 0; i < V; ++i) k[i] = nk[i], v[i] = nv[i];
-        const int pos = it.first + tile * s.KS + warp * 8 + quad;
+        const int pos = it.first + tile * KS + warp * 8 + quad;
         if (left > 1) load();
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
@@ -1303,7 +1347,7 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             left -= kItemCost;
             fresh = true;
             first_item = false;
-            it = next_item(a, s, it, a.lens[min(it.b + 1, a.B - 1)]);
+            it = next_item<KS>(s, it, a.lens[min(it.b + 1, a.B - 1)]);
         }
     }
 }
@@ -1343,10 +1387,9 @@ cudaError_t launch_join(const PagedArgs &a, const Shape &s, cudaStream_t stream)
 }
 
 template <int D, bool F8, int NQ, int WR>
-cudaError_t launch_mma(const PagedArgs &a, Shape s, cudaStream_t stream) {
+cudaError_t launch_mma(const PagedArgs &a, const Shape &s, cudaStream_t stream) {
     using C = Cfg<D, F8, NQ, WR>;
     static std::atomic<uint64_t> done[4];
-    s.KS = C::KS;
     cudaError_t e = allow_smem(k_paged_mma<D, F8, NQ, WR>, C::SMEM, done);
     if (e != cudaSuccess) return e;
     k_paged_mma<D, F8, NQ, WR><<<s.ncta, kThreads, C::SMEM, stream>>>(a, s);
@@ -1355,8 +1398,7 @@ cudaError_t launch_mma(const PagedArgs &a, Shape s, cudaStream_t stream) {
 }
 
 template <int D, int NR>
-cudaError_t launch_f32(const PagedArgs &a, Shape s, cudaStream_t stream) {
-    s.KS = 8 * kF32Warps;
+cudaError_t launch_f32(const PagedArgs &a, const Shape &s, cudaStream_t stream) {
     k_paged_f32<D, NR><<<s.ncta, kThreads, 0, stream>>>(a, s);
     const cudaError_t e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_join<float, D>(a, s, stream);
@@ -1367,6 +1409,12 @@ cudaError_t launch_f32(const PagedArgs &a, Shape s, cudaStream_t stream) {
 // blocks, each of which reads the cache.
 Shape make_shape(const PagedArgs &a) {
     Shape s{};
+    s.lens = a.lens;
+    s.B = a.B;
+    s.T = a.T;
+    s.Hkv = a.c.Hkv;
+    s.cap = a.M * a.c.ps;
+    s.window = int(a.window);
     s.G = a.Hq / a.c.Hkv;
     const int64_t rows = int64_t(a.T) * s.G;
     if (a.c.dt == DT_F32)      // (the outputs of NR rows are NR D / 4 registers)
