@@ -13,9 +13,13 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <cmath>
+#include <optional>
 
 #include "ssd.h"
 
@@ -91,12 +95,22 @@ const at::Tensor *tensor(PyObject *o) {
     return nullptr;
 }
 
+// A new packed tensor beside `like` (at::empty without its dispatch: a call that makes
+// its output, its log sums and its workspace spends half its host time there).
+at::Tensor make(const at::Tensor &like, at::IntArrayRef shape, at::ScalarType dtype) {
+    TORCH_CHECK_VALUE(like.is_cuda(), "all tensors must be CUDA tensors (the library takes device pointers)");
+    return at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt);
+}
+
 // Every function: C++ exceptions (torch's allocator) become Python's, and a
 // status of the library is returned as an int for the caller to raise.
 template <typename F>
 PyObject *guarded(F &&f) {
     try {
         return f();
+    } catch (const c10::ValueError &e) {
+        PyErr_SetString(PyExc_ValueError, e.what_without_backtrace());
+        return nullptr;
     } catch (const std::exception &e) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
         return nullptr;
@@ -120,7 +134,7 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!q) return nullptr;
         at::Tensor out;
         if (a[15] == Py_None) {
-            out = at::empty(q->sizes(), q->options());
+            out = make(*q, q->sizes(), q->scalar_type());
         } else {
             const at::Tensor *o = tensor(a[15]);
             if (!o) return nullptr;
@@ -167,7 +181,7 @@ PyObject *kv_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
             }
             at::ScalarType dt = pool->scalar_type();
             if (dt == at::kFloat8_e4m3fn) dt = f32 ? at::kFloat : at::kBFloat16;
-            kv[i] = at::empty({tokens, pool->size(1), pool->size(3)}, pool->options().dtype(dt));
+            kv[i] = make(*pool, {tokens, pool->size(1), pool->size(3)}, dt);
         }
         Call c;
         ssd_tensor *in[7];
@@ -211,23 +225,26 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
         ssd_tensor *in[7];
         for (int i = 0; i < 7; ++i) in[i] = c.add(a[i]);
         if (c.bad) return nullptr;
-        at::Tensor out, lse, ws;
+        at::Tensor out, lse;
+        c10::DataPtr own;          // a workspace of this call: back to the cache when it returns
+        void *room = nullptr;
+        size_t bytes = 0;
         if (a[10] == Py_None) {
-            out = at::empty({B, T, H, D}, q->options());
+            out = make(*q, {B, T, H, D}, q->scalar_type());
         } else {
             const at::Tensor *t = tensor(a[10]);
             if (!t) return nullptr;
             out = *t;
         }
-        if (want_lse) lse = at::empty({B, T, H}, q->options().dtype(at::kFloat));
+        if (want_lse) lse = make(*q, {B, T, H}, at::kFloat);
         ssd_tensor *o = c.add(out), *l = !c.bad && want_lse ? c.add(lse) : nullptr;
         if (c.bad) return nullptr;
         if (a[11] == Py_None) {
-            size_t need = 0;
             const ssd_status st = g_ws_size(B, T, H, pool->size(1), D, code_of(pool->scalar_type()),
-                                            &need);
+                                            &bytes);
             if (st) return PyLong_FromLong(st);
-            if (need) ws = at::empty({int64_t(need)}, q->options().dtype(at::kByte));
+            if (bytes) own = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
+            room = own.get();
         } else {
             const at::Tensor *t = tensor(a[11]);
             if (!t) return nullptr;
@@ -239,10 +256,9 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 PyErr_SetString(PyExc_ValueError, "workspace: must be contiguous");
                 return nullptr;
             }
-            ws = *t;
+            bytes = t->nbytes();
+            room = bytes ? t->data_ptr() : nullptr;
         }
-        void *room = ws.defined() && ws.numel() > 0 ? ws.data_ptr() : nullptr;
-        const size_t bytes = ws.defined() ? size_t(ws.nbytes()) : 0;
         void *stream = c.stream();
         ssd_status st;
         Py_BEGIN_ALLOW_THREADS

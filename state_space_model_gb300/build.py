@@ -94,8 +94,8 @@ def build_binding() -> str:
            "-I", os.path.join(ROOT, "include"), "-I", os.path.join(troot, "include"),
            "-I", os.path.join(troot, "include", "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
-           "-L", os.path.join(troot, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
-           "-lc10_cuda", "-Wl,-rpath," + os.path.join(troot, "lib")]
+           "-L", os.path.join(troot, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+           "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath," + os.path.join(troot, "lib")]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on attn_ext.cpp:\n{r.stdout}\n{r.stderr}")
