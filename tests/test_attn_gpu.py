@@ -495,3 +495,58 @@ def test_empty_calls(attn):
     q = torch.ones(2, 1, 4, 64, dtype=BF, device="cuda")   # no table columns: no positions
     out = attn.paged_attention(q, kc, vc, torch.zeros(2, 0, **i32), torch.full((2,), 9, **i32))
     assert (out == 0).all()
+
+
+@pytest.mark.parametrize("cache", ["fp8", "bf16"])
+def test_example_runs_them_together(cache):
+    """The hybrid example: its checks compare bf16 results of the same tokens by two paths.  The
+    attention check differs by the probabilities' and the output's rounding (2^-8 each, of values
+    up to a few times the largest output); decoding against one prompt accumulates a layer's
+    bf16 roundings."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "hybrid_decode.py")
+    spec = importlib.util.spec_from_file_location("hybrid_decode", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    last, apart = mod.main(cache)
+    assert last < 2e-2 and apart < 2e-2
+
+
+DEBUG_CHILD = r"""
+import ctypes, json, sys
+sys.path[:0] = [sys.argv[1], sys.argv[1] + "/tests"]
+import test_attn_gpu as t
+from state_space_model_gb300 import _native, attn
+import torch
+assert _native.LIB_PATH.endswith("libssd_gb300_debug.so"), _native.LIB_PATH
+for case in t.APPEND[:6]:
+    t.check_append(attn, case)
+for pdt in (t.BF, t.F8, t.F32):
+    for case in t.ATTN[2:16:3]:
+        T, Hq, Hkv, D, ps, lens, window = case
+        prob = t.attn_problem(len(lens), T, Hq, Hkv, D, ps, lens, pdt, seed=T + Hq + ps)
+        t.check_attn(attn, prob, pdt, window)
+    prob = t.attn_problem(40, 1, 8, 2, 128, 16, [9 * i for i in range(39)] + [3000], pdt, seed=3)
+    t.check_attn(attn, prob, pdt)
+    t.test_read_matches_oracle(attn, pdt, t.BF if pdt == t.F8 else pdt, 64, 16, [5, 0, 33, 1])
+lib = _native.load()
+st = lib.ssd_device_status(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+print(json.dumps({"status": st, "detail": lib.ssd_last_error_detail().decode()}))
+"""
+
+
+def test_debug_build_finds_every_index_in_bounds(attn):
+    """The bounds-checked build runs the same checks, and none of its own fires."""
+    import json
+    import os
+    import subprocess
+    import sys
+    from state_space_model_gb300 import build
+    build.build(debug_bounds=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", DEBUG_CHILD, root], env=dict(os.environ, SSD_DEBUG_BOUNDS="1"),
+                       cwd=root, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout + r.stderr
+    out = json.loads(r.stdout.strip().splitlines()[-1])
+    assert out["status"] == 0, out["detail"]
