@@ -40,9 +40,13 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 4;                 // of a CTA that compute
-constexpr int kCopyWarps = 2;             // and that copy
+constexpr int kCopyWarps = 4;             // and that copy
 constexpr int kThreads = 32 * (kWarps + kCopyWarps);
 constexpr int kCtasPerSm = 2;
+// Registers of a thread: 128 at the launch (two CTAs of 256 threads fill an SM's file),
+// shared out again as 208 and 48, 128 x (208 + 48) = 256 x 128.
+constexpr int kComputeRegs = 208, kCopyRegs = 48;
+constexpr int kF32Warps = 6;              // of a CTA of the fp32 kernel
 constexpr int kStages = 3;                // tiles that a CTA has room for
 
 // ---- the schedule -----------------------------------------------------------------
@@ -60,8 +64,7 @@ constexpr int kStages = 3;                // tiles that a CTA has room for
 // so that somebody writes its rows.
 constexpr int kItemCost = 3;
 
-// What both kernels derive the schedule from (by value, so that functions out of line
-// have it in registers).
+// What both kernels derive the schedule from.
 struct Shape {
     const int32_t *lens;
     int B, T, Hkv;
@@ -82,9 +85,10 @@ struct Item {
     int ntiles;
 };
 
-// (What runs once for an item or a CTA is kept small or out of line, so that the loop
-// over tiles stays small: with all of it inlined the kernel was 120 KB of code, and a
-// fifth of the loop's time was spent waiting for instructions.)
+// (What runs once for an item or a CTA is kept small, so that the loop over tiles stays
+// near: when a kernel was 120 KB of code, a fifth of the loop's time was spent waiting
+// for instructions.  Calls out of line are no way, they fix the registers of both
+// kinds of warps.)
 template <int KS>
 __device__ __forceinline__ void item_range(const Shape &s, Item &it) {
     it.emin = it.len - s.T;
@@ -123,7 +127,8 @@ __device__ __forceinline__ int64_t warp_scan(int64_t w) {
     }
     return w;
 }
-// The same over the threads of a CTA, and the sum of all.
+// The same over the threads of a CTA of NW warps, and the sum of all.
+template <int NW>
 __device__ __forceinline__ int64_t block_scan(int64_t w, int64_t *sums, int64_t &total) {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     w = warp_scan(w);
@@ -133,16 +138,15 @@ __device__ __forceinline__ int64_t block_scan(int64_t w, int64_t *sums, int64_t 
     int64_t before = 0;
     total = 0;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
+    for (int i = 0; i < NW; ++i) {
         if (i < warp) before += sums[i];
         total += sums[i];
     }
     return w + before;
 }
 
-__device__ __noinline__ int64_t divide_long(int64_t x, int64_t y) { return x / y; }
 __device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {   // both >= 0; mostly short
-    return ((x | y) >> 32) == 0 ? int64_t(uint32_t(x) / uint32_t(y)) : divide_long(x, y);
+    return ((x | y) >> 32) == 0 ? int64_t(uint32_t(x) / uint32_t(y)) : x / y;
 }
 
 // A stretch of the line: CTA c takes units [c part, (c + 1) part) of the total.
@@ -168,7 +172,7 @@ __device__ __forceinline__ void place(const Shape &s, int64_t rest, int64_t per,
 }
 
 struct FinderRoom {
-    int64_t sums[kThreads / 32], rest, per;
+    int64_t sums[32], rest, per;
     int b, len;
 };
 
@@ -193,15 +197,15 @@ __device__ __forceinline__ Stretch find_few(const Shape &s, int cta) {
     place<KS>(s, f.beg - __shfl_sync(~0u, upto - w, who), __shfl_sync(~0u, per, who), f);
     return f;
 }
-template <int KS>
-__device__ __noinline__ Stretch find_many(const Shape s, int cta, FinderRoom *room) {
+template <int KS, int NW>
+__device__ __forceinline__ Stretch find_many(const Shape s, int cta, FinderRoom *room) {
     Stretch f;
     int64_t total = 0;
 #pragma unroll 1
-    for (int base = 0; base < s.B; base += kThreads) {
+    for (int base = 0; base < s.B; base += 32 * NW) {
         const int i = base + threadIdx.x;
         int64_t sum;
-        block_scan(i < s.B ? head_cost<KS>(s, max(s.lens[i], 0)) * s.Hkv : 0, room->sums, sum);
+        block_scan<NW>(i < s.B ? head_cost<KS>(s, max(s.lens[i], 0)) * s.Hkv : 0, room->sums, sum);
         total += sum;
     }
     f.part = divide(total + s.ncta - 1, s.ncta);
@@ -210,12 +214,12 @@ __device__ __noinline__ Stretch find_many(const Shape s, int cta, FinderRoom *ro
     if (f.left <= 0) return f;
     int64_t run = 0;
 #pragma unroll 1
-    for (int base = 0; base < s.B && run <= f.beg; base += kThreads) {
+    for (int base = 0; base < s.B && run <= f.beg; base += 32 * NW) {
         const int i = base + threadIdx.x;
         const int len = i < s.B ? max(s.lens[i], 0) : 0;
         const int64_t per = head_cost<KS>(s, len), w = i < s.B ? per * s.Hkv : 0;
         int64_t sum;
-        const int64_t upto = run + block_scan(w, room->sums, sum);
+        const int64_t upto = run + block_scan<NW>(w, room->sums, sum);
         run += sum;
         if (f.beg < upto && f.beg >= upto - w) {
             room->b = i;
@@ -230,14 +234,14 @@ __device__ __noinline__ Stretch find_many(const Shape s, int cta, FinderRoom *ro
     place<KS>(s, room->rest, room->per, f);
     return f;
 }
-template <int KS>
+template <int KS, int NW>
 __device__ __forceinline__ Stretch find(const Shape &s, int cta, FinderRoom *room) {
-    return s.B <= 32 ? find_few<KS>(s, cta) : find_many<KS>(s, cta, room);
+    return s.B <= 32 ? find_few<KS>(s, cta) : find_many<KS, NW>(s, cta, room);
 }
 
 // len: the length of the next sequence
 template <int KS>
-__device__ __noinline__ Item next_item(const Shape s, Item it, int len) {
+__device__ __forceinline__ Item next_item(const Shape s, Item it, int len) {
     if (++it.rb == s.nrb) {
         it.rb = 0;
         if (++it.hk == s.Hkv) {
@@ -372,9 +376,10 @@ __device__ __forceinline__ void let_next_start() {
 //
 // Four warps compute, as WK groups of WR: the WR warps of a group take 8 NQ
 // query rows each and share the group's positions, the groups take different
-// positions.  Two more warps copy, up to kStages tiles ahead, across items:
+// positions.  Four more warps copy, up to kStages tiles ahead, across items:
 // looking up pages and making addresses took a third of the computing warps'
-// instructions when each copied its own, and one warp cannot keep up.  Two CTAs fill an SM, so 128 KB of
+// instructions when each copied its own, and one warp cannot keep up; they also give
+// the computing warps most of their registers.  Two CTAs fill an SM, so 128 KB of
 // copies are under way while two tiles are worked on.
 template <int D_, bool F8_, int NQ_, int WR_>
 struct Cfg {
@@ -424,7 +429,7 @@ struct Room {
     }
     // the key scales of a tile, then its value scales
     __device__ __forceinline__ float *scales(int st) const { return reinterpret_cast<float *>(aux(st)); }
-    // bit r % 32 of word r / 32: position r is there
+    // bit r % KW of word r / KW: position r is there
     __device__ __forceinline__ uint32_t *masks(int st) const {
         return reinterpret_cast<uint32_t *>(aux(st) + C::AUX - 16);
     }
@@ -483,27 +488,28 @@ __device__ __forceinline__ uint32_t finite2(uint32_t v) {
     return v;
 }
 
-// Waits for a phase of bar (bounded: false after two seconds); the wait itself is out
-// of line.
-__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity) {
-    return ptx::mbar_wait(bar, parity);
-}
+// Waits for a phase of bar; false after two seconds.
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
-    return __all_sync(~0u, ptx::mbar_try_wait(bar, parity)) ||
-           __all_sync(~0u, wait_long(bar, parity));
+    bool done = ptx::mbar_try_wait(bar, parity);
+    if (!__all_sync(~0u, done)) {
+        const uint64_t t0 = ptx::globaltimer_ns();
+#pragma unroll 1
+        while (!done && ptx::globaltimer_ns() - t0 < 2000000000ull) done = ptx::mbar_try_wait(bar, parity);
+    }
+    return __all_sync(~0u, done);
 }
 
-// A copying warp: fills its part of the stages with the stretch's tiles, one after
-// another.  full[st] is arrived at by each lane's copies as they land and by lane 0
-// for the masks, empty[st] by each computing warp.
+// A copying warp: fills KW positions of each stage, from the first-th on, with the
+// stretch's tiles, one after another.  full[st] is arrived at by each lane's copies as
+// they land and by lane 0 for the mask, empty[st] by each computing warp.
 template <typename C>
 __device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, const Room<C> room,
                                            uint64_t *full, uint64_t *empty, Item it, int tile,
                                            int64_t left, int first) {
-    constexpr int KS = C::KS, ROW = C::ROW, D = C::D, ES = C::F8 ? 1 : 2;
-    constexpr int N = KS / 32 / kCopyWarps;                 // runs of 32 positions: first.. of a tile
+    constexpr int KS = C::KS, KW = C::KW, ROW = C::ROW, D = C::D, ES = C::F8 ? 1 : 2;
     constexpr int LPR = ROW / 16, RPI = 32 / LPR;           // lanes a row, rows a copy
     constexpr int RUN = 16;
+    constexpr uint32_t kAll = 0xffffffffu >> (32 - KW);
     const int lane = threadIdx.x % 32;
     const int lrow = lane / LPR, lch = lane % LPR;
     const int shift = (a.c.ps & (a.c.ps - 1)) ? -1 : __ffs(a.c.ps) - 1;
@@ -512,65 +518,56 @@ __device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, c
     const char *const kpool = static_cast<const char *>(a.c.k);
     const char *const vpool = static_cast<const char *>(a.c.v);
 
-    // Where this lane's positions of the next tile lie (lane + 32 i), looked up a tile
-    // early, and the length of the next sequence.
-    int page[N], at[N];
+    // Where this lane's position of the next tile lies, looked up a tile early, and the
+    // length of the next sequence.
+    int page, at;
     int len = a.lens[min(it.b + 1, a.B - 1)];
     auto look_up = [&]() {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            page[i] = -1;
-            const int pos = it.first + tile * KS + 32 * (first + i) + lane;
-            const int p = shift >= 0 ? pos >> shift : pos / a.c.ps;
-            at[i] = pos - p * a.c.ps;
-            if (left > 0 && pos >= it.lo && pos < it.hi) page[i] = a.table[it.b * a.tb + p];
-        }
+        page = -1;
+        const int pos = it.first + tile * KS + first + lane;
+        const int p = shift >= 0 ? pos >> shift : pos / a.c.ps;
+        at = pos - p * a.c.ps;
+        if (left > 0 && lane < KW && pos >= it.lo && pos < it.hi) page = a.table[it.b * a.tb + p];
     };
     look_up();
     for (int n = 0, st = 0; left > 0; ++n, st = st + 1 == kStages ? 0 : st + 1) {
-        if (n >= kStages && !wait_for(&empty[st], (n / kStages - 1) & 1))
-            return false;
-        uint32_t mask[N];
+        if (n >= kStages && !wait_for(&empty[st], (n / kStages - 1) & 1)) return false;
+        const bool ok = page >= 0 && page < a.c.pages;
+        const uint32_t mask = __ballot_sync(~0u, ok);
+        const int64_t off = ok ? page * a.c.sp + it.hk * a.c.sh + at * a.c.st : 0;
+        const uint32_t kdst = room.keys(st) + first * ROW, vdst = room.values(st) + first * ROW;
+        if (__all_sync(~0u, runs && mask == kAll)) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const bool ok = page[i] >= 0 && page[i] < a.c.pages;
-            mask[i] = __ballot_sync(~0u, ok);
-            const int64_t off = ok ? page[i] * a.c.sp + it.hk * a.c.sh + at[i] * a.c.st : 0;
-            const uint32_t kdst = room.keys(st) + 32 * (first + i) * ROW;
-            const uint32_t vdst = room.values(st) + 32 * (first + i) * ROW;
-            if (__all_sync(~0u, runs && mask[i] == ~0u)) {
+            for (int h = 0; h < KW / RUN; ++h) {
+                const int64_t mine = __shfl_sync(~0u, off, h * RUN) * ES + lrow * ROW + lch * 16;
 #pragma unroll
-                for (int h = 0; h < 32 / RUN; ++h) {
-                    const int64_t mine = __shfl_sync(~0u, off, h * RUN) * ES + lrow * ROW + lch * 16;
-#pragma unroll
-                    for (int j = 0; j < RUN / RPI; ++j) {
-                        const uint32_t d = chunk_at<ROW>(h * RUN + j * RPI + lrow, lch);
-                        const bool in = SSD_IDX_OK(a.err, mine + j * RPI * ROW + 15, a.c.n * ES);
-                        copy16(kdst + d, kpool + mine + j * RPI * ROW, in);
-                        copy16(vdst + d, vpool + mine + j * RPI * ROW, in);
-                    }
+                for (int j = 0; j < RUN / RPI; ++j) {
+                    const uint32_t d = chunk_at<ROW>(h * RUN + j * RPI + lrow, lch);
+                    const bool in = SSD_IDX_OK(a.err, mine + j * RPI * ROW + 15, a.c.n * ES);
+                    copy16(kdst + d, kpool + mine + j * RPI * ROW, in);
+                    copy16(vdst + d, vpool + mine + j * RPI * ROW, in);
                 }
-            } else if (__any_sync(~0u, mask[i] != 0)) {
+            }
+        } else {
+            // zeros where there is no position (a pass may take another warp's along)
 #pragma unroll 1
-                for (int j = 0; j < LPR; ++j) {
-                    const int r = j * RPI + lrow;
-                    const int64_t o = __shfl_sync(~0u, off, r) * ES + lch * 16;
-                    const bool in = (mask[i] >> r) & 1 && SSD_IDX_OK(a.err, o + 15, a.c.n * ES);
-                    copy16(kdst + chunk_at<ROW>(r, lch), kpool + o, in);
-                    copy16(vdst + chunk_at<ROW>(r, lch), vpool + o, in);
-                }
+            for (int r0 = 0; r0 < KW; r0 += RPI) {
+                const int r = r0 + lrow;
+                const int64_t o = __shfl_sync(~0u, off, r) * ES + lch * 16;
+                const bool in = (mask >> r) & 1 && SSD_IDX_OK(a.err, o + 15, a.c.n * ES);
+                copy16(kdst + chunk_at<ROW>(r, lch), kpool + o, in);
+                copy16(vdst + chunk_at<ROW>(r, lch), vpool + o, in);
             }
-            if constexpr (C::F8) {
-                const int64_t so = ok ? page[i] * a.c.ssp + it.hk * a.c.ssh + at[i] : 0;
-                const uint32_t d = smem_addr(room.scales(st)) + (32 * (first + i) + lane) * 4;
-                copy4(d, a.c.ks + so, ok);
-                copy4(d + KS * 4, a.c.vs + so, ok);
-            }
+        }
+        if constexpr (C::F8) {
+            const int64_t so = ok ? page * a.c.ssp + it.hk * a.c.ssh + at : 0;
+            const uint32_t d = smem_addr(room.scales(st)) + (first + lane) * 4;
+            copy4(d, a.c.ks + so, ok);
+            copy4(d + KS * 4, a.c.vs + so, ok);
         }
         copies_arrive(&full[st]);
         if (lane == 0) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) room.masks(st)[first + i] = mask[i];
+            room.masks(st)[first / KW] = mask;
             ptx::mbar_arrive(&full[st]);
         }
         --left;
@@ -605,7 +602,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
         ptx::mbar_init(&empty[threadIdx.x], kWarps);
     }
     __syncthreads();
-    const Stretch span = find<KS>(s, blockIdx.x, &finder);
+    const Stretch span = find<KS, kThreads / 32>(s, blockIdx.x, &finder);
     if (threadIdx.x == 0) reinterpret_cast<Cut *>(a.ws)[blockIdx.x].parts = 0;
     // A cursor: an item, a tile of it, and the units left; the tiles of an item come
     // after its constant.
@@ -614,12 +611,14 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     int64_t left = span.left - max(0, kItemCost - span.unit);
     if (span.left <= 0 || left <= 0) return;
     const Room<C> room{smem};
+    static_assert(kCopyWarps == kWarps && 128 * (kComputeRegs + kCopyRegs) <= kThreads * 128, "");
     if (warp >= kWarps) {
-        if (!copy_tiles<C>(a, s, room, full, empty, it, tile, left,
-                           (warp - kWarps) * (KS / 32 / kCopyWarps)) && lane == 0)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
+        if (!copy_tiles<C>(a, s, room, full, empty, it, tile, left, (warp - kWarps) * KW) && lane == 0)
             atomicOr(a.err, kErrTimeout);
         return;
     }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
     const int kg = warp / WR, wr = warp % WR;     // key group, row warp
     const int g = lane >> 2, c = lane & 3;        // fragment row and column pair
 
@@ -718,7 +717,8 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
 #pragma unroll 1
         for (int sub = 0; sub < KW * WR / KP; ++sub) {
             const int x0 = kg * WR * KW + sub * KP, k0 = kbase + sub * KP;   // the pass's first position
-            const uint32_t mask = (room.masks(st)[x0 / 32] >> (x0 % 32)) & (0xffffffffu >> (32 - KP));
+            uint32_t mask = room.masks(st)[x0 / KW];
+            if constexpr (KP > KW) mask |= room.masks(st)[x0 / KW + 1] << KW;
             // (votes, so that the compiler knows these for the same in all lanes)
             if (!__any_sync(~0u, mask != 0)) continue;
             const bool partial = __any_sync(~0u, k0 + KP - 1 > it.emin ||
@@ -1162,9 +1162,8 @@ k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape 
 // its position's key and value, loaded straight into registers a tile ahead, and
 // of the outputs of NR rows.  Each quad of lanes keeps maxima and sums of its own, so
 // nothing but the quarter scores crosses lanes until an item ends.
-constexpr int kF32Warps = kThreads / 32;
 template <int D, int NR>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(32 * kF32Warps, kCtasPerSm)
 k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
     constexpr int V = D / 16;                    // float4 of a lane's quarter
     __shared__ FinderRoom finder;
@@ -1175,7 +1174,7 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int quad = lane / 4, part4 = lane % 4;
     constexpr int KS = 8 * kF32Warps;
-    const Stretch span = find<KS>(s, blockIdx.x, &finder);
+    const Stretch span = find<KS, kF32Warps>(s, blockIdx.x, &finder);
     if (threadIdx.x == 0) reinterpret_cast<Cut *>(a.ws)[blockIdx.x].parts = 0;
     Item it = span.it;
     int tile = max(0, span.unit - kItemCost);
@@ -1228,7 +1227,7 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
         if (fresh) {
             fresh = false;
             __syncthreads();
-            for (int i = threadIdx.x; i < NR * D; i += kThreads) {
+            for (int i = threadIdx.x; i < NR * D; i += 32 * kF32Warps) {
                 const int r = min(it.rb * NR + i / D, rows - 1), t = r / s.G;
                 qsm[i / D][i % D] = static_cast<const float *>(a.q)[it.b * a.q_sb + t * a.q_st +
                                                                     (it.hk * s.G + r - t * s.G) * a.q_sh + i % D] *
@@ -1314,7 +1313,7 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             cut.rb = it.rb;
             reinterpret_cast<Cut *>(a.ws)[blockIdx.x] = cut;
         }
-        for (int i = threadIdx.x; i < NR * D; i += kThreads) {
+        for (int i = threadIdx.x; i < NR * D; i += 32 * kF32Warps) {
             const int rr = i / D, d = i % D, row = it.rb * NR + rr;
             if (row >= rows) break;
             float mt = -INFINITY, lt = 0.f, x = 0.f;
@@ -1399,7 +1398,7 @@ cudaError_t launch_mma(const PagedArgs &a, const Shape &s, cudaStream_t stream) 
 
 template <int D, int NR>
 cudaError_t launch_f32(const PagedArgs &a, const Shape &s, cudaStream_t stream) {
-    k_paged_f32<D, NR><<<s.ncta, kThreads, 0, stream>>>(a, s);
+    k_paged_f32<D, NR><<<s.ncta, 32 * kF32Warps, 0, stream>>>(a, s);
     const cudaError_t e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_join<float, D>(a, s, stream);
 }

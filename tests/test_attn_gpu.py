@@ -391,6 +391,20 @@ def test_attention_unseen_nan_stays_out(attn, pdt):
     assert not torch.isfinite(bad[:, 0, :, 5]).any()
 
 
+@pytest.mark.parametrize("pdt", [BF, F8], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_leftovers_of_other_calls_stay_out(attn, pdt, D):
+    """A call whose cache is NaN leaves NaN in shared memory; short sequences right after it, whose
+    tiles are mostly empty, see none of it (1 to 64 query rows a key/value head)."""
+    bad = attn_problem(64, 1, 8, 2, D, 16, [512] * 64, pdt, seed=30, nan=False)
+    for p in bad[1:3]:
+        (p.view(torch.uint8) if pdt == F8 else p)[:] = 0x7F if pdt == F8 else float("nan")
+    for T, Hq in ((1, 2), (1, 24), (1, 40), (1, 100), (3, 20)):
+        prob = attn_problem(6, T, Hq, 2, D, 16, [1, 5, 16, 17, 33, 49], pdt, seed=31 + Hq)
+        attn.paged_attention(*bad[:5], k_scale=bad[5], v_scale=bad[6])
+        check_attn(attn, prob, pdt)
+
+
 def test_attention_strided_and_token_major(attn):
     """Queries and outputs as views of wider tensors, pools laid out token by token."""
     q, kc, vc, table, lens, _, _ = attn_problem(2, 2, 8, 2, 64, 16, [77, 30], BF, seed=17)
