@@ -1157,23 +1157,25 @@ k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape 
 // ---- fp32 -------------------------------------------------------------------------------
 //
 // The same line, cuts and join, with products on the CUDA cores (tensor cores would
-// round the operands).  Six warps of a CTA take eight positions of a tile each, four
-// lanes a position: a lane holds a quarter of the places, in float4 steps of 16, of
-// its position's key and value, loaded straight into registers a tile ahead, and
-// of the outputs of NR rows.  Each quad of lanes keeps maxima and sums of its own, so
-// nothing but the quarter scores crosses lanes until an item ends.
+// round the operands).  D / 16 lanes take a position, six warps of a CTA 512 / D
+// positions of a tile each: a lane holds 16 places of its position's key and value,
+// loaded straight into registers a tile ahead, and of the outputs of NR rows.  The
+// lanes of a position keep maxima and sums of their own, so nothing but parts of
+// scores crosses lanes until an item ends.  (More places a lane leave room for fewer
+// rows, and rows of another block read the cache again.)
 template <int D, int NR>
 __global__ void __launch_bounds__(32 * kF32Warps, kCtasPerSm)
 k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
-    constexpr int V = D / 16;                    // float4 of a lane's quarter
+    constexpr int LP = D / 16, PW = 32 / LP;     // lanes of a position, positions of a warp
+    constexpr int V = 4;                         // float4 of a lane
+    constexpr int KS = PW * kF32Warps;
     __shared__ FinderRoom finder;
     __shared__ __align__(16) float qsm[NR][D];   // queries times scale log2(e)
     __shared__ __align__(16) float outs[kF32Warps][NR][D];
     __shared__ float top_of[kF32Warps][NR], sum_of[kF32Warps][NR];
     let_next_start();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int quad = lane / 4, part4 = lane % 4;
-    constexpr int KS = 8 * kF32Warps;
+    const int at_pos = lane / LP, at_place = 4 * (lane % LP);   // places at_place + 4 LP i ..
     const Stretch span = find<KS, kF32Warps>(s, blockIdx.x, &finder);
     if (threadIdx.x == 0) reinterpret_cast<Cut *>(a.ws)[blockIdx.x].parts = 0;
     Item it = span.it;
@@ -1188,7 +1190,7 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     int64_t ld_left = left;
     auto look_up = [&]() {
         page = -1;
-        const int pos = ld.first + ld_tile * KS + warp * 8 + quad;
+        const int pos = ld.first + ld_tile * KS + warp * PW + at_pos;
         const int p = pos / a.c.ps;
         at = pos - p * a.c.ps;
         if (ld_left > 0 && pos >= ld.lo && pos < ld.hi) page = a.table[ld.b * a.tb + p];
@@ -1202,7 +1204,7 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
         for (int i = 0; i < V; ++i) {
             nk[i] = nv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (nthere) {
-                const int64_t o = off + 16 * i + 4 * part4;
+                const int64_t o = off + 4 * LP * i + at_place;
                 nk[i] = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(a.c.k) + o));
                 nv[i] = __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(a.c.v) + o));
             }
@@ -1247,18 +1249,18 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
         const bool there = nthere;
 #pragma unroll
         for (int i = 0; i < V; ++i) k[i] = nk[i], v[i] = nv[i];
-        const int pos = it.first + tile * KS + warp * 8 + quad;
+        const int pos = it.first + tile * KS + warp * PW + at_pos;
         if (left > 1) load();
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             float sc = 0.f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float4 q = *reinterpret_cast<const float4 *>(&qsm[r][16 * i + 4 * part4]);
+                const float4 q = *reinterpret_cast<const float4 *>(&qsm[r][4 * LP * i + at_place]);
                 sc = fmaf(q.x, k[i].x, fmaf(q.y, k[i].y, fmaf(q.z, k[i].z, fmaf(q.w, k[i].w, sc))));
             }
-            sc += __shfl_xor_sync(~0u, sc, 1);
-            sc += __shfl_xor_sync(~0u, sc, 2);
+#pragma unroll
+            for (int w = 1; w < LP; w <<= 1) sc += __shfl_xor_sync(~0u, sc, w);
             if (there && pos <= e[r] && (a.window == 0 || pos > e[r] - int(a.window))) {
                 const float mt = fmaxf(m[r], sc), base = mt == -INFINITY ? 0.f : mt;
                 const float f = ex2(m[r] - base), p = ex2(sc - base);
@@ -1277,25 +1279,25 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
         const bool item_end = ++tile == it.ntiles;
         if (!item_end && left > 0) continue;
 
-        // join the quads of each warp, then the warps
+        // join the positions of each warp, then the warps
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             float mt = m[r];
 #pragma unroll
-            for (int w = 4; w < 32; w <<= 1) mt = fmaxf(mt, __shfl_xor_sync(~0u, mt, w));
+            for (int w = LP; w < 32; w <<= 1) mt = fmaxf(mt, __shfl_xor_sync(~0u, mt, w));
             const float f = m[r] == -INFINITY ? 0.f : ex2(m[r] - mt);
             l[r] *= f;
 #pragma unroll
-            for (int w = 4; w < 32; w <<= 1) l[r] += __shfl_xor_sync(~0u, l[r], w);
+            for (int w = LP; w < 32; w <<= 1) l[r] += __shfl_xor_sync(~0u, l[r], w);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 float x[4] = {o[r][i].x * f, o[r][i].y * f, o[r][i].z * f, o[r][i].w * f};
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int w = 4; w < 32; w <<= 1) x[j] += __shfl_xor_sync(~0u, x[j], w);
-                if (quad == 0)
-                    *reinterpret_cast<float4 *>(&outs[warp][r][16 * i + 4 * part4]) =
+                    for (int w = LP; w < 32; w <<= 1) x[j] += __shfl_xor_sync(~0u, x[j], w);
+                if (at_pos == 0)
+                    *reinterpret_cast<float4 *>(&outs[warp][r][4 * LP * i + at_place]) =
                         make_float4(x[0], x[1], x[2], x[3]);
             }
             if (lane == 0) top_of[warp][r] = mt, sum_of[warp][r] = l[r];
@@ -1416,8 +1418,8 @@ Shape make_shape(const PagedArgs &a) {
     s.window = int(a.window);
     s.G = a.Hq / a.c.Hkv;
     const int64_t rows = int64_t(a.T) * s.G;
-    if (a.c.dt == DT_F32)      // (the outputs of NR rows are NR D / 4 registers)
-        s.RB = rows == 1 ? 1 : rows == 2 || a.c.D == 128 ? 2 : 4;
+    if (a.c.dt == DT_F32)      // (the outputs of NR rows are 16 NR registers)
+        s.RB = rows == 1 ? 1 : rows == 2 ? 2 : 4;
     else
         s.RB = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     s.nrb = int((rows + s.RB - 1) / s.RB);
@@ -1442,7 +1444,7 @@ cudaError_t launch_d(const PagedArgs &a, cudaStream_t stream) {
         const Shape s = make_shape(a);
         if (s.RB == 1) return launch_f32<D, 1>(a, s, stream);
         if (s.RB == 2) return launch_f32<D, 2>(a, s, stream);
-        return launch_f32<D, D == 64 ? 4 : 2>(a, s, stream);
+        return launch_f32<D, 4>(a, s, stream);
     }
     return a.c.dt == DT_BF16 ? launch_rows<D, false>(a, stream) : launch_rows<D, true>(a, stream);
 }
