@@ -23,6 +23,7 @@
 #include "ssd_attn.h"
 #include "ssd_block_math.cuh"
 #include "ssd_debug.cuh"
+#include "ssd_f32x2.cuh"
 #include "ssd_tc.cuh"
 
 #include <cuda_bf16.h>
@@ -1163,6 +1164,11 @@ k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape 
 // lanes of a position keep maxima and sums of their own, so nothing but parts of
 // scores crosses lanes until an item ends.  (More places a lane leave room for fewer
 // rows, and rows of another block read the cache again.)
+//
+// The maximum in use follows the true one when that is ahead by kSlack (log2 units:
+// probabilities reach 2^kSlack until then), not at every new one, since moving it means
+// to go over the outputs.
+constexpr float kSlack = 8.f;
 template <int D, int NR>
 __global__ void __launch_bounds__(32 * kF32Warps, kCtasPerSm)
 k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
@@ -1220,7 +1226,7 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     look_up();
     load();
 
-    float4 o[NR][V];
+    F2 o[NR][V][2];
     float m[NR], l[NR];
     int e[NR];
     bool fresh = true, first_item = true;
@@ -1242,36 +1248,48 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                 m[r] = -INFINITY;
                 l[r] = 0.f;
 #pragma unroll
-                for (int i = 0; i < V; ++i) o[r][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int i = 0; i < V; ++i) o[r][i][0] = o[r][i][1] = f2(0.f, 0.f);
             }
         }
-        float4 k[V], v[V];
+        F2 k[V][2], v[V][2];
         const bool there = nthere;
 #pragma unroll
-        for (int i = 0; i < V; ++i) k[i] = nk[i], v[i] = nv[i];
+        for (int i = 0; i < V; ++i) {
+            k[i][0] = f2(nk[i].x, nk[i].y), k[i][1] = f2(nk[i].z, nk[i].w);
+            v[i][0] = f2(nv[i].x, nv[i].y), v[i][1] = f2(nv[i].z, nv[i].w);
+        }
         const int pos = it.first + tile * KS + warp * PW + at_pos;
         if (left > 1) load();
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-            float sc = 0.f;
+            F2 sum = f2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float4 q = *reinterpret_cast<const float4 *>(&qsm[r][4 * LP * i + at_place]);
-                sc = fmaf(q.x, k[i].x, fmaf(q.y, k[i].y, fmaf(q.z, k[i].z, fmaf(q.w, k[i].w, sc))));
+                sum = fma(f2(q.x, q.y), k[i][0], fma(f2(q.z, q.w), k[i][1], sum));
             }
+            float sc = parts(sum).x + parts(sum).y;
 #pragma unroll
             for (int w = 1; w < LP; w <<= 1) sc += __shfl_xor_sync(~0u, sc, w);
             if (there && pos <= e[r] && (a.window == 0 || pos > e[r] - int(a.window))) {
-                const float mt = fmaxf(m[r], sc), base = mt == -INFINITY ? 0.f : mt;
-                const float f = ex2(m[r] - base), p = ex2(sc - base);
-                m[r] = mt;
-                l[r] = fmaf(l[r], f, p);
+                if (sc - m[r] > kSlack || (m[r] == -INFINITY && sc != m[r])) {
+                    const float f = m[r] == -INFINITY ? 0.f : ex2(m[r] - sc);
+                    const F2 ff = f2(f, f);
+                    m[r] = sc;
+                    l[r] *= f;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        o[r][i][0] = mul(o[r][i][0], ff);
+                        o[r][i][1] = mul(o[r][i][1], ff);
+                    }
+                }
+                const float p = ex2(sc - (m[r] == -INFINITY ? 0.f : m[r]));
+                const F2 pp = f2(p, p);
+                l[r] += p;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    o[r][i].x = fmaf(o[r][i].x, f, p * v[i].x);
-                    o[r][i].y = fmaf(o[r][i].y, f, p * v[i].y);
-                    o[r][i].z = fmaf(o[r][i].z, f, p * v[i].z);
-                    o[r][i].w = fmaf(o[r][i].w, f, p * v[i].w);
+                    o[r][i][0] = fma(pp, v[i][0], o[r][i][0]);
+                    o[r][i][1] = fma(pp, v[i][1], o[r][i][1]);
                 }
             }
         }
@@ -1291,7 +1309,8 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             for (int w = LP; w < 32; w <<= 1) l[r] += __shfl_xor_sync(~0u, l[r], w);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                float x[4] = {o[r][i].x * f, o[r][i].y * f, o[r][i].z * f, o[r][i].w * f};
+                const float2 lo = parts(o[r][i][0]), hi = parts(o[r][i][1]);
+                float x[4] = {lo.x * f, lo.y * f, hi.x * f, hi.y * f};
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll

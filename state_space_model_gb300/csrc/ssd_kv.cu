@@ -2,6 +2,7 @@
 // pools) quantised write of new tokens, and the read back of cached ones.
 #include "ssd_attn.h"
 #include "ssd_debug.cuh"
+#include "ssd_f32x2.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -118,31 +119,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// Two fp32 numbers in one register pair and operations on both (one instruction
-// each; the norm and the rotation are a third of a row's instructions without).
-struct F2 {
-    uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 parts(F2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
 __device__ __forceinline__ void pairs(const float (&v)[8], F2 (&r)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) r[i] = f2(v[2 * i], v[2 * i + 1]);
