@@ -440,7 +440,7 @@ ssd_status ssd_mixer_prologue(const ssd_tensor *xBC, const ssd_tensor *conv_weig
  * do); slots [T], positions [T] SSD_I32 contiguous; R a multiple of 16, R <= D;
  * k_scale, v_scale with SSD_F8E4M3 pools only.  A token whose slot lies outside
  * [0, pages * ps) or whose position lies outside [0, S) is padding: nothing is
- * read or written for it, its q_out rows included.  Tokens must name distinct
+ * written for it, its q_out rows included.  Tokens must name distinct
  * slots (not checked: two on one slot race).  One launch. */
 ssd_status ssd_kv_append(const ssd_tensor *q, const ssd_tensor *k, const ssd_tensor *v,
                          const ssd_tensor *slots, const ssd_tensor *positions,
@@ -486,9 +486,9 @@ ssd_status ssd_paged_attention_workspace_size(int64_t batch, int64_t tokens, int
  * q, out [B, T, Hq, D] (f32 with f32 pools, else bf16); page_table [B, M]
  * SSD_I32, innermost stride 1; lens [B] SSD_I32; lse [B, T, Hq] f32
  * contiguous, may be NULL; workspace as above, 256-byte aligned, contents
- * ignored.  Two launches; scores, sums and partial results in f32, the
- * probabilities rounded to 16 bits for the product with bf16 values or 8-bit
- * codes. */
+ * ignored.  T (Hq / Hkv) at most 2^24.  Two launches; scores, sums and partial
+ * results in f32, the probabilities rounded to 16 bits for the product with bf16
+ * values or 8-bit codes. */
 ssd_status ssd_paged_attention(const ssd_tensor *q, const ssd_tensor *k_cache,
                                const ssd_tensor *v_cache, const ssd_tensor *k_scale,
                                const ssd_tensor *v_scale, const ssd_tensor *page_table,

@@ -15,6 +15,7 @@ constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
 // Positions leave room below 2^31 for a tile and for the new tokens, so that
 // the kernels count them in 32 bits.
 constexpr int64_t kMaxPos = kMaxInt - (1 << 17);
+constexpr int64_t kMaxRows = 1 << 24;   // of a sequence and key/value head
 
 int64_t extent(const ssd_tensor *t) {
     int64_t last = 0;
@@ -293,6 +294,9 @@ static ssd_status check_paged(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int
     if (B > 65535 || Hq > 65535 || T > 65535)
         return fail(SSD_ERR_UNSUPPORTED, "batch %lld, %lld tokens or %lld query heads above 65535",
                     (long long)B, (long long)T, (long long)Hq);
+    if (T * (Hq / Hkv) > kMaxRows)
+        return fail(SSD_ERR_UNSUPPORTED, "%lld tokens of %lld query heads a key/value head: more "
+                    "than 2^24 rows", (long long)T, (long long)(Hq / Hkv));
     return SSD_OK;
 }
 

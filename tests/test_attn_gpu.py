@@ -358,6 +358,15 @@ def test_attention_ragged_batch(attn):
     check_attn(attn, prob, BF)
 
 
+@pytest.mark.parametrize("pdt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("B", [32, 33, 600])
+def test_attention_many_sequences(attn, pdt, B):
+    """Either way of finding a CTA's stretch, and more sequences than a CTA has threads."""
+    lens = [(7 * i) % 41 for i in range(B)]
+    prob = attn_problem(B, 1, 2, 1, 64, 16, lens, pdt, seed=21 + B)
+    check_attn(attn, prob, pdt)
+
+
 @pytest.mark.parametrize("pdt", [BF, F8, F32], ids=["bf16", "fp8", "f32"])
 def test_attention_missing_pages(attn, pdt):
     q, kc, vc, table, lens, ks, vs = attn_problem(3, 2, 4, 2, 64, 8, [100, 100, 30], pdt, seed=14, nan=False)

@@ -247,7 +247,8 @@ def test_attention_refuses_overlap_and_workspace(lib):
 
 @pytest.mark.parametrize("bad,status", [((-1, 1, 8, 2, 64, BF16), INVALID), ((1, 1, 7, 2, 64, BF16), INVALID),
                                         ((1, 1, 8, 0, 64, BF16), INVALID), ((1, 1, 8, 2, 32, BF16), UNSUPPORTED),
-                                        ((1, 1, 8, 2, 64, I32), INVALID), ((70000, 1, 8, 2, 64, F8), UNSUPPORTED)])
+                                        ((1, 1, 8, 2, 64, I32), INVALID),
+                                        ((1, 60000, 60000, 1, 64, BF16), UNSUPPORTED), ((70000, 1, 8, 2, 64, F8), UNSUPPORTED)])
 def test_workspace_size_refusals(lib, bad, status):
     need = ctypes.c_size_t(7)
     assert lib.ssd_paged_attention_workspace_size(*bad, ctypes.byref(need)) == status
