@@ -119,6 +119,9 @@ __device__ __forceinline__ int64_t head_cost(const Shape &s, int len) {
     return n;
 }
 
+// The token of row r of a sequence and head.
+__device__ __forceinline__ int token_of(const Shape &s, int r) { return s.T == 1 ? 0 : r / s.G; }
+
 // The inclusive prefix of w over the lanes of a warp.
 __device__ __forceinline__ int64_t warp_scan(int64_t w) {
 #pragma unroll
@@ -649,7 +652,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     auto load_queries = [&]() {           // of the item at `it`, used once `fresh` is seen
 #pragma unroll
         for (int b = 0; b < NQ; ++b) {
-            const int r = min(it.rb * RB + wr * 8 * NQ + 8 * b + g, rows - 1), t = r / s.G;
+            const int r = min(it.rb * RB + wr * 8 * NQ + 8 * b + g, rows - 1), t = token_of(s, r);
             const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + it.b * a.q_sb +
                                      t * a.q_st + (it.hk * s.G + r - t * s.G) * a.q_sh;
 #pragma unroll
@@ -710,7 +713,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                 for (int p = 0; p < 2; ++p) {
                     const int row = it.rb * RB + wr * 8 * NQ + 8 * b + 2 * c + p;
                     qs[b][p] = F8 ? __shfl_sync(~0u, factor, (2 * c + p) * 4) : qscale;
-                    e[b][p] = it.len - a.T + min(row, rows - 1) / s.G;
+                    e[b][p] = it.len - a.T + token_of(s, min(row, rows - 1));
                     m[b][p] = -INFINITY;
                     l[b][p] = 0.f;
                 }
@@ -733,8 +736,10 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             if constexpr (KP > KW) mask |= room.masks(st)[x0 / KW + 1] << KW;
             // (votes, so that the compiler knows these for the same in all lanes)
             if (!__any_sync(~0u, mask != 0)) continue;
-            const bool partial = __any_sync(~0u, k0 + KP - 1 > it.emin ||
-                                                     (a.window > 0 && k0 <= it.emax - int(a.window)));
+            // partial: rows of the block see different positions of the pass
+            const bool partial = __any_sync(~0u, it.emin != it.emax &&
+                                                     (k0 + KP - 1 > it.emin ||
+                                                      (a.window > 0 && k0 <= it.emax - int(a.window))));
             const bool all = __all_sync(~0u, !partial && mask == 0xffffffffu >> (32 - KP));
             const uint32_t ksm = room.keys(st) + x0 * ROW, vsm = room.values(st) + x0 * ROW;
             const float *ksc = room.scales(st) + x0, *vsc = ksc + KS;
@@ -1059,7 +1064,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                 for (int i = 0; i < E; ++i) v[i] = fmaf(src[i], f, v[i]);
             }
             if (whole) {
-                const int row = done.rb * RB + rr, t = row / s.G, h = done.hk * s.G + row - t * s.G;
+                const int row = done.rb * RB + rr, t = token_of(s, row), h = done.hk * s.G + row - t * s.G;
                 const float inv = lt == 0.f ? 0.f : 1.f / lt;
                 uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + done.b * a.o_sb +
                                                              t * a.o_st + h * a.o_sh + E * lane);
@@ -1156,7 +1161,7 @@ k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape 
 #pragma unroll
             for (int j = 0; j < E; ++j) o[j] = fmaf(sm_o[warp + w][lane * E + j], f, o[j]);
         }
-        const int r = it.rb * s.RB + rr, t = r / s.G, h = it.hk * s.G + r - t * s.G;
+        const int r = it.rb * s.RB + rr, t = token_of(s, r), h = it.hk * s.G + r - t * s.G;
         T *dst = static_cast<T *>(a.out) + it.b * a.o_sb + t * a.o_st + h * a.o_sh + lane * E;
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
@@ -1247,7 +1252,7 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             fresh = false;
             __syncthreads();
             for (int i = threadIdx.x; i < NR * D; i += 32 * kF32Warps) {
-                const int r = min(it.rb * NR + i / D, rows - 1), t = r / s.G;
+                const int r = min(it.rb * NR + i / D, rows - 1), t = token_of(s, r);
                 qsm[i / D][i % D] = static_cast<const float *>(a.q)[it.b * a.q_sb + t * a.q_st +
                                                                     (it.hk * s.G + r - t * s.G) * a.q_sh + i % D] *
                                     (a.scale * kLog2e);
@@ -1255,7 +1260,7 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             __syncthreads();
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
-                e[r] = it.len - a.T + min(it.rb * NR + r, rows - 1) / s.G;
+                e[r] = it.len - a.T + token_of(s, min(it.rb * NR + r, rows - 1));
                 m[r] = -INFINITY;
                 l[r] = 0.f;
 #pragma unroll
@@ -1359,7 +1364,7 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                 x = fmaf(outs[w][rr][d], f, x);
             }
             if (whole) {
-                const int t = row / s.G, h = it.hk * s.G + row - t * s.G;
+                const int t = token_of(s, row), h = it.hk * s.G + row - t * s.G;
                 static_cast<float *>(a.out)[it.b * a.o_sb + t * a.o_st + h * a.o_sh + d] =
                     lt == 0.f ? 0.f : x / lt;
                 if (a.lse && d == 0)
