@@ -1049,33 +1049,44 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
         }
 #pragma unroll 1
         for (int rr = warp; rr < min(RB, rows - done.rb * RB); rr += kWarps) {
-            constexpr int E = D / 32;
+            constexpr int E = D / 32;                           // places of a lane: one vector
+            using Vec = std::conditional_t<E == 4, float4, float2>;
+            union Places {
+                Vec x;
+                float f[E];
+            };
             const int w0 = rr / (8 * NQ), r = rr % (8 * NQ);    // the row's warp of the first group
-            float mt = -INFINITY, lt = 0.f, v[E] = {};
+            float mt = -INFINITY, lt = 0.f;
+            Places v;
 #pragma unroll
             for (int k = 0; k < WK; ++k) mt = fmaxf(mt, top_of[k * WR + w0][r]);
             const float base = mt == -INFINITY ? 0.f : mt;
 #pragma unroll
+            for (int i = 0; i < E; ++i) v.f[i] = 0.f;
+#pragma unroll
             for (int k = 0; k < WK; ++k) {
                 const float f = ex2(top_of[k * WR + w0][r] - base);
-                const float *src = outs + spot(k * WR + w0, r, E * lane);
+                Places src;
+                src.x = *reinterpret_cast<const Vec *>(outs + spot(k * WR + w0, r, E * lane));
                 lt = fmaf(sum_of[k * WR + w0][r], f, lt);
 #pragma unroll
-                for (int i = 0; i < E; ++i) v[i] = fmaf(src[i], f, v[i]);
+                for (int i = 0; i < E; ++i) v.f[i] = fmaf(src.f[i], f, v.f[i]);
             }
             if (whole) {
                 const int row = done.rb * RB + rr, t = token_of(s, row), h = done.hk * s.G + row - t * s.G;
                 const float inv = lt == 0.f ? 0.f : 1.f / lt;
-                uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + done.b * a.o_sb +
-                                                             t * a.o_st + h * a.o_sh + E * lane);
-#pragma unroll
-                for (int i = 0; i < E; i += 2) dst[i / 2] = pack_bf16(v[i] * inv, v[i + 1] * inv);
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + done.b * a.o_sb + t * a.o_st +
+                                     h * a.o_sh + E * lane;
+                if constexpr (E == 4)
+                    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(v.f[0] * inv, v.f[1] * inv),
+                                                                 pack_bf16(v.f[2] * inv, v.f[3] * inv));
+                else
+                    *reinterpret_cast<uint32_t *>(dst) = pack_bf16(v.f[0] * inv, v.f[1] * inv);
                 if (a.lse && lane == 0)
                     a.lse[(int64_t(done.b) * a.T + t) * a.Hq + h] =
                         lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
             } else {
-#pragma unroll
-                for (int i = 0; i < E; ++i) part[rr * D + E * lane + i] = v[i];
+                *reinterpret_cast<Vec *>(part + rr * D + E * lane) = v.x;
                 if (lane == 0) {
                     part[RB * D + rr] = mt;
                     part[RB * (D + 1) + rr] = lt;
