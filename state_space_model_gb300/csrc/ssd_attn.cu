@@ -59,10 +59,11 @@ constexpr int kStages = 3;                // tiles that a CTA has room for
 // to a CTA, wherever the cuts fall: sequences of any lengths fill the GPU
 // evenly, and lengths are needed on the device only.  (Without the constant, a
 // CTA whose part is 40 one-tile items takes as long as 120 tiles of one item: 96
-// sequences of 17 to 16384 positions in 8 bits took 160 us where they took 94 with it.)  An item that a
-// cut falls into is finished by the join kernel from the parts that its CTAs
-// leave in the workspace.  An item without positions has one (masked) tile,
-// so that somebody writes its rows.
+// sequences of 17 to 16384 positions in 8 bits took 160 us where they took 94
+// with it.  2 is 2% better there now, and 14% worse for a few short ones.)  An
+// item that a cut falls into is finished by the join kernel from the parts that
+// its CTAs leave in the workspace.  An item without positions has one (masked)
+// tile, so that somebody writes its rows.
 constexpr int kItemCost = 3;
 
 // What both kernels derive the schedule from.
@@ -391,9 +392,9 @@ __device__ __forceinline__ void let_next_start() {
 // Measured (GB300, of the rate of a large copy, 6765 GB/s): 64 sequences of 4096, 64
 // query heads over 8 of 128, bf16: 170 us, 93%; the same in fp8 97 us, 85%; one
 // sequence of 131072, 32 over 8: 86 us, 92%; 96 of 17 to 16384 over fp8: 77 us, 82%.
-// Query rows cost nothing up to 16 a key/value head in bf16 (172 us) and little in fp8
-// (105 us); at 32 rows 187 and 170 us, at 64 in bf16 261 us, the products then take
-// longer than the reads.
+// Query rows cost little up to 32 a key/value head in bf16 (177 us) and 16 in fp8
+// (105 us); at 64 in bf16 (261 us) and 32 in fp8 (170 us) the products take longer than
+// the reads.
 template <int D_, bool F8_, int NQ_, int WR_>
 struct Cfg {
     static constexpr int D = D_, NQ = NQ_, WR = WR_, WK = kWarps / WR_;
@@ -526,7 +527,8 @@ __device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, c
     const int lane = threadIdx.x % 32;
     const int lrow = lane / LPR, lch = lane % LPR;
     const int shift = (a.c.ps & (a.c.ps - 1)) ? -1 : __ffs(a.c.ps) - 1;
-    // RUN positions of one page after another in memory
+    // RUN positions of one page after another in memory: no addresses from other lanes
+    // (96 ragged sequences over fp8 77.0 us, without this way 79.0; bf16 alike)
     const bool runs = a.c.ps % RUN == 0 && a.c.st == D;
     const char *const kpool = static_cast<const char *>(a.c.k);
     const char *const vpool = static_cast<const char *>(a.c.v);
@@ -1453,7 +1455,11 @@ cudaError_t launch_f32(const PagedArgs &a, const Shape &s, cudaStream_t stream) 
 
 // Rows of a block: 8 or 16 to a warp, then up to four warps along the rows (and
 // the rest of the four along the positions).  More rows than 64 are several row
-// blocks, each of which reads the cache.
+// blocks, each of which reads the cache.  64 sequences of 4096 over 8 key/value heads of
+// 128, microseconds for bf16 / fp8 with blocks of half the rows, this rule's, twice:
+//   8 rows              -  170 /  97  170 / 101
+//   16 rows     325 / 175  174 / 105  173 / 164
+//   32 rows     330 / 192  177 / 170  246 / 289
 Shape make_shape(const PagedArgs &a) {
     Shape s{};
     s.lens = a.lens;

@@ -324,8 +324,10 @@ cudaError_t append_u(const KvAppendArgs &a, cudaStream_t s) {
 
 // As few warps a token as take at most four passes each (fp32: two, for their
 // registers), the passes spread evenly over them, where that still fills the GPU with
-// warps: one load of the angles for a warp's passes, all their loads in flight.  Else a
-// warp a pass, so that a few tokens spread over as many SMs as they can.
+// warps: one load of the angles for a warp's passes, all their loads in flight (4999
+// tokens of 24 + 2 x 4 heads 12.3 us, with a warp a pass 14.4).  Else a warp a pass, so
+// that a few tokens spread over as many SMs as they can (the kernel alone, 64 tokens of
+// 64 + 2 x 8 heads in fp8 4.1 us, with four passes a warp 5.5; one token 3.7 and 5.8).
 template <typename T, int D, bool kCodes>
 cudaError_t append_t(const KvAppendArgs &a, cudaStream_t s) {
     constexpr int RPP = 512 / D, kMost = sizeof(T) == 4 ? 2 : 4;
@@ -366,7 +368,8 @@ __global__ void __launch_bounds__(256, 4) k_kv_read(const __grid_constant__ KvRe
     __shared__ int32_t near_cu[kNearLens];
     const int64_t i0 = int64_t(blockIdx.x) * TB;
     const int n = int(min(int64_t(TB), a.T - i0));
-    // the bisection's loads depend on one another: from shared memory where they fit
+    // the bisection's loads depend on one another: from shared memory where they fit (the
+    // kernel alone, 300 sequences of up to 20: 5.7 us, from global memory 6.5)
     const int32_t *cu = a.cu;
     if (a.B < kNearLens) {
         for (int i = threadIdx.x; i <= a.B; i += 256) near_cu[i] = a.cu[i];
@@ -452,7 +455,8 @@ __global__ void __launch_bounds__(256, 4) k_kv_read(const __grid_constant__ KvRe
 
 template <typename T, typename P, int D>
 cudaError_t read_t(const KvReadArgs &a, cudaStream_t s) {
-    // tokens of a CTA: 1024 vectors' worth, fewer where that leaves SMs without one
+    // tokens of a CTA: 1024 vectors' worth, fewer where that leaves SMs without one (the
+    // kernel alone, 300 tokens of 4 heads of 64: 4.4 us, with 32 a CTA 4.7)
     int TB = 1024 / (a.c.Hkv * (D / 8));
     TB = TB < 1 ? 1 : TB > kReadTokens ? kReadTokens : TB;
     while (TB > 1 && (a.T + TB - 1) / TB < 152) TB /= 2;
