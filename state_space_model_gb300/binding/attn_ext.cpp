@@ -3,10 +3,9 @@
 // the C ABI is called on the current torch stream.  Marshalling only; the
 // checks and the computation are the library's.
 //
-// It is compiled because these calls run once for each layer and token: the
-// same marshalling in Python (a descriptor packed with struct, the call made
-// through ctypes) takes 20 us of host time for the 12 tensors of a kv_append,
-// this takes 2, beside 5 in the library for the checks and the launch.
+// It is compiled because these calls run once for each layer and token: a kv_append
+// of 12 tensors takes 4.1 us of host time, checks and launch included; with the
+// descriptors packed in Python and the call made through ctypes it took 24.5.
 //
 // The library's functions come as addresses (bind), so the one that _native
 // loaded is the one that runs.
