@@ -144,7 +144,10 @@ __device__ __forceinline__ void unpair(const F2 (&r)[4], float (&v)[8]) {
 // row); in fp8 37 us, 75%, where the instructions begin to count.  Few key heads leave
 // lanes of their passes idle (4 of 64: half): 4999 tokens of 24 + 2 x 4 take 12.3 us.
 constexpr int kAppendWarps = 4;
-template <typename T, int D, bool kCodes, int U>
+// kWhole: every row is turned whole (R = D).  Elsewhere places that are not turned keep what
+// they hold, by a choice of results: a factor of 0 would bring infinities and NaN over from
+// their neighbours.  (The choice in every lane of the 8192 tokens: 36.2 us.)
+template <typename T, int D, bool kCodes, bool kWhole, int U>
 __global__ void __launch_bounds__(32 * kAppendWarps, 6)
 k_kv_append(const __grid_constant__ KvAppendArgs a, int warps) {
     constexpr int LR = D / 16, RPP = 32 / LR;
@@ -251,8 +254,9 @@ k_kv_append(const __grid_constant__ KvAppendArgs a, int warps) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const F2 p = x0[i], q = x1[i];
-                    x0[i] = fma(p, c[i], mul(mul(q, n[i]), minus));
-                    x1[i] = fma(q, c[i], mul(p, n[i]));
+                    const F2 u = fma(p, c[i], mul(mul(q, n[i]), minus)), v = fma(q, c[i], mul(p, n[i]));
+                    x0[i] = kWhole || turn ? u : p;
+                    x1[i] = kWhole || turn ? v : q;
                 }
                 unpair(x0, y0);
                 unpair(x1, y1);
@@ -318,7 +322,11 @@ cudaError_t append_u(const KvAppendArgs &a, cudaStream_t s) {
     const int warps = (passes + U - 1) / U;
     const int64_t blocks = (a.T * warps + kAppendWarps - 1) / kAppendWarps;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    k_kv_append<T, D, kCodes, U><<<unsigned(blocks), 32 * kAppendWarps, 0, s>>>(a, warps);
+    // (a warp a pass waits for its loads, whatever it computes)
+    if (U > 1 && a.R == D)
+        k_kv_append<T, D, kCodes, (U > 1), U><<<unsigned(blocks), 32 * kAppendWarps, 0, s>>>(a, warps);
+    else
+        k_kv_append<T, D, kCodes, false, U><<<unsigned(blocks), 32 * kAppendWarps, 0, s>>>(a, warps);
     return cudaGetLastError();
 }
 
