@@ -488,7 +488,9 @@ ssd_status ssd_paged_attention_workspace_size(int64_t batch, int64_t tokens, int
  * contiguous, may be NULL; workspace as above, 256-byte aligned, contents
  * ignored.  T (Hq / Hkv) at most 2^24.  Two launches; scores, sums and partial
  * results in f32, the probabilities rounded to 16 bits for the product with bf16
- * values or 8-bit codes. */
+ * values or 8-bit codes.  Scales may be any finite numbers; a row's probability times a
+ * value's scale is held in 11 bits down to 2^-22 of the row's largest such weight, and
+ * value scales below 2^-114 in fewer (ssd_kv_append writes none below 2^-105). */
 ssd_status ssd_paged_attention(const ssd_tensor *q, const ssd_tensor *k_cache,
                                const ssd_tensor *v_cache, const ssd_tensor *k_scale,
                                const ssd_tensor *v_scale, const ssd_tensor *page_table,

@@ -40,6 +40,12 @@ namespace ssd {
 namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
+// 8-bit values: the row's largest weight is 2^kLift in fp16 (so weights keep their 11 bits
+// down to 2^-22 of it), with log2 of a value's scale taken as [kLeastLog, kMostLog].  At the lower
+// end the fp32 sum of 2^27 probabilities of 2^(kLift - kLeastLog) is finite, and scales down to
+// 2^(kLeastLog - 22) still have weights of 11 bits; at the upper end a probability of 2^-kMostLog
+// is a normal number, and the largest finite scales stay below fp16's end.
+constexpr float kLift = 8.f, kLeastLog = -92.f, kMostLog = 119.f;
 constexpr int kWarps = 4;                 // of a CTA that compute
 constexpr int kCopyWarps = 4;             // and that copy
 constexpr int kThreads = 32 * (kWarps + kCopyWarps);
@@ -493,6 +499,20 @@ __device__ __forceinline__ void value_tiles(uint32_t vsm, int j, Use &&use) {
     }
 }
 
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// ln(2^m l).  The sum's exponent is added to m before anything is rounded: with codes they
+// may be far apart and nearly cancel.
+__device__ __forceinline__ float log_sum(float m, float l) {
+    if (l == 0.f) return -INFINITY;
+    const uint32_t u = __float_as_uint(l), e = u >> 23;
+    if (e == 0 || e >= 255) return (m + log2f(l)) * kLn2;     // subnormal, infinite, NaN (or negative)
+    return ((m + (float(e) - 127.f)) + log2f(__uint_as_float((u & 0x7fffffu) | 0x3f800000u))) * kLn2;
+}
+
 // Infinities and NaN of a pair of 16-bit values, replaced by 0.
 template <bool F16>
 __device__ __forceinline__ uint32_t finite2(uint32_t v) {
@@ -644,12 +664,15 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     // over this thread's positions, and the output.  Scores stay as the product leaves
     // them (times the key's scale): a row's factor qs >= 0 (scale log2(e), the sign of
     // the scale being in the queries) enters with the exponential, p = 2^(qs s - qs m).
+    // Codes: a weight p vs (vs: the value's scale) goes to fp16, so the row's reference m is the
+    // largest qs s + log2 vs (less kLift) over the positions that the row sees: the largest weight is
+    // 2^kLift, whatever the scales are, and positions that it does not see have no part in it.
+    // p, summed in fp32, may then be as large as 2^(kLift - kLeastLog) and as small as 2^-kMostLog.
     uint32_t qf[NQ][D / 16][2];
     float o[MT][NQ][4], m[NQ][2], l[NQ][2], qs[NQ][2];
     int e[NQ][2];                         // the rows' own places
     const float qscale = fabsf(a.scale) * kLog2e;
     const uint32_t qsign = a.scale < 0.f ? 0x80008000u : 0u;
-    float xs = 0.f, xmax = 0.f;           // codes: the values' common factor (a power of two)
     const int rows = a.T * s.G;
     auto load_queries = [&]() {           // of the item at `it`, used once `fresh` is seen
 #pragma unroll
@@ -724,7 +747,6 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             for (int j = 0; j < MT; ++j)
 #pragma unroll
                 for (int b = 0; b < NQ; ++b) o[j][b][0] = o[j][b][1] = o[j][b][2] = o[j][b][3] = 0.f;
-            if constexpr (F8) xs = xmax = 0.f;
         }
         if (!wait_for(&full[st], (n / kStages) & 1)) {
             if (lane == 0) atomicOr(a.err, kErrTimeout);
@@ -816,6 +838,16 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                             if (!see) sc[j][b][i] = -INFINITY;
                         }
             }
+            float vs[KT][2], lv[KT][2];      // codes: value scales, and log2 of them
+            if constexpr (F8) {
+#pragma unroll
+                for (int j = 0; j < KT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        vs[j][i] = vsc[pos_of(j, i)];
+                        lv[j][i] = fminf(fmaxf(lg2(fabsf(vs[j][i])), kLeastLog), kMostLog) - kLift;
+                    }
+            }
             float mn[NQ][2];
             bool moved = false;
 #pragma unroll
@@ -824,44 +856,35 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                 for (int p = 0; p < 2; ++p) {
                     float v = m[b][p];
 #pragma unroll
-                    for (int j = 0; j < KT; ++j) v = fmaxf(v, fmaxf(sc[j][b][p], sc[j][b][2 + p]));
+                    for (int j = 0; j < KT; ++j) {
+                        if constexpr (F8)
+                            v = fmaxf(v, fmaxf(fmaf(sc[j][b][p], qs[b][p], lv[j][0]),
+                                               fmaf(sc[j][b][2 + p], qs[b][p], lv[j][1])));
+                        else
+                            v = fmaxf(v, fmaxf(sc[j][b][p], sc[j][b][2 + p]));
+                    }
                     v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
                     v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
                     mn[b][p] = v;
                     moved = moved || v != m[b][p];
                 }
-            float grow = 1.f;
-            if constexpr (F8) {
-                // the values' factor must cover this tile's largest finite scale
-                const float vs = (mask >> lane) & 1 ? vsc[lane] : 0.f;
-                const bool more = vs > xmax && vs < INFINITY;
-                if (__any_sync(~0u, more)) {
-                    float top = more ? vs : 0.f;
-#pragma unroll
-                    for (int q = 16; q; q >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, q));
-                    // xmax: a power of two of at least top, at most 2^126
-                    uint32_t ex = (__float_as_uint(top) + 0x7fffffu) & 0x7f800000u;
-                    ex = min(max(ex, 0x01000000u), 0x7e800000u);
-                    const float was = xmax;
-                    xmax = __uint_as_float(ex);
-                    // probability times scale goes to fp16 as p vs 2^14 / xmax <= 2^14
-                    const float down = __uint_as_float(0x7f000000u - ex);
-                    xs = down * 16384.f;
-                    grow = was * down;    // 0 on the first tile, where o is 0
-                    moved = true;
-                }
-            }
             if (__any_sync(~0u, moved)) {
 #pragma unroll
                 for (int b = 0; b < NQ; ++b) {
                     float f[2];
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
-                        f[p] = m[b][p] == -INFINITY ? 0.f : ex2((m[b][p] - mn[b][p]) * qs[b][p]);
+                        // codes: by halves, as the sum may be large where the factor is below 2^-126
+                        f[p] = m[b][p] == -INFINITY
+                                   ? 0.f
+                                   : ex2((m[b][p] - mn[b][p]) * (F8 ? 0.5f : qs[b][p]));
                         m[b][p] = mn[b][p];
                         l[b][p] *= f[p];
-                        f[p] *= grow;
+                        if constexpr (F8) {
+                            l[b][p] *= f[p];
+                            f[p] *= f[p];
+                        }
                     }
 #pragma unroll
                     for (int j = 0; j < MT; ++j)
@@ -869,12 +892,14 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                         for (int i = 0; i < 4; ++i) o[j][b][i] *= f[i & 1];
                 }
             }
-            // probabilities (unnormalised, at most 1), summed in fp32 and rounded to
-            // 16 bits as the right operand of the second product
+            // probabilities (unnormalised; at most 1, with codes after their values' scales at most
+            // 2^kLift), summed in fp32 and rounded to 16 bits as the right operand of the second product
 #pragma unroll
             for (int b = 0; b < NQ; ++b) {
-                const float base[2] = {m[b][0] == -INFINITY ? 0.f : m[b][0] * qs[b][0],
-                                       m[b][1] == -INFINITY ? 0.f : m[b][1] * qs[b][1]};
+                float base[2];
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    base[p] = m[b][p] == -INFINITY ? 0.f : F8 ? m[b][p] : m[b][p] * qs[b][p];
 #pragma unroll
                 for (int j = 0; j < KT; ++j)
 #pragma unroll
@@ -902,14 +927,12 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
 #pragma unroll
                 for (int j = 0; j < KT; ++j)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float f = vsc[pos_of(j, i)] * xs;
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int b = 0; b < NQ; ++b) {
-                            sc[j][b][2 * i] *= f;
-                            sc[j][b][2 * i + 1] *= f;
+                            sc[j][b][2 * i] *= vs[j][i];
+                            sc[j][b][2 * i + 1] *= vs[j][i];
                         }
-                    }
                 if (!all) blank();    // (whatever its scale is)
             }
             uint32_t pf[KT][NQ][2];   // transposed: query g, positions 2 c and 2 c + 1
@@ -1006,7 +1029,6 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             if (left > 0) load_queries();
         }
         warps_sync();
-        const float back = F8 ? xmax * (1.f / 16384.f) : 1.f;
         // place d of row r: turned by 4 r places, so that neither side meets in one bank
         float *const outs = reinterpret_cast<float *>(smem + st * C::STAGE);
         auto spot = [&](int w, int r, int d) { return (w * 8 * NQ + r) * D + ((d + 4 * r) & (D - 1)); };
@@ -1018,15 +1040,14 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
 #pragma unroll
                 for (int q = 4; q < 32; q <<= 1) l[b][p] += __shfl_xor_sync(~0u, l[b][p], q);
                 if (g == 0) {
-                    top_of[warp][r] = m[b][p] == -INFINITY ? m[b][p] : m[b][p] * qs[b][p];
+                    top_of[warp][r] = F8 || m[b][p] == -INFINITY ? m[b][p] : m[b][p] * qs[b][p];
                     sum_of[warp][r] = l[b][p];
                 }
                 if constexpr (F8) {      // places (D / 8) g + 2 j + i
 #pragma unroll
                     for (int j = 0; j < MT; j += 2)
                         *reinterpret_cast<float4 *>(outs + spot(warp, r, (D / 8) * g + 2 * j)) =
-                            make_float4(o[j][b][p] * back, o[j][b][2 + p] * back, o[j + 1][b][p] * back,
-                                        o[j + 1][b][2 + p] * back);
+                            make_float4(o[j][b][p], o[j][b][2 + p], o[j + 1][b][p], o[j + 1][b][2 + p]);
                 } else {                 // places 16 j + 8 i + g
 #pragma unroll
                     for (int j = 0; j < MT; ++j)
@@ -1067,12 +1088,12 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             for (int i = 0; i < E; ++i) v.f[i] = 0.f;
 #pragma unroll
             for (int k = 0; k < WK; ++k) {
-                const float f = ex2(top_of[k * WR + w0][r] - base);
+                const float f = ex2(0.5f * (top_of[k * WR + w0][r] - base));   // by halves, as above
                 Places src;
                 src.x = *reinterpret_cast<const Vec *>(outs + spot(k * WR + w0, r, E * lane));
-                lt = fmaf(sum_of[k * WR + w0][r], f, lt);
+                lt = fmaf(sum_of[k * WR + w0][r] * f, f, lt);
 #pragma unroll
-                for (int i = 0; i < E; ++i) v.f[i] = fmaf(src.f[i], f, v.f[i]);
+                for (int i = 0; i < E; ++i) v.f[i] = fmaf(src.f[i], f * f, v.f[i]);
             }
             if (whole) {
                 const int row = done.rb * RB + rr, t = token_of(s, row), h = done.hk * s.G + row - t * s.G;
@@ -1086,7 +1107,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                     *reinterpret_cast<uint32_t *>(dst) = pack_bf16(v.f[0] * inv, v.f[1] * inv);
                 if (a.lse && lane == 0)
                     a.lse[(int64_t(done.b) * a.T + t) * a.Hq + h] =
-                        lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
+                        log_sum(mt, lt);
             } else {
                 *reinterpret_cast<Vec *>(part + rr * D + E * lane) = v.x;
                 if (lane == 0) {
@@ -1143,17 +1164,18 @@ k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape 
             float mt = m;
 #pragma unroll
             for (int u = 0; u < kJoinAhead; ++u) mt = fmaxf(mt, pm[u]);
-            const float base = mt == -INFINITY ? 0.f : mt, old = ex2(m - base);
+            // factors by halves: a sum may be large where its factor is below 2^-126
+            const float base = mt == -INFINITY ? 0.f : mt, old = ex2(0.5f * (m - base));
             m = mt;
-            l *= old;
+            l = l * old * old;
 #pragma unroll
-            for (int j = 0; j < E; ++j) o[j] *= old;
+            for (int j = 0; j < E; ++j) o[j] *= old * old;
 #pragma unroll
             for (int u = 0; u < kJoinAhead; ++u) {
-                const float f = ex2(pm[u] - base);
-                l = fmaf(pl[u], f, l);
+                const float f = ex2(0.5f * (pm[u] - base));
+                l = fmaf(pl[u] * f, f, l);
 #pragma unroll
-                for (int j = 0; j < E; ++j) o[j] = fmaf(v[u][j], f, o[j]);
+                for (int j = 0; j < E; ++j) o[j] = fmaf(v[u][j], f * f, o[j]);
             }
         }
         __syncthreads();          // the rows before have been read
@@ -1169,10 +1191,10 @@ k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape 
 #pragma unroll
         for (int j = 0; j < E; ++j) o[j] = 0.f;
         for (int w = 0; w < per; ++w) {
-            const float f = ex2(sm_m[warp + w] - base);
-            l = fmaf(sm_l[warp + w], f, l);
+            const float f = ex2(0.5f * (sm_m[warp + w] - base));
+            l = fmaf(sm_l[warp + w] * f, f, l);
 #pragma unroll
-            for (int j = 0; j < E; ++j) o[j] = fmaf(sm_o[warp + w][lane * E + j], f, o[j]);
+            for (int j = 0; j < E; ++j) o[j] = fmaf(sm_o[warp + w][lane * E + j], f * f, o[j]);
         }
         const int r = it.rb * s.RB + rr, t = token_of(s, r), h = it.hk * s.G + r - t * s.G;
         T *dst = static_cast<T *>(a.out) + it.b * a.o_sb + t * a.o_st + h * a.o_sh + lane * E;
@@ -1180,7 +1202,7 @@ k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape 
 #pragma unroll
         for (int j = 0; j < E; ++j) dst[j] = T(o[j] * inv);
         if (a.lse && lane == 0)
-            a.lse[(int64_t(it.b) * a.T + t) * a.Hq + h] = l == 0.f ? -INFINITY : (mt + log2f(l)) * kLn2;
+            a.lse[(int64_t(it.b) * a.T + t) * a.Hq + h] = log_sum(mt, l);
     }
 }
 
@@ -1382,7 +1404,7 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                     lt == 0.f ? 0.f : x / lt;
                 if (a.lse && d == 0)
                     a.lse[(int64_t(it.b) * a.T + t) * a.Hq + h] =
-                        lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
+                        log_sum(mt, lt);
             } else {
                 part[rr * D + d] = x;
                 if (d == 0) {

@@ -58,3 +58,91 @@ def test_append_copies_unrotated_places(attn, T, dt, D, R, interleaved):
     nan = torch.isnan(held)
     assert torch.equal(torch.isnan(kept), nan)
     assert torch.equal(bits(kept)[~nan], bits(held)[~nan])
+
+
+# ---- value scales of any size ------------------------------------------------------
+
+
+def check_rows(attn, prob, window=0):
+    """Every row of an 8-bit problem against float64, with bounds from what the row itself sees.
+
+    With weights w_j = p_j vs_j (p the softmax over the row's positions) and vbar = sum p_j |v_j|: a
+    probability is off by 2 ds + (n + 8) 2^-22 and its weight by one rounding to fp16, 2^-11, where that is
+    not below fp16's normal numbers, else by 2^-33 of the row's largest weight, times a code of up to
+    448; scales under 2^-92 count as 2^-92 there, which leaves 2^-125 times 448 a position."""
+    q, kc, vc, table, lens, ks, vs = prob
+    out, lse = attn.paged_attention(q, kc, vc, table, lens, k_scale=ks, v_scale=vs, window=window, return_lse=True)
+    Q, K, V, S, KS = np64(q), np64(kc), np64(vc), np64(vs), np64(ks)
+    o, l, tab = np64(out), np64(lse), table.cpu().numpy()
+    B, T, Hq, D = Q.shape
+    ps, G = K.shape[2], Hq // K.shape[1]
+    for b in range(B):
+        n = int(lens[b])
+        for t in range(T):
+            at = np.arange(max(0, n - T + t + 1 - window) if window else 0, n - T + t + 1)
+            page, slot = tab[b, at // ps], at % ps
+            for h in range(Hq):
+                hk = h // G
+                key = K[page, hk, slot] * KS[page, hk, slot][:, None]
+                code, scale = V[page, hk, slot], S[page, hk, slot]
+                s = key @ Q[b, t, h] * D ** -0.5
+                p = np.exp(s - s.max())
+                total = p.sum()
+                ref = (p * scale) @ code / total
+                ds = (D + 8) * 2.0 ** -22 * (np.abs(key) @ np.abs(Q[b, t, h])).max() * D ** -0.5
+                rel = 2 * ds + (len(at) + 8) * 2.0 ** -22 + 2.0 ** -11
+                bound = (p * scale) @ np.abs(code) / total * rel
+                bound += len(at) * 448 * (2.0 ** -33 * (p * scale).max() / total + 2.0 ** -125)
+                err = np.abs(o[b, t, h] - ref)
+                assert (err <= bound * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref)).all(), (b, t, h, err.max())
+                want = s.max() + math.log(total)
+                assert abs(l[b, t, h] - want) <= ds + len(at) * 2.0 ** -22 + 2.0 ** -21 * (1 + abs(want))
+    return out, lse
+
+
+def scale_problem(D, T, Hq, lens, seed):
+    return attn_problem(len(lens), T, Hq, 2, D, 16, lens, F8, seed=seed, nan=False)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sizes", [[1e-36], [2.0 ** -126], [0.0], [2.0 ** -105], [0.0, 2.0 ** -105, 0.01],
+                                   [1e-36, 2.0 ** -100, 1e-20, 1e-5, 1.0], [1e-30, 1e12], [2.0 ** -105, 2.0 ** 60]],
+                         ids=str)
+def test_attention_value_scales_of_any_size(attn, sizes, D):
+    """Scales all tiny, all zero, or tiny, zero and ordinary ones mixed, one token and drafts."""
+    for T, Hq in ((1, 8), (3, 24)):
+        prob = scale_problem(D, T, Hq, [300, 5, 40], seed=40 + T)
+        g = torch.Generator().manual_seed(7)
+        pick = torch.randint(0, len(sizes), prob[6].shape, generator=g)
+        prob[6][:] = torch.tensor(sizes)[pick].cuda() * (0.5 + torch.rand(pick.shape, generator=g).cuda())
+        check_rows(attn, prob)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 35, 2.0 ** 45, 2.0 ** 100])
+def test_attention_unseen_large_scale_stays_out(attn, size, D):
+    """A later draft token's large finite scale does not reach the rows before it, nor what a window has
+    left behind the rows after it."""
+    T, n = 4, 50
+    prob = scale_problem(D, T, 8, [n], seed=50)
+    kw = dict(k_scale=prob[5], v_scale=prob[6], return_lse=True)
+    good, lg = attn.paged_attention(*prob[:5], **kw)
+    prob[6][int(prob[3][0, (n - 1) // 16]), :, (n - 1) % 16] *= size
+    bad, lb = check_rows(attn, prob)
+    assert (np.abs(np64(bad[:, :3]) - np64(good[:, :3])) <= 2.0 ** -7 * np.abs(np64(good[:, :3])) + 1e-4).all()
+    assert torch.allclose(lb, lg, rtol=0, atol=1e-5)
+    prob = scale_problem(D, T, 8, [n], seed=51)
+    prob[6][int(prob[3][0, 0]), :, 10] *= size       # inside the first row's window (n - 4 - 36 = 10) only
+    check_rows(attn, prob, window=37)
+
+
+def test_attention_improbable_large_value(attn):
+    """A row's own position with a large scale and no weight in the softmax leaves the others their
+    precision: score -90, scale 2^70 times theirs."""
+    q, kc, vc, table, lens, ks, vs = scale_problem(64, 1, 2, [200], seed=52)
+    q[:] = 1.0
+    page = int(table[0, 3])
+    kc.view(torch.uint8)[page, :, 5] = torch.full((2, 64), -1.0, device="cuda").to(F8).view(torch.uint8)
+    ks[page, :, 5] = 90 / 8.0                        # 64 places of -90 / 8, times 1 / 8
+    vs[page, :, 5] *= 2.0 ** 70
+    check_rows(attn, (q, kc, vc, table, lens, ks, vs))
