@@ -40,12 +40,13 @@ namespace ssd {
 namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
-// 8-bit values: the row's largest weight is 2^kLift in fp16 (so weights keep their 11 bits
-// down to 2^-22 of it), with log2 of a value's scale taken as [kLeastLog, kMostLog].  At the lower
-// end the fp32 sum of 2^27 probabilities of 2^(kLift - kLeastLog) is finite, and scales down to
-// 2^(kLeastLog - 22) still have weights of 11 bits; at the upper end a probability of 2^-kMostLog
-// is a normal number, and the largest finite scales stay below fp16's end.
-constexpr float kLift = 8.f, kLeastLog = -92.f, kMostLog = 119.f;
+// 8-bit values: a row's largest weight is 2^kLift to 2^(kLift + kAhead) in fp16 (so weights
+// keep their 11 bits down to 2^-22 of it), with log2 of a value's scale taken as [kLeastLog,
+// kMostLog].  At the lower end the fp32 sum of 2^25 probabilities of 2^(kLift + kAhead - kLeastLog) is
+// finite, and scales down to 2^(kLeastLog - 22) still have weights of 11 bits; at the upper end
+// a probability of 2^-kMostLog is a normal number, and the largest finite scales stay below
+// fp16's end.
+constexpr float kLift = 8.f, kAhead = 2.f, kLeastLog = -92.f, kMostLog = 119.f;
 constexpr int kWarps = 4;                 // of a CTA that compute
 constexpr int kCopyWarps = 4;             // and that copy
 constexpr int kThreads = 32 * (kWarps + kCopyWarps);
@@ -663,13 +664,16 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     // 8 n + 2 c + p, which this thread's columns hold, the running maximum, the sum
     // over this thread's positions, and the output.  Scores stay as the product leaves
     // them (times the key's scale): a row's factor qs >= 0 (scale log2(e), the sign of
-    // the scale being in the queries) enters with the exponential, p = 2^(qs s - qs m).
-    // Codes: a weight p vs (vs: the value's scale) goes to fp16, so the row's reference m is the
-    // largest qs s + log2 vs (less kLift) over the positions that the row sees: the largest weight is
-    // 2^kLift, whatever the scales are, and positions that it does not see have no part in it.
-    // p, summed in fp32, may then be as large as 2^(kLift - kLeastLog) and as small as 2^-kMostLog.
+    // the scale being in the queries) enters with the exponential, p = 2^(qs (s - m)).
+    // (The difference first: qs m rounded would be off by any power of two for large scores.)
+    // Codes: a weight p vs (vs: the value's scale) goes to fp16, so p = 2^(qs (s - m) - k), with k
+    // following the largest qs (s - m) + log2 vs (less kLift) over the positions that the row sees:
+    // the largest weight is about 2^kLift, whatever the scales are, and positions that it does
+    // not see have no part in it.  k follows when that is ahead by kAhead, since
+    // moving it means to go over the outputs; where m moves alone, k takes the difference.
+    // p, summed in fp32, may be as large as 2^(kLift + kAhead - kLeastLog) and as small as 2^-kMostLog.
     uint32_t qf[NQ][D / 16][2];
-    float o[MT][NQ][4], m[NQ][2], l[NQ][2], qs[NQ][2];
+    float o[MT][NQ][4], m[NQ][2], l[NQ][2], qs[NQ][2], k[NQ][2];
     int e[NQ][2];                         // the rows' own places
     const float qscale = fabsf(a.scale) * kLog2e;
     const uint32_t qsign = a.scale < 0.f ? 0x80008000u : 0u;
@@ -739,7 +743,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                     const int row = it.rb * RB + wr * 8 * NQ + 8 * b + 2 * c + p;
                     qs[b][p] = F8 ? __shfl_sync(~0u, factor, (2 * c + p) * 4) : qscale;
                     e[b][p] = it.len - a.T + token_of(s, min(row, rows - 1));
-                    m[b][p] = -INFINITY;
+                    m[b][p] = k[b][p] = -INFINITY;
                     l[b][p] = 0.f;
                 }
             }
@@ -838,16 +842,6 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                             if (!see) sc[j][b][i] = -INFINITY;
                         }
             }
-            float vs[KT][2], lv[KT][2];      // codes: value scales, and log2 of them
-            if constexpr (F8) {
-#pragma unroll
-                for (int j = 0; j < KT; ++j)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        vs[j][i] = vsc[pos_of(j, i)];
-                        lv[j][i] = fminf(fmaxf(lg2(fabsf(vs[j][i])), kLeastLog), kMostLog) - kLift;
-                    }
-            }
             float mn[NQ][2];
             bool moved = false;
 #pragma unroll
@@ -856,55 +850,108 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                 for (int p = 0; p < 2; ++p) {
                     float v = m[b][p];
 #pragma unroll
-                    for (int j = 0; j < KT; ++j) {
-                        if constexpr (F8)
-                            v = fmaxf(v, fmaxf(fmaf(sc[j][b][p], qs[b][p], lv[j][0]),
-                                               fmaf(sc[j][b][2 + p], qs[b][p], lv[j][1])));
-                        else
-                            v = fmaxf(v, fmaxf(sc[j][b][p], sc[j][b][2 + p]));
-                    }
+                    for (int j = 0; j < KT; ++j) v = fmaxf(v, fmaxf(sc[j][b][p], sc[j][b][2 + p]));
                     v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
                     v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
                     mn[b][p] = v;
                     moved = moved || v != m[b][p];
                 }
-            if (__any_sync(~0u, moved)) {
-#pragma unroll
-                for (int b = 0; b < NQ; ++b) {
-                    float f[2];
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        // codes: by halves, as the sum may be large where the factor is below 2^-126
-                        f[p] = m[b][p] == -INFINITY
-                                   ? 0.f
-                                   : ex2((m[b][p] - mn[b][p]) * (F8 ? 0.5f : qs[b][p]));
-                        m[b][p] = mn[b][p];
-                        l[b][p] *= f[p];
-                        if constexpr (F8) {
-                            l[b][p] *= f[p];
-                            f[p] *= f[p];
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < MT; ++j)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[j][b][i] *= f[i & 1];
-                }
-            }
-            // probabilities (unnormalised; at most 1, with codes after their values' scales at most
-            // 2^kLift), summed in fp32 and rounded to 16 bits as the right operand of the second product
-#pragma unroll
-            for (int b = 0; b < NQ; ++b) {
-                float base[2];
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    base[p] = m[b][p] == -INFINITY ? 0.f : F8 ? m[b][p] : m[b][p] * qs[b][p];
+            float vs[KT][2], f[NQ][2];       // codes: value scales; what the outputs are multiplied by
+            if constexpr (F8) {
+                float lv[KT][2], kn[NQ][2];
 #pragma unroll
                 for (int j = 0; j < KT; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        sc[j][b][i] = ex2(fmaf(sc[j][b][i], qs[b][i & 1], -base[i & 1]));
+                    for (int i = 0; i < 2; ++i) {
+                        vs[j][i] = vsc[pos_of(j, i)];
+                        lv[j][i] = fminf(fmaxf(lg2(fabsf(vs[j][i])), kLeastLog), kMostLog) - kLift;
+                    }
+                if (__any_sync(~0u, moved)) {
+#pragma unroll
+                    for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            if (m[b][p] != -INFINITY) k[b][p] -= (mn[b][p] - m[b][p]) * qs[b][p];
+                            m[b][p] = mn[b][p];
+                        }
+                }
+                moved = false;
+#pragma unroll
+                for (int b = 0; b < NQ; ++b) {
+                    const F2 q = f2(qs[b][0], qs[b][1]);
+                    const F2 z = f2(m[b][0] == -INFINITY ? 0.f : -m[b][0], m[b][1] == -INFINITY ? 0.f : -m[b][1]);
+                    kn[b][0] = k[b][0];
+                    kn[b][1] = k[b][1];
+#pragma unroll
+                    for (int j = 0; j < KT; ++j)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const F2 d = mul(add(f2(sc[j][b][2 * i], sc[j][b][2 * i + 1]), z), q);
+                            const float2 x = parts(d), t = parts(add(d, f2(lv[j][i], lv[j][i])));
+                            sc[j][b][2 * i] = x.x;
+                            sc[j][b][2 * i + 1] = x.y;
+                            kn[b][0] = fmaxf(kn[b][0], t.x);
+                            kn[b][1] = fmaxf(kn[b][1], t.y);
+                        }
+                    moved = moved || kn[b][0] > k[b][0] + kAhead || kn[b][1] > k[b][1] + kAhead;
+                }
+                moved = __any_sync(~0u, moved);
+                if (moved) {
+#pragma unroll
+                    for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            float v = kn[b][p];
+                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
+                            // by halves: the sum may be large where the factor is below 2^-126
+                            f[b][p] = k[b][p] == -INFINITY ? 0.f : ex2(0.5f * (k[b][p] - v));
+                            k[b][p] = v;
+                            l[b][p] = l[b][p] * f[b][p] * f[b][p];
+                            f[b][p] *= f[b][p];
+                        }
+                }
+            } else {
+                moved = __any_sync(~0u, moved);
+                if (moved) {
+#pragma unroll
+                    for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            f[b][p] = m[b][p] == -INFINITY ? 0.f : ex2((m[b][p] - mn[b][p]) * qs[b][p]);
+                            m[b][p] = mn[b][p];
+                            l[b][p] *= f[b][p];
+                        }
+                }
+            }
+            if (moved) {
+#pragma unroll
+                for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                    for (int j = 0; j < MT; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[j][b][i] *= f[b][i & 1];
+            }
+            // probabilities (unnormalised; at most 1, with codes after their values' scales at most
+            // 2^(kLift + kAhead)), summed in fp32 and rounded to 16 bits as the right operand of the
+            // second product
+#pragma unroll
+            for (int b = 0; b < NQ; ++b) {
+                const float *const from = F8 ? k[b] : m[b];
+                const F2 q = f2(qs[b][0], qs[b][1]);
+                const F2 z = f2(from[0] == -INFINITY ? 0.f : -from[0], from[1] == -INFINITY ? 0.f : -from[1]);
+#pragma unroll
+                for (int j = 0; j < KT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        F2 d = add(f2(sc[j][b][2 * i], sc[j][b][2 * i + 1]), z);
+                        if constexpr (!F8) d = mul(d, q);
+                        const float2 x = parts(d);
+                        sc[j][b][2 * i] = ex2(x.x);
+                        sc[j][b][2 * i + 1] = ex2(x.y);
+                    }
             }
             auto blank = [&]() {      // what a row does not see
 #pragma unroll
@@ -1040,7 +1087,9 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
 #pragma unroll
                 for (int q = 4; q < 32; q <<= 1) l[b][p] += __shfl_xor_sync(~0u, l[b][p], q);
                 if (g == 0) {
-                    top_of[warp][r] = F8 || m[b][p] == -INFINITY ? m[b][p] : m[b][p] * qs[b][p];
+                    top_of[warp][r] = m[b][p] == -INFINITY ? m[b][p]
+                                      : F8                 ? fmaf(m[b][p], qs[b][p], k[b][p])
+                                                           : m[b][p] * qs[b][p];
                     sum_of[warp][r] = l[b][p];
                 }
                 if constexpr (F8) {      // places (D / 8) g + 2 j + i

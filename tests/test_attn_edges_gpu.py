@@ -146,3 +146,38 @@ def test_attention_improbable_large_value(attn):
     ks[page, :, 5] = 90 / 8.0                        # 64 places of -90 / 8, times 1 / 8
     vs[page, :, 5] *= 2.0 ** 70
     check_rows(attn, (q, kc, vc, table, lens, ks, vs))
+
+
+# ---- scores of any size ---------------------------------------------------------------
+
+
+@pytest.mark.parametrize("size", [1e4, 1e9, 1e12, 1e20])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("pdt", [BF, F8, F32], ids=["bf16", "fp8", "f32"])
+def test_attention_huge_scores_are_one_hot(attn, pdt, D, size):
+    """Finite scores so large that one position has all the weight: the output is its value (rounded to 16 bits
+    at most twice, as a weight and as the result), whatever the size."""
+    q, kc, vc, table, lens, ks, vs = attn_problem(3, 2, 6, 2, D, 16, [400, 37, 2], pdt, seed=60)
+    q *= size
+    out, lse = attn.paged_attention(q, kc, vc, table, lens, k_scale=ks, v_scale=vs, return_lse=True)
+    o, l, Q, tab, found = np64(out), np64(lse), np64(q), table.cpu().numpy(), 0
+    for b in range(3):
+        for t in range(2):
+            n = int(lens[b]) - 2 + t + 1
+            at = np.arange(n)
+            page, slot = tab[b, at // 16], at % 16
+            for h in range(6):
+                k, v = (np64(p)[page, h // 3, slot] for p in (kc, vc))
+                if ks is not None:
+                    k, v = (x * np64(s)[page, h // 3, slot][:, None] for x, s in ((k, ks), (v, vs)))
+                s = k @ Q[b, t, h] * D ** -0.5
+                smax = (np.abs(k) @ np.abs(Q[b, t, h])).max() * D ** -0.5
+                order = np.argsort(s)
+                # the runner-up is out of reach of the scores' rounding, and its weight below 2^-58
+                if n > 1 and s[order[-1]] - s[order[-2]] < 2 * (D + 8) * 2.0 ** -22 * smax + 40:
+                    continue
+                found += 1
+                want = v[order[-1]]
+                assert (np.abs(o[b, t, h] - want) <= 2.0 ** -7 * np.abs(want) + 2.0 ** -40).all(), (b, t, h)
+                assert abs(l[b, t, h] - s[order[-1]]) <= (D + 8) * 2.0 ** -22 * smax + 1e-5
+    assert found > 20
