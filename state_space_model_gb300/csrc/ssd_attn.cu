@@ -715,8 +715,9 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                         for (int i = 0; i < 2; ++i) qf[b][k][i] ^= qsign;
                 } else {
                     // fp16 for the product with widened codes: the row is scaled by a
-                    // power of two that brings its largest value to [1, 2), so all but
-                    // values 2^-14 times as large stay exact
+                    // power of two that brings its largest value to [1, 2) (to [2, 4) from
+                    // 2^127 on, the inverse being a normal number), so all but values 2^-14
+                    // times as large stay exact
                     float top = 0.f;
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
@@ -727,7 +728,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
                     uint32_t ex = __float_as_uint(top) & 0x7f800000u;
-                    ex = ex == 0 || ex > 0x7e800000u ? 0x3f800000u : ex;
+                    ex = ex == 0 ? 0x3f800000u : min(ex, 0x7e800000u);
                     const float down = __uint_as_float(0x7f000000u - ex);
                     factor *= __uint_as_float(ex);
 #pragma unroll

@@ -181,3 +181,16 @@ def test_attention_huge_scores_are_one_hot(attn, pdt, D, size):
                 assert (np.abs(o[b, t, h] - want) <= 2.0 ** -7 * np.abs(want) + 2.0 ** -40).all(), (b, t, h)
                 assert abs(l[b, t, h] - s[order[-1]]) <= (D + 8) * 2.0 ** -22 * smax + 1e-5
     assert found > 20
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_largest_queries_over_codes(attn, D):
+    """Queries in the topmost binade of bf16 against small keys: ordinary scores."""
+    q, kc, vc, table, lens, ks, vs = attn_problem(2, 1, 4, 2, D, 16, [100, 7], F8, seed=61)
+    q *= 2.0 ** 126 / float(q.abs().max())
+    q[0, 0, 1] *= 1.9
+    q[0, 0, 2] *= 2 ** -126
+    for i in range(2):
+        q[i, 0, 0, 3], q[i, 0, 3, 5] = 2.0 ** 127 * 1.5, -2.0 ** 127 * 1.5
+    ks *= 2.0 ** -125
+    check_attn(attn, (q, kc, vc, table, lens, ks, vs), F8)
