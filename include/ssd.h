@@ -432,9 +432,9 @@ ssd_status ssd_mixer_prologue(const ssd_tensor *xBC, const ssd_tensor *conv_weig
  *       places: (i, i + R/2), or (2i, 2i + 1) if interleaved != 0, with row
  *       positions[t] of cos and sin; places R.. stay
  *   q_out[t] = u rounded once;  key and value rounded once to the pools' dtype,
- *   or with scales: scale = max(amax, 2^-96) / 448 over the head's row, code =
- *   u / scale rounded to nearest even (a row that holds an infinity or NaN
- *   reads back as NaN)
+ *   or with scales: scale = max(amax, 2^-96) * (1 / 448) over the head's row, in
+ *   f32, code = u / scale, with that scale, rounded to nearest even (a row that
+ *   holds an infinity or NaN reads back as NaN)
  *
  * q, q_out [T, Hq, D], k, v [T, Hkv, D], bf16 or f32 (views of one projection
  * do); slots [T], positions [T] SSD_I32 contiguous; R a multiple of 16, R <= D;

@@ -132,6 +132,23 @@ __device__ __forceinline__ void unpair(const F2 (&r)[4], float (&v)[8]) {
     }
 }
 
+// v / scale for each element, given the rounded inverse: the rounded product is corrected by
+// its remainder, which a fused multiply-add gives exactly (P. Markstein, 1990).  An exact
+// quotient, such as a tie between two codes, comes out exact: bf16 rows hold many (0.1% of
+// their codes differed with the product alone).  4999 tokens of 24 + 2 x 4 heads of 64: 12.45
+// us, with the product alone 12.3, with the division operator 14.4.
+__device__ __forceinline__ void quotients(float (&v)[8], float scale, float inv) {
+    F2 x[4];
+    pairs(v, x);
+    const F2 s = f2(-scale, -scale), r = f2(inv, inv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const F2 q = mul(x[i], r);
+        x[i] = fma(fma(q, s, x[i]), r, q);
+    }
+    unpair(x, v);
+}
+
 // A token's query, key and value rows are taken in passes of 512 / D rows of one kind,
 // D / 16 lanes to a row, two vectors of eight elements a lane; a warp takes U passes
 // of one token.  The two vectors of a lane hold partners of the rotation (i and
@@ -293,19 +310,16 @@ k_kv_append(const __grid_constant__ KvAppendArgs a, int warps) {
             for (int i = 0; i < 8; ++i) amax = max_nan(amax, max_nan(fabsf(y0[i]), fabsf(y1[i])));
 #pragma unroll
             for (int o = LR / 2; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(~0u, amax, o));
-            const float inv = kCodeMax / amax;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                y0[i] *= inv;
-                y1[i] *= inv;
-            }
+            const float scale = amax * (1.f / kCodeMax), inv = 1.f / scale;
+            quotients(y0, scale, inv);
+            quotients(y1, scale, inv);
             if (in) {
                 uint8_t *o = static_cast<uint8_t *>(kind == 2 ? a.c.v : a.c.k) + off;
                 store8_codes(o + 8 * v0, y0);
                 store8_codes(o + 8 * v1, y1);
                 const int64_t soff = page * a.c.ssp + h * a.c.ssh + at;
                 if (l == 0 && SSD_IDX_OK(a.err, soff, a.c.ns))
-                    (kind == 2 ? a.c.vs : a.c.ks)[soff] = amax * (1.f / kCodeMax);
+                    (kind == 2 ? a.c.vs : a.c.ks)[soff] = scale;
             }
         } else if (in) {
             T *o = static_cast<T *>(a.c.k) + off;

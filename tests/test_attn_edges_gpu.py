@@ -194,3 +194,29 @@ def test_attention_largest_queries_over_codes(attn, D):
         q[i, 0, 0, 3], q[i, 0, 3, 5] = 2.0 ** 127 * 1.5, -2.0 ** 127 * 1.5
     ks *= 2.0 ** -125
     check_attn(attn, (q, kc, vc, table, lens, ks, vs), F8)
+
+
+# ---- codes ---------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,dt", [(70, 8, 4, 64, BF), (300, 8, 8, 128, BF), (200, 8, 8, 64, F32),
+                                           (1300, 16, 8, 128, BF)])
+def test_append_codes_are_the_quotient_rounded_once(attn, T, Hq, Hkv, D, dt):
+    """Without norm and rotation, scale = max(amax, 2^-96) (1 / 448) and code = x / scale rounded to nearest
+    even are bit for bit torch's: bf16 rows often hold quotients next to a tie (wherever 448 x / amax
+    ends between two codes), which an inexact quotient sends either way."""
+    g = torch.Generator().manual_seed(T)
+    x = (torch.randn(T, Hq + 2 * Hkv, D, generator=g) * 2).to(BF).to(dt).cuda()
+    x[1] *= 1e-33
+    x[2] *= 2.0 ** 100
+    x[3] = 0
+    kc, vc, ks, vs = new_pools(-(-T // 16), Hkv, 16, D, F8)
+    slots = torch.arange(T, dtype=torch.int32).cuda()
+    attn.kv_append(x[:, :Hq], x[:, Hq: Hq + Hkv], x[:, Hq + Hkv:], slots, kc, vc, k_scale=ks, v_scale=vs)
+    for pool, scale, rows in ((kc, ks, x[:, Hq: Hq + Hkv]), (vc, vs, x[:, Hq + Hkv:])):
+        size = rows.float().abs().amax(-1).clamp(min=2.0 ** -96) * (1 / 448)
+        codes = (rows.float() / size[..., None]).clamp(-448, 448).to(F8)
+        got = pool.view(torch.uint8).transpose(1, 2).reshape(-1, Hkv, D)[:T]
+        assert torch.equal(scale.transpose(1, 2).reshape(-1, Hkv)[:T], size)
+        apart = (got != codes.view(torch.uint8)).sum()
+        assert apart == 0, int(apart)
