@@ -523,15 +523,21 @@ __device__ __forceinline__ uint32_t finite2(uint32_t v) {
     return v;
 }
 
-// Waits for a phase of bar; false after two seconds.
-__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
+// Waits for a phase of bar; false after two seconds, and at once where some warp of the CTA
+// has given up.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *gave_up) {
     bool done = ptx::mbar_try_wait(bar, parity);
     if (!__all_sync(~0u, done)) {
         const uint64_t t0 = ptx::globaltimer_ns();
 #pragma unroll 1
-        while (!done && ptx::globaltimer_ns() - t0 < 2000000000ull) done = ptx::mbar_try_wait(bar, parity);
+        while (!done && !*gave_up && ptx::globaltimer_ns() - t0 < 2000000000ull)
+            done = ptx::mbar_try_wait(bar, parity);
+        if (!__all_sync(~0u, done)) {
+            *gave_up = 1;
+            return false;
+        }
     }
-    return __all_sync(~0u, done);
+    return true;
 }
 
 // A copying warp: fills KW positions of each stage, from the first-th on, with the
@@ -539,8 +545,8 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
 // they land and by lane 0 for the mask, empty[st] by each computing warp.
 template <typename C>
 __device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, const Room<C> room,
-                                           uint64_t *full, uint64_t *empty, Item it, int tile,
-                                           int64_t left, int first) {
+                                           uint64_t *full, uint64_t *empty, volatile int *gave_up,
+                                           Item it, int tile, int64_t left, int first) {
     constexpr int KS = C::KS, KW = C::KW, ROW = C::ROW, D = C::D, ES = C::F8 ? 1 : 2;
     constexpr int LPR = ROW / 16, RPI = 32 / LPR;           // lanes a row, rows a copy
     constexpr int RUN = 16;
@@ -567,7 +573,7 @@ __device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, c
     };
     look_up();
     for (int n = 0, st = 0; left > 0; ++n, st = st + 1 == kStages ? 0 : st + 1) {
-        if (n >= kStages && !wait_for(&empty[st], (n / kStages - 1) & 1)) return false;
+        if (n >= kStages && !wait_for(&empty[st], (n / kStages - 1) & 1, gave_up)) return false;
         const bool ok = page >= 0 && page < a.c.pages;
         const uint32_t mask = __ballot_sync(~0u, ok);
         const int64_t off = ok ? page * a.c.sp + it.hk * a.c.sh + at * a.c.st : 0;
@@ -629,10 +635,12 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ FinderRoom finder;
     __shared__ uint64_t full[kStages], empty[kStages];
+    __shared__ int gave_up;
     __shared__ float top_of[kWarps][8 * NQ], sum_of[kWarps][8 * NQ];
 
     let_next_start();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    if (threadIdx.x == 0) gave_up = 0;
     if (threadIdx.x < kStages) {
         ptx::mbar_init(&full[threadIdx.x], kCopyWarps * (32 + 1));
         ptx::mbar_init(&empty[threadIdx.x], kWarps);
@@ -650,7 +658,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     static_assert(kCopyWarps == kWarps && 128 * (kComputeRegs + kCopyRegs) <= kThreads * 128, "");
     if (warp >= kWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
-        if (!copy_tiles<C>(a, s, room, full, empty, it, tile, left, (warp - kWarps) * KW)) {
+        if (!copy_tiles<C>(a, s, room, full, empty, &gave_up, it, tile, left, (warp - kWarps) * KW)) {
             copies_wait();
             if (lane == 0) atomicOr(a.err, kErrTimeout);
         }
@@ -753,10 +761,10 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
 #pragma unroll
                 for (int b = 0; b < NQ; ++b) o[j][b][0] = o[j][b][1] = o[j][b][2] = o[j][b][3] = 0.f;
         }
-        if (!wait_for(&full[st], (n / kStages) & 1)) {
-            if (lane == 0) atomicOr(a.err, kErrTimeout);
-            return;      // all four warps wait for the same copies, so none is left at a barrier
-        }
+        // A warp whose wait ran out goes on without waiting, over whatever the stages hold:
+        // others may have seen the same copies land, and would wait for it at the barriers
+        // below for ever.
+        if (!wait_for(&full[st], (n / kStages) & 1, &gave_up) && lane == 0) atomicOr(a.err, kErrTimeout);
         const int kbase = it.first + tile * KS + kg * WR * KW;
 #pragma unroll 1
         for (int sub = 0; sub < KW * WR / KP; ++sub) {
