@@ -410,7 +410,8 @@ ssd_status ssd_mixer_prologue(const ssd_tensor *xBC, const ssd_tensor *conv_weig
  * The cache is two pools of pages, one of keys and one of values, each
  * [pages, Hkv, ps, D] (ps tokens a page) with free page, head and token
  * strides, the same for both pools (so [pages, ps, Hkv, D] memory is passed
- * as a transposed view).  A pool holds the dtype of the layer (bf16 or f32),
+ * as a transposed view, and one allocation [pages, 2, Hkv, ps, D] as its two
+ * halves).  A pool holds the dtype of the layer (bf16 or f32),
  * or SSD_F8E4M3 with one f32 scale for each token and head, [pages, Hkv, ps]
  * (innermost stride 1, the same strides for both): a held element stands for
  * code * scale.  Slot s of a pool is token s % ps of page s / ps; a page

@@ -109,15 +109,14 @@ struct Named {
     const ssd_tensor *t;
     const char *name;
 };
-// No output may overlap an input or another output.
+// No output may share an element with an input or another output.
 ssd_status check_aliasing(std::initializer_list<Named> outs, std::initializer_list<Named> ins) {
     for (const Named *o = outs.begin(); o != outs.end(); ++o) {
-        const Range r = range_of(o->t);
         for (const Named &i : ins)
-            if (overlap(r, range_of(i.t)))
+            if (overlap(o->t, i.t))
                 return fail(SSD_ERR_INVALID_ARG, "%s overlaps %s", o->name, i.name);
         for (const Named *p = o + 1; p != outs.end(); ++p)
-            if (overlap(r, range_of(p->t)))
+            if (overlap(o->t, p->t))
                 return fail(SSD_ERR_INVALID_ARG, "%s overlaps %s", o->name, p->name);
     }
     return SSD_OK;

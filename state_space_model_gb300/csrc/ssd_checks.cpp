@@ -57,6 +57,29 @@ bool overlap(Range a, Range b) {
     return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi;
 }
 
+// Modulo some stride m of either, every element of a tensor lies within the span of those of its
+// dimensions whose strides are no multiples of m; spans that stay apart modulo m share nothing.
+bool overlap(const ssd_tensor *a, const ssd_tensor *b) {
+    const Range ra = range_of(a), rb = range_of(b);
+    if (!overlap(ra, rb)) return false;
+    auto span = [](const ssd_tensor *t, uint64_t m) {
+        const uint64_t es = elem_size(t->dtype);
+        uint64_t n = es;
+        for (int i = 0; i < t->ndim; ++i)
+            if (uint64_t(t->stride[i]) * es % m) n += uint64_t(t->shape[i] - 1) * t->stride[i] * es;
+        return n;
+    };
+    for (const ssd_tensor *t : {a, b})
+        for (int i = 0; i < t->ndim; ++i) {
+            if (t->shape[i] <= 1 || t->stride[i] <= 0) continue;
+            const uint64_t m = uint64_t(t->stride[i]) * elem_size(t->dtype);
+            // where b begins modulo m, seen from a
+            const uint64_t at = rb.lo >= ra.lo ? (rb.lo - ra.lo) % m : (m - (ra.lo - rb.lo) % m) % m;
+            if (at >= span(a, m) && at + span(b, m) <= m) return false;
+        }
+    return true;
+}
+
 ssd_status check_tensor(const ssd_tensor *t, const char *name, int ndim,
                         const int64_t *shape, int dtype, bool contiguous,
                         bool align_strides16) {

@@ -28,6 +28,9 @@ struct Range {
 Range range_of(const ssd_tensor *t);
 Range range_raw(const void *p, size_t bytes);
 bool overlap(Range a, Range b);
+// Two tensors that may share an element: their ranges meet, and no stride shows that they lie
+// side by side (keys and values of a page next to one another in one allocation, say).
+bool overlap(const ssd_tensor *a, const ssd_tensor *b);
 
 // Checks one tensor's rank, dtype, shape, unit inner stride and alignment.
 // dtype < 0 accepts f32 or bf16 (the others only where asked for by name).
