@@ -7,7 +7,8 @@ the first CUDA call).  Usage: ``python -m state_space_model_gb300.build``.
 
 The compiled Python binding of the attention entry points
 (``binding/attn_ext.cpp`` -> ``_attn_ext.so``) is built beside it with the host
-compiler against the installed torch.
+compiler against the installed torch, again when that torch or the Python
+changes.  Without torch or g++ the library is built alone.
 
 ``--debug-bounds`` builds ``libssd_gb300_debug.so`` instead (objects in
 ``_build_debug/``), compiled with ``-DSSD_DEBUG_BOUNDS``: the kernels check
@@ -19,7 +20,9 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
+import platform
 import shutil
 import subprocess
 import sys
@@ -34,6 +37,7 @@ BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libssd_gb300_debug.so")
 BINDING_SRC = os.path.join(PKG, "binding", "attn_ext.cpp")
 BINDING = os.path.join(PKG, "_attn_ext.so")
+BINDING_STAMP = os.path.join(BUILD, "attn_ext.stamp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -74,17 +78,39 @@ def up_to_date(debug_bounds: bool = False) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _binding_stamp() -> str | None:
+    """What the binding is built against, or None without a torch: the Python, and the place and
+    date of torch's library (found without importing it)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    torch_lib = os.path.join(os.path.dirname(spec.origin), "lib", "libtorch_python.so")
+    if not os.path.exists(torch_lib):
+        return None
+    return "\n".join([sys.version, str(sysconfig.get_config_var("SOABI")), platform.machine(),
+                      torch_lib, str(os.stat(torch_lib).st_mtime_ns)])
+
+
 def _binding_up_to_date() -> bool:
-    if not os.path.exists(BINDING):
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING_STAMP):
         return False
+    with open(BINDING_STAMP) as f:
+        if f.read() != _binding_stamp():
+            return False
     t = os.path.getmtime(BINDING)
     return all(os.path.getmtime(p) <= t for p in (
         BINDING_SRC, os.path.join(ROOT, "include", "ssd.h"), os.path.abspath(__file__)))
 
 
-def build_binding() -> str:
+def build_binding() -> str | None:
     """Compiles ``_attn_ext.so``.  It links the torch that is installed and calls the
-    library through addresses that ``attn`` gives it."""
+    library through addresses that ``attn`` gives it.  None, with a line on stderr, where
+    torch or the host compiler is missing: only ``attn`` needs it, and says so when called."""
+    stamp = _binding_stamp()
+    missing = "torch" if stamp is None else None if shutil.which("g++") else "g++"
+    if missing:
+        sys.stderr.write(f"_attn_ext.so not built: {missing} not found\n")
+        return None
     import torch
     troot = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
@@ -100,6 +126,9 @@ def build_binding() -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on attn_ext.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(stamp)
     return BINDING
 
 
