@@ -19,6 +19,7 @@ Python loads it when SSD_DEBUG_BOUNDS=1 is set.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import errno
 import glob
 import importlib.util
 import os
@@ -39,6 +40,17 @@ BINDING_SRC = os.path.join(PKG, "binding", "attn_ext.cpp")
 BINDING = os.path.join(PKG, "_attn_ext.so")
 BINDING_STAMP = os.path.join(BUILD, "attn_ext.stamp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
+
+
+def _run(cmd: list[str]) -> subprocess.CompletedProcess:
+    """A compiler's run.  Starting one while other threads start theirs has failed with EFAULT
+    once (aarch64, sandboxed), which is not the command's fault: it is tried again."""
+    for last in (False, False, True):
+        try:
+            return subprocess.run(cmd, capture_output=True, text=True)
+        except OSError as e:
+            if e.errno != errno.EFAULT or last:
+                raise
 
 
 def _nvcc() -> str:
@@ -122,7 +134,7 @@ def build_binding() -> str | None:
            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
            "-L", os.path.join(troot, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
            "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath," + os.path.join(troot, "lib")]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    r = _run(cmd)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on attn_ext.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
@@ -153,7 +165,7 @@ def build(force: bool = False, verbose_ptxas: bool | None = None,
     def compile_one(src: str) -> str:
         obj = os.path.join(out_dir, os.path.basename(src) + ".o")
         cmd = [nvcc] + flags + ["-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
+        r = _run(cmd)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
         if verbose_ptxas and r.stderr:
@@ -165,7 +177,7 @@ def build(force: bool = False, verbose_ptxas: bool | None = None,
         objs = list(ex.map(compile_one, srcs))
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    r = _run(cmd)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)

@@ -70,3 +70,23 @@ def test_library_is_built_without_torch_or_host_compiler(own_binding, monkeypatc
     assert build.build() == build.LIB and os.path.exists(build.LIB)
     assert not os.path.exists(build.BINDING)
     assert missing in capfd.readouterr().err
+
+
+def test_compiler_that_fails_to_start_is_tried_again(monkeypatch):
+    """Starting a process can fail with EFAULT while other threads start theirs."""
+    real, left = build.subprocess.run, [2]
+
+    def run(cmd, *a, **k):
+        if left[0]:
+            left[0] -= 1
+            raise OSError(14, "Bad address", cmd[0])
+        return real(cmd, *a, **k)
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    assert build._run(["true"]).returncode == 0
+    left[0] = 3
+    with pytest.raises(OSError):
+        build._run(["true"])
+    left[0] = 0
+    with pytest.raises(FileNotFoundError):
+        build._run(["no-such-compiler"])
