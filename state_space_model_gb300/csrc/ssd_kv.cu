@@ -356,13 +356,10 @@ cudaError_t append_t(const KvAppendArgs &a, cudaStream_t s) {
     const int passes = (a.Hq + RPP - 1) / RPP + 2 * ((a.c.Hkv + RPP - 1) / RPP);
     const int warps = (passes + kMost - 1) / kMost;
     if (a.T * warps < kFillWarps) return append_u<T, D, kCodes, 1>(a, s);
-    switch ((passes + warps - 1) / warps) {
-    case 4:
-        if constexpr (kMost == 4) return append_u<T, D, kCodes, 4>(a, s);
-    case 3:
-        if constexpr (kMost == 4) return append_u<T, D, kCodes, 3>(a, s);
-    default: return append_u<T, D, kCodes, 2>(a, s);
-    }
+    // three passes and more (a kind has at least one) spread as kMost or kMost - 1 to a warp
+    if constexpr (kMost == 2) return append_u<T, D, kCodes, 2>(a, s);
+    else if ((passes + warps - 1) / warps == 4) return append_u<T, D, kCodes, 4>(a, s);
+    else return append_u<T, D, kCodes, 3>(a, s);
 }
 
 template <int D>
