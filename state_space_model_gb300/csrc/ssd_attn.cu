@@ -284,6 +284,20 @@ __device__ __forceinline__ float *part_at(const PagedArgs &a, const Shape &s, in
            size_t(i) * part_floats(s.RB, a.c.D);
 }
 
+// The debug build's look at a record, and at the last place of row rr of part i.
+__device__ __forceinline__ bool cut_ok(const PagedArgs &a, const Shape &s, int i) {
+    return SSD_IDX_OK(a.err, i, s.ncta) && SSD_IDX_OK(a.err, (i + 1) * int64_t(sizeof(Cut)) - 1, a.ws_n);
+}
+__device__ __forceinline__ bool part_ok(const PagedArgs &a, const Shape &s, int i, int rr) {
+    return SSD_IDX_OK(a.err, rr, s.RB) &&
+           SSD_IDX_OK(a.err,
+                      int64_t(s.ncta * sizeof(Cut) + (i + 1) * part_floats(s.RB, a.c.D) * sizeof(float)) - 1,
+                      a.ws_n);
+}
+__device__ __forceinline__ bool lse_ok(const PagedArgs &a, int64_t i) {
+    return SSD_IDX_OK(a.err, i, int64_t(a.B) * a.T * a.Hq);
+}
+
 // ---- PTX ---------------------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
@@ -569,7 +583,9 @@ __device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, c
         const int pos = it.first + tile * KS + first + lane;
         const int p = shift >= 0 ? pos >> shift : pos / a.c.ps;
         at = pos - p * a.c.ps;
-        if (left > 0 && lane < KW && pos >= it.lo && pos < it.hi) page = a.table[it.b * a.tb + p];
+        if (left > 0 && lane < KW && pos >= it.lo && pos < it.hi &&
+            SSD_IDX_OK(a.err, it.b * a.tb + p, a.t_n))
+            page = a.table[it.b * a.tb + p];
     };
     look_up();
     for (int n = 0, st = 0; left > 0; ++n, st = st + 1 == kStages ? 0 : st + 1) {
@@ -604,8 +620,9 @@ __device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, c
         if constexpr (C::F8) {
             const int64_t so = ok ? page * a.c.ssp + it.hk * a.c.ssh + at : 0;
             const uint32_t d = smem_addr(room.scales(st)) + (first + lane) * 4;
-            copy4(d, a.c.ks + so, ok);
-            copy4(d + KS * 4, a.c.vs + so, ok);
+            const bool in = ok && SSD_IDX_OK(a.err, so, a.c.ns);
+            copy4(d, a.c.ks + so, in);
+            copy4(d + KS * 4, a.c.vs + so, in);
         }
         copies_arrive(&full[st]);
         if (lane == 0) {
@@ -647,7 +664,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     }
     __syncthreads();
     const Stretch span = find<KS, kThreads / 32>(s, blockIdx.x, &finder);
-    if (threadIdx.x == 0) reinterpret_cast<Cut *>(a.ws)[blockIdx.x].parts = 0;
+    if (threadIdx.x == 0 && cut_ok(a, s, blockIdx.x)) reinterpret_cast<Cut *>(a.ws)[blockIdx.x].parts = 0;
     // A cursor: an item, a tile of it, and the units left; the tiles of an item come
     // after its constant.
     Item it = span.it;
@@ -690,8 +707,9 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
 #pragma unroll
         for (int b = 0; b < NQ; ++b) {
             const int r = min(it.rb * RB + wr * 8 * NQ + 8 * b + g, rows - 1), t = token_of(s, r);
-            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + it.b * a.q_sb +
-                                     t * a.q_st + (it.hk * s.G + r - t * s.G) * a.q_sh;
+            const int64_t off = it.b * a.q_sb + t * a.q_st + (it.hk * s.G + r - t * s.G) * a.q_sh;
+            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) +
+                                     (SSD_IDX_OK(a.err, off + D - 1, a.q_n) ? off : 0);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 if constexpr (F8) {       // places 64 h + 16 c + 4 (k % 4)
@@ -1104,14 +1122,16 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                 if constexpr (F8) {      // places (D / 8) g + 2 j + i
 #pragma unroll
                     for (int j = 0; j < MT; j += 2)
-                        *reinterpret_cast<float4 *>(outs + spot(warp, r, (D / 8) * g + 2 * j)) =
+                        if (SSD_IDX_OK(a.err, spot(warp, r, (D / 8) * g + 2 * j) + 3, C::STAGE / 4))
+                            *reinterpret_cast<float4 *>(outs + spot(warp, r, (D / 8) * g + 2 * j)) =
                             make_float4(o[j][b][p], o[j][b][2 + p], o[j + 1][b][p], o[j + 1][b][2 + p]);
                 } else {                 // places 16 j + 8 i + g
 #pragma unroll
                     for (int j = 0; j < MT; ++j)
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
-                            outs[spot(warp, r, 16 * j + 8 * i + g)] = o[j][b][2 * i + p];
+                            if (SSD_IDX_OK(a.err, spot(warp, r, 16 * j + 8 * i + g), C::STAGE / 4))
+                                outs[spot(warp, r, 16 * j + 8 * i + g)] = o[j][b][2 * i + p];
                 }
             }
         warps_sync();
@@ -1126,7 +1146,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             cut.b = done.b;
             cut.hk = done.hk;
             cut.rb = done.rb;
-            reinterpret_cast<Cut *>(a.ws)[blockIdx.x] = cut;
+            if (cut_ok(a, s, blockIdx.x)) reinterpret_cast<Cut *>(a.ws)[blockIdx.x] = cut;
         }
 #pragma unroll 1
         for (int rr = warp; rr < min(RB, rows - done.rb * RB); rr += kWarps) {
@@ -1156,17 +1176,17 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             if (whole) {
                 const int row = done.rb * RB + rr, t = token_of(s, row), h = done.hk * s.G + row - t * s.G;
                 const float inv = lt == 0.f ? 0.f : 1.f / lt;
-                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + done.b * a.o_sb + t * a.o_st +
-                                     h * a.o_sh + E * lane;
+                const int64_t off = done.b * a.o_sb + t * a.o_st + h * a.o_sh + E * lane;
+                if (!SSD_IDX_OK(a.err, off + E - 1, a.o_n)) continue;
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + off;
                 if constexpr (E == 4)
                     *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(v.f[0] * inv, v.f[1] * inv),
                                                                  pack_bf16(v.f[2] * inv, v.f[3] * inv));
                 else
                     *reinterpret_cast<uint32_t *>(dst) = pack_bf16(v.f[0] * inv, v.f[1] * inv);
-                if (a.lse && lane == 0)
-                    a.lse[(int64_t(done.b) * a.T + t) * a.Hq + h] =
-                        log_sum(mt, lt);
-            } else {
+                const int64_t at = (int64_t(done.b) * a.T + t) * a.Hq + h;
+                if (a.lse && lane == 0 && lse_ok(a, at)) a.lse[at] = log_sum(mt, lt);
+            } else if (part_ok(a, s, 2 * blockIdx.x + (first_item ? 0 : 1), rr)) {
                 *reinterpret_cast<Vec *>(part + rr * D + E * lane) = v.x;
                 if (lane == 0) {
                     part[RB * D + rr] = mt;
@@ -1194,6 +1214,7 @@ k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape 
     __shared__ float sm_m[4], sm_l[4], sm_o[4][D];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, x = blockIdx.x;
     wait_for_previous();
+    if (!cut_ok(a, s, x)) return;
     const Cut it = reinterpret_cast<const Cut *>(a.ws)[x];
     if (it.parts == 0) return;
     const int rows = min(s.RB, a.T * s.G - it.rb * s.RB);
@@ -1208,7 +1229,7 @@ k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape 
                 const int c = c0 + per * u;
                 pm[u] = -INFINITY;
                 pl[u] = 0.f;
-                if (c < it.parts) {
+                if (c < it.parts && part_ok(a, s, 2 * (x + c) + (c == 0 ? it.first : 0), rr)) {
                     const float *part = part_at(a, s, 2 * (x + c) + (c == 0 ? it.first : 0));
                     pm[u] = part[s.RB * D + rr];
                     pl[u] = part[s.RB * (D + 1) + rr];
@@ -1255,12 +1276,14 @@ k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape 
             for (int j = 0; j < E; ++j) o[j] = fmaf(sm_o[warp + w][lane * E + j], f * f, o[j]);
         }
         const int r = it.rb * s.RB + rr, t = token_of(s, r), h = it.hk * s.G + r - t * s.G;
-        T *dst = static_cast<T *>(a.out) + it.b * a.o_sb + t * a.o_st + h * a.o_sh + lane * E;
+        const int64_t off = it.b * a.o_sb + t * a.o_st + h * a.o_sh + lane * E;
+        if (!SSD_IDX_OK(a.err, off + E - 1, a.o_n)) continue;
+        T *dst = static_cast<T *>(a.out) + off;
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
         for (int j = 0; j < E; ++j) dst[j] = T(o[j] * inv);
-        if (a.lse && lane == 0)
-            a.lse[(int64_t(it.b) * a.T + t) * a.Hq + h] = log_sum(mt, l);
+        const int64_t at = (int64_t(it.b) * a.T + t) * a.Hq + h;
+        if (a.lse && lane == 0 && lse_ok(a, at)) a.lse[at] = log_sum(mt, l);
     }
 }
 
@@ -1292,7 +1315,7 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int at_pos = lane / LP, at_place = 4 * (lane % LP);   // places at_place + 4 LP i ..
     const Stretch span = find<KS, kF32Warps>(s, blockIdx.x, &finder);
-    if (threadIdx.x == 0) reinterpret_cast<Cut *>(a.ws)[blockIdx.x].parts = 0;
+    if (threadIdx.x == 0 && cut_ok(a, s, blockIdx.x)) reinterpret_cast<Cut *>(a.ws)[blockIdx.x].parts = 0;
     Item it = span.it;
     int tile = max(0, span.unit - kItemCost);
     int64_t left = span.left - max(0, kItemCost - span.unit);
@@ -1308,7 +1331,8 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
         const int pos = ld.first + ld_tile * KS + warp * PW + at_pos;
         const int p = pos / a.c.ps;
         at = pos - p * a.c.ps;
-        if (ld_left > 0 && pos >= ld.lo && pos < ld.hi) page = a.table[ld.b * a.tb + p];
+        if (ld_left > 0 && pos >= ld.lo && pos < ld.hi && SSD_IDX_OK(a.err, ld.b * a.tb + p, a.t_n))
+            page = a.table[ld.b * a.tb + p];
     };
     float4 nk[V], nv[V];
     bool nthere = false;
@@ -1346,9 +1370,9 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             __syncthreads();
             for (int i = threadIdx.x; i < NR * D; i += 32 * kF32Warps) {
                 const int r = min(it.rb * NR + i / D, rows - 1), t = token_of(s, r);
-                qsm[i / D][i % D] = static_cast<const float *>(a.q)[it.b * a.q_sb + t * a.q_st +
-                                                                    (it.hk * s.G + r - t * s.G) * a.q_sh + i % D] *
-                                    (a.scale * kLog2e);
+                const int64_t off = it.b * a.q_sb + t * a.q_st + (it.hk * s.G + r - t * s.G) * a.q_sh + i % D;
+                const float q = SSD_IDX_OK(a.err, off, a.q_n) ? static_cast<const float *>(a.q)[off] : 0.f;
+                qsm[i / D][i % D] = q * (a.scale * kLog2e);
             }
             __syncthreads();
 #pragma unroll
@@ -1441,7 +1465,7 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             cut.b = it.b;
             cut.hk = it.hk;
             cut.rb = it.rb;
-            reinterpret_cast<Cut *>(a.ws)[blockIdx.x] = cut;
+            if (cut_ok(a, s, blockIdx.x)) reinterpret_cast<Cut *>(a.ws)[blockIdx.x] = cut;
         }
         for (int i = threadIdx.x; i < NR * D; i += 32 * kF32Warps) {
             const int rr = i / D, d = i % D, row = it.rb * NR + rr;
@@ -1458,12 +1482,11 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             }
             if (whole) {
                 const int t = token_of(s, row), h = it.hk * s.G + row - t * s.G;
-                static_cast<float *>(a.out)[it.b * a.o_sb + t * a.o_st + h * a.o_sh + d] =
-                    lt == 0.f ? 0.f : x / lt;
-                if (a.lse && d == 0)
-                    a.lse[(int64_t(it.b) * a.T + t) * a.Hq + h] =
-                        log_sum(mt, lt);
-            } else {
+                const int64_t off = it.b * a.o_sb + t * a.o_st + h * a.o_sh + d;
+                if (SSD_IDX_OK(a.err, off, a.o_n)) static_cast<float *>(a.out)[off] = lt == 0.f ? 0.f : x / lt;
+                const int64_t at = (int64_t(it.b) * a.T + t) * a.Hq + h;
+                if (a.lse && d == 0 && lse_ok(a, at)) a.lse[at] = log_sum(mt, lt);
+            } else if (part_ok(a, s, 2 * blockIdx.x + (first_item ? 0 : 1), rr)) {
                 part[rr * D + d] = x;
                 if (d == 0) {
                     part[NR * D + rr] = mt;

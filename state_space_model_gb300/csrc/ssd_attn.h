@@ -39,6 +39,7 @@ struct KvAppendArgs {
     const float *cos = nullptr, *sin = nullptr;   // [S, R/2], null = no rotation
     int64_t S = 0, cs_st = 0, sn_st = 0;
     const float *qw = nullptr, *kw = nullptr;     // [D], null = no norm
+    int64_t q_n = 0, k_n = 0, v_n = 0, o_n = 0, cs_n = 0, sn_n = 0;   // extents, debug build
     unsigned int *err = nullptr;
 };
 cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s);
@@ -52,6 +53,7 @@ struct KvReadArgs {
     const int32_t *cu = nullptr, *starts = nullptr;
     void *k = nullptr; int64_t k_st = 0, k_sh = 0;
     void *v = nullptr; int64_t v_st = 0, v_sh = 0;
+    int64_t t_n = 0, k_n = 0, v_n = 0;                // extents, debug build
     unsigned int *err = nullptr;
 };
 cudaError_t launch_kv_read(const KvReadArgs &a, cudaStream_t s);
@@ -67,6 +69,7 @@ struct PagedArgs {
     const int32_t *table = nullptr; int64_t tb = 0;
     const int32_t *lens = nullptr;
     char *ws = nullptr;
+    int64_t q_n = 0, o_n = 0, t_n = 0, ws_n = 0;      // extents (ws_n: bytes), debug build
     unsigned int *err = nullptr;
 };
 // Workspace for this problem (c.dt, c.Hkv, c.D, B, T, Hq set).

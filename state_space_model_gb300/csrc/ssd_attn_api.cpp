@@ -176,6 +176,8 @@ ssd_status ssd_kv_append(const ssd_tensor *q, const ssd_tensor *k, const ssd_ten
         a.sin = static_cast<const float *>(sin->data);
         a.cs_st = cos->stride[0];
         a.sn_st = sin->stride[0];
+        a.cs_n = extent(cos);
+        a.sn_n = extent(sin);
         a.positions = static_cast<const int32_t *>(positions->data);
     }
     if (q_weight && (st = check_tensor(q_weight, "q_weight", 1, sd, SSD_F32, true, true)))
@@ -218,6 +220,10 @@ ssd_status ssd_kv_append(const ssd_tensor *q, const ssd_tensor *k, const ssd_ten
     a.out = q_out->data;
     a.o_st = q_out->stride[0];
     a.o_sh = q_out->stride[1];
+    a.q_n = extent(q);
+    a.k_n = extent(k);
+    a.v_n = extent(v);
+    a.o_n = extent(q_out);
     a.slots = static_cast<const int32_t *>(slots->data);
     a.qw = q_weight ? static_cast<const float *>(q_weight->data) : nullptr;
     a.kw = k_weight ? static_cast<const float *>(k_weight->data) : nullptr;
@@ -273,6 +279,9 @@ ssd_status ssd_kv_read(const ssd_tensor *k_cache, const ssd_tensor *v_cache,
     a.v = v->data;
     a.v_st = v->stride[0];
     a.v_sh = v->stride[1];
+    a.t_n = extent(page_table);
+    a.k_n = extent(k);
+    a.v_n = extent(v);
     if ((st = cuda_status(ssd::launch_kv_read(a, static_cast<cudaStream_t>(stream)), "kv read")))
         return st;
     return ok();
@@ -387,6 +396,10 @@ ssd_status ssd_paged_attention(const ssd_tensor *q, const ssd_tensor *k_cache,
     a.tb = page_table->stride[0];
     a.lens = static_cast<const int32_t *>(lens->data);
     a.ws = static_cast<char *>(workspace);
+    a.q_n = extent(q);
+    a.o_n = extent(out);
+    a.t_n = extent(page_table);
+    a.ws_n = int64_t(need);
     if ((st = cuda_status(ssd::launch_paged(a, static_cast<cudaStream_t>(stream)),
                           "paged attention")))
         return st;

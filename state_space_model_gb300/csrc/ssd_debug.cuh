@@ -10,6 +10,12 @@
 // through ssd_device_status.  TMA copies are bounds-checked by the hardware
 // (out-of-range boxes are filled or clipped); their shared-memory destinations
 // are checked here.  In the normal build the checks compile to `true`.
+//
+// In the attention cache's kernels (ssd_kv.cu, ssd_attn.cu) the checks cover pools, scales, page
+// tables, angles, the rows of inputs and outputs, log sums, and the workspace's records and
+// parts; in shared memory the exchange of outputs between warps.  Not checked again there:
+// indices that the code has just compared with their bound or clamped to it (lengths, slots,
+// positions), and offsets into stages, which are functions of lane and stage numbers alone.
 #pragma once
 
 #include <stdint.h>

@@ -185,10 +185,12 @@ k_kv_append(const __grid_constant__ KvAppendArgs a, int warps) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int p = p0 + u, kind = kind_of(p), h = head_of(p);
-        if (h < (kind == 0 ? a.Hq : a.c.Hkv)) {
-            const T *src = kind == 0   ? static_cast<const T *>(a.q) + t * a.q_st + h * a.q_sh
-                           : kind == 1 ? static_cast<const T *>(a.k) + t * a.k_st + h * a.k_sh
-                                       : static_cast<const T *>(a.v) + t * a.v_st + h * a.v_sh;
+        const int64_t off = kind == 0   ? t * a.q_st + h * a.q_sh
+                            : kind == 1 ? t * a.k_st + h * a.k_sh
+                                        : t * a.v_st + h * a.v_sh;
+        if (h < (kind == 0 ? a.Hq : a.c.Hkv) &&
+            SSD_IDX_OK(a.err, off + 8 * v1 + 7, kind == 0 ? a.q_n : kind == 1 ? a.k_n : a.v_n)) {
+            const T *src = static_cast<const T *>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + off;
             x[u][0].load(src + 8 * v0);
             x[u][1].load(src + 8 * v1);
         } else {
@@ -201,7 +203,11 @@ k_kv_append(const __grid_constant__ KvAppendArgs a, int warps) {
     const int page = slot / a.c.ps, at = slot - page * a.c.ps;
 
     float cs[8], sn[8];       // interleaved: four for each vector
-    const bool turn = a.cos && l < half;
+    bool turn = a.cos && l < half;
+    if (turn) {       // the last column read: R/2 - 1
+        [[maybe_unused]] const int64_t last = a.interleaved ? 4 * v1 + 3 : 8 * l + 7;
+        turn = SSD_IDX_OK(a.err, pos * a.cs_st + last, a.cs_n) && SSD_IDX_OK(a.err, pos * a.sn_st + last, a.sn_n);
+    }
     if (turn) {
         const float *cp = a.cos + pos * a.cs_st, *sp = a.sin + pos * a.sn_st;
         if (a.interleaved) {
@@ -293,8 +299,9 @@ k_kv_append(const __grid_constant__ KvAppendArgs a, int warps) {
             }
         }
         if (kind == 0) {
-            if (live) {
-                T *o = static_cast<T *>(a.out) + t * a.o_st + h * a.o_sh;
+            const int64_t off = t * a.o_st + h * a.o_sh;
+            if (live && SSD_IDX_OK(a.err, off + 8 * v1 + 7, a.o_n)) {
+                T *o = static_cast<T *>(a.out) + off;
                 store8(o + 8 * v0, y0);
                 store8(o + 8 * v1, y1);
             }
@@ -408,7 +415,8 @@ __global__ void __launch_bounds__(256, 4) k_kv_read(const __grid_constant__ KvRe
             const int64_t pos = (a.starts ? a.starts[lo] : 0) + (i - cu[lo]);
             if (pos >= 0 && pos < int64_t(a.M) * a.c.ps) {
                 const int pi = int(pos) / a.c.ps, at = int(pos) - pi * a.c.ps;
-                const int page = a.table[lo * a.tb + pi];
+                const int64_t entry = lo * a.tb + pi;
+                const int page = SSD_IDX_OK(a.err, entry, a.t_n) ? a.table[entry] : -1;
                 if (page >= 0 && page < a.c.pages) {
                     off = page * a.c.sp + at * a.c.st;
                     soff = page * a.c.ssp + at;
@@ -440,8 +448,10 @@ __global__ void __launch_bounds__(256, 4) k_kv_read(const __grid_constant__ KvRe
                     kx[u].load(static_cast<const P *>(a.c.k) + off);
                     vx[u].load(static_cast<const P *>(a.c.v) + off);
                     if constexpr (sizeof(P) == 1) {
-                        ks[u] = a.c.ks[soff_of[i] + sin];
-                        vs[u] = a.c.vs[soff_of[i] + sin];
+                        if (SSD_IDX_OK(a.err, soff_of[i] + sin, a.c.ns)) {
+                            ks[u] = a.c.ks[soff_of[i] + sin];
+                            vs[u] = a.c.vs[soff_of[i] + sin];
+                        }
                     }
                 } else {
                     kx[u].zero();
@@ -452,6 +462,9 @@ __global__ void __launch_bounds__(256, 4) k_kv_read(const __grid_constant__ KvRe
             for (int u = 0; u < kReadAhead; ++u) {
                 const int i = tok + u * apart;
                 if (i >= n) break;
+                if (!SSD_IDX_OK(a.err, (i0 + i) * a.k_st + h * a.k_sh + 8 * vec + 7, a.k_n) ||
+                    !SSD_IDX_OK(a.err, (i0 + i) * a.v_st + h * a.v_sh + 8 * vec + 7, a.v_n))
+                    continue;
                 if constexpr (sizeof(P) == 1) {
                     float k[8], v[8];
                     kx[u].get(k);

@@ -201,3 +201,45 @@ def test_attention_pieces_of_prompts(attn, T, Hq, Hkv, D, lens, window, pdt):
 def test_attention_negative_scale(attn, T, Hq, pdt):
     prob = attn_problem(3, T, Hq, 2, 64, 16, [200, 3, 70], pdt, seed=90)
     check_attn(attn, prob, pdt, scale=-0.25)
+
+
+# ---- the bounds-checked build on the same paths -------------------------------------------------
+
+DEBUG_CHILD = r"""
+import ctypes, json, sys
+sys.path[:0] = [sys.argv[1], sys.argv[1] + "/tests"]
+import test_attn_paths_gpu as t
+from state_space_model_gb300 import _native, attn
+import torch
+assert _native.LIB_PATH.endswith("libssd_gb300_debug.so"), _native.LIB_PATH
+for dt, pdt in ((t.BF, t.BF), (t.BF, t.F8), (t.F32, t.F8)):
+    t.test_append_prompts(attn, 2501, 4, 2, 128, dt, pdt, 48, True, True)
+    t.test_append_prompts(attn, 1301, 40, 8, 64, dt, pdt, "D", False, True)
+for pdt, odt in ((t.BF, t.BF), (t.F8, t.F32), (t.F32, t.F32)):
+    t.test_read_of_many(attn, 512, 2, 64, 40, pdt, odt)
+    t.test_read_of_many(attn, 3, 20, 128, 300, pdt, odt)
+    t.test_read_of_many(attn, 5, 4, 128, 2000, pdt, odt)
+for pdt in (t.BF, t.F8, t.F32):
+    t.test_attention_pieces_of_prompts(attn, 500, 8, 2, 64, [500, 1200, 499, 3], 0, pdt)
+    t.test_attention_pieces_of_prompts(attn, 700, 16, 2, 128, [2000], 300, pdt)
+    t.test_attention_many_tiles(attn, (4, 32, 8, 128, 64, 40, 1500, 0), pdt)
+    t.test_attention_many_tiles(attn, (1, 12, 4, 64, 100, 300, 500, 0), pdt)
+lib = _native.load()
+st = lib.ssd_device_status(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+print(json.dumps({"status": st, "detail": lib.ssd_last_error_detail().decode()}))
+"""
+
+
+def test_debug_build_on_every_path(attn):
+    import json
+    import os
+    import subprocess
+    import sys
+    from state_space_model_gb300 import build
+    build.build(debug_bounds=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", DEBUG_CHILD, root], env=dict(os.environ, SSD_DEBUG_BOUNDS="1"),
+                       cwd=root, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout + r.stderr
+    out = json.loads(r.stdout.strip().splitlines()[-1])
+    assert out["status"] == 0, out["detail"]
