@@ -111,14 +111,17 @@ struct Named {
 };
 // No output may share an element with an input or another output.
 ssd_status check_aliasing(std::initializer_list<Named> outs, std::initializer_list<Named> ins) {
-    for (const Named *o = outs.begin(); o != outs.end(); ++o) {
-        for (const Named &i : ins)
-            if (overlap(o->t, i.t))
-                return fail(SSD_ERR_INVALID_ARG, "%s overlaps %s", o->name, i.name);
-        for (const Named *p = o + 1; p != outs.end(); ++p)
-            if (overlap(o->t, p->t))
-                return fail(SSD_ERR_INVALID_ARG, "%s overlaps %s", o->name, p->name);
-    }
+    const Named *all[16];
+    Range at[16];
+    int n = 0;
+    for (const Named &o : outs) all[n++] = &o;
+    for (const Named &i : ins) all[n++] = &i;
+    for (int i = 0; i < n; ++i) at[i] = range_of(all[i]->t);
+    const int nouts = int(outs.size());
+    for (int o = 0; o < nouts; ++o)
+        for (int i = o + 1; i < n; ++i)
+            if (overlap(at[o], at[i]) && overlap(all[o]->t, all[i]->t))   // (ranges seldom meet)
+                return fail(SSD_ERR_INVALID_ARG, "%s overlaps %s", all[o]->name, all[i]->name);
     return SSD_OK;
 }
 
