@@ -42,11 +42,11 @@ namespace {
 constexpr float kLn2 = 0.6931471805599453f;
 // 8-bit values: a row's largest weight is 2^kLift to 2^(kLift + kAhead) in fp16 (so weights
 // keep their 11 bits down to 2^-22 of it), with log2 of a value's scale taken as [kLeastLog,
-// kMostLog].  At the lower end the fp32 sum of 2^25 probabilities of 2^(kLift + kAhead - kLeastLog) is
+// kMostLog].  At the lower end the fp32 sum of 2^22 probabilities of 2^(kLift + kAhead - kLeastLog) is
 // finite, and scales down to 2^(kLeastLog - 22) still have weights of 11 bits; at the upper end
 // a probability of 2^-kMostLog is a normal number, and the largest finite scales stay below
 // fp16's end.
-constexpr float kLift = 8.f, kAhead = 2.f, kLeastLog = -92.f, kMostLog = 119.f;
+constexpr float kLift = 8.f, kAhead = 5.f, kLeastLog = -92.f, kMostLog = 119.f;
 constexpr int kWarps = 4;                 // of a CTA that compute
 constexpr int kCopyWarps = 4;             // and that copy
 constexpr int kThreads = 32 * (kWarps + kCopyWarps);
@@ -694,7 +694,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     // Codes: a weight p vs (vs: the value's scale) goes to fp16, so p = 2^(qs (s - m) - k), with k
     // following the largest qs (s - m) + log2 vs (less kLift) over the positions that the row sees:
     // the largest weight is about 2^kLift, whatever the scales are, and positions that it does
-    // not see have no part in it.  k follows when that is ahead by kAhead, since
+    // not see have no part in it.  k follows when that may be ahead by kAhead, since
     // moving it means to go over the outputs; where m moves alone, k takes the difference.
     // p, summed in fp32, may be as large as 2^(kLift + kAhead - kLeastLog) and as small as 2^-kMostLog.
     uint32_t qf[NQ][D / 16][2];
@@ -885,14 +885,18 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                     moved = moved || v != m[b][p];
                 }
             float vs[KT][2], f[NQ][2];       // codes: value scales; what the outputs are multiplied by
+            auto less = [&](float (&x)[2]) {     // two rows' references, subtracted
+                return f2(x[0] == -INFINITY ? 0.f : -x[0], x[1] == -INFINITY ? 0.f : -x[1]);
+            };
             if constexpr (F8) {
-                float lv[KT][2], kn[NQ][2];
+                float lv[KT][2], most = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < KT; ++j)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         vs[j][i] = vsc[pos_of(j, i)];
                         lv[j][i] = fminf(fmaxf(lg2(fabsf(vs[j][i])), kLeastLog), kMostLog) - kLift;
+                        most = fmaxf(most, lv[j][i]);
                     }
                 if (__any_sync(~0u, moved)) {
 #pragma unroll
@@ -903,33 +907,30 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                             m[b][p] = mn[b][p];
                         }
                 }
+                // no weight is above its value's scale: mostly that bound is near enough to k
                 moved = false;
 #pragma unroll
-                for (int b = 0; b < NQ; ++b) {
-                    const F2 q = f2(qs[b][0], qs[b][1]);
-                    const F2 z = f2(m[b][0] == -INFINITY ? 0.f : -m[b][0], m[b][1] == -INFINITY ? 0.f : -m[b][1]);
-                    kn[b][0] = k[b][0];
-                    kn[b][1] = k[b][1];
+                for (int b = 0; b < NQ; ++b)
 #pragma unroll
-                    for (int j = 0; j < KT; ++j)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const F2 d = mul(add(f2(sc[j][b][2 * i], sc[j][b][2 * i + 1]), z), q);
-                            const float2 x = parts(d), t = parts(add(d, f2(lv[j][i], lv[j][i])));
-                            sc[j][b][2 * i] = x.x;
-                            sc[j][b][2 * i + 1] = x.y;
-                            kn[b][0] = fmaxf(kn[b][0], t.x);
-                            kn[b][1] = fmaxf(kn[b][1], t.y);
-                        }
-                    moved = moved || kn[b][0] > k[b][0] + kAhead || kn[b][1] > k[b][1] + kAhead;
-                }
+                    for (int p = 0; p < 2; ++p) moved = moved || most > k[b][p] + kAhead;
                 moved = __any_sync(~0u, moved);
                 if (moved) {
 #pragma unroll
-                    for (int b = 0; b < NQ; ++b)
+                    for (int b = 0; b < NQ; ++b) {
+                        const F2 q = f2(qs[b][0], qs[b][1]), z = less(m[b]);
+                        float kn[2] = {k[b][0], k[b][1]};
+#pragma unroll
+                        for (int j = 0; j < KT; ++j)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const float2 t = parts(fma(add(f2(sc[j][b][2 * i], sc[j][b][2 * i + 1]), z),
+                                                           q, f2(lv[j][i], lv[j][i])));
+                                kn[0] = fmaxf(kn[0], t.x);
+                                kn[1] = fmaxf(kn[1], t.y);
+                            }
 #pragma unroll
                         for (int p = 0; p < 2; ++p) {
-                            float v = kn[b][p];
+                            float v = kn[p];
                             v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
                             v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
                             v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
@@ -939,6 +940,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                             l[b][p] = l[b][p] * f[b][p] * f[b][p];
                             f[b][p] *= f[b][p];
                         }
+                    }
                 }
             } else {
                 moved = __any_sync(~0u, moved);
@@ -966,16 +968,17 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             // second product
 #pragma unroll
             for (int b = 0; b < NQ; ++b) {
-                const float *const from = F8 ? k[b] : m[b];
-                const F2 q = f2(qs[b][0], qs[b][1]);
-                const F2 z = f2(from[0] == -INFINITY ? 0.f : -from[0], from[1] == -INFINITY ? 0.f : -from[1]);
+                const F2 q = f2(qs[b][0], qs[b][1]), z = less(m[b]);
+                F2 zk;
+                if constexpr (F8) zk = less(k[b]);
 #pragma unroll
                 for (int j = 0; j < KT; ++j)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        F2 d = add(f2(sc[j][b][2 * i], sc[j][b][2 * i + 1]), z);
-                        if constexpr (!F8) d = mul(d, q);
-                        const float2 x = parts(d);
+                        const F2 d = add(f2(sc[j][b][2 * i], sc[j][b][2 * i + 1]), z);
+                        float2 x;
+                        if constexpr (F8) x = parts(fma(d, q, zk));
+                        else x = parts(mul(d, q));
                         sc[j][b][2 * i] = ex2(x.x);
                         sc[j][b][2 * i + 1] = ex2(x.y);
                     }
