@@ -14,13 +14,14 @@ namespace ssd {
 namespace {
 
 constexpr float kCodeMax = 448.f;          // largest e4m3 value
-constexpr int kFillWarps = 152 * 16;       // warps that fill the GPU
+constexpr int kSms = 152;                  // of a GB300, for the launches' rules
+constexpr int kFillWarps = kSms * 16;      // warps that fill the GPU
 constexpr float kAmaxFloor = 0x1p-96f;     // keeps the scale and its inverse normal numbers
 
 // Eight consecutive elements of a row as they lie in memory (held like that while
 // loads are under way: a kernel's registers decide how many can be), and in fp32.
-// Everything is read and written once, with streaming hints (32768 cached tokens read
-// back: 38.9 us without, 36.9 with).
+// Everything is read and written once; bf16 loads and stores and code loads carry streaming
+// hints (32768 cached tokens read back: 38.9 us without, 36.9 with).
 template <typename T>
 struct Raw8;
 template <>
@@ -158,7 +159,7 @@ __device__ __forceinline__ void quotients(float (&v)[8], float scale, float inv)
 // warp go out before its token's slot, position and angles (which the passes share)
 // are known.  Measured: 8192 tokens of 32 + 2 x 8 heads of 128 in bf16 35.3 us, 86% of
 // the copy rate (57 us with a row a thread group and its angles read again for each
-// row); in fp8 37 us, 75%, where the instructions begin to count.  Few key heads leave
+// row); in fp8 38 us, 73%, where the instructions begin to count; in fp32 65 us, 93%.  Few key heads leave
 // lanes of their passes idle (4 of 64: half): 4999 tokens of 24 + 2 x 4 take 12.3 us.
 constexpr int kAppendWarps = 4;
 // kWhole: every row is turned whole (R = D).  Elsewhere places that are not turned keep what
@@ -491,7 +492,7 @@ cudaError_t read_t(const KvReadArgs &a, cudaStream_t s) {
     // kernel alone, 300 tokens of 4 heads of 64: 4.4 us, with 32 a CTA 4.7)
     int TB = 1024 / (a.c.Hkv * (D / 8));
     TB = TB < 1 ? 1 : TB > kReadTokens ? kReadTokens : TB;
-    while (TB > 1 && (a.T + TB - 1) / TB < 152) TB /= 2;
+    while (TB > 1 && (a.T + TB - 1) / TB < kSms) TB /= 2;
     const int64_t blocks = (a.T + TB - 1) / TB;
     k_kv_read<T, P, D><<<unsigned(blocks), 256, 0, s>>>(a, TB);
     return cudaGetLastError();
