@@ -11,7 +11,8 @@ D], bf16 or f32, or ``torch.float8_e4m3fn`` with scales ``k_scale`` and
 ``v_scale`` [pages, Hkv, ps] f32 (an element stands for code * scale).  Slot s
 is token s % ps of page s // ps; ``page_table`` [B, M] int32 names each
 sequence's pages in order.  Memory laid out [pages, ps, Hkv, D] is passed as
-``pool.transpose(1, 2)``.
+``pool.transpose(1, 2)``, one allocation [pages, 2, Hkv, ps, D] as
+``pool.unbind(1)``.
 """
 from __future__ import annotations
 

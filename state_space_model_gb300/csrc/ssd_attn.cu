@@ -414,8 +414,9 @@ __device__ __forceinline__ void let_next_start() {
 // query heads over 8 of 128, bf16: 170 us, 93%; the same in fp8 97 us, 85%; one
 // sequence of 131072, 32 over 8: 86 us, 92%; 96 of 17 to 16384 over fp8: 77 us, 82%.
 // Query rows cost little up to 32 a key/value head in bf16 (177 us) and 16 in fp8
-// (105 us); at 64 in bf16 (261 us) and 32 in fp8 (170 us) the products take longer than
-// the reads.
+// (106 us); at 64 in bf16 (265 us) and 32 in fp8 (174 us) the products take longer than
+// the reads.  Pieces of prompts are blocks of 64 rows: 8192 tokens of 32 over 8 heads
+// take 2.1 ms in bf16, 258 TFLOP/s.
 template <int D_, bool F8_, int NQ_, int WR_>
 struct Cfg {
     static constexpr int D = D_, NQ = NQ_, WR = WR_, WK = kWarps / WR_;
@@ -965,7 +966,10 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             }
             // probabilities (unnormalised; at most 1, with codes after their values' scales at most
             // 2^(kLift + kAhead)), summed in fp32 and rounded to 16 bits as the right operand of the
-            // second product
+            // second product: its type is that of the values (bf16, or fp16 for codes).  (A second
+            // bf16 product with what the rounding leaves costs nothing at 8 and 16 rows of 64 x
+            // 4096, but 175 -> 189 us at 32, 265 -> 329 at 64 and 23.0 -> 24.7 for 128 short
+            // sequences; the output, bf16 too, is off by 2.1e-3 as it is, 1.7e-3 by its own rounding.)
 #pragma unroll
             for (int b = 0; b < NQ; ++b) {
                 const F2 q = f2(qs[b][0], qs[b][1]), z = less(m[b]);
@@ -1564,8 +1568,8 @@ cudaError_t launch_f32(const PagedArgs &a, const Shape &s, cudaStream_t stream) 
 // blocks, each of which reads the cache.  64 sequences of 4096 over 8 key/value heads of
 // 128, microseconds for bf16 / fp8 with blocks of half the rows, this rule's, twice:
 //   8 rows              -  170 /  97  170 / 101
-//   16 rows     325 / 175  174 / 105  173 / 164
-//   32 rows     330 / 192  177 / 170  246 / 289
+//   16 rows     325 / 175  174 / 106  173 / 170
+//   32 rows     330 / 195  177 / 174  252 / 301
 Shape make_shape(const PagedArgs &a) {
     Shape s{};
     s.lens = a.lens;
