@@ -44,7 +44,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 def _run(cmd: list[str]) -> subprocess.CompletedProcess:
     """A compiler's run.  Starting one while other threads start theirs has failed with EFAULT
-    once (aarch64, sandboxed), which is not the command's fault: it is tried again."""
+    once (aarch64), which is not the command's fault: it is tried again."""
     for last in (False, False, True):
         try:
             return subprocess.run(cmd, capture_output=True, text=True)
