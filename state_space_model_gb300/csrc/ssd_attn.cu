@@ -520,14 +520,26 @@ __device__ __forceinline__ float lg2(float x) {
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// ln(2^m l).  The sum's exponent is added to m before anything is rounded: with codes they
-// may be far apart and nearly cancel.
+// ln(2^m l).  Codes: the sum's exponent is added to m before anything is rounded, as they may be
+// far apart and nearly cancel.
+template <bool F8>
 __device__ __forceinline__ float log_sum(float m, float l) {
     if (l == 0.f) return -INFINITY;
+    if constexpr (!F8) return (m + log2f(l)) * kLn2;
     const uint32_t u = __float_as_uint(l), e = u >> 23;
     if (e == 0 || e >= 255) return (m + log2f(l)) * kLn2;     // subnormal, infinite, NaN (or negative)
     return ((m + (float(e) - 127.f)) + log2f(__uint_as_float((u & 0x7fffffu) | 0x3f800000u))) * kLn2;
 }
+
+// The factor 2^x, x <= 0, of a part's sum and outputs.  Codes: by halves, as a sum may be large
+// where its factor is below 2^-126 (in every join: 0.2 us of a short call's 4.5).
+template <bool F8>
+struct Factor {
+    float f;
+    __device__ __forceinline__ explicit Factor(float x) : f(ex2(F8 ? 0.5f * x : x)) {}
+    __device__ __forceinline__ float sum(float l) const { return F8 ? l * f * f : l * f; }
+    __device__ __forceinline__ float out() const { return F8 ? f * f : f; }
+};
 
 // Infinities and NaN of a pair of 16-bit values, replaced by 0.
 template <bool F16>
@@ -935,11 +947,10 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                             v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
                             v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
                             v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
-                            // by halves: the sum may be large where the factor is below 2^-126
-                            f[b][p] = k[b][p] == -INFINITY ? 0.f : ex2(0.5f * (k[b][p] - v));
+                            const Factor<true> old(k[b][p] == -INFINITY ? -INFINITY : k[b][p] - v);
+                            f[b][p] = old.out();
+                            l[b][p] = old.sum(l[b][p]);
                             k[b][p] = v;
-                            l[b][p] = l[b][p] * f[b][p] * f[b][p];
-                            f[b][p] *= f[b][p];
                         }
                     }
                 }
@@ -1173,12 +1184,12 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             for (int i = 0; i < E; ++i) v.f[i] = 0.f;
 #pragma unroll
             for (int k = 0; k < WK; ++k) {
-                const float f = ex2(0.5f * (top_of[k * WR + w0][r] - base));   // by halves, as above
+                const Factor<F8> f(top_of[k * WR + w0][r] - base);
                 Places src;
                 src.x = *reinterpret_cast<const Vec *>(outs + spot(k * WR + w0, r, E * lane));
-                lt = fmaf(sum_of[k * WR + w0][r] * f, f, lt);
+                lt += f.sum(sum_of[k * WR + w0][r]);
 #pragma unroll
-                for (int i = 0; i < E; ++i) v.f[i] = fmaf(src.f[i], f * f, v.f[i]);
+                for (int i = 0; i < E; ++i) v.f[i] = fmaf(src.f[i], f.out(), v.f[i]);
             }
             if (whole) {
                 const int row = done.rb * RB + rr, t = token_of(s, row), h = done.hk * s.G + row - t * s.G;
@@ -1192,7 +1203,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                 else
                     *reinterpret_cast<uint32_t *>(dst) = pack_bf16(v.f[0] * inv, v.f[1] * inv);
                 const int64_t at = (int64_t(done.b) * a.T + t) * a.Hq + h;
-                if (a.lse && lane == 0 && lse_ok(a, at)) a.lse[at] = log_sum(mt, lt);
+                if (a.lse && lane == 0 && lse_ok(a, at)) a.lse[at] = log_sum<F8>(mt, lt);
             } else if (part_ok(a, s, 2 * blockIdx.x + (first_item ? 0 : 1), rr)) {
                 *reinterpret_cast<Vec *>(part + rr * D + E * lane) = v.x;
                 if (lane == 0) {
@@ -1214,7 +1225,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
 // them apart.  A CTA for every row of a wide block would mostly be CTAs that find
 // nothing to do (32 rows: 9 us in place of 4).
 constexpr int kJoinAhead = 8;     // parts that a warp loads at once
-template <typename T, int D>
+template <typename T, int D, bool F8>
 __global__ void __launch_bounds__(128)
 k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s, int per) {
     constexpr int E = D / 32;
@@ -1250,18 +1261,18 @@ k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape 
             float mt = m;
 #pragma unroll
             for (int u = 0; u < kJoinAhead; ++u) mt = fmaxf(mt, pm[u]);
-            // factors by halves: a sum may be large where its factor is below 2^-126
-            const float base = mt == -INFINITY ? 0.f : mt, old = ex2(0.5f * (m - base));
+            const float base = mt == -INFINITY ? 0.f : mt;
+            const Factor<F8> old(m - base);
             m = mt;
-            l = l * old * old;
+            l = old.sum(l);
 #pragma unroll
-            for (int j = 0; j < E; ++j) o[j] *= old * old;
+            for (int j = 0; j < E; ++j) o[j] *= old.out();
 #pragma unroll
             for (int u = 0; u < kJoinAhead; ++u) {
-                const float f = ex2(0.5f * (pm[u] - base));
-                l = fmaf(pl[u] * f, f, l);
+                const Factor<F8> f(pm[u] - base);
+                l += f.sum(pl[u]);
 #pragma unroll
-                for (int j = 0; j < E; ++j) o[j] = fmaf(v[u][j], f * f, o[j]);
+                for (int j = 0; j < E; ++j) o[j] = fmaf(v[u][j], f.out(), o[j]);
             }
         }
         __syncthreads();          // the rows before have been read
@@ -1277,10 +1288,10 @@ k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape 
 #pragma unroll
         for (int j = 0; j < E; ++j) o[j] = 0.f;
         for (int w = 0; w < per; ++w) {
-            const float f = ex2(0.5f * (sm_m[warp + w] - base));
-            l = fmaf(sm_l[warp + w] * f, f, l);
+            const Factor<F8> f(sm_m[warp + w] - base);
+            l += f.sum(sm_l[warp + w]);
 #pragma unroll
-            for (int j = 0; j < E; ++j) o[j] = fmaf(sm_o[warp + w][lane * E + j], f * f, o[j]);
+            for (int j = 0; j < E; ++j) o[j] = fmaf(sm_o[warp + w][lane * E + j], f.out(), o[j]);
         }
         const int r = it.rb * s.RB + rr, t = token_of(s, r), h = it.hk * s.G + r - t * s.G;
         const int64_t off = it.b * a.o_sb + t * a.o_st + h * a.o_sh + lane * E;
@@ -1290,7 +1301,7 @@ k_paged_join(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape 
 #pragma unroll
         for (int j = 0; j < E; ++j) dst[j] = T(o[j] * inv);
         const int64_t at = (int64_t(it.b) * a.T + t) * a.Hq + h;
-        if (a.lse && lane == 0 && lse_ok(a, at)) a.lse[at] = log_sum(mt, l);
+        if (a.lse && lane == 0 && lse_ok(a, at)) a.lse[at] = log_sum<F8>(mt, l);
     }
 }
 
@@ -1492,7 +1503,7 @@ k_paged_f32(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                 const int64_t off = it.b * a.o_sb + t * a.o_st + h * a.o_sh + d;
                 if (SSD_IDX_OK(a.err, off, a.o_n)) static_cast<float *>(a.out)[off] = lt == 0.f ? 0.f : x / lt;
                 const int64_t at = (int64_t(it.b) * a.T + t) * a.Hq + h;
-                if (a.lse && d == 0 && lse_ok(a, at)) a.lse[at] = log_sum(mt, lt);
+                if (a.lse && d == 0 && lse_ok(a, at)) a.lse[at] = log_sum<false>(mt, lt);
             } else if (part_ok(a, s, 2 * blockIdx.x + (first_item ? 0 : 1), rr)) {
                 part[rr * D + d] = x;
                 if (d == 0) {
@@ -1529,7 +1540,7 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t> (&done)[4]) {
 
 // The join may start while the last parts are being computed; it waits for them before
 // it reads any.
-template <typename T, int D>
+template <typename T, int D, bool F8>
 cudaError_t launch_join(const PagedArgs &a, const Shape &s, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at{};
@@ -1542,7 +1553,7 @@ cudaError_t launch_join(const PagedArgs &a, const Shape &s, cudaStream_t stream)
     cfg.stream = stream;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_paged_join<T, D>, a, s, per);
+    return cudaLaunchKernelEx(&cfg, k_paged_join<T, D, F8>, a, s, per);
 }
 
 template <int D, bool F8, int NQ, int WR>
@@ -1553,14 +1564,14 @@ cudaError_t launch_mma(const PagedArgs &a, const Shape &s, cudaStream_t stream) 
     if (e != cudaSuccess) return e;
     k_paged_mma<D, F8, NQ, WR><<<s.ncta, kThreads, C::SMEM, stream>>>(a, s);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_join<__nv_bfloat16, D>(a, s, stream);
+    return launch_join<__nv_bfloat16, D, F8>(a, s, stream);
 }
 
 template <int D, int NR>
 cudaError_t launch_f32(const PagedArgs &a, const Shape &s, cudaStream_t stream) {
     k_paged_f32<D, NR><<<s.ncta, 32 * kF32Warps, 0, stream>>>(a, s);
     const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_join<float, D>(a, s, stream);
+    return e != cudaSuccess ? e : launch_join<float, D, false>(a, s, stream);
 }
 
 // Rows of a block: 8 or 16 to a warp, then up to four warps along the rows (and
