@@ -704,11 +704,11 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     // them (times the key's scale): a row's factor qs >= 0 (scale log2(e), the sign of
     // the scale being in the queries) enters with the exponential, p = 2^(qs (s - m)).
     // (The difference first: qs m rounded would be off by any power of two for large scores.)
-    // Codes: a weight p vs (vs: the value's scale) goes to fp16, so p = 2^(qs (s - m) - k), with k
-    // following the largest qs (s - m) + log2 vs (less kLift) over the positions that the row sees:
-    // the largest weight is about 2^kLift, whatever the scales are, and positions that it does
-    // not see have no part in it.  k follows when that may be ahead by kAhead, since
-    // moving it means to go over the outputs; where m moves alone, k takes the difference.
+    // Codes: a weight p vs (vs: the value's scale) goes to fp16, so p = 2^(qs (s - m) - k), where m
+    // is some score that the row has seen and k the largest qs (s - m) + log2 vs (less kLift) over
+    // the positions that it sees: the largest weight is about 2^kLift, whatever the scales are, and
+    // positions that it does not see have no part in it.  m and k follow, together, when
+    // a weight may be ahead by kAhead, since moving them means to go over the outputs.
     // p, summed in fp32, may be as large as 2^(kLift + kAhead - kLeastLog) and as small as 2^-kMostLog.
     uint32_t qf[NQ][D / 16][2];
     float o[MT][NQ][4], m[NQ][2], l[NQ][2], qs[NQ][2], k[NQ][2];
@@ -783,7 +783,8 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                     const int row = it.rb * RB + wr * 8 * NQ + 8 * b + 2 * c + p;
                     qs[b][p] = F8 ? __shfl_sync(~0u, factor, (2 * c + p) * 4) : qscale;
                     e[b][p] = it.len - a.T + token_of(s, min(row, rows - 1));
-                    m[b][p] = k[b][p] = -INFINITY;
+                    m[b][p] = F8 ? 0.f : -INFINITY;
+                    k[b][p] = -INFINITY;
                     l[b][p] = 0.f;
                 }
             }
@@ -882,25 +883,23 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                             if (!see) sc[j][b][i] = -INFINITY;
                         }
             }
-            float mn[NQ][2];
-            bool moved = false;
+            float mn[NQ][2];                 // this thread's largest scores
 #pragma unroll
             for (int b = 0; b < NQ; ++b)
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    float v = m[b][p];
+                    float v = F8 ? -INFINITY : m[b][p];
 #pragma unroll
                     for (int j = 0; j < KT; ++j) v = fmaxf(v, fmaxf(sc[j][b][p], sc[j][b][2 + p]));
-                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
-                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
-                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
                     mn[b][p] = v;
-                    moved = moved || v != m[b][p];
                 }
-            float vs[KT][2], f[NQ][2];       // codes: value scales; what the outputs are multiplied by
-            auto less = [&](float (&x)[2]) {     // two rows' references, subtracted
-                return f2(x[0] == -INFINITY ? 0.f : -x[0], x[1] == -INFINITY ? 0.f : -x[1]);
+            auto row_max = [](float v) {     // over the lanes that hold the row
+                v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+                v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+                return fmaxf(v, __shfl_xor_sync(~0u, v, 16));
             };
+            bool moved = false;
+            float vs[KT][2], f[NQ][2];       // codes: value scales; what the outputs are multiplied by
             if constexpr (F8) {
                 float lv[KT][2], most = -INFINITY;
 #pragma unroll
@@ -911,50 +910,44 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                         lv[j][i] = fminf(fmaxf(lg2(fabsf(vs[j][i])), kLeastLog), kMostLog) - kLift;
                         most = fmaxf(most, lv[j][i]);
                     }
-                if (__any_sync(~0u, moved)) {
+                // the largest score with the largest scale: mostly no weight is ahead of that bound
+#pragma unroll
+                for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+                        moved = moved || fmaf(mn[b][p] - m[b][p], qs[b][p], most) > k[b][p] + kAhead;
+                moved = __any_sync(~0u, moved);
+                if (moved) {
 #pragma unroll
                     for (int b = 0; b < NQ; ++b)
 #pragma unroll
                         for (int p = 0; p < 2; ++p) {
-                            if (m[b][p] != -INFINITY) k[b][p] -= (mn[b][p] - m[b][p]) * qs[b][p];
-                            m[b][p] = mn[b][p];
+                            const float top = row_max(mn[b][p]);
+                            const bool none = k[b][p] == -INFINITY;      // nothing seen before
+                            const float to = top == -INFINITY ? m[b][p] : none ? top : fmaxf(m[b][p], top);
+                            const float was = none ? k[b][p] : fmaf(m[b][p] - to, qs[b][p], k[b][p]);
+                            float v = was;
+#pragma unroll
+                            for (int j = 0; j < KT; ++j)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    v = fmaxf(v, fmaf(sc[j][b][2 * i + p] - to, qs[b][p], lv[j][i]));
+                            v = row_max(v);
+                            const Factor<true> old(was == -INFINITY ? was : was - v);
+                            f[b][p] = old.out();
+                            l[b][p] = old.sum(l[b][p]);
+                            m[b][p] = to;
+                            k[b][p] = v;
                         }
                 }
-                // no weight is above its value's scale: mostly that bound is near enough to k
-                moved = false;
+            } else {
 #pragma unroll
                 for (int b = 0; b < NQ; ++b)
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) moved = moved || most > k[b][p] + kAhead;
-                moved = __any_sync(~0u, moved);
-                if (moved) {
-#pragma unroll
-                    for (int b = 0; b < NQ; ++b) {
-                        const F2 q = f2(qs[b][0], qs[b][1]), z = less(m[b]);
-                        float kn[2] = {k[b][0], k[b][1]};
-#pragma unroll
-                        for (int j = 0; j < KT; ++j)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const float2 t = parts(fma(add(f2(sc[j][b][2 * i], sc[j][b][2 * i + 1]), z),
-                                                           q, f2(lv[j][i], lv[j][i])));
-                                kn[0] = fmaxf(kn[0], t.x);
-                                kn[1] = fmaxf(kn[1], t.y);
-                            }
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            float v = kn[p];
-                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
-                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
-                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
-                            const Factor<true> old(k[b][p] == -INFINITY ? -INFINITY : k[b][p] - v);
-                            f[b][p] = old.out();
-                            l[b][p] = old.sum(l[b][p]);
-                            k[b][p] = v;
-                        }
+                    for (int p = 0; p < 2; ++p) {
+                        mn[b][p] = row_max(mn[b][p]);
+                        moved = moved || mn[b][p] != m[b][p];
                     }
-                }
-            } else {
                 moved = __any_sync(~0u, moved);
                 if (moved) {
 #pragma unroll
@@ -983,6 +976,9 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             // sequences; the output, bf16 too, is off by 2.1e-3 as it is, 1.7e-3 by its own rounding.)
 #pragma unroll
             for (int b = 0; b < NQ; ++b) {
+                auto less = [](const float (&x)[2]) {     // two rows' references, to be added
+                    return f2(x[0] == -INFINITY ? 0.f : -x[0], x[1] == -INFINITY ? 0.f : -x[1]);
+                };
                 const F2 q = f2(qs[b][0], qs[b][1]), z = less(m[b]);
                 F2 zk;
                 if constexpr (F8) zk = less(k[b]);
@@ -1132,9 +1128,9 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
 #pragma unroll
                 for (int q = 4; q < 32; q <<= 1) l[b][p] += __shfl_xor_sync(~0u, l[b][p], q);
                 if (g == 0) {
-                    top_of[warp][r] = m[b][p] == -INFINITY ? m[b][p]
-                                      : F8                 ? fmaf(m[b][p], qs[b][p], k[b][p])
-                                                           : m[b][p] * qs[b][p];
+                    top_of[warp][r] = (F8 ? k[b][p] : m[b][p]) == -INFINITY ? -INFINITY
+                                      : F8 ? fmaf(m[b][p], qs[b][p], k[b][p])
+                                           : m[b][p] * qs[b][p];
                     sum_of[warp][r] = l[b][p];
                 }
                 if constexpr (F8) {      // places (D / 8) g + 2 j + i
