@@ -411,10 +411,10 @@ __device__ __forceinline__ void let_next_start() {
 // copies are under way while two tiles are worked on.
 //
 // Measured (GB300, of the rate of a large copy, 6765 GB/s): 64 sequences of 4096, 64
-// query heads over 8 of 128, bf16: 170 us, 93%; the same in fp8 97 us, 85%; one
+// query heads over 8 of 128, bf16: 170 us, 93%; the same in fp8 95 us, 86%; one
 // sequence of 131072, 32 over 8: 86 us, 92%; 96 of 17 to 16384 over fp8: 77 us, 82%.
 // Query rows cost little up to 32 a key/value head in bf16 (177 us) and 16 in fp8
-// (106 us); at 64 in bf16 (265 us) and 32 in fp8 (174 us) the products take longer than
+// (105 us); at 64 in bf16 (265 us) and 32 in fp8 (168 us) the products take longer than
 // the reads.  Pieces of prompts are blocks of 64 rows: 8192 tokens of 32 over 8 heads
 // take 2.1 ms in bf16, 258 TFLOP/s.
 template <int D_, bool F8_, int NQ_, int WR_>
@@ -1574,9 +1574,9 @@ cudaError_t launch_f32(const PagedArgs &a, const Shape &s, cudaStream_t stream) 
 // the rest of the four along the positions).  More rows than 64 are several row
 // blocks, each of which reads the cache.  64 sequences of 4096 over 8 key/value heads of
 // 128, microseconds for bf16 / fp8 with blocks of half the rows, this rule's, twice:
-//   8 rows              -  170 /  97  170 / 101
-//   16 rows     325 / 175  174 / 106  173 / 170
-//   32 rows     330 / 195  177 / 174  252 / 301
+//   8 rows              -  170 /  95  170 /  99
+//   16 rows     327 / 176  174 / 105  171 / 163
+//   32 rows     334 / 191  177 / 168  252 / 290
 Shape make_shape(const PagedArgs &a) {
     Shape s{};
     s.lens = a.lens;
