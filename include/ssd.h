@@ -78,8 +78,10 @@ typedef enum {
  * the conv-state slot indices of ssd_mixer_prologue and the slots, positions,
  * page tables and lengths of the key/value cache; SSD_F8E4M3 (8 bits: sign, 4
  * exponent, 3 mantissa bits, no infinities, largest value 448) only for that
- * cache's pools. */
-typedef enum { SSD_F32 = 0, SSD_BF16 = 1, SSD_I32 = 2, SSD_F8E4M3 = 3 } ssd_dtype;
+ * cache's pools and group scales; SSD_F4E2M1X2 (a byte of two 4-bit codes: sign, 2
+ * exponent, 1 mantissa bit, that is 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives;
+ * shapes and strides count bytes) only for its pools. */
+typedef enum { SSD_F32 = 0, SSD_BF16 = 1, SSD_I32 = 2, SSD_F8E4M3 = 3, SSD_F4E2M1X2 = 4 } ssd_dtype;
 
 typedef struct {
     void *data;          /* device pointer                                   */
@@ -414,7 +416,11 @@ ssd_status ssd_mixer_prologue(const ssd_tensor *xBC, const ssd_tensor *conv_weig
  * halves).  A pool holds the dtype of the layer (bf16 or f32),
  * or SSD_F8E4M3 with one f32 scale for each token and head, [pages, Hkv, ps]
  * (innermost stride 1, the same strides for both): a held element stands for
- * code * scale.  Slot s of a pool is token s % ps of page s / ps; a page
+ * code * scale; or SSD_F4E2M1X2 (the calls that end in _ex), two codes a byte, the
+ * even place in the low bits, so that a pool is [pages, Hkv, ps, D/2], with those
+ * scales and an SSD_F8E4M3 scale for each group of 16 places besides, [pages, Hkv, ps,
+ * D/16] (innermost stride 1, outer strides and base multiples of D/16 bytes, the same
+ * strides for both): an element stands for code * group scale * scale.  Slot s of a pool is token s % ps of page s / ps; a page
  * table [B, M] names the pages of each sequence in order, so that position n
  * of sequence b lies in page table[b, n / ps].  D is 64 or 128; ps any
  * positive size; Hq (query heads) a multiple of Hkv, query head h reads
@@ -451,6 +457,34 @@ ssd_status ssd_kv_append(const ssd_tensor *q, const ssd_tensor *k, const ssd_ten
                          ssd_tensor *k_scale, ssd_tensor *v_scale, ssd_tensor *q_out,
                          void *stream);
 
+/* ssd_kv_append with two more forms.
+ *
+ * Positions of several axes (the time, height and width of a token of a video): with
+ * nsections > 0 positions is [A, T], 2 <= A <= 4, and sections is a HOST array of the
+ * lengths (> 0, their sum R/2) of runs of pairs, which go round the axes: the pairs of
+ * run j (with interleaved != 0 too, pair i is column i of cos and sin) are rotated by
+ * row positions[j % A][t].  A token one of whose A positions lies outside [0, S) is
+ * padding.  (Three sections (n0, n1, n2) give an axis one run; (1, 1, 1, 1, ...) deals
+ * the pairs out in turn.)  With nsections = 0 positions is [T].
+ *
+ * Pools of 4-bit codes: k_group_scale, v_group_scale, with SSD_F4E2M1X2 pools only.  In f32,
+ *   scale = max(amax, 2^-96) / 2688 over the head's row (2688 = 6 * 448),
+ *   group scale = gmax / (6 * scale) over 16 places, rounded to nearest even to e4m3 (at
+ *       most 448),
+ *   code = u / (group scale * scale) rounded to nearest even, saturated at 6; 0 where the
+ *       group scale is 0 (a group 2^-10 times as large as 448 or less)
+ * (each operation rounded on its own; a row that holds an infinity or NaN reads back as
+ * NaN). */
+ssd_status ssd_kv_append_ex(const ssd_tensor *q, const ssd_tensor *k, const ssd_tensor *v,
+                            const ssd_tensor *slots, const ssd_tensor *positions,
+                            const ssd_tensor *cos, const ssd_tensor *sin,
+                            const int32_t *sections, int32_t nsections,
+                            const ssd_tensor *q_weight, const ssd_tensor *k_weight, float eps,
+                            int32_t interleaved, ssd_tensor *k_cache, ssd_tensor *v_cache,
+                            ssd_tensor *k_scale, ssd_tensor *v_scale,
+                            ssd_tensor *k_group_scale, ssd_tensor *v_group_scale,
+                            ssd_tensor *q_out, void *stream);
+
 /* Cached keys and values as contiguous rows: with cu_lens [B + 1] (SSD_I32,
  * not decreasing) row i belongs to the sequence b with cu_lens[b] <= i <
  * cu_lens[b + 1] and is its position starts[b] + i - cu_lens[b] (starts [B]
@@ -462,6 +496,14 @@ ssd_status ssd_kv_read(const ssd_tensor *k_cache, const ssd_tensor *v_cache,
                        const ssd_tensor *k_scale, const ssd_tensor *v_scale,
                        const ssd_tensor *page_table, const ssd_tensor *cu_lens,
                        const ssd_tensor *starts, ssd_tensor *k, ssd_tensor *v, void *stream);
+
+/* ssd_kv_read, pools of 4-bit codes included: rows are (code * group scale) * scale, the
+ * first product exact, the second rounded to f32 and then to k's dtype. */
+ssd_status ssd_kv_read_ex(const ssd_tensor *k_cache, const ssd_tensor *v_cache,
+                          const ssd_tensor *k_scale, const ssd_tensor *v_scale,
+                          const ssd_tensor *k_group_scale, const ssd_tensor *v_group_scale,
+                          const ssd_tensor *page_table, const ssd_tensor *cu_lens,
+                          const ssd_tensor *starts, ssd_tensor *k, ssd_tensor *v, void *stream);
 
 /* Bytes of workspace ssd_paged_attention needs for this problem (written to
  * *bytes): the partial results of sequences that several CTAs share.
@@ -498,6 +540,20 @@ ssd_status ssd_paged_attention(const ssd_tensor *q, const ssd_tensor *k_cache,
                                const ssd_tensor *lens, float scale, int64_t window,
                                ssd_tensor *out, ssd_tensor *lse, void *workspace,
                                size_t workspace_bytes, void *stream);
+
+/* ssd_paged_attention with sinks beside the window, and over pools of 4-bit codes too.  With
+ * window > 0 a row at position e sees j <= e with j > e - window or j < sinks (>= 0): the
+ * first tokens of a sequence stay visible.  Without a window every earlier position is
+ * visible and sinks changes nothing.  Pages between the sinks and the window are not
+ * looked at (their table entries may be -1).  The same workspace. */
+ssd_status ssd_paged_attention_ex(const ssd_tensor *q, const ssd_tensor *k_cache,
+                                  const ssd_tensor *v_cache, const ssd_tensor *k_scale,
+                                  const ssd_tensor *v_scale, const ssd_tensor *k_group_scale,
+                                  const ssd_tensor *v_group_scale,
+                                  const ssd_tensor *page_table, const ssd_tensor *lens,
+                                  float scale, int64_t window, int64_t sinks, ssd_tensor *out,
+                                  ssd_tensor *lse, void *workspace, size_t workspace_bytes,
+                                  void *stream);
 
 /* ---- stage entry points (the four steps of ssd_chunked_fwd, one call each;
  *      same conventions; used to check each step on its own) ---------------- */

@@ -17,16 +17,18 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <optional>
+#include <vector>
 
 #include "ssd.h"
 
 namespace {
 
-decltype(&ssd_kv_append) g_append = nullptr;
-decltype(&ssd_kv_read) g_read = nullptr;
-decltype(&ssd_paged_attention) g_attention = nullptr;
+decltype(&ssd_kv_append_ex) g_append = nullptr;
+decltype(&ssd_kv_read_ex) g_read = nullptr;
+decltype(&ssd_paged_attention_ex) g_attention = nullptr;
 decltype(&ssd_paged_attention_workspace_size) g_ws_size = nullptr;
 
 int code_of(at::ScalarType t) {
@@ -35,13 +37,14 @@ int code_of(at::ScalarType t) {
     case at::kBFloat16: return SSD_BF16;
     case at::kInt: return SSD_I32;
     case at::kFloat8_e4m3fn: return SSD_F8E4M3;
+    case at::kFloat4_e2m1fn_x2: return SSD_F4E2M1X2;
     default: return 99;      // the library names it
     }
 }
 
 // The descriptors of one call and the device that its tensors share.
 struct Call {
-    ssd_tensor room[16];
+    ssd_tensor room[20];
     int n = 0, device = -1;
     bool bad = false;        // a Python exception is set
 
@@ -121,52 +124,76 @@ bool count(Py_ssize_t n, Py_ssize_t want) {
     return n == want;
 }
 
+// A sequence of integers (None: empty), false with an exception set otherwise.
+bool integers(PyObject *o, const char *name, std::vector<int32_t> &out) {
+    if (o == Py_None) return true;
+    PyObject *s = PySequence_Fast(o, name);
+    if (!s) return false;
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(s);
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        const long v = PyLong_AsLong(PySequence_Fast_GET_ITEM(s, i));
+        if (v == -1 && PyErr_Occurred()) break;
+        out.push_back(int32_t(std::max(std::min(v, long(INT32_MAX)), long(INT32_MIN))));
+    }
+    Py_DECREF(s);
+    return !PyErr_Occurred();
+}
+
 // (q, k, v, slots, positions, cos, sin, q_weight, k_weight, eps, interleaved,
-//  k_cache, v_cache, k_scale, v_scale, out) -> out, or a status
+//  k_cache, v_cache, k_scale, v_scale, k_group_scale, v_group_scale, sections, out)
+//  -> out, or a status
 PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
-        if (!count(n, 16)) return nullptr;
+        if (!count(n, 19)) return nullptr;
         const double eps = PyFloat_AsDouble(a[9]);
         const int inter = PyObject_IsTrue(a[10]);
         if (PyErr_Occurred()) return nullptr;
+        std::vector<int32_t> sections;
+        if (!integers(a[17], "sections: a sequence of integers expected", sections)) return nullptr;
+        if (a[17] != Py_None && sections.empty()) {
+            PyErr_SetString(PyExc_ValueError, "sections: empty");
+            return nullptr;
+        }
         const at::Tensor *q = tensor(a[0]);
         if (!q) return nullptr;
         at::Tensor out;
-        if (a[15] == Py_None) {
+        if (a[18] == Py_None) {
             out = make(*q, q->sizes(), q->scalar_type());
         } else {
-            const at::Tensor *o = tensor(a[15]);
+            const at::Tensor *o = tensor(a[18]);
             if (!o) return nullptr;
             out = *o;
         }
         Call c;
-        ssd_tensor *in[9], *pool[4];
+        ssd_tensor *in[9], *pool[6];
         for (int i = 0; i < 9; ++i) in[i] = c.add(a[i]);
-        for (int i = 0; i < 4; ++i) pool[i] = c.add(a[11 + i]);
+        for (int i = 0; i < 6; ++i) pool[i] = c.add(a[11 + i]);
         ssd_tensor *o = c.bad ? nullptr : c.add(out);
         if (c.bad) return nullptr;
         void *stream = c.stream();
         ssd_status st;
         Py_BEGIN_ALLOW_THREADS
-        st = g_append(in[0], in[1], in[2], in[3], in[4], in[5], in[6], in[7], in[8], float(eps),
-                      inter, pool[0], pool[1], pool[2], pool[3], o, stream);
+        st = g_append(in[0], in[1], in[2], in[3], in[4], in[5], in[6], sections.data(),
+                      int32_t(sections.size()), in[7], in[8], float(eps), inter, pool[0], pool[1],
+                      pool[2], pool[3], pool[4], pool[5], o, stream);
         Py_END_ALLOW_THREADS
         return st ? PyLong_FromLong(st) : THPVariable_Wrap(out);
     });
 }
 
-// (k_cache, v_cache, k_scale, v_scale, page_table, cu_lens, starts, tokens, f32 out,
-//  k, v) -> (k, v), or a status.  f32 out: the dtype of rows read from codes.
+// (k_cache, v_cache, k_scale, v_scale, k_group_scale, v_group_scale, page_table, cu_lens,
+//  starts, tokens, f32 out, k, v) -> (k, v), or a status.  f32 out: the dtype of rows read
+//  from codes.
 PyObject *kv_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
-        if (!count(n, 11)) return nullptr;
-        const int64_t tokens = PyLong_AsLongLong(a[7]);
-        const int f32 = PyObject_IsTrue(a[8]);
+        if (!count(n, 13)) return nullptr;
+        const int64_t tokens = PyLong_AsLongLong(a[9]);
+        const int f32 = PyObject_IsTrue(a[10]);
         if (PyErr_Occurred()) return nullptr;
         at::Tensor kv[2];
         for (int i = 0; i < 2; ++i) {
-            if (a[9 + i] != Py_None) {
-                const at::Tensor *t = tensor(a[9 + i]);
+            if (a[11 + i] != Py_None) {
+                const at::Tensor *t = tensor(a[11 + i]);
                 if (!t) return nullptr;
                 kv[i] = *t;
                 continue;
@@ -179,19 +206,21 @@ PyObject *kv_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 return nullptr;
             }
             at::ScalarType dt = pool->scalar_type();
-            if (dt == at::kFloat8_e4m3fn) dt = f32 ? at::kFloat : at::kBFloat16;
-            kv[i] = make(*pool, {tokens, pool->size(1), pool->size(3)}, dt);
+            const int64_t D = pool->size(3) * (dt == at::kFloat4_e2m1fn_x2 ? 2 : 1);
+            if (dt == at::kFloat8_e4m3fn || dt == at::kFloat4_e2m1fn_x2)
+                dt = f32 ? at::kFloat : at::kBFloat16;
+            kv[i] = make(*pool, {tokens, pool->size(1), D}, dt);
         }
         Call c;
-        ssd_tensor *in[7];
-        for (int i = 0; i < 7; ++i) in[i] = c.add(a[i]);
+        ssd_tensor *in[9];
+        for (int i = 0; i < 9; ++i) in[i] = c.add(a[i]);
         ssd_tensor *k = c.bad ? nullptr : c.add(kv[0]);
         ssd_tensor *v = c.bad ? nullptr : c.add(kv[1]);
         if (c.bad) return nullptr;
         void *stream = c.stream();
         ssd_status st;
         Py_BEGIN_ALLOW_THREADS
-        st = g_read(in[0], in[1], in[2], in[3], in[4], in[5], in[6], k, v, stream);
+        st = g_read(in[0], in[1], in[2], in[3], in[4], in[5], in[6], in[7], in[8], k, v, stream);
         Py_END_ALLOW_THREADS
         if (st) return PyLong_FromLong(st);
         PyObject *pk = THPVariable_Wrap(kv[0]), *pv = THPVariable_Wrap(kv[1]);
@@ -202,14 +231,14 @@ PyObject *kv_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// (q, k_cache, v_cache, k_scale, v_scale, page_table, lens, scale or None, window, want lse,
-//  out, workspace) -> out or (out, lse), or a status
+// (q, k_cache, v_cache, k_scale, v_scale, k_group_scale, v_group_scale, page_table, lens,
+//  scale or None, window, sinks, want lse, out, workspace) -> out or (out, lse), or a status
 PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
-        if (!count(n, 12)) return nullptr;
-        const int64_t window = PyLong_AsLongLong(a[8]);
-        const int want_lse = PyObject_IsTrue(a[9]);
-        double scale = a[7] == Py_None ? 0.0 : PyFloat_AsDouble(a[7]);
+        if (!count(n, 15)) return nullptr;
+        const int64_t window = PyLong_AsLongLong(a[10]), sinks = PyLong_AsLongLong(a[11]);
+        const int want_lse = PyObject_IsTrue(a[12]);
+        double scale = a[9] == Py_None ? 0.0 : PyFloat_AsDouble(a[9]);
         if (PyErr_Occurred()) return nullptr;
         const at::Tensor *q = tensor(a[0]), *pool = q ? tensor(a[1]) : nullptr;
         if (!pool) return nullptr;
@@ -219,33 +248,33 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
             return nullptr;
         }
         const int64_t B = q->size(0), T = q->size(1), H = q->size(2), D = q->size(3);
-        if (a[7] == Py_None) scale = 1.0 / std::sqrt(double(D));
+        if (a[9] == Py_None) scale = 1.0 / std::sqrt(double(D));
         Call c;
-        ssd_tensor *in[7];
-        for (int i = 0; i < 7; ++i) in[i] = c.add(a[i]);
+        ssd_tensor *in[9];
+        for (int i = 0; i < 9; ++i) in[i] = c.add(a[i]);
         if (c.bad) return nullptr;
         at::Tensor out, lse;
         c10::DataPtr own;          // a workspace of this call: back to the cache when it returns
         void *room = nullptr;
         size_t bytes = 0;
-        if (a[10] == Py_None) {
+        if (a[13] == Py_None) {
             out = make(*q, {B, T, H, D}, q->scalar_type());
         } else {
-            const at::Tensor *t = tensor(a[10]);
+            const at::Tensor *t = tensor(a[13]);
             if (!t) return nullptr;
             out = *t;
         }
         if (want_lse) lse = make(*q, {B, T, H}, at::kFloat);
         ssd_tensor *o = c.add(out), *l = !c.bad && want_lse ? c.add(lse) : nullptr;
         if (c.bad) return nullptr;
-        if (a[11] == Py_None) {
+        if (a[14] == Py_None) {
             const ssd_status st = g_ws_size(B, T, H, pool->size(1), D, code_of(pool->scalar_type()),
                                             &bytes);
             if (st) return PyLong_FromLong(st);
             if (bytes) own = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
             room = own.get();
         } else {
-            const at::Tensor *t = tensor(a[11]);
+            const at::Tensor *t = tensor(a[14]);
             if (!t) return nullptr;
             if (!t->is_cuda() || t->get_device() != c.device) {
                 PyErr_SetString(PyExc_ValueError, "workspace: not on the device of the tensors");
@@ -261,8 +290,8 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
         void *stream = c.stream();
         ssd_status st;
         Py_BEGIN_ALLOW_THREADS
-        st = g_attention(in[0], in[1], in[2], in[3], in[4], in[5], in[6], float(scale), window, o,
-                         l, room, bytes, stream);
+        st = g_attention(in[0], in[1], in[2], in[3], in[4], in[5], in[6], in[7], in[8], float(scale),
+                         window, sinks, o, l, room, bytes, stream);
         Py_END_ALLOW_THREADS
         if (st) return PyLong_FromLong(st);
         PyObject *po = THPVariable_Wrap(out);
@@ -274,7 +303,7 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// Addresses of ssd_kv_append, ssd_kv_read, ssd_paged_attention and
+// Addresses of ssd_kv_append_ex, ssd_kv_read_ex, ssd_paged_attention_ex and
 // ssd_paged_attention_workspace_size
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!count(n, 4)) return nullptr;

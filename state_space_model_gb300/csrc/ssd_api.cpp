@@ -227,7 +227,7 @@ ssd_status ssd_device_status(void *stream) {
         if (v[0] & 4u) {
             static const char *const files[] = {"?", "ssd_fused.cu", "ssd_pair.cu", "ssd_tc.cu",
                                                 "ssd_simt.cu", "ssd_selftest.cu", "ssd_tc_f32.cu",
-                                                "ssd_kv.cu", "ssd_attn.cu"};
+                                                "ssd_kv.cuh", "ssd_attn.cuh"};
             const unsigned f = v[1] >> 16;
             return fail(SSD_ERR_DEVICE_BOUNDS,
                         "a device bounds check failed (flags 0x%x), first at %s line %u; the "

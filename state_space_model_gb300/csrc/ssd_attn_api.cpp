@@ -5,6 +5,7 @@
 #include "ssd_attn.h"
 #include "ssd_checks.h"
 
+#include <algorithm>
 #include <cmath>
 
 namespace {
@@ -32,12 +33,53 @@ bool same_strides(const ssd_tensor *a, const ssd_tensor *b) {
     return true;
 }
 
+bool are_codes(int dt) { return dt == SSD_F8E4M3 || dt == SSD_F4E2M1X2; }
+
+// The pools of a call with their scales.
+struct Pools {
+    const ssd_tensor *k, *v, *ks, *vs, *kg, *vg;
+};
+
+// The scales of the groups [pages, Hkv, ps, D/16]; fills p.
+ssd_status check_groups(const Pools &t, bool out, ssd::KvPools *p) {
+    if (!t.kg || !t.vg)
+        return fail(SSD_ERR_INVALID_ARG, "f4e2m1x2 pools need k_group_scale and v_group_scale");
+    const int64_t n = p->D / ssd::kGroup, shape[4] = {p->pages, p->Hkv, p->ps, n};
+    ssd_status st;
+    for (int i = 0; i < 2; ++i) {
+        const ssd_tensor *g = i ? t.vg : t.kg;
+        const char *name = i ? "v_group_scale" : "k_group_scale";
+        if ((st = check_tensor(g, name, 4, shape, SSD_F8E4M3, false, false))) return st;
+        // a token's scales of a head are copied at once
+        if (reinterpret_cast<uintptr_t>(g->data) % n)
+            return fail(SSD_ERR_ALIGNMENT, "%s: base pointer %p not %lld-byte aligned", name, g->data,
+                        (long long)n);
+        for (int d = 0; d < 3; ++d)
+            if (shape[d] > 1 && g->stride[d] % n)
+                return fail(SSD_ERR_ALIGNMENT, "%s: stride[%d] = %lld is not a multiple of %lld "
+                            "bytes", name, d, (long long)g->stride[d], (long long)n);
+        if (out && (st = check_distinct(g, name))) return st;
+    }
+    if (!same_strides(t.kg, t.vg))
+        return fail(SSD_ERR_INVALID_ARG, "k_group_scale and v_group_scale must have the same strides");
+    p->kg = static_cast<uint8_t *>(t.kg->data);
+    p->vg = static_cast<uint8_t *>(t.vg->data);
+    p->sgp = t.kg->stride[0];
+    p->sgh = t.kg->stride[1];
+    p->sgt = t.kg->stride[2];
+    p->ng = extent(t.kg);
+    return SSD_OK;
+}
+
 // The pools and their scales; fills p.  out: they are written.
-ssd_status check_pools(const ssd_tensor *k, const ssd_tensor *v, const ssd_tensor *ks,
-                       const ssd_tensor *vs, bool out, ssd::KvPools *p) {
+ssd_status check_pools(const Pools &t, bool out, ssd::KvPools *p) {
+    const ssd_tensor *const k = t.k, *const v = t.v, *const ks = t.ks, *const vs = t.vs;
     if (!k || !v) return fail(SSD_ERR_INVALID_ARG, "k_cache / v_cache: null tensor descriptor");
     if (k->ndim != 4) return fail(SSD_ERR_INVALID_ARG, "k_cache: ndim %d, expected 4", k->ndim);
-    const int64_t pages = k->shape[0], Hkv = k->shape[1], ps = k->shape[2], D = k->shape[3];
+    const int dt = k->dtype;
+    const bool four = dt == SSD_F4E2M1X2;
+    const int64_t pages = k->shape[0], Hkv = k->shape[1], ps = k->shape[2];
+    const int64_t D = k->shape[3] * (four ? 2 : 1);
     if (pages < 0 || Hkv <= 0 || ps <= 0)
         return fail(SSD_ERR_INVALID_ARG, "k_cache: %lld pages of %lld tokens, %lld heads",
                     (long long)pages, (long long)ps, (long long)Hkv);
@@ -48,24 +90,26 @@ ssd_status check_pools(const ssd_tensor *k, const ssd_tensor *v, const ssd_tenso
     if (pages > kMaxInt || ps > kMaxInt || pages * ps > kMaxInt)
         return fail(SSD_ERR_UNSUPPORTED, "%lld pages of %lld tokens: more than 2^31 - 1 slots",
                     (long long)pages, (long long)ps);
-    const int dt = k->dtype;
     if (dt == SSD_I32) return fail(SSD_ERR_INVALID_ARG, "k_cache: dtype i32");
-    const int64_t shape[4] = {pages, Hkv, ps, D}, sscale[3] = {pages, Hkv, ps};
+    const int64_t shape[4] = {pages, Hkv, ps, k->shape[3]}, sscale[3] = {pages, Hkv, ps};
     ssd_status st;
     if ((st = check_tensor(k, "k_cache", 4, shape, dt, false, true))) return st;
     if ((st = check_tensor(v, "v_cache", 4, shape, dt, false, true))) return st;
     if (!same_strides(k, v))
         return fail(SSD_ERR_INVALID_ARG, "k_cache and v_cache must have the same strides");
-    if (dt == SSD_F8E4M3) {
+    if (are_codes(dt)) {
         if (!ks || !vs)
-            return fail(SSD_ERR_INVALID_ARG, "f8e4m3 pools need k_scale and v_scale");
+            return fail(SSD_ERR_INVALID_ARG, "%s pools need k_scale and v_scale",
+                        four ? "f4e2m1x2" : "f8e4m3");
         if ((st = check_tensor(ks, "k_scale", 3, sscale, SSD_F32, false, false))) return st;
         if ((st = check_tensor(vs, "v_scale", 3, sscale, SSD_F32, false, false))) return st;
         if (!same_strides(ks, vs))
             return fail(SSD_ERR_INVALID_ARG, "k_scale and v_scale must have the same strides");
     } else if (ks || vs) {
-        return fail(SSD_ERR_INVALID_ARG, "k_scale / v_scale: only with f8e4m3 pools");
+        return fail(SSD_ERR_INVALID_ARG, "k_scale / v_scale: only with f8e4m3 or f4e2m1x2 pools");
     }
+    if (!four && (t.kg || t.vg))
+        return fail(SSD_ERR_INVALID_ARG, "k_group_scale / v_group_scale: only with f4e2m1x2 pools");
     if (out) {
         if ((st = check_distinct(k, "k_cache")) || (st = check_distinct(v, "v_cache"))) return st;
         if (ks && ((st = check_distinct(ks, "k_scale")) || (st = check_distinct(vs, "v_scale"))))
@@ -89,7 +133,7 @@ ssd_status check_pools(const ssd_tensor *k, const ssd_tensor *v, const ssd_tenso
         p->ssh = ks->stride[1];
         p->ns = extent(ks);
     }
-    return SSD_OK;
+    return four ? check_groups(t, out, p) : SSD_OK;
 }
 
 // A page table [B, M]: innermost stride 1.
@@ -111,8 +155,8 @@ struct Named {
 };
 // No output may share an element with an input or another output.
 ssd_status check_aliasing(std::initializer_list<Named> outs, std::initializer_list<Named> ins) {
-    const Named *all[16];
-    Range at[16];
+    const Named *all[20];
+    Range at[20];
     int n = 0;
     for (const Named &o : outs) all[n++] = &o;
     for (const Named &i : ins) all[n++] = &i;
@@ -138,9 +182,25 @@ ssd_status ssd_kv_append(const ssd_tensor *q, const ssd_tensor *k, const ssd_ten
                          int32_t interleaved, ssd_tensor *k_cache, ssd_tensor *v_cache,
                          ssd_tensor *k_scale, ssd_tensor *v_scale, ssd_tensor *q_out,
                          void *stream) {
+    return ssd_kv_append_ex(q, k, v, slots, positions, cos, sin, nullptr, 0, q_weight, k_weight,
+                            eps, interleaved, k_cache, v_cache, k_scale, v_scale, nullptr, nullptr,
+                            q_out, stream);
+}
+
+ssd_status ssd_kv_append_ex(const ssd_tensor *q, const ssd_tensor *k, const ssd_tensor *v,
+                            const ssd_tensor *slots, const ssd_tensor *positions,
+                            const ssd_tensor *cos, const ssd_tensor *sin,
+                            const int32_t *sections, int32_t nsections,
+                            const ssd_tensor *q_weight, const ssd_tensor *k_weight, float eps,
+                            int32_t interleaved, ssd_tensor *k_cache, ssd_tensor *v_cache,
+                            ssd_tensor *k_scale, ssd_tensor *v_scale,
+                            ssd_tensor *k_group_scale, ssd_tensor *v_group_scale,
+                            ssd_tensor *q_out, void *stream) {
     ssd::KvAppendArgs a;
     ssd_status st;
-    if ((st = check_pools(k_cache, v_cache, k_scale, v_scale, true, &a.c))) return st;
+    if ((st = check_pools({k_cache, v_cache, k_scale, v_scale, k_group_scale, v_group_scale}, true,
+                          &a.c)))
+        return st;
     if (!q) return fail(SSD_ERR_INVALID_ARG, "q: null tensor descriptor");
     if (q->ndim != 3) return fail(SSD_ERR_INVALID_ARG, "q: ndim %d, expected 3", q->ndim);
     const int64_t T = q->shape[0], Hq = q->shape[1], Hkv = a.c.Hkv, D = a.c.D;
@@ -158,11 +218,16 @@ ssd_status ssd_kv_append(const ssd_tensor *q, const ssd_tensor *k, const ssd_ten
     const int xdt = q->dtype;
     if ((st = check_tensor(k, "k", 3, skv, xdt, false, true))) return st;
     if ((st = check_tensor(v, "v", 3, skv, xdt, false, true))) return st;
-    if (a.c.dt != SSD_F8E4M3 && a.c.dt != xdt)
-        return fail(SSD_ERR_INVALID_ARG, "k_cache: the pools hold the dtype of q or f8e4m3 codes");
+    if (!are_codes(a.c.dt) && a.c.dt != xdt)
+        return fail(SSD_ERR_INVALID_ARG, "k_cache: the pools hold the dtype of q or f8e4m3 or "
+                    "f4e2m1x2 codes");
     if ((st = check_tensor(slots, "slots", 1, st1, SSD_I32, true, false))) return st;
     if (!cos != !sin || !cos != !positions)
         return fail(SSD_ERR_INVALID_ARG, "positions, cos and sin come together");
+    if (nsections < 0 || (nsections > 0 && !sections))
+        return fail(SSD_ERR_INVALID_ARG, "sections: %d of them at %p", int(nsections),
+                    static_cast<const void *>(sections));
+    if (nsections && !cos) return fail(SSD_ERR_INVALID_ARG, "sections without positions");
     if (cos) {
         if (cos->ndim != 2) return fail(SSD_ERR_INVALID_ARG, "cos: ndim %d, expected 2", cos->ndim);
         const int64_t S = cos->shape[0], R = 2 * cos->shape[1], scs[2] = {S, R / 2};
@@ -172,7 +237,30 @@ ssd_status ssd_kv_append(const ssd_tensor *q, const ssd_tensor *k, const ssd_ten
                         (long long)R, (long long)D);
         if ((st = check_tensor(cos, "cos", 2, scs, SSD_F32, false, true))) return st;
         if ((st = check_tensor(sin, "sin", 2, scs, SSD_F32, false, true))) return st;
-        if ((st = check_tensor(positions, "positions", 1, st1, SSD_I32, true, false))) return st;
+        if (!nsections) {
+            if ((st = check_tensor(positions, "positions", 1, st1, SSD_I32, true, false))) return st;
+        } else {
+            if (positions->ndim != 2)
+                return fail(SSD_ERR_INVALID_ARG, "positions: ndim %d, expected 2 (axes, tokens) with "
+                            "sections", positions->ndim);
+            const int64_t axes = positions->shape[0], sp[2] = {axes, T};
+            if (axes < 2 || axes > ssd::kMaxAxes)
+                return fail(SSD_ERR_UNSUPPORTED, "positions of %lld axes: 2 to %d are supported",
+                            (long long)axes, ssd::kMaxAxes);
+            if ((st = check_tensor(positions, "positions", 2, sp, SSD_I32, true, false))) return st;
+            int64_t at = 0;
+            for (int32_t j = 0; j < nsections; ++j) {
+                if (sections[j] <= 0 || sections[j] > R / 2 - at)
+                    return fail(SSD_ERR_INVALID_ARG, "sections[%d] = %d after %lld of %lld pairs",
+                                int(j), int(sections[j]), (long long)at, (long long)(R / 2));
+                for (int32_t i = 0; i < sections[j]; ++i, ++at)
+                    a.axis_of[at / 16] |= uint32_t(j % axes) << (2 * (at % 16));
+            }
+            if (at != R / 2)
+                return fail(SSD_ERR_INVALID_ARG, "sections: %lld pairs, cos and sin have %lld",
+                            (long long)at, (long long)(R / 2));
+            a.axes = int(axes);
+        }
         a.R = int(R);
         a.S = S;
         a.cos = static_cast<const float *>(cos->data);
@@ -192,7 +280,8 @@ ssd_status ssd_kv_append(const ssd_tensor *q, const ssd_tensor *k, const ssd_ten
     if ((st = check_tensor(q_out, "q_out", 3, sq, xdt, false, true))) return st;
     if ((st = check_distinct(q_out, "q_out"))) return st;
     if ((st = check_aliasing({{k_cache, "k_cache"}, {v_cache, "v_cache"}, {k_scale, "k_scale"},
-                              {v_scale, "v_scale"}, {q_out, "q_out"}},
+                              {v_scale, "v_scale"}, {k_group_scale, "k_group_scale"},
+                              {v_group_scale, "v_group_scale"}, {q_out, "q_out"}},
                              {{q, "q"}, {k, "k"}, {v, "v"}, {slots, "slots"},
                               {positions, "positions"}, {cos, "cos"}, {sin, "sin"},
                               {q_weight, "q_weight"}, {k_weight, "k_weight"}})))
@@ -204,7 +293,8 @@ ssd_status ssd_kv_append(const ssd_tensor *q, const ssd_tensor *k, const ssd_ten
                                  {dp(q_weight), "q_weight"}, {dp(k_weight), "k_weight"},
                                  {dp(k_cache), "k_cache"}, {dp(v_cache), "v_cache"},
                                  {dp(k_scale), "k_scale"}, {dp(v_scale), "v_scale"},
-                                 {dp(q_out), "q_out"}})))
+                                 {dp(k_group_scale), "k_group_scale"},
+                                 {dp(v_group_scale), "v_group_scale"}, {dp(q_out), "q_out"}})))
         return st;
     a.xdt = xdt;
     a.T = T;
@@ -240,9 +330,20 @@ ssd_status ssd_kv_read(const ssd_tensor *k_cache, const ssd_tensor *v_cache,
                        const ssd_tensor *k_scale, const ssd_tensor *v_scale,
                        const ssd_tensor *page_table, const ssd_tensor *cu_lens,
                        const ssd_tensor *starts, ssd_tensor *k, ssd_tensor *v, void *stream) {
+    return ssd_kv_read_ex(k_cache, v_cache, k_scale, v_scale, nullptr, nullptr, page_table, cu_lens,
+                          starts, k, v, stream);
+}
+
+ssd_status ssd_kv_read_ex(const ssd_tensor *k_cache, const ssd_tensor *v_cache,
+                          const ssd_tensor *k_scale, const ssd_tensor *v_scale,
+                          const ssd_tensor *k_group_scale, const ssd_tensor *v_group_scale,
+                          const ssd_tensor *page_table, const ssd_tensor *cu_lens,
+                          const ssd_tensor *starts, ssd_tensor *k, ssd_tensor *v, void *stream) {
     ssd::KvReadArgs a;
     ssd_status st;
-    if ((st = check_pools(k_cache, v_cache, k_scale, v_scale, false, &a.c))) return st;
+    if ((st = check_pools({k_cache, v_cache, k_scale, v_scale, k_group_scale, v_group_scale}, false,
+                          &a.c)))
+        return st;
     if (!page_table || !k) return fail(SSD_ERR_INVALID_ARG, "page_table / k: null tensor descriptor");
     const int64_t B = page_table->ndim > 0 ? page_table->shape[0] : 0;
     if ((st = check_table(page_table, B, a.c.ps))) return st;
@@ -253,18 +354,21 @@ ssd_status ssd_kv_read(const ssd_tensor *k_cache, const ssd_tensor *v_cache,
     if (T > kMaxInt) return fail(SSD_ERR_UNSUPPORTED, "%lld tokens above 2^31 - 1", (long long)T);
     if ((st = check_tensor(cu_lens, "cu_lens", 1, scu, SSD_I32, true, false))) return st;
     if (starts && (st = check_tensor(starts, "starts", 1, sb, SSD_I32, true, false))) return st;
-    if ((st = check_tensor(k, "k", 3, skv, a.c.dt == SSD_F8E4M3 ? -1 : a.c.dt, false, true)))
+    if ((st = check_tensor(k, "k", 3, skv, are_codes(a.c.dt) ? -1 : a.c.dt, false, true)))
         return st;
     if ((st = check_tensor(v, "v", 3, skv, k->dtype, false, true))) return st;
     if ((st = check_distinct(k, "k")) || (st = check_distinct(v, "v"))) return st;
     if ((st = check_aliasing({{k, "k"}, {v, "v"}},
                              {{k_cache, "k_cache"}, {v_cache, "v_cache"}, {k_scale, "k_scale"},
-                              {v_scale, "v_scale"}, {page_table, "page_table"},
+                              {v_scale, "v_scale"}, {k_group_scale, "k_group_scale"},
+                              {v_group_scale, "v_group_scale"}, {page_table, "page_table"},
                               {cu_lens, "cu_lens"}, {starts, "starts"}})))
         return st;
     if (T == 0) return ok();
     if ((st = check_device_ptrs({{dp(k_cache), "k_cache"}, {dp(v_cache), "v_cache"},
                                  {dp(k_scale), "k_scale"}, {dp(v_scale), "v_scale"},
+                                 {dp(k_group_scale), "k_group_scale"},
+                                 {dp(v_group_scale), "v_group_scale"},
                                  {dp(page_table), "page_table"}, {dp(cu_lens), "cu_lens"},
                                  {dp(starts), "starts"}, {dp(k), "k"}, {dp(v), "v"}})))
         return st;
@@ -300,8 +404,9 @@ static ssd_status check_paged(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int
                     "heads", (long long)Hq, (long long)Hkv);
     if (D != 64 && D != 128)
         return fail(SSD_ERR_UNSUPPORTED, "headdim %lld unsupported (64 or 128)", (long long)D);
-    if (dt != SSD_F32 && dt != SSD_BF16 && dt != SSD_F8E4M3)
-        return fail(SSD_ERR_INVALID_ARG, "cache dtype code %d: f32, bf16 or f8e4m3 expected", dt);
+    if (dt != SSD_F32 && dt != SSD_BF16 && !are_codes(dt))
+        return fail(SSD_ERR_INVALID_ARG, "cache dtype code %d: f32, bf16, f8e4m3 or f4e2m1x2 "
+                    "expected", dt);
     if (B > 65535 || Hq > 65535 || T > 65535)
         return fail(SSD_ERR_UNSUPPORTED, "batch %lld, %lld tokens or %lld query heads above 65535",
                     (long long)B, (long long)T, (long long)Hq);
@@ -335,9 +440,24 @@ ssd_status ssd_paged_attention(const ssd_tensor *q, const ssd_tensor *k_cache,
                                const ssd_tensor *lens, float scale, int64_t window,
                                ssd_tensor *out, ssd_tensor *lse, void *workspace,
                                size_t workspace_bytes, void *stream) {
+    return ssd_paged_attention_ex(q, k_cache, v_cache, k_scale, v_scale, nullptr, nullptr, page_table,
+                                  lens, scale, window, 0, out, lse, workspace, workspace_bytes,
+                                  stream);
+}
+
+ssd_status ssd_paged_attention_ex(const ssd_tensor *q, const ssd_tensor *k_cache,
+                                  const ssd_tensor *v_cache, const ssd_tensor *k_scale,
+                                  const ssd_tensor *v_scale, const ssd_tensor *k_group_scale,
+                                  const ssd_tensor *v_group_scale,
+                                  const ssd_tensor *page_table, const ssd_tensor *lens,
+                                  float scale, int64_t window, int64_t sinks, ssd_tensor *out,
+                                  ssd_tensor *lse, void *workspace, size_t workspace_bytes,
+                                  void *stream) {
     ssd::PagedArgs a;
     ssd_status st;
-    if ((st = check_pools(k_cache, v_cache, k_scale, v_scale, false, &a.c))) return st;
+    if ((st = check_pools({k_cache, v_cache, k_scale, v_scale, k_group_scale, v_group_scale}, false,
+                          &a.c)))
+        return st;
     if (!q) return fail(SSD_ERR_INVALID_ARG, "q: null tensor descriptor");
     if (q->ndim != 4) return fail(SSD_ERR_INVALID_ARG, "q: ndim %d, expected 4", q->ndim);
     const int64_t B = q->shape[0], T = q->shape[1], Hq = q->shape[2], D = a.c.D;
@@ -349,12 +469,14 @@ ssd_status ssd_paged_attention(const ssd_tensor *q, const ssd_tensor *k_cache,
     if ((st = check_tensor(lens, "lens", 1, sb, SSD_I32, true, false))) return st;
     if (!std::isfinite(scale)) return fail(SSD_ERR_INVALID_ARG, "scale %g is not finite", double(scale));
     if (window < 0) return fail(SSD_ERR_INVALID_ARG, "window %lld is negative", (long long)window);
+    if (sinks < 0) return fail(SSD_ERR_INVALID_ARG, "sinks %lld is negative", (long long)sinks);
     if ((st = check_tensor(out, "out", 4, sq, xdt, false, true))) return st;
     if ((st = check_distinct(out, "out"))) return st;
     if (lse && (st = check_tensor(lse, "lse", 3, slse, SSD_F32, true, false))) return st;
     if ((st = check_aliasing({{out, "out"}, {lse, "lse"}},
                              {{q, "q"}, {k_cache, "k_cache"}, {v_cache, "v_cache"},
                               {k_scale, "k_scale"}, {v_scale, "v_scale"},
+                              {k_group_scale, "k_group_scale"}, {v_group_scale, "v_group_scale"},
                               {page_table, "page_table"}, {lens, "lens"}})))
         return st;
     a.B = int(B);
@@ -371,6 +493,7 @@ ssd_status ssd_paged_attention(const ssd_tensor *q, const ssd_tensor *k_cache,
         const Range rw = range_raw(workspace, need);
         const Named others[] = {{q, "q"}, {k_cache, "k_cache"}, {v_cache, "v_cache"},
                                 {k_scale, "k_scale"}, {v_scale, "v_scale"},
+                                {k_group_scale, "k_group_scale"}, {v_group_scale, "v_group_scale"},
                                 {page_table, "page_table"}, {lens, "lens"}, {out, "out"},
                                 {lse, "lse"}};
         for (const Named &o : others)
@@ -379,12 +502,15 @@ ssd_status ssd_paged_attention(const ssd_tensor *q, const ssd_tensor *k_cache,
     }
     if ((st = check_device_ptrs({{dp(q), "q"}, {dp(k_cache), "k_cache"}, {dp(v_cache), "v_cache"},
                                  {dp(k_scale), "k_scale"}, {dp(v_scale), "v_scale"},
+                                 {dp(k_group_scale), "k_group_scale"},
+                                 {dp(v_group_scale), "v_group_scale"},
                                  {dp(page_table), "page_table"}, {dp(lens), "lens"},
                                  {dp(out), "out"}, {dp(lse), "lse"},
                                  {need ? workspace : nullptr, "workspace"}})))
         return st;
     a.scale = scale;
     a.window = window > kMaxPos ? 0 : window;   // such a window hides nothing
+    a.sinks = a.window ? std::min(sinks, kMaxPos) : 0;
     a.q = q->data;
     a.q_sb = q->stride[0];
     a.q_st = q->stride[1];

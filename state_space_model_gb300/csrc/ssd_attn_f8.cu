@@ -1,0 +1,10 @@
+// Attention over the paged cache (ssd_attn.cuh): pools of 8-bit codes.
+#include "ssd_attn.cuh"
+
+namespace ssd {
+
+cudaError_t launch_paged_f8(const PagedArgs &a, cudaStream_t s) {
+    return a.c.D == 64 ? launch_rows<64, kEight>(a, s) : launch_rows<128, kEight>(a, s);
+}
+
+}  // namespace ssd

@@ -31,7 +31,7 @@ ssd_status ok() {
     return SSD_OK;
 }
 
-size_t elem_size(int dt) { return dt == SSD_BF16 ? 2 : dt == SSD_F8E4M3 ? 1 : 4; }
+size_t elem_size(int dt) { return dt == SSD_BF16 ? 2 : dt == SSD_F8E4M3 || dt == SSD_F4E2M1X2 ? 1 : 4; }
 
 Range range_of(const ssd_tensor *t) {
     Range r;
@@ -87,9 +87,10 @@ ssd_status check_tensor(const ssd_tensor *t, const char *name, int ndim,
     if (t->ndim != ndim)
         return fail(SSD_ERR_INVALID_ARG, "%s: ndim %d, expected %d", name, t->ndim, ndim);
     auto dname = [](int d) {
-        return d == SSD_F32 ? "f32" : d == SSD_BF16 ? "bf16" : d == SSD_I32 ? "i32" : "f8e4m3";
+        return d == SSD_F32 ? "f32" : d == SSD_BF16 ? "bf16" : d == SSD_I32 ? "i32"
+               : d == SSD_F8E4M3 ? "f8e4m3" : "f4e2m1x2";
     };
-    if (t->dtype < SSD_F32 || t->dtype > SSD_F8E4M3)
+    if (t->dtype < SSD_F32 || t->dtype > SSD_F4E2M1X2)
         return fail(SSD_ERR_INVALID_ARG, "%s: unknown dtype code %d", name, t->dtype);
     if ((dtype >= 0 && t->dtype != dtype) || (dtype < 0 && t->dtype != SSD_F32 && t->dtype != SSD_BF16))
         return fail(SSD_ERR_INVALID_ARG, "%s: dtype %s, expected %s", name, dname(t->dtype),
