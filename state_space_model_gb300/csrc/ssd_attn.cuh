@@ -1,6 +1,8 @@
 // Attention of new tokens over the paged key/value cache (ssd_paged_attention): the kernels and
 // their launch rules.  ssd_attn.cu, ssd_attn_f8.cu and ssd_attn_f4.cu compile them for the
-// pools' types.
+// pools' types, ssd_attn_sinks*.cu the same with sinks beside the window (SSD_ATTN_SINKS; as a
+// choice at run time they cost the calls without 4% at 16 sequences of four tokens under a
+// window, and 1.5% in fp32).
 //
 //   out = softmax(scale q K^T over the positions a row sees) V
 //
@@ -43,6 +45,11 @@
 namespace ssd {
 namespace {
 
+#ifdef SSD_ATTN_SINKS
+constexpr bool kSinks = true;
+#else
+constexpr bool kSinks = false;
+#endif
 constexpr float kLn2 = 0.6931471805599453f;
 // 8-bit values: a row's largest weight is 2^kLift to 2^(kLift + kAhead) in fp16 (so weights
 // keep their 11 bits down to 2^-22 of it), with log2 of a value's scale taken as [kLeastLog,
@@ -117,22 +124,27 @@ __device__ __forceinline__ void item_range(const Shape &s, Item &it) {
     it.hi = min(it.emax + 1, s.cap);
     it.lo = s.window > 0 ? min(max(0, it.emin + 1 - s.window), s.cap) : 0;
     it.first = it.lo / KS * KS;
-    it.nsink = s.sinks > 0 ? min((s.sinks - 1) / KS + 1, it.first / KS) : 0;
-    it.ntiles = max(1, it.nsink + max(0, it.hi - it.first + KS - 1) / KS);
+    if constexpr (kSinks) {
+        it.nsink = s.sinks > 0 ? min((s.sinks - 1) / KS + 1, it.first / KS) : 0;
+        it.ntiles = max(1, it.nsink + max(0, it.hi - it.first + KS - 1) / KS);
+    } else {
+        it.ntiles = max(1, (it.hi - it.first + KS - 1) / KS);
+    }
 }
 
 // The first position of tile t of an item.
 template <int KS>
 __device__ __forceinline__ int tile_at(const Item &it, int t) {
+    if constexpr (!kSinks) return it.first + t * KS;
     return t < it.nsink ? t * KS : it.first + (t - it.nsink) * KS;
 }
 // Whether some row of the item's block may see position pos.
 __device__ __forceinline__ bool in_range(const Shape &s, const Item &it, int pos) {
-    return pos < it.hi && (pos >= it.lo || pos < s.sinks);
+    return pos < it.hi && (pos >= it.lo || (kSinks && pos < s.sinks));
 }
 // Whether the row at place `own` sees position pos.
 __device__ __forceinline__ bool sees(const Shape &s, int own, int pos) {
-    return pos <= own && (s.window == 0 || pos > own - s.window || pos < s.sinks);
+    return pos <= own && (s.window == 0 || pos > own - s.window || (kSinks && pos < s.sinks));
 }
 
 // The cost of one key/value head of a sequence.
@@ -929,7 +941,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             const bool partial = __any_sync(~0u, it.emin != it.emax &&
                                                      (k0 + KP - 1 > it.emin ||
                                                       (s.window > 0 && k0 <= it.emax - s.window &&
-                                                       k0 + KP > s.sinks)));
+                                                       (!kSinks || k0 + KP > s.sinks))));
             const bool all = __all_sync(~0u, !partial && mask == 0xffffffffu >> (32 - KP));
             const uint32_t ksm = room.keys(st) + x0 * ROW, vsm = room.values(st) + x0 * ROW;
             const float *ksc = room.scales(st) + x0, *vsc = ksc + KS;
@@ -1758,6 +1770,14 @@ inline Shape make_shape(const PagedArgs &a) {
     s.nrb = int((rows + s.RB - 1) / s.RB);
     s.ncta = device_sm_count() * kCtasPerSm;
     return s;
+}
+
+template <int D>
+cudaError_t launch_f32_rows(const PagedArgs &a, cudaStream_t stream) {
+    const Shape s = make_shape(a);
+    if (s.RB == 1) return launch_f32<D, 1>(a, s, stream);
+    if (s.RB == 2) return launch_f32<D, 2>(a, s, stream);
+    return launch_f32<D, 4>(a, s, stream);
 }
 
 template <int D, int FMT>

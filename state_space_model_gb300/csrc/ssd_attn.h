@@ -85,7 +85,13 @@ struct PagedArgs {
 // Workspace for this problem (c.dt, c.Hkv, c.D, B, T, Hq set).
 size_t paged_workspace(const PagedArgs &a);
 cudaError_t launch_paged(const PagedArgs &a, cudaStream_t s);
-cudaError_t launch_paged_f8(const PagedArgs &a, cudaStream_t s);   // its pools of codes
+// its parts: many rows, pools of codes, calls with sinks
+bool prompt_fits(const PagedArgs &a);
+cudaError_t launch_paged_prompt(const PagedArgs &a, cudaStream_t s);
+cudaError_t launch_paged_f8(const PagedArgs &a, cudaStream_t s);
 cudaError_t launch_paged_f4(const PagedArgs &a, cudaStream_t s);
+cudaError_t launch_paged_sinks(const PagedArgs &a, cudaStream_t s);
+cudaError_t launch_paged_sinks_f8(const PagedArgs &a, cudaStream_t s);
+cudaError_t launch_paged_sinks_f4(const PagedArgs &a, cudaStream_t s);
 
 }  // namespace ssd

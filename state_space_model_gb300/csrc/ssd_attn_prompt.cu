@@ -1,0 +1,689 @@
+// Attention of many new tokens over the paged cache (pieces of prompts, bf16 pools): the same
+// sum as in ssd_attn.cuh, on the tensor cores' own path.
+//
+// Rows (the T G queries of a sequence and key/value head, in order of their tokens) stand in the
+// 128 lanes of tensor memory, two blocks of 128 to a CTA, which share every tile of 128 cached
+// positions:
+//
+//   S = Q K^T       tcgen05, both operands in shared memory, S in tensor memory (fp32)
+//   P = 2^(..)      a thread a row: its scores to registers, the running maximum and sum, P (bf16)
+//                   back over S
+//   O += P V        tcgen05, P from tensor memory, O in tensor memory (fp32)
+//
+// What bounds it is the products, 4 D flops a row and position: with 256 rows to a tile the
+// reads from L2 are 64 KB for 2 x 4.2 Mflop of them each.  So one thread issues nothing but
+// products, in the order S0, S1, then for every tile O0, S0 (next), O1, S1 (next): while a
+// block's exponentials run, the tensor core has the other's products.  Three warps copy, tiles
+// ahead and across items, and the CTA goes from item to item (sequence, head, 256 rows) with
+// the next one's queries and keys already there.
+//
+// The positions that some row of an item sees, sinks first and then the window's, are counted
+// through as one run, so that a tile holds what is needed and nothing else, whatever the page
+// size and wherever the window begins.
+#include "ptx_sm100.cuh"
+#include "ssd_attn.h"
+#include "ssd_block_math.cuh"
+#include "ssd_debug.cuh"
+#include "ssd_f32x2.cuh"
+#include "ssd_tc.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#define SSD_DBG_FILE 9u   // kDbgPrompt
+
+namespace ssd {
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kRows = 128, kItemRows = 2 * kRows;   // rows of a block, of an item
+constexpr int kTile = 128;                          // positions of a tile
+constexpr int kCopyWarps = 3;
+constexpr int kThreads = 2 * kRows + 32 + 32 * kCopyWarps;
+// Registers of a thread: 168 at the launch (65536 / 384), shared out as 208 for the rows'
+// threads and 88 for the others: 256 x 208 + 128 x 88 = 384 x 168.
+constexpr int kRowRegs = 208, kOtherRegs = 88;
+// The maximum in use follows the true one when that is ahead by so much (log2 units): moving it
+// means to go over the outputs in tensor memory.
+constexpr float kSlack = 8.f;
+constexpr int kLag = 4;                             // copy groups of a warp under way
+
+template <int D>
+struct Cfg {
+    static constexpr int HALF = kTile * 128;        // 128 rows of 64 places, 128-byte swizzle
+    static constexpr int OPERAND = HALF * (D / 64);
+    static constexpr int NK = D == 64 ? 3 : 2, NV = 3;
+    static constexpr int Q = 0, K = 2 * OPERAND, V = K + NK * OPERAND;
+    static constexpr int SMEM = V + NV * OPERAND + 1024;   // and what aligns it
+    static constexpr int LPR = D / 8, RPI = 32 / LPR;      // 16-byte chunks of a row, rows a copy
+};
+static_assert(Cfg<128>::SMEM + 1024 <= 227 * 1024, "a CTA fits an SM");
+// Tensor memory: scores of the two blocks (P over them), outputs.
+constexpr uint32_t kS = 0, kO = 256;
+
+struct Shape {
+    const int32_t *lens;
+    int B, T, Hkv, G, cap, window, sinks, rows, nrb, items;
+};
+
+// Row block rb of sequence b and head hk.  Index v < total of the run of positions that some row
+// sees: sink v below ns, then lo + v - ns.
+struct Item {
+    int b, hk, rb;
+    int len, emin, emax;
+    int lo, ns, total, ntiles;
+};
+
+// Item number x: the last rows come first, which see most where there is no window.
+__device__ __forceinline__ Item item_of(const Shape &s, int x) {
+    Item it;
+    const int heads = s.B * s.Hkv, y = x / heads, bh = x - y * heads;
+    it.rb = s.nrb - 1 - y;
+    it.b = bh / s.Hkv;
+    it.hk = bh - it.b * s.Hkv;
+    it.len = max(s.lens[it.b], 0);
+    const int r0 = it.rb * kItemRows, r1 = min(r0 + kItemRows, s.rows) - 1;
+    it.emin = it.len - s.T + r0 / s.G;
+    it.emax = it.len - s.T + r1 / s.G;
+    const int hi = min(it.emax + 1, s.cap);
+    it.lo = s.window > 0 ? min(max(0, it.emin + 1 - s.window), s.cap) : 0;
+    it.ns = min(s.sinks, min(it.lo, max(hi, 0)));
+    it.total = it.ns + max(0, hi - it.lo);
+    it.ntiles = (it.total + kTile - 1) / kTile;
+    return it;
+}
+__device__ __forceinline__ int pos_of(const Item &it, int v) { return v < it.ns ? v : it.lo + (v - it.ns); }
+// Positions of tile t of an item, rounded up to whole groups of 32.
+__device__ __forceinline__ int width_of(const Item &it, int t) {
+    return min(kTile, (it.total - t * kTile + 31) & ~31);
+}
+
+// Waits for a phase of bar: false after two seconds, and at once where some thread of the CTA
+// has given up.
+__device__ __forceinline__ bool wait_one(uint64_t *bar, uint32_t parity, volatile int *gave_up) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+#pragma unroll 1
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (*gave_up) return false;
+        if (ptx::globaltimer_ns() - t0 > 2000000000ull) {
+            *gave_up = 1;
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *gave_up) {
+    return __all_sync(~0u, wait_one(bar, parity, gave_up));
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                 "l"(__cvta_generic_to_global(src)), "r"(ok ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at));
+    return v;
+}
+__device__ __forceinline__ void sts16(uint32_t at, const uint4 &v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+    ptx::tmem_ld_wait();
+    return __uint_as_float(r);
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v))
+                 : "memory");
+    ptx::tmem_st_wait();
+}
+
+// Chunk c (16 bytes) of row r of an operand: 64 places to a row of 128 bytes, chunks exchanged
+// by the 128-byte swizzle, the second 64 places behind all rows' first.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    return (c / 8) * Cfg<D>::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+struct Barriers {
+    uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t done;
+};
+// What a tile's copies leave for the rows' threads, for the last four tiles (a tile's copies begin
+// when the products of scores of the tile NK before it are done, so two blocks of rows are at
+// most three tiles behind).
+struct Notes {
+    uint32_t there[4][kTile / 32];    // which positions exist
+    int foul[4];                      // the tile's number + 1 if some value that not every row sees
+                                      // is infinite or NaN
+};
+struct Pending {
+    uint64_t *bar;
+    uint32_t slot, check;             // values: positions of the group that not every row sees
+    int row0, tile;
+};
+
+// ---- the copying warps ------------------------------------------------------------------
+template <int D>
+struct Copier {
+    using C = Cfg<D>;
+    const PagedArgs &a;
+    const Shape &s;
+    Barriers &bar;
+    Notes &notes;
+    Pending *queue;                   // of this warp, kLag + 1 entries
+    volatile int *gave_up;
+    uint32_t base;
+    int lane;
+    int made = 0, landed = 0;         // copy groups
+
+    // The oldest group has landed: looks for infinities and NaN among values that some row does
+    // not see (its probability of 0 would make NaN of them), which leave as zeros, and arrives.
+    __device__ __forceinline__ void land() {
+        const Pending p = queue[landed % (kLag + 1)];
+        if (p.check) {
+            bool foul = false;
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += C::RPI) {
+                const int r = r0 + lane / C::LPR;
+                if (!(p.check >> r & 1)) continue;
+                const uint32_t at = p.slot + chunk_at<D>(p.row0 + r, lane % C::LPR);
+                uint4 u = lds16(at);
+                uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                bool mine = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u, mine = true;
+                    if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu, mine = true;
+                }
+                if (mine) sts16(at, make_uint4(w[0], w[1], w[2], w[3]));
+                foul |= mine;
+            }
+            if (__any_sync(~0u, foul) && lane == 0) notes.foul[p.tile & 3] = p.tile + 1;
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(p.bar);
+        ++landed;
+    }
+    template <int N>
+    __device__ __forceinline__ void land_to() {
+        ptx::cp_async_wait<N>();
+        while (made - landed > N) land();
+    }
+    __device__ __forceinline__ void push(const Pending &p) {
+        ptx::cp_async_commit();
+        if (lane == 0) queue[made % (kLag + 1)] = p;
+        __syncwarp();
+        ++made;
+        land_to<kLag>();
+    }
+    // Before anything is waited for, what has been copied is handed over.
+    __device__ __forceinline__ bool wait_empty(uint64_t *b, uint32_t parity) {
+        if (__all_sync(~0u, ptx::mbar_try_wait(b, parity))) return true;
+        land_to<0>();
+        return wait_warp(b, parity, gave_up);
+    }
+    __device__ __forceinline__ void rows(uint32_t slot, int row0, const void *pool, int64_t off,
+                                         uint32_t mask) {
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += C::RPI) {
+            const int r = r0 + lane / C::LPR;
+            const int64_t o = __shfl_sync(~0u, off, r) + (lane % C::LPR) * 8;
+            const bool ok = mask >> r & 1 && SSD_IDX_OK(a.err, o + 7, a.c.n);
+            copy16(slot + chunk_at<D>(row0 + r, lane % C::LPR),
+                   static_cast<const __nv_bfloat16 *>(pool) + (ok ? o : 0), ok);
+        }
+    }
+
+    __device__ __forceinline__ void run(int warp) {
+        int jt = 0;                   // tile of the CTA
+#pragma unroll 1
+        for (int x = blockIdx.x; x < s.items; x += gridDim.x) {
+            const Item it = item_of(s, x);
+#pragma unroll 1
+            for (int t = 0; t < it.ntiles; ++t, ++jt) {
+                const int ks = jt % C::NK, vs = jt % C::NV;
+                const uint32_t kslot = base + C::K + ks * C::OPERAND, vslot = base + C::V + vs * C::OPERAND;
+#pragma unroll 1
+                for (int g = 0; g < kTile / 32; ++g) {
+                    if ((jt * (kTile / 32) + g) % kCopyWarps != warp) continue;
+                    const int v = t * kTile + g * 32 + lane, pos = pos_of(it, v);
+                    const int p = pos / a.c.ps;
+                    int page = -1;
+                    if (v < it.total && SSD_IDX_OK(a.err, it.b * a.tb + p, a.t_n))
+                        page = a.table[it.b * a.tb + p];
+                    const bool ok = page >= 0 && page < a.c.pages;
+                    const uint32_t mask = __ballot_sync(~0u, ok);
+                    const bool every = pos <= it.emin &&
+                                       (s.window == 0 || pos > it.emax - s.window || pos < s.sinks);
+                    const uint32_t check = __ballot_sync(~0u, ok && !every);
+                    const int64_t off = ok ? page * a.c.sp + it.hk * a.c.sh + (pos - p * a.c.ps) * a.c.st : 0;
+                    const bool any = g * 32 < width_of(it, t);
+                    if (jt >= C::NK && !wait_empty(&bar.k_empty[ks], (jt / C::NK - 1) & 1)) return;
+                    if (any) rows(kslot, g * 32, a.c.k, off, mask);
+                    if (lane == 0) notes.there[jt & 3][g] = mask;
+                    push({&bar.k_full[ks], 0, 0, 0, 0});
+                    if (jt >= C::NV && !wait_empty(&bar.v_empty[vs], (jt / C::NV - 1) & 1)) return;
+                    if (any) rows(vslot, g * 32, a.c.v, off, mask);
+                    push({&bar.v_full[vs], vslot, check, g * 32, jt});
+                }
+            }
+        }
+        land_to<0>();
+    }
+};
+
+// ---- the issuing thread -------------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile int *gave_up, uint32_t base,
+                                      uint32_t tmem) {
+    using C = Cfg<D>;
+    constexpr uint32_t kIdS = ptx::idesc_bf16_f32(kRows, 0, false, false);
+    constexpr uint32_t kIdO = ptx::idesc_bf16_f32(kRows, D, false, true);
+    int x = blockIdx.x, t = 0, jt = 0, nitem = 0;
+    Item it = {};
+    auto next_nonempty = [&]() {
+        while (x < s.items) {
+            it = item_of(s, x);
+            if (it.ntiles) return true;
+            x += gridDim.x;
+        }
+        return false;
+    };
+    // scores of tile t of item number nitem, tile jt of the CTA
+    auto scores = [&](int blk) {
+        if (t == 0 && !wait_one(&bar.q_full[blk], nitem & 1, gave_up)) return false;
+        const int ks = jt % C::NK;
+        if (!wait_one(&bar.k_full[ks], (jt / C::NK) & 1, gave_up)) return false;
+        ptx::tc_fence_after();
+        const uint32_t id = kIdS | uint32_t(width_of(it, t) >> 3) << 17;
+        const uint64_t q = ptx::sdesc(base + C::Q + blk * C::OPERAND, 16, 1024);
+        const uint64_t k = ptx::sdesc(base + C::K + ks * C::OPERAND, 16, 1024);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            const uint64_t o = uint64_t((i / 4) * C::HALF + (i % 4) * 32) >> 4;
+            ptx::mma_bf16_ss(tmem + kS + 128 * blk, q + o, k + o, id, i != 0);
+        }
+        ptx::mma_commit(&bar.s_full[blk]);
+        if (blk == 1) ptx::mma_commit(&bar.k_empty[ks]);
+        return true;
+    };
+    if (!next_nonempty()) return;
+    if (!scores(0) || !scores(1)) return;
+    for (;;) {
+        const int vs = jt % C::NV, steps = width_of(it, t) / 16, at = jt;
+        const bool last = t + 1 == it.ntiles;
+        bool more = true;
+        if (last) {
+            x += gridDim.x;
+            t = 0;
+            ++nitem;
+            more = next_nonempty();
+        } else {
+            ++t;
+        }
+        ++jt;
+#pragma unroll 1
+        for (int blk = 0; blk < 2; ++blk) {
+            if (!wait_one(&bar.p_full[blk], at & 1, gave_up) ||
+                !wait_one(&bar.v_full[vs], (at / C::NV) & 1, gave_up))
+                return;
+            ptx::tc_fence_after();
+            const uint64_t v = ptx::sdesc(base + C::V + vs * C::OPERAND, C::HALF, 1024);
+            for (int i = 0; i < steps; ++i)
+                ptx::mma_bf16_ts(tmem + kO + 128 * blk, tmem + kS + 128 * blk + 8 * i, v + uint64_t(i * 128),
+                                 kIdO, 1);
+            if (last) ptx::mma_commit(&bar.o_full[blk]);
+            if (blk == 1) ptx::mma_commit(&bar.v_empty[vs]);
+            if (more && !scores(blk)) return;
+        }
+        if (!more) return;
+    }
+}
+
+// ---- the rows' threads ----------------------------------------------------------------------
+template <int D>
+struct RowThread {
+    using C = Cfg<D>;
+    const PagedArgs &a;
+    const Shape &s;
+    Barriers &bar;
+    Notes &notes;
+    volatile int *gave_up;
+    uint32_t base, ts, to;            // shared memory; this warp's lanes of S and O
+    int blk, lane, warp;              // warp: 0 to 3 of its block
+
+    // This warp's 32 rows of an item's queries, a row's offset in each lane's hands.  (The products
+    // of scores that read the item before's are done.)
+    __device__ __forceinline__ void load_queries(const Item &it) {
+        const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
+        const int r = min(it.rb * kItemRows + blk * kRows + warp * 32 + lane, s.rows - 1);
+        const int t = r / s.G;
+        const int64_t off = it.b * a.q_sb + t * a.q_st + (it.hk * s.G + r - t * s.G) * a.q_sh;
+        const uint32_t dst = base + C::Q + blk * C::OPERAND;
+#pragma unroll 4
+        for (int r0 = 0; r0 < 32; r0 += C::RPI) {
+            const int row = r0 + lane / C::LPR;
+            const int64_t o = __shfl_sync(~0u, off, row) + (lane % C::LPR) * 8;
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (SSD_IDX_OK(a.err, o + 7, a.q_n))
+                u = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + o);
+            u.x ^= sign, u.y ^= sign, u.z ^= sign, u.w ^= sign;
+            sts16(dst + chunk_at<D>(warp * 32 + row, lane % C::LPR), u);
+        }
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(&bar.q_full[blk]);
+    }
+    __device__ __forceinline__ void zero_outputs() {
+        uint32_t z[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) z[i] = 0;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) ptx::tmem_st32(to + c, z);
+        ptx::tmem_st_wait();
+    }
+    // Infinities and NaN of a tile's values, added to the rows that see them (the copies have put
+    // zeros in their place; a probability makes no difference to them).
+    __device__ __forceinline__ void add_foul(const Item &it, int t, int own) {
+#pragma unroll 1
+        for (int v = t * kTile; v < min(it.total, (t + 1) * kTile); ++v) {
+            const int pos = pos_of(it, v), p = pos / a.c.ps;
+            if (pos <= it.emin && (s.window == 0 || pos > it.emax - s.window || pos < s.sinks)) continue;
+            const int page = SSD_IDX_OK(a.err, it.b * a.tb + p, a.t_n) ? a.table[it.b * a.tb + p] : -1;
+            if (page < 0 || page >= a.c.pages) continue;
+            const int64_t off = page * a.c.sp + it.hk * a.c.sh + (pos - p * a.c.ps) * a.c.st;
+            const bool see = pos <= own && (s.window == 0 || pos > own - s.window || pos < s.sinks);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                const float x = SSD_IDX_OK(a.err, off + c + lane, a.c.n)
+                                    ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.c.v)[off + c + lane])
+                                    : 0.f;
+                for (uint32_t bad = __ballot_sync(~0u, !isfinite(x)); bad; bad &= bad - 1) {
+                    const int d = __ffs(bad) - 1;
+                    const float add = __shfl_sync(~0u, x, d), was = tmem_ld1(to + c + d);
+                    tmem_st1(to + c + d, see ? was + add : was);
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ bool run() {
+        const float qs = fabsf(a.scale) * kLog2e;
+        int jt = 0, nitem = 0;
+        bool ready = false;           // this item's queries are in shared memory
+#pragma unroll 1
+        for (int x = blockIdx.x; x < s.items; x += gridDim.x) {
+            const Item it = item_of(s, x);
+            const int r = it.rb * kItemRows + blk * kRows + warp * 32 + lane, rr = min(r, s.rows - 1);
+            const int own = it.len - s.T + rr / s.G;
+            // its run of positions: [va, vb) and what lies below vsink of it
+            const int vb = own < it.lo ? min(own + 1, it.ns) : it.ns + own - it.lo + 1;
+            const int va = s.window > 0 ? it.ns + max(own - s.window + 1, it.lo) - it.lo : 0;
+            const int vsink = it.ns + max(0, s.sinks - it.lo);
+            const int vb_least = it.ns + it.emin - it.lo + 1;     // (emin < lo: nothing or less)
+            const int va_most = s.window > 0 ? it.ns + max(it.emax - s.window + 1, it.lo) - it.lo : 0;
+            float m = -INFINITY, l = 0.f;
+            if (it.ntiles) {
+                if (!ready) load_queries(it);
+                ready = false;
+                zero_outputs();
+            }
+#pragma unroll 1
+            for (int t = 0; t < it.ntiles; ++t, ++jt) {
+                if (!wait_warp(&bar.s_full[blk], jt & 1, gave_up)) return false;
+                ptx::tc_fence_after();
+                const int v0 = t * kTile, width = width_of(it, t);
+                uint32_t raw[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (32 * c < width) ptx::tmem_ld32(ts + 32 * c, raw[c]);
+                ptx::tmem_ld_wait();
+                // every row of the warp sees the whole tile?
+                uint32_t vis[4];
+                bool all = width == kTile && v0 + kTile <= vb && (va <= v0 || v0 + kTile <= vsink);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    vis[c] = notes.there[jt & 3][c];
+                    all = all && vis[c] == ~0u;
+                }
+                all = __all_sync(~0u, all);
+                if (!all) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int b = v0 + 32 * c;
+                        auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
+                        vis[c] &= below(vb - b) & (~below(va - b) | below(vsink - b));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(vis[c] >> i & 1)) raw[c][i] = 0xff800000u;
+                    }
+                }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2)
+                        top[c] = fmaxf(top[c], fmaxf(__uint_as_float(raw[c][i]), __uint_as_float(raw[c][i + 1])));
+                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                if (__any_sync(~0u, (mx - m) * qs > kSlack || (m == -INFINITY && mx != m))) {
+                    const float to_m = fmaxf(m, mx);
+                    const float f = m == -INFINITY ? 1.f : ex2((m - to_m) * qs);
+                    m = to_m;
+                    l *= f;
+                    if (t > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            ptx::tmem_ld16(to + c, o);
+                            ptx::tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            ptx::tmem_st16(to + c, o);
+                        }
+                        ptx::tmem_st_wait();
+                    }
+                }
+                // Some row of the item may not see all of the tile, if none of this warp's: what the
+                // copies noted of its values comes with them.
+                if (v0 + kTile > vb_least || (va_most > v0 && v0 + kTile > vsink)) {
+                    if (!wait_warp(&bar.v_full[jt % C::NV], (jt / C::NV) & 1, gave_up)) return false;
+                    if (notes.foul[jt & 3] == jt + 1) add_foul(it, t, own);
+                }
+                const float minus = m == -INFINITY ? 0.f : -m;
+                const F2 mm = f2(minus, minus), qq = f2(qs, qs);
+                F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (32 * c >= width) break;
+                    uint32_t p[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 e = parts(mul(add(f2(__uint_as_float(raw[c][2 * i]),
+                                                          __uint_as_float(raw[c][2 * i + 1])), mm), qq));
+                        float x0 = ex2(e.x), x1 = ex2(e.y);
+                        if (!all) {   // (a scale of 0 makes NaN of what is hidden)
+                            if (!(vis[c] >> (2 * i) & 1)) x0 = 0.f;
+                            if (!(vis[c] >> (2 * i + 1) & 1)) x1 = 0.f;
+                        }
+                        sum[i & 1] = add(sum[i & 1], f2(x0, x1));
+                        p[i] = pack_bf16(x0, x1);
+                    }
+                    ptx::tmem_st16(ts + 16 * c, p);
+                }
+                const float2 s0 = parts(add(sum[0], sum[1]));
+                l += s0.x + s0.y;
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&bar.p_full[blk]);
+            }
+            // The scores of this item are done with: the next one's queries.
+            if (it.ntiles) {
+#pragma unroll 1
+                for (int y = x + gridDim.x; y < s.items && !ready; y += gridDim.x) {
+                    const Item nx = item_of(s, y);
+                    if (!nx.ntiles) continue;
+                    load_queries(nx);
+                    ready = true;
+                }
+                if (!wait_warp(&bar.o_full[blk], nitem & 1, gave_up)) return false;
+                ptx::tc_fence_after();
+                ++nitem;
+            }
+            const int tk = rr / s.G, h = it.hk * s.G + rr - tk * s.G;
+            const int64_t off = it.b * a.o_sb + tk * a.o_st + h * a.o_sh;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                if (it.ntiles) {
+                    ptx::tmem_ld32(to + c, o);
+                    ptx::tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0;
+                }
+                if (r < s.rows && SSD_IDX_OK(a.err, off + c + 31, a.o_n)) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + off + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = pack_bf16(__uint_as_float(o[8 * i + 2 * j]) * inv,
+                                             __uint_as_float(o[8 * i + 2 * j + 1]) * inv);
+                        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            const int64_t at = (int64_t(it.b) * s.T + tk) * a.Hq + h;
+            if (a.lse && r < s.rows && SSD_IDX_OK(a.err, at, int64_t(s.B) * s.T * a.Hq))
+                a.lse[at] = l == 0.f ? -INFINITY : (m * qs + log2f(l)) * kLn2;
+        }
+        return true;
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+k_paged_prompt(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
+    using C = Cfg<D>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ Barriers bar;
+    __shared__ Notes notes;
+    __shared__ Pending queue[kCopyWarps][kLag + 1];
+    __shared__ int gave_up;
+    __shared__ uint32_t tmem_at;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const uint32_t base = (ptx::smem_u32(smem_raw) + 1023) & ~1023u;
+    if (threadIdx.x == 0) {
+        gave_up = 0;
+        notes.foul[0] = notes.foul[1] = notes.foul[2] = notes.foul[3] = 0;
+        for (int i = 0; i < 3; ++i) {
+            ptx::mbar_init(&bar.k_full[i], kTile / 32);
+            ptx::mbar_init(&bar.v_full[i], kTile / 32);
+            ptx::mbar_init(&bar.k_empty[i], 1);
+            ptx::mbar_init(&bar.v_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&bar.q_full[i], kRows);
+            ptx::mbar_init(&bar.p_full[i], kRows);
+            ptx::mbar_init(&bar.s_full[i], 1);
+            ptx::mbar_init(&bar.o_full[i], 1);
+        }
+        ptx::mbar_init(&bar.done, 1);
+        ptx::fence_mbar_init();
+    }
+    if (warp == 8) {
+        ptx::tmem_alloc(&tmem_at, 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = tmem_at;
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
+        const int blk = warp / 4;
+        const uint32_t lanes = uint32_t(warp % 4 * 32) << 16;
+        RowThread<D> rows{a, s, bar, notes, &gave_up, base, tmem + lanes + kS + 128 * blk,
+                          tmem + lanes + kO + 128 * blk, blk, lane, warp % 4};
+        rows.run();
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 8) {
+            if (lane == 0) {
+                issue<D>(s, bar, &gave_up, base, tmem);
+                // nothing is under way when tensor memory is given back
+                ptx::mma_commit(&bar.done);
+                ptx::mbar_wait(&bar.done, 0);
+            }
+            __syncwarp();
+        } else {
+            Copier<D> copier{a, s, bar, notes, queue[warp - 9], &gave_up, base, lane};
+            copier.run(warp - 9);
+            ptx::cp_async_wait<0>();
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && gave_up) atomicOr(a.err, kErrTimeout);
+    if (warp == 8) ptx::tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch_d(const PagedArgs &a, const Shape &s, cudaStream_t stream) {
+    static std::atomic<uint64_t> done[4];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 256 || !((done[dev / 64].load(std::memory_order_acquire) >> (dev % 64)) & 1)) {
+        e = cudaFuncSetAttribute(k_paged_prompt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev < 256) done[dev / 64].fetch_or(uint64_t(1) << (dev % 64));
+    }
+    const int grid = s.items < device_sm_count() ? s.items : device_sm_count();
+    k_paged_prompt<D><<<grid, kThreads, Cfg<D>::SMEM, stream>>>(a, s);
+    return cudaGetLastError();
+}
+
+int64_t items_of(const PagedArgs &a) {
+    const int64_t rows = int64_t(a.T) * (a.Hq / a.c.Hkv);
+    return int64_t(a.B) * a.c.Hkv * ((rows + kItemRows - 1) / kItemRows);
+}
+
+}  // namespace
+
+bool prompt_fits(const PagedArgs &a) {
+    const int64_t rows = int64_t(a.T) * (a.Hq / a.c.Hkv), items = items_of(a);
+    return a.c.dt == DT_BF16 && rows >= kItemRows / 2 && items * 4 >= device_sm_count() && items < (1 << 30);
+}
+
+cudaError_t launch_paged_prompt(const PagedArgs &a, cudaStream_t stream) {
+    Shape s{};
+    s.lens = a.lens;
+    s.B = a.B;
+    s.T = a.T;
+    s.Hkv = a.c.Hkv;
+    s.G = a.Hq / a.c.Hkv;
+    s.cap = a.M * a.c.ps;
+    s.window = int(a.window);
+    s.sinks = int(a.sinks);
+    s.rows = a.T * s.G;
+    s.nrb = (s.rows + kItemRows - 1) / kItemRows;
+    s.items = int(items_of(a));
+    return a.c.D == 64 ? launch_d<64>(a, s, stream) : launch_d<128>(a, s, stream);
+}
+
+}  // namespace ssd

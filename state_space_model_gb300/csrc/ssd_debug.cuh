@@ -11,7 +11,7 @@
 // (out-of-range boxes are filled or clipped); their shared-memory destinations
 // are checked here.  In the normal build the checks compile to `true`.
 //
-// In the attention cache's kernels (ssd_kv.cuh, ssd_attn.cuh) the checks cover pools, scales, page
+// In the attention cache's kernels (ssd_kv.cuh, ssd_attn.cuh, ssd_attn_prompt.cu) the checks cover pools, scales, page
 // tables, angles, the rows of inputs and outputs, log sums, and the workspace's records and
 // parts; in shared memory the exchange of outputs between warps.  Not checked again there:
 // indices that the code has just compared with their bound or clamped to it (lengths, slots,
@@ -27,7 +27,7 @@ constexpr unsigned kErrBounds = 4u;   // a debug-build bounds check failed
 // File codes of the kernels' translation units (word 1 holds code << 16 | line).
 enum : unsigned {
     kDbgFused = 1, kDbgPair = 2, kDbgTc = 3, kDbgSimt = 4, kDbgSelftest = 5, kDbgTcF32 = 6,
-    kDbgKv = 7, kDbgAttn = 8,
+    kDbgKv = 7, kDbgAttn = 8, kDbgPrompt = 9,
 };
 
 #ifdef SSD_DEBUG_BOUNDS
