@@ -13,19 +13,22 @@
 // What bounds it is the products, 4 D flops a row and position: with 256 rows to a tile the
 // reads from L2 are 64 KB for 2 x 4.2 Mflop of them each.  So one thread issues nothing but
 // products, in the order S0, S1, then for every tile O0, S0 (next), O1, S1 (next): while a
-// block's exponentials run, the tensor core has the other's products.  Three warps copy, tiles
-// ahead and across items, and the CTA goes from item to item (sequence, head, 256 rows) with
-// the next one's queries and keys already there.
+// block's exponentials run, the tensor core has the other's products.  One warp loads (TMA),
+// tiles ahead and across items, and the CTA goes from item to item (sequence, head, 256 rows)
+// with the next one's queries and keys already there.
 //
 // The positions that some row of an item sees, sinks first and then the window's, are counted
-// through as one run, so that a tile holds what is needed and nothing else, whatever the page
-// size and wherever the window begins.
+// through as one run in boxes of 16 of a page (so pages are multiples of 16; others take the
+// kernels of ssd_attn.cuh), so that a tile holds little that nobody needs wherever the window
+// begins.  (Copies by three warps, 16 bytes a lane, took any page size and four times as long: 253
+// us where the loads make 4096 tokens under a window of 1024 take 123.)
 #include "ptx_sm100.cuh"
 #include "ssd_attn.h"
 #include "ssd_block_math.cuh"
 #include "ssd_debug.cuh"
 #include "ssd_f32x2.cuh"
 #include "ssd_tc.cuh"
+#include "ssd_tmap.h"
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,15 +43,15 @@ namespace {
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kRows = 128, kItemRows = 2 * kRows;   // rows of a block, of an item
 constexpr int kTile = 128;                          // positions of a tile
-constexpr int kCopyWarps = 3;
-constexpr int kThreads = 2 * kRows + 32 + 32 * kCopyWarps;
+constexpr int kBox = 16;                             // positions of a load
+constexpr int kCheckWarps = 2;
+constexpr int kThreads = 2 * kRows + 32 * (2 + kCheckWarps);
 // Registers of a thread: 168 at the launch (65536 / 384), shared out as 208 for the rows'
 // threads and 88 for the others: 256 x 208 + 128 x 88 = 384 x 168.
 constexpr int kRowRegs = 208, kOtherRegs = 88;
 // The maximum in use follows the true one when that is ahead by so much (log2 units): moving it
 // means to go over the outputs in tensor memory.
 constexpr float kSlack = 8.f;
-constexpr int kLag = 4;                             // copy groups of a warp under way
 
 template <int D>
 struct Cfg {
@@ -57,7 +60,8 @@ struct Cfg {
     static constexpr int NK = D == 64 ? 3 : 2, NV = 3;
     static constexpr int Q = 0, K = 2 * OPERAND, V = K + NK * OPERAND;
     static constexpr int SMEM = V + NV * OPERAND + 1024;   // and what aligns it
-    static constexpr int LPR = D / 8, RPI = 32 / LPR;      // 16-byte chunks of a row, rows a copy
+    static constexpr int LPR = D / 8, RPI = 32 / LPR;      // 16-byte chunks of a row, rows a pass
+    static constexpr int BOX = kBox * D * 2;               // bytes of a box
 };
 static_assert(Cfg<128>::SMEM + 1024 <= 227 * 1024, "a CTA fits an SM");
 // Tensor memory: scores of the two blocks (P over them), outputs.
@@ -69,7 +73,7 @@ struct Shape {
 };
 
 // Row block rb of sequence b and head hk.  Index v < total of the run of positions that some row
-// sees: sink v below ns, then lo + v - ns.
+// sees: position v below ns, then lo + v - ns; ns and lo are multiples of a box.
 struct Item {
     int b, hk, rb;
     int len, emin, emax;
@@ -88,8 +92,9 @@ __device__ __forceinline__ Item item_of(const Shape &s, int x) {
     it.emin = it.len - s.T + r0 / s.G;
     it.emax = it.len - s.T + r1 / s.G;
     const int hi = min(it.emax + 1, s.cap);
-    it.lo = s.window > 0 ? min(max(0, it.emin + 1 - s.window), s.cap) : 0;
-    it.ns = min(s.sinks, min(it.lo, max(hi, 0)));
+    it.lo = s.window > 0 ? min(max(0, it.emin + 1 - s.window), s.cap) / kBox * kBox : 0;
+    it.ns = s.sinks < it.lo ? (s.sinks + kBox - 1) / kBox * kBox : it.lo;
+    if (s.sinks == 0 || hi <= 0) it.ns = 0;
     it.total = it.ns + max(0, hi - it.lo);
     it.ntiles = (it.total + kTile - 1) / kTile;
     return it;
@@ -119,11 +124,6 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volati
     return __all_sync(~0u, wait_one(bar, parity, gave_up));
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                 "l"(__cvta_generic_to_global(src)), "r"(ok ? 16 : 0)
-                 : "memory");
-}
 __device__ __forceinline__ uint4 lds16(uint32_t at) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -155,135 +155,133 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return (c / 8) * Cfg<D>::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, uint64_t *bar, int c0, int c1,
+                                         int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(ptx::smem_u32(bar))
+        : "memory");
+}
+
 struct Barriers {
-    uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
+    uint64_t k_full[3], k_empty[3], v_land[3], v_full[3], v_empty[3];
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
     uint64_t done;
 };
-// What a tile's copies leave for the rows' threads, for the last four tiles (a tile's copies begin
-// when the products of scores of the tile NK before it are done, so two blocks of rows are at
-// most three tiles behind).
+// What is known of the last four tiles (a tile's loads begin when the products of scores of the
+// tile NK before it are done, so the rows' threads are at most three tiles behind).
 struct Notes {
-    uint32_t there[4][kTile / 32];    // which positions exist
-    int foul[4];                      // the tile's number + 1 if some value that not every row sees
-                                      // is infinite or NaN
-};
-struct Pending {
-    uint64_t *bar;
-    uint32_t slot, check;             // values: positions of the group that not every row sees
-    int row0, tile;
+    uint32_t there[4];                // bit i: box i's page exists
+    int foul[4];                      // the tile's number + 1 if a value that was looked at is infinite
+                                      // or NaN
 };
 
-// ---- the copying warps ------------------------------------------------------------------
+// The rows of an item: from where on some do not see all that is there (v >= least), and below
+// where some don't any more (v < most, sinks apart).
+__device__ __forceinline__ bool all_see(const Shape &s, const Item &it, int v0) {
+    const int least = it.ns + it.emin - it.lo + 1;
+    const int most = s.window > 0 ? it.ns + max(it.emax - s.window + 1 - it.lo, 0) : 0;
+    return v0 + kTile <= least && (most <= v0 || v0 + kTile <= s.sinks);
+}
+
+// ---- the loading warp -------------------------------------------------------------------
 template <int D>
-struct Copier {
+__device__ __forceinline__ void load_tiles(const PagedArgs &a, const Shape &s, const CUtensorMap *kmap,
+                                           const CUtensorMap *vmap, Barriers &bar, Notes &notes,
+                                           volatile int *gave_up, uint32_t base) {
     using C = Cfg<D>;
-    const PagedArgs &a;
-    const Shape &s;
-    Barriers &bar;
-    Notes &notes;
-    Pending *queue;                   // of this warp, kLag + 1 entries
-    volatile int *gave_up;
-    uint32_t base;
-    int lane;
-    int made = 0, landed = 0;         // copy groups
-
-    // The oldest group has landed: looks for infinities and NaN among values that some row does
-    // not see (its probability of 0 would make NaN of them), which leave as zeros, and arrives.
-    __device__ __forceinline__ void land() {
-        const Pending p = queue[landed % (kLag + 1)];
-        if (p.check) {
-            bool foul = false;
+    const int lane = threadIdx.x % 32;
+    int jt = 0;                       // tile of the CTA
+    // Where a wait ran out: what is under way lands before the CTA leaves.
+    auto settle = [&](int nk, int nv) {
+        for (int i = max(0, nk - C::NK); i < nk; ++i) ptx::mbar_wait(&bar.k_full[i % C::NK], (i / C::NK) & 1);
+        for (int i = max(0, nv - C::NV); i < nv; ++i) ptx::mbar_wait(&bar.v_land[i % C::NV], (i / C::NV) & 1);
+    };
 #pragma unroll 1
-            for (int r0 = 0; r0 < 32; r0 += C::RPI) {
-                const int r = r0 + lane / C::LPR;
-                if (!(p.check >> r & 1)) continue;
-                const uint32_t at = p.slot + chunk_at<D>(p.row0 + r, lane % C::LPR);
-                uint4 u = lds16(at);
-                uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                bool mine = false;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u, mine = true;
-                    if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu, mine = true;
-                }
-                if (mine) sts16(at, make_uint4(w[0], w[1], w[2], w[3]));
-                foul |= mine;
+    for (int x = blockIdx.x; x < s.items; x += gridDim.x) {
+        const Item it = item_of(s, x);
+#pragma unroll 1
+        for (int t = 0; t < it.ntiles; ++t, ++jt) {
+            const int ks = jt % C::NK, vs = jt % C::NV;
+            const int v = t * kTile + lane * kBox, pos = pos_of(it, v);
+            const int p = pos / a.c.ps, at = pos - p * a.c.ps;
+            const int boxes = min(kTile / kBox, (it.total - t * kTile + kBox - 1) / kBox);
+            int page = -1;
+            if (lane < boxes && SSD_IDX_OK(a.err, it.b * a.tb + p, a.t_n)) page = a.table[it.b * a.tb + p];
+            const bool ok = page >= 0 && page < a.c.pages;
+            const uint32_t there = __ballot_sync(~0u, ok);
+            if (!ok) page = a.c.pages;        // outside: zeros
+            if (jt >= C::NK && !wait_warp(&bar.k_empty[ks], (jt / C::NK - 1) & 1, gave_up)) return settle(jt, jt);
+            if (lane == 0) {
+                notes.there[jt & 3] = there;
+                ptx::mbar_arrive_expect_tx(&bar.k_full[ks], boxes * C::BOX);
             }
-            if (__any_sync(~0u, foul) && lane == 0) notes.foul[p.tile & 3] = p.tile + 1;
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(p.bar);
-        ++landed;
-    }
-    template <int N>
-    __device__ __forceinline__ void land_to() {
-        ptx::cp_async_wait<N>();
-        while (made - landed > N) land();
-    }
-    __device__ __forceinline__ void push(const Pending &p) {
-        ptx::cp_async_commit();
-        if (lane == 0) queue[made % (kLag + 1)] = p;
-        __syncwarp();
-        ++made;
-        land_to<kLag>();
-    }
-    // Before anything is waited for, what has been copied is handed over.
-    __device__ __forceinline__ bool wait_empty(uint64_t *b, uint32_t parity) {
-        if (__all_sync(~0u, ptx::mbar_try_wait(b, parity))) return true;
-        land_to<0>();
-        return wait_warp(b, parity, gave_up);
-    }
-    __device__ __forceinline__ void rows(uint32_t slot, int row0, const void *pool, int64_t off,
-                                         uint32_t mask) {
+            __syncwarp();
+            if (lane < boxes) {
 #pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += C::RPI) {
-            const int r = r0 + lane / C::LPR;
-            const int64_t o = __shfl_sync(~0u, off, r) + (lane % C::LPR) * 8;
-            const bool ok = mask >> r & 1 && SSD_IDX_OK(a.err, o + 7, a.c.n);
-            copy16(slot + chunk_at<D>(row0 + r, lane % C::LPR),
-                   static_cast<const __nv_bfloat16 *>(pool) + (ok ? o : 0), ok);
-        }
-    }
-
-    __device__ __forceinline__ void run(int warp) {
-        int jt = 0;                   // tile of the CTA
-#pragma unroll 1
-        for (int x = blockIdx.x; x < s.items; x += gridDim.x) {
-            const Item it = item_of(s, x);
-#pragma unroll 1
-            for (int t = 0; t < it.ntiles; ++t, ++jt) {
-                const int ks = jt % C::NK, vs = jt % C::NV;
-                const uint32_t kslot = base + C::K + ks * C::OPERAND, vslot = base + C::V + vs * C::OPERAND;
-#pragma unroll 1
-                for (int g = 0; g < kTile / 32; ++g) {
-                    if ((jt * (kTile / 32) + g) % kCopyWarps != warp) continue;
-                    const int v = t * kTile + g * 32 + lane, pos = pos_of(it, v);
-                    const int p = pos / a.c.ps;
-                    int page = -1;
-                    if (v < it.total && SSD_IDX_OK(a.err, it.b * a.tb + p, a.t_n))
-                        page = a.table[it.b * a.tb + p];
-                    const bool ok = page >= 0 && page < a.c.pages;
-                    const uint32_t mask = __ballot_sync(~0u, ok);
-                    const bool every = pos <= it.emin &&
-                                       (s.window == 0 || pos > it.emax - s.window || pos < s.sinks);
-                    const uint32_t check = __ballot_sync(~0u, ok && !every);
-                    const int64_t off = ok ? page * a.c.sp + it.hk * a.c.sh + (pos - p * a.c.ps) * a.c.st : 0;
-                    const bool any = g * 32 < width_of(it, t);
-                    if (jt >= C::NK && !wait_empty(&bar.k_empty[ks], (jt / C::NK - 1) & 1)) return;
-                    if (any) rows(kslot, g * 32, a.c.k, off, mask);
-                    if (lane == 0) notes.there[jt & 3][g] = mask;
-                    push({&bar.k_full[ks], 0, 0, 0, 0});
-                    if (jt >= C::NV && !wait_empty(&bar.v_empty[vs], (jt / C::NV - 1) & 1)) return;
-                    if (any) rows(vslot, g * 32, a.c.v, off, mask);
-                    push({&bar.v_full[vs], vslot, check, g * 32, jt});
-                }
+                for (int h = 0; h < D / 64; ++h)
+                    load_box(base + C::K + ks * C::OPERAND + h * C::HALF + lane * kBox * 128, kmap,
+                             &bar.k_full[ks], 64 * h, at, it.hk, page);
+            }
+            if (jt >= C::NV && !wait_warp(&bar.v_empty[vs], (jt / C::NV - 1) & 1, gave_up)) return settle(jt + 1, jt);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&bar.v_land[vs], boxes * C::BOX);
+            __syncwarp();
+            if (lane < boxes) {
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h)
+                    load_box(base + C::V + vs * C::OPERAND + h * C::HALF + lane * kBox * 128, vmap,
+                             &bar.v_land[vs], 64 * h, at, it.hk, page);
             }
         }
-        land_to<0>();
     }
-};
+    if (*gave_up) settle(jt, jt);
+}
+
+// ---- the checking warps -----------------------------------------------------------------
+//
+// A probability of 0 would make NaN of an infinity or NaN that a row does not see: where some row
+// of the item does not see all of a tile, those of its values become zeros here, and the rows'
+// threads add them to the rows that see them.  Other tiles pass as they are.
+template <int D>
+__device__ __forceinline__ void check_values(const Shape &s, Barriers &bar, Notes &notes,
+                                             volatile int *gave_up, uint32_t base, int warp) {
+    using C = Cfg<D>;
+    const int lane = threadIdx.x % 32;
+    int jt = 0;
+#pragma unroll 1
+    for (int x = blockIdx.x; x < s.items; x += gridDim.x) {
+        const Item it = item_of(s, x);
+#pragma unroll 1
+        for (int t = 0; t < it.ntiles; ++t, ++jt) {
+            const int vs = jt % C::NV;
+            if (!wait_warp(&bar.v_land[vs], (jt / C::NV) & 1, gave_up)) return;
+            if (!all_see(s, it, t * kTile)) {
+                const int rows = min(kTile, (it.total - t * kTile + kBox - 1) / kBox * kBox);
+                const uint32_t slot = base + C::V + vs * C::OPERAND;
+                bool foul = false;
+#pragma unroll 4
+                for (int r0 = warp * C::RPI; r0 < rows; r0 += kCheckWarps * C::RPI) {
+                    const uint32_t at = slot + chunk_at<D>(r0 + lane / C::LPR, lane % C::LPR);
+                    const uint4 u = lds16(at);
+                    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                    bool mine = false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u, mine = true;
+                        if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu, mine = true;
+                    }
+                    if (mine) sts16(at, make_uint4(w[0], w[1], w[2], w[3]));
+                    foul |= mine;
+                }
+                if (__any_sync(~0u, foul) && lane == 0) notes.foul[jt & 3] = jt + 1;
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+            }
+            if (lane == 0) ptx::mbar_arrive(&bar.v_full[vs]);
+        }
+    }
+}
 
 // ---- the issuing thread -------------------------------------------------------------------
 template <int D>
@@ -323,7 +321,8 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
     if (!next_nonempty()) return;
     if (!scores(0) || !scores(1)) return;
     for (;;) {
-        const int vs = jt % C::NV, steps = width_of(it, t) / 16, at = jt;
+        const int vs = jt % C::NV, at = jt;
+        const int steps = min(kTile / 16, (it.total - t * kTile + 15) / 16);
         const bool last = t + 1 == it.ntiles;
         bool more = true;
         if (last) {
@@ -394,13 +393,12 @@ struct RowThread {
         for (int c = 0; c < D; c += 32) ptx::tmem_st32(to + c, z);
         ptx::tmem_st_wait();
     }
-    // Infinities and NaN of a tile's values, added to the rows that see them (the copies have put
-    // zeros in their place; a probability makes no difference to them).
+    // Infinities and NaN of a tile's values, added to the rows that see them (zeros stand in their
+    // place; a probability makes no difference to them).
     __device__ __forceinline__ void add_foul(const Item &it, int t, int own) {
 #pragma unroll 1
         for (int v = t * kTile; v < min(it.total, (t + 1) * kTile); ++v) {
             const int pos = pos_of(it, v), p = pos / a.c.ps;
-            if (pos <= it.emin && (s.window == 0 || pos > it.emax - s.window || pos < s.sinks)) continue;
             const int page = SSD_IDX_OK(a.err, it.b * a.tb + p, a.t_n) ? a.table[it.b * a.tb + p] : -1;
             if (page < 0 || page >= a.c.pages) continue;
             const int64_t off = page * a.c.sp + it.hk * a.c.sh + (pos - p * a.c.ps) * a.c.st;
@@ -428,12 +426,10 @@ struct RowThread {
             const Item it = item_of(s, x);
             const int r = it.rb * kItemRows + blk * kRows + warp * 32 + lane, rr = min(r, s.rows - 1);
             const int own = it.len - s.T + rr / s.G;
-            // its run of positions: [va, vb) and what lies below vsink of it
+            // what it sees of the item's run: [va, vb), and below vb what lies below `sinks` too (where
+            // ns < sinks it is lo, and the run has no gap)
             const int vb = own < it.lo ? min(own + 1, it.ns) : it.ns + own - it.lo + 1;
-            const int va = s.window > 0 ? it.ns + max(own - s.window + 1, it.lo) - it.lo : 0;
-            const int vsink = it.ns + max(0, s.sinks - it.lo);
-            const int vb_least = it.ns + it.emin - it.lo + 1;     // (emin < lo: nothing or less)
-            const int va_most = s.window > 0 ? it.ns + max(it.emax - s.window + 1, it.lo) - it.lo : 0;
+            const int va = s.window > 0 ? it.ns + max(own - s.window + 1 - it.lo, 0) : 0;
             float m = -INFINITY, l = 0.f;
             if (it.ntiles) {
                 if (!ready) load_queries(it);
@@ -452,19 +448,16 @@ struct RowThread {
                 ptx::tmem_ld_wait();
                 // every row of the warp sees the whole tile?
                 uint32_t vis[4];
-                bool all = width == kTile && v0 + kTile <= vb && (va <= v0 || v0 + kTile <= vsink);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    vis[c] = notes.there[jt & 3][c];
-                    all = all && vis[c] == ~0u;
-                }
-                all = __all_sync(~0u, all);
+                const uint32_t there = notes.there[jt & 3];
+                const bool all = __all_sync(~0u, v0 + kTile <= vb && (va <= v0 || v0 + kTile <= s.sinks) &&
+                                                     there == (1u << kTile / kBox) - 1);
                 if (!all) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const int b = v0 + 32 * c;
                         auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
-                        vis[c] &= below(vb - b) & (~below(va - b) | below(vsink - b));
+                        vis[c] = (there >> (2 * c) & 1 ? 0xffffu : 0u) | (there >> (2 * c + 1) & 1 ? 0xffff0000u : 0u);
+                        vis[c] &= below(vb - b) & (~below(va - b) | below(s.sinks - b));
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (!(vis[c] >> i & 1)) raw[c][i] = 0xff800000u;
@@ -495,9 +488,8 @@ struct RowThread {
                         ptx::tmem_st_wait();
                     }
                 }
-                // Some row of the item may not see all of the tile, if none of this warp's: what the
-                // copies noted of its values comes with them.
-                if (v0 + kTile > vb_least || (va_most > v0 && v0 + kTile > vsink)) {
+                // (also where all of this warp's rows see what another's don't)
+                if (!all_see(s, it, v0)) {
                     if (!wait_warp(&bar.v_full[jt % C::NV], (jt / C::NV) & 1, gave_up)) return false;
                     if (notes.foul[jt & 3] == jt + 1) add_foul(it, t, own);
                 }
@@ -577,12 +569,12 @@ struct RowThread {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-k_paged_prompt(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
+k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+               const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
     using C = Cfg<D>;
     extern __shared__ unsigned char smem_raw[];
     __shared__ Barriers bar;
     __shared__ Notes notes;
-    __shared__ Pending queue[kCopyWarps][kLag + 1];
     __shared__ int gave_up;
     __shared__ uint32_t tmem_at;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -591,8 +583,9 @@ k_paged_prompt(const __grid_constant__ PagedArgs a, const __grid_constant__ Shap
         gave_up = 0;
         notes.foul[0] = notes.foul[1] = notes.foul[2] = notes.foul[3] = 0;
         for (int i = 0; i < 3; ++i) {
-            ptx::mbar_init(&bar.k_full[i], kTile / 32);
-            ptx::mbar_init(&bar.v_full[i], kTile / 32);
+            ptx::mbar_init(&bar.k_full[i], 1);
+            ptx::mbar_init(&bar.v_land[i], 1);
+            ptx::mbar_init(&bar.v_full[i], kCheckWarps);
             ptx::mbar_init(&bar.k_empty[i], 1);
             ptx::mbar_init(&bar.v_empty[i], 1);
         }
@@ -630,10 +623,10 @@ k_paged_prompt(const __grid_constant__ PagedArgs a, const __grid_constant__ Shap
                 ptx::mbar_wait(&bar.done, 0);
             }
             __syncwarp();
+        } else if (warp == 9) {
+            load_tiles<D>(a, s, &kmap, &vmap, bar, notes, &gave_up, base);
         } else {
-            Copier<D> copier{a, s, bar, notes, queue[warp - 9], &gave_up, base, lane};
-            copier.run(warp - 9);
-            ptx::cp_async_wait<0>();
+            check_values<D>(s, bar, notes, &gave_up, base, warp - 10);
         }
     }
     ptx::tc_fence_before();
@@ -653,8 +646,17 @@ cudaError_t launch_d(const PagedArgs &a, const Shape &s, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         if (dev < 256) done[dev / 64].fetch_or(uint64_t(1) << (dev % 64));
     }
+    CUtensorMap map[2];
+    for (int i = 0; i < 2; ++i) {
+        // (a stride of a dimension of one is whatever the caller's tensor has: any will do)
+        auto stride = [](int64_t n, int64_t elements) { return uint64_t(n > 1 ? elements * 2 : 16); };
+        const uint64_t dims[4] = {uint64_t(D), uint64_t(a.c.ps), uint64_t(a.c.Hkv), uint64_t(a.c.pages)};
+        const uint64_t strides[3] = {stride(a.c.ps, a.c.st), stride(a.c.Hkv, a.c.sh), stride(a.c.pages, a.c.sp)};
+        const uint32_t box[4] = {64, kBox, 1, 1};
+        if ((e = make_tmap_bf16(&map[i], i ? a.c.v : a.c.k, 4, dims, strides, box)) != cudaSuccess) return e;
+    }
     const int grid = s.items < device_sm_count() ? s.items : device_sm_count();
-    k_paged_prompt<D><<<grid, kThreads, Cfg<D>::SMEM, stream>>>(a, s);
+    k_paged_prompt<D><<<grid, kThreads, Cfg<D>::SMEM, stream>>>(map[0], map[1], a, s);
     return cudaGetLastError();
 }
 
@@ -667,7 +669,7 @@ int64_t items_of(const PagedArgs &a) {
 
 bool prompt_fits(const PagedArgs &a) {
     const int64_t rows = int64_t(a.T) * (a.Hq / a.c.Hkv), items = items_of(a);
-    return a.c.dt == DT_BF16 && rows >= kItemRows / 2 && items * 4 >= device_sm_count() && items < (1 << 30);
+    return a.c.dt == DT_BF16 && a.c.ps % kBox == 0 && a.c.pages > 0 && rows >= kItemRows / 2 && items * 4 >= device_sm_count() && items < (1 << 30);
 }
 
 cudaError_t launch_paged_prompt(const PagedArgs &a, cudaStream_t stream) {
