@@ -34,6 +34,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #define SSD_DBG_FILE 9u   // kDbgPrompt
 
@@ -57,9 +58,9 @@ template <int D>
 struct Cfg {
     static constexpr int HALF = kTile * 128;        // 128 rows of 64 places, 128-byte swizzle
     static constexpr int OPERAND = HALF * (D / 64);
-    static constexpr int NK = D == 64 ? 3 : 2, NV = 3;
-    static constexpr int Q = 0, K = 2 * OPERAND, V = K + NK * OPERAND;
-    static constexpr int SMEM = V + NV * OPERAND + 1024;   // and what aligns it
+    static constexpr int NK = D == 64 ? 3 : 2, NV = NK;
+    static constexpr int Q = 0, K = 2 * OPERAND, V = K + NK * OPERAND, OUT = V + NV * OPERAND;
+    static constexpr int SMEM = OUT + 8 * 32 * 128 + 1024; // 64 places of a warp's rows; alignment
     static constexpr int LPR = D / 8, RPI = 32 / LPR;      // 16-byte chunks of a row, rows a pass
     static constexpr int BOX = kBox * D * 2;               // bytes of a box
 };
@@ -124,6 +125,11 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volati
     return __all_sync(~0u, wait_one(bar, parity, gave_up));
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                 "l"(__cvta_generic_to_global(src)), "r"(ok ? 16 : 0)
+                 : "memory");
+}
 __device__ __forceinline__ uint4 lds16(uint32_t at) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -166,7 +172,7 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, uin
 
 struct Barriers {
     uint64_t k_full[3], k_empty[3], v_land[3], v_full[3], v_empty[3];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2];
     uint64_t done;
 };
 // What is known of the last four tiles (a tile's loads begin when the products of scores of the
@@ -240,18 +246,48 @@ __device__ __forceinline__ void load_tiles(const PagedArgs &a, const Shape &s, c
 
 // ---- the checking warps -----------------------------------------------------------------
 //
+// They load the queries, a warp a block of rows, when the scores of the item before are made, and
+// look through the values.
+//
 // A probability of 0 would make NaN of an infinity or NaN that a row does not see: where some row
 // of the item does not see all of a tile, those of its values become zeros here, and the rows'
 // threads add them to the rows that see them.  Other tiles pass as they are.
 template <int D>
-__device__ __forceinline__ void check_values(const Shape &s, Barriers &bar, Notes &notes,
+__device__ __forceinline__ void load_queries(const PagedArgs &a, const Shape &s, const Item &it, int blk,
+                                             uint32_t dst) {
+    using C = Cfg<D>;
+    const int lane = threadIdx.x % 32;
+#pragma unroll 1
+    for (int k = 0; k < kRows / 32; ++k) {
+        const int r = min(it.rb * kItemRows + blk * kRows + k * 32 + lane, s.rows - 1), t = r / s.G;
+        const int64_t off = it.b * a.q_sb + t * a.q_st + (it.hk * s.G + r - t * s.G) * a.q_sh;
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += C::RPI) {
+            const int row = r0 + lane / C::LPR;
+            const int64_t o = __shfl_sync(~0u, off, row) + (lane % C::LPR) * 8;
+            const bool ok = SSD_IDX_OK(a.err, o + 7, a.q_n);
+            copy16(dst + chunk_at<D>(k * 32 + row, lane % C::LPR),
+                   static_cast<const __nv_bfloat16 *>(a.q) + (ok ? o : 0), ok);
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+}
+template <int D>
+__device__ __forceinline__ void check_values(const PagedArgs &a, const Shape &s, Barriers &bar, Notes &notes,
                                              volatile int *gave_up, uint32_t base, int warp) {
     using C = Cfg<D>;
     const int lane = threadIdx.x % 32;
-    int jt = 0;
+    int jt = 0, nitem = 0;
 #pragma unroll 1
     for (int x = blockIdx.x; x < s.items; x += gridDim.x) {
         const Item it = item_of(s, x);
+        if (it.ntiles == 0) continue;
+        if (nitem > 0 && !wait_warp(&bar.q_empty[warp], (nitem - 1) & 1, gave_up)) return;
+        load_queries<D>(a, s, it, warp, base + C::Q + warp * C::OPERAND);
+        if (lane == 0) ptx::mbar_arrive(&bar.q_full[warp]);
+        ++nitem;
 #pragma unroll 1
         for (int t = 0; t < it.ntiles; ++t, ++jt) {
             const int vs = jt % C::NV;
@@ -316,6 +352,7 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
         }
         ptx::mma_commit(&bar.s_full[blk]);
         if (blk == 1) ptx::mma_commit(&bar.k_empty[ks]);
+        if (t + 1 == it.ntiles) ptx::mma_commit(&bar.q_empty[blk]);
         return true;
     };
     if (!next_nonempty()) return;
@@ -336,14 +373,24 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
         ++jt;
 #pragma unroll 1
         for (int blk = 0; blk < 2; ++blk) {
-            if (!wait_one(&bar.p_full[blk], at & 1, gave_up) ||
+            const uint64_t v = ptx::sdesc(base + C::V + vs * C::OPERAND, C::HALF, 1024);
+            // the first 64 positions while the rows' threads work on the others
+            if (!wait_one(&bar.p_half[blk], at & 1, gave_up) ||
                 !wait_one(&bar.v_full[vs], (at / C::NV) & 1, gave_up))
                 return;
             ptx::tc_fence_after();
-            const uint64_t v = ptx::sdesc(base + C::V + vs * C::OPERAND, C::HALF, 1024);
-            for (int i = 0; i < steps; ++i)
-                ptx::mma_bf16_ts(tmem + kO + 128 * blk, tmem + kS + 128 * blk + 8 * i, v + uint64_t(i * 128),
-                                 kIdO, 1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < steps)
+                    ptx::mma_bf16_ts(tmem + kO + 128 * blk, tmem + kS + 128 * blk + 8 * i, v + uint64_t(i * 128),
+                                     kIdO, 1);
+            if (!wait_one(&bar.p_full[blk], at & 1, gave_up)) return;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int i = 4; i < 8; ++i)
+                if (i < steps)
+                    ptx::mma_bf16_ts(tmem + kO + 128 * blk, tmem + kS + 128 * blk + 8 * i, v + uint64_t(i * 128),
+                                     kIdO, 1);
             if (last) ptx::mma_commit(&bar.o_full[blk]);
             if (blk == 1) ptx::mma_commit(&bar.v_empty[vs]);
             if (more && !scores(blk)) return;
@@ -364,27 +411,6 @@ struct RowThread {
     uint32_t base, ts, to;            // shared memory; this warp's lanes of S and O
     int blk, lane, warp;              // warp: 0 to 3 of its block
 
-    // This warp's 32 rows of an item's queries, a row's offset in each lane's hands.  (The products
-    // of scores that read the item before's are done.)
-    __device__ __forceinline__ void load_queries(const Item &it) {
-        const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
-        const int r = min(it.rb * kItemRows + blk * kRows + warp * 32 + lane, s.rows - 1);
-        const int t = r / s.G;
-        const int64_t off = it.b * a.q_sb + t * a.q_st + (it.hk * s.G + r - t * s.G) * a.q_sh;
-        const uint32_t dst = base + C::Q + blk * C::OPERAND;
-#pragma unroll 4
-        for (int r0 = 0; r0 < 32; r0 += C::RPI) {
-            const int row = r0 + lane / C::LPR;
-            const int64_t o = __shfl_sync(~0u, off, row) + (lane % C::LPR) * 8;
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (SSD_IDX_OK(a.err, o + 7, a.q_n))
-                u = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + o);
-            u.x ^= sign, u.y ^= sign, u.z ^= sign, u.w ^= sign;
-            sts16(dst + chunk_at<D>(warp * 32 + row, lane % C::LPR), u);
-        }
-        ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(&bar.q_full[blk]);
-    }
     __device__ __forceinline__ void zero_outputs() {
         uint32_t z[32];
 #pragma unroll
@@ -420,7 +446,7 @@ struct RowThread {
     __device__ __forceinline__ bool run() {
         const float qs = fabsf(a.scale) * kLog2e;
         int jt = 0, nitem = 0;
-        bool ready = false;           // this item's queries are in shared memory
+        const uint32_t sign = a.scale < 0.f ? 0x80000000u : 0u;
 #pragma unroll 1
         for (int x = blockIdx.x; x < s.items; x += gridDim.x) {
             const Item it = item_of(s, x);
@@ -431,11 +457,7 @@ struct RowThread {
             const int vb = own < it.lo ? min(own + 1, it.ns) : it.ns + own - it.lo + 1;
             const int va = s.window > 0 ? it.ns + max(own - s.window + 1 - it.lo, 0) : 0;
             float m = -INFINITY, l = 0.f;
-            if (it.ntiles) {
-                if (!ready) load_queries(it);
-                ready = false;
-                zero_outputs();
-            }
+            if (it.ntiles) zero_outputs();
 #pragma unroll 1
             for (int t = 0; t < it.ntiles; ++t, ++jt) {
                 if (!wait_warp(&bar.s_full[blk], jt & 1, gave_up)) return false;
@@ -446,6 +468,12 @@ struct RowThread {
                 for (int c = 0; c < 4; ++c)
                     if (32 * c < width) ptx::tmem_ld32(ts + 32 * c, raw[c]);
                 ptx::tmem_ld_wait();
+                if (sign) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) raw[c][i] ^= sign;
+                }
                 // every row of the warp sees the whole tile?
                 uint32_t vis[4];
                 const uint32_t there = notes.there[jt & 3];
@@ -496,16 +524,14 @@ struct RowThread {
                 const float minus = m == -INFINITY ? 0.f : -m;
                 const F2 mm = f2(minus, minus), qq = f2(qs, qs);
                 F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (32 * c >= width) break;
+                auto weights = [&](auto whole, int c) {
                     uint32_t p[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float2 e = parts(mul(add(f2(__uint_as_float(raw[c][2 * i]),
                                                           __uint_as_float(raw[c][2 * i + 1])), mm), qq));
                         float x0 = ex2(e.x), x1 = ex2(e.y);
-                        if (!all) {   // (a scale of 0 makes NaN of what is hidden)
+                        if constexpr (!decltype(whole)::value) {   // (a scale of 0 makes NaN of what is hidden)
                             if (!(vis[c] >> (2 * i) & 1)) x0 = 0.f;
                             if (!(vis[c] >> (2 * i + 1) & 1)) x1 = 0.f;
                         }
@@ -513,41 +539,52 @@ struct RowThread {
                         p[i] = pack_bf16(x0, x1);
                     }
                     ptx::tmem_st16(ts + 16 * c, p);
+                };
+                auto half_done = [&](uint64_t *b) {
+                    ptx::tmem_st_wait();
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(b);
+                };
+                if (all) {
+                    weights(std::true_type{}, 0);
+                    weights(std::true_type{}, 1);
+                    half_done(&bar.p_half[blk]);
+                    weights(std::true_type{}, 2);
+                    weights(std::true_type{}, 3);
+                } else {
+                    weights(std::false_type{}, 0);
+                    if (32 < width) weights(std::false_type{}, 1);
+                    half_done(&bar.p_half[blk]);
+                    if (64 < width) weights(std::false_type{}, 2);
+                    if (96 < width) weights(std::false_type{}, 3);
                 }
+                half_done(&bar.p_full[blk]);
                 const float2 s0 = parts(add(sum[0], sum[1]));
                 l += s0.x + s0.y;
-                ptx::tmem_st_wait();
-                ptx::tc_fence_before();
-                ptx::mbar_arrive(&bar.p_full[blk]);
             }
-            // The scores of this item are done with: the next one's queries.
             if (it.ntiles) {
-#pragma unroll 1
-                for (int y = x + gridDim.x; y < s.items && !ready; y += gridDim.x) {
-                    const Item nx = item_of(s, y);
-                    if (!nx.ntiles) continue;
-                    load_queries(nx);
-                    ready = true;
-                }
                 if (!wait_warp(&bar.o_full[blk], nitem & 1, gave_up)) return false;
                 ptx::tc_fence_after();
                 ++nitem;
             }
+            // Rows of 64 places go through shared memory, so that stores are whole lines (a row a
+            // thread, 16 bytes at a time, took 3800 cycles an item).
             const int tk = rr / s.G, h = it.hk * s.G + rr - tk * s.G;
-            const int64_t off = it.b * a.o_sb + tk * a.o_st + h * a.o_sh;
+            const int64_t off = r < s.rows ? it.b * a.o_sb + tk * a.o_st + h * a.o_sh : -1;
             const float inv = l == 0.f ? 0.f : 1.f / l;
+            const uint32_t stage = base + C::OUT + (blk * 4 + warp) * 32 * 128;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                if (it.ntiles) {
-                    ptx::tmem_ld32(to + c, o);
-                    ptx::tmem_ld_wait();
-                } else {
+            for (int c = 0; c < D; c += 64) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0;
-                }
-                if (r < s.rows && SSD_IDX_OK(a.err, off + c + 31, a.o_n)) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + off + c);
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t o[32];
+                    if (it.ntiles) {
+                        ptx::tmem_ld32(to + c + 32 * k, o);
+                        ptx::tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = 0;
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t w[4];
@@ -555,9 +592,19 @@ struct RowThread {
                         for (int j = 0; j < 4; ++j)
                             w[j] = pack_bf16(__uint_as_float(o[8 * i + 2 * j]) * inv,
                                              __uint_as_float(o[8 * i + 2 * j + 1]) * inv);
-                        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        sts16(stage + lane * 128 + (((4 * k + i) ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
                     }
                 }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int row = 4 * k + lane / 8, chunk = lane % 8;
+                    const int64_t at = __shfl_sync(~0u, off, row);
+                    const uint4 u = lds16(stage + row * 128 + ((chunk ^ (row & 7)) << 4));
+                    if (at >= 0 && SSD_IDX_OK(a.err, at + c + chunk * 8 + 7, a.o_n))
+                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at + c + chunk * 8) = u;
+                }
+                __syncwarp();
             }
             const int64_t at = (int64_t(it.b) * s.T + tk) * a.Hq + h;
             if (a.lse && r < s.rows && SSD_IDX_OK(a.err, at, int64_t(s.B) * s.T * a.Hq))
@@ -590,7 +637,9 @@ k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             ptx::mbar_init(&bar.v_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&bar.q_full[i], kRows);
+            ptx::mbar_init(&bar.q_full[i], 1);
+            ptx::mbar_init(&bar.q_empty[i], 1);
+            ptx::mbar_init(&bar.p_half[i], kRows);
             ptx::mbar_init(&bar.p_full[i], kRows);
             ptx::mbar_init(&bar.s_full[i], 1);
             ptx::mbar_init(&bar.o_full[i], 1);
@@ -626,7 +675,7 @@ k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         } else if (warp == 9) {
             load_tiles<D>(a, s, &kmap, &vmap, bar, notes, &gave_up, base);
         } else {
-            check_values<D>(s, bar, notes, &gave_up, base, warp - 10);
+            check_values<D>(a, s, bar, notes, &gave_up, base, warp - 10);
         }
     }
     ptx::tc_fence_before();
