@@ -34,7 +34,6 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
-#include <type_traits>
 
 #define SSD_DBG_FILE 9u   // kDbgPrompt
 
@@ -141,6 +140,11 @@ __device__ __forceinline__ void sts16(uint32_t at, const uint4 &v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z),
                  "r"(v.w)
                  : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 __device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
     uint32_t r;
@@ -327,24 +331,31 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
     constexpr uint32_t kIdS = ptx::idesc_bf16_f32(kRows, 0, false, false);
     constexpr uint32_t kIdO = ptx::idesc_bf16_f32(kRows, D, false, true);
     int x = blockIdx.x, t = 0, jt = 0, nitem = 0;
-    Item it = {};
-    auto next_nonempty = [&]() {
-        while (x < s.items) {
-            it = item_of(s, x);
-            if (it.ntiles) return true;
-            x += gridDim.x;
+    // this item's positions and tiles, and the next one's (found while rows are worked on; what
+    // this thread waits for, the tensor core waits for)
+    int total = 0, ntiles = 0, next_total = 0, next_tiles = 0;
+    auto find_next = [&]() {
+        next_tiles = 0;
+        for (; x < s.items && next_tiles == 0; x += gridDim.x) {
+            const Item it = item_of(s, x);
+            next_total = it.total;
+            next_tiles = it.ntiles;
         }
-        return false;
     };
-    // scores of tile t of item number nitem, tile jt of the CTA
+    auto take_next = [&]() {
+        total = next_total;
+        ntiles = next_tiles;
+    };
+    // scores of tile t of the item, tile jt of the CTA
     auto scores = [&](int blk) {
-        if (t == 0 && !wait_one(&bar.q_full[blk], nitem & 1, gave_up)) return false;
         const int ks = jt % C::NK;
-        if (!wait_one(&bar.k_full[ks], (jt / C::NK) & 1, gave_up)) return false;
-        ptx::tc_fence_after();
-        const uint32_t id = kIdS | uint32_t(width_of(it, t) >> 3) << 17;
+        const uint32_t id = kIdS | uint32_t(min(kTile, (total - t * kTile + 31) & ~31) >> 3) << 17;
         const uint64_t q = ptx::sdesc(base + C::Q + blk * C::OPERAND, 16, 1024);
         const uint64_t k = ptx::sdesc(base + C::K + ks * C::OPERAND, 16, 1024);
+        if (t == 0) {
+            if (!wait_one(&bar.q_full[blk], nitem & 1, gave_up)) return false;
+            ptx::tc_fence_after();
+        }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
             const uint64_t o = uint64_t((i / 4) * C::HALF + (i % 4) * 32) >> 4;
@@ -352,32 +363,34 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
         }
         ptx::mma_commit(&bar.s_full[blk]);
         if (blk == 1) ptx::mma_commit(&bar.k_empty[ks]);
-        if (t + 1 == it.ntiles) ptx::mma_commit(&bar.q_empty[blk]);
+        if (t + 1 == ntiles) ptx::mma_commit(&bar.q_empty[blk]);
         return true;
     };
-    if (!next_nonempty()) return;
-    if (!scores(0) || !scores(1)) return;
+    auto keys_there = [&]() { return wait_one(&bar.k_full[jt % C::NK], (jt / C::NK) & 1, gave_up); };
+    find_next();
+    take_next();
+    if (ntiles == 0 || !keys_there() || !scores(0) || !scores(1)) return;
     for (;;) {
         const int vs = jt % C::NV, at = jt;
-        const int steps = min(kTile / 16, (it.total - t * kTile + 15) / 16);
-        const bool last = t + 1 == it.ntiles;
+        const int steps = min(kTile / 16, (total - t * kTile + 15) / 16);
+        const bool last = t + 1 == ntiles;
         bool more = true;
+        if (t == 0) find_next();
         if (last) {
-            x += gridDim.x;
             t = 0;
             ++nitem;
-            more = next_nonempty();
+            take_next();
+            more = ntiles > 0;
         } else {
             ++t;
         }
         ++jt;
+        if (!wait_one(&bar.v_full[vs], (at / C::NV) & 1, gave_up) || (more && !keys_there())) return;
+        const uint64_t v = ptx::sdesc(base + C::V + vs * C::OPERAND, C::HALF, 1024);
 #pragma unroll 1
         for (int blk = 0; blk < 2; ++blk) {
-            const uint64_t v = ptx::sdesc(base + C::V + vs * C::OPERAND, C::HALF, 1024);
             // the first 64 positions while the rows' threads work on the others
-            if (!wait_one(&bar.p_half[blk], at & 1, gave_up) ||
-                !wait_one(&bar.v_full[vs], (at / C::NV) & 1, gave_up))
-                return;
+            if (!wait_one(&bar.p_half[blk], at & 1, gave_up)) return;
             ptx::tc_fence_after();
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -444,12 +457,14 @@ struct RowThread {
     }
 
     __device__ __forceinline__ bool run() {
-        const float qs = fabsf(a.scale) * kLog2e;
+        // (a scale of 0 makes scores of 0, or NaN, before anything is hidden)
+        const bool flat = a.scale == 0.f;
+        const float qs = flat ? 1.f : fabsf(a.scale) * kLog2e;
         int jt = 0, nitem = 0;
         const uint32_t sign = a.scale < 0.f ? 0x80000000u : 0u;
+        Item it = item_of(s, blockIdx.x), next = it;
 #pragma unroll 1
-        for (int x = blockIdx.x; x < s.items; x += gridDim.x) {
-            const Item it = item_of(s, x);
+        for (int x = blockIdx.x; x < s.items; x += gridDim.x, it = next) {
             const int r = it.rb * kItemRows + blk * kRows + warp * 32 + lane, rr = min(r, s.rows - 1);
             const int own = it.len - s.T + rr / s.G;
             // what it sees of the item's run: [va, vb), and below vb what lies below `sinks` too (where
@@ -464,40 +479,43 @@ struct RowThread {
                 ptx::tc_fence_after();
                 const int v0 = t * kTile, width = width_of(it, t);
                 uint32_t raw[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (32 * c < width) ptx::tmem_ld32(ts + 32 * c, raw[c]);
-                ptx::tmem_ld_wait();
-                if (sign) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) raw[c][i] ^= sign;
-                }
+                ptx::tmem_ld32(ts, raw[0]);
+                if (32 < width) ptx::tmem_ld32(ts + 32, raw[1]);
                 // every row of the warp sees the whole tile?
-                uint32_t vis[4];
                 const uint32_t there = notes.there[jt & 3];
                 const bool all = __all_sync(~0u, v0 + kTile <= vb && (va <= v0 || v0 + kTile <= s.sinks) &&
                                                      there == (1u << kTile / kBox) - 1);
-                if (!all) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int b = v0 + 32 * c;
-                        auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
-                        vis[c] = (there >> (2 * c) & 1 ? 0xffffu : 0u) | (there >> (2 * c + 1) & 1 ? 0xffff0000u : 0u);
-                        vis[c] &= below(vb - b) & (~below(va - b) | below(s.sinks - b));
+                float mx = -INFINITY;
+                auto look = [&](int c) {
+                    if (sign | flat) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (!(vis[c] >> i & 1)) raw[c][i] = 0xff800000u;
+                            raw[c][i] = __float_as_uint(__uint_as_float(raw[c][i] ^ sign) * (flat ? 0.f : 1.f));
                     }
-                }
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    if (!all) {
+                        const int b = v0 + 32 * c;
+                        auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
+                        uint32_t vis = (there >> (2 * c) & 1 ? 0xffffu : 0u) | (there >> (2 * c + 1) & 1 ? 0xffff0000u : 0u);
+                        vis &= below(vb - b) & (~below(va - b) | below(s.sinks - b));
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                        for (int i = 0; i < 32; ++i) raw[c][i] = vis & (1u << i) ? raw[c][i] : 0xff800000u;
+                    }
+                    float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2)
-                        top[c] = fmaxf(top[c], fmaxf(__uint_as_float(raw[c][i]), __uint_as_float(raw[c][i + 1])));
-                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    for (int i = 0; i < 32; i += 4)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            top[k] = max3(top[k], __uint_as_float(raw[c][i + 2 * k]), __uint_as_float(raw[c][i + 2 * k + 1]));
+                    mx = max3(mx, top[0], top[1]);
+                };
+                ptx::tmem_ld_wait();
+                if (64 < width) ptx::tmem_ld32(ts + 64, raw[2]);
+                if (96 < width) ptx::tmem_ld32(ts + 96, raw[3]);
+                look(0);
+                if (32 < width) look(1);
+                ptx::tmem_ld_wait();
+                if (64 < width) look(2);
+                if (96 < width) look(3);
                 if (__any_sync(~0u, (mx - m) * qs > kSlack || (m == -INFINITY && mx != m))) {
                     const float to_m = fmaxf(m, mx);
                     const float f = m == -INFINITY ? 1.f : ex2((m - to_m) * qs);
@@ -524,17 +542,13 @@ struct RowThread {
                 const float minus = m == -INFINITY ? 0.f : -m;
                 const F2 mm = f2(minus, minus), qq = f2(qs, qs);
                 F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-                auto weights = [&](auto whole, int c) {
+                auto weights = [&](int c) {
                     uint32_t p[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float2 e = parts(mul(add(f2(__uint_as_float(raw[c][2 * i]),
                                                           __uint_as_float(raw[c][2 * i + 1])), mm), qq));
-                        float x0 = ex2(e.x), x1 = ex2(e.y);
-                        if constexpr (!decltype(whole)::value) {   // (a scale of 0 makes NaN of what is hidden)
-                            if (!(vis[c] >> (2 * i) & 1)) x0 = 0.f;
-                            if (!(vis[c] >> (2 * i + 1) & 1)) x1 = 0.f;
-                        }
+                        const float x0 = ex2(e.x), x1 = ex2(e.y);
                         sum[i & 1] = add(sum[i & 1], f2(x0, x1));
                         p[i] = pack_bf16(x0, x1);
                     }
@@ -545,23 +559,16 @@ struct RowThread {
                     ptx::tc_fence_before();
                     ptx::mbar_arrive(b);
                 };
-                if (all) {
-                    weights(std::true_type{}, 0);
-                    weights(std::true_type{}, 1);
-                    half_done(&bar.p_half[blk]);
-                    weights(std::true_type{}, 2);
-                    weights(std::true_type{}, 3);
-                } else {
-                    weights(std::false_type{}, 0);
-                    if (32 < width) weights(std::false_type{}, 1);
-                    half_done(&bar.p_half[blk]);
-                    if (64 < width) weights(std::false_type{}, 2);
-                    if (96 < width) weights(std::false_type{}, 3);
-                }
+                weights(0);
+                if (32 < width) weights(1);
+                half_done(&bar.p_half[blk]);
+                if (64 < width) weights(2);
+                if (96 < width) weights(3);
                 half_done(&bar.p_full[blk]);
                 const float2 s0 = parts(add(sum[0], sum[1]));
                 l += s0.x + s0.y;
             }
+            if (x + gridDim.x < s.items) next = item_of(s, x + gridDim.x);
             if (it.ntiles) {
                 if (!wait_warp(&bar.o_full[blk], nitem & 1, gave_up)) return false;
                 ptx::tc_fence_after();
@@ -575,16 +582,18 @@ struct RowThread {
             const uint32_t stage = base + C::OUT + (blk * 4 + warp) * 32 * 128;
 #pragma unroll 1
             for (int c = 0; c < D; c += 64) {
+                uint32_t out[2][32];
+                if (it.ntiles) {
+                    ptx::tmem_ld32(to + c, out[0]);
+                    ptx::tmem_ld32(to + c + 32, out[1]);
+                    ptx::tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) out[0][i] = out[1][i] = 0;
+                }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    uint32_t o[32];
-                    if (it.ntiles) {
-                        ptx::tmem_ld32(to + c + 32 * k, o);
-                        ptx::tmem_ld_wait();
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = 0;
-                    }
+                    const uint32_t(&o)[32] = out[k];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t w[4];
