@@ -13,7 +13,7 @@
 // What bounds it is the products, 4 D flops a row and position: with 256 rows to a tile the
 // reads from L2 are 64 KB for 2 x 4.2 Mflop of them each.  So one thread issues nothing but
 // products, in the order S0, S1, then for every tile O0, S0 (next), O1, S1 (next): while a
-// block's exponentials run, the tensor core has the other's products.  One warp loads (TMA),
+// block's exponentials run, the tensor core has the other's products.  Two warps load (TMA),
 // tiles ahead and across items, and the CTA goes from item to item (sequence, head, 256 rows)
 // with the next one's queries and keys already there.
 //
@@ -44,8 +44,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kRows = 128, kItemRows = 2 * kRows;   // rows of a block, of an item
 constexpr int kTile = 128;                          // positions of a tile
 constexpr int kBox = 16;                             // positions of a load
-constexpr int kCheckWarps = 2;
-constexpr int kThreads = 2 * kRows + 32 * (2 + kCheckWarps);
+constexpr int kThreads = 2 * kRows + 32 * 4;         // and a warp that issues, two that load, one that checks
 // Registers of a thread: 168 at the launch (65536 / 384), shared out as 208 for the rows'
 // threads and 88 for the others: 256 x 208 + 128 x 88 = 384 x 168.
 constexpr int kRowRegs = 208, kOtherRegs = 88;
@@ -100,10 +99,6 @@ __device__ __forceinline__ Item item_of(const Shape &s, int x) {
     return it;
 }
 __device__ __forceinline__ int pos_of(const Item &it, int v) { return v < it.ns ? v : it.lo + (v - it.ns); }
-// Positions of tile t of an item, rounded up to whole groups of 32.
-__device__ __forceinline__ int width_of(const Item &it, int t) {
-    return min(kTile, (it.total - t * kTile + 31) & ~31);
-}
 
 // Waits for a phase of bar: false after two seconds, and at once where some thread of the CTA
 // has given up.
@@ -176,15 +171,15 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, uin
 
 struct Barriers {
     uint64_t k_full[3], k_empty[3], v_land[3], v_full[3], v_empty[3];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2];
+    uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
     uint64_t done;
 };
 // What is known of the last four tiles (a tile's loads begin when the products of scores of the
 // tile NK before it are done, so the rows' threads are at most three tiles behind).
 struct Notes {
     uint32_t there[4];                // bit i: box i's page exists
-    int foul[4];                      // the tile's number + 1 if a value that was looked at is infinite
-                                      // or NaN
+    int foul[4];                      // of the last four items: the item's number + 1 if a value that was
+                                      // looked at is infinite or NaN
 };
 
 // The rows of an item: from where on some do not see all that is there (v >= least), and below
@@ -195,25 +190,28 @@ __device__ __forceinline__ bool all_see(const Shape &s, const Item &it, int v0) 
     return v0 + kTile <= least && (most <= v0 || v0 + kTile <= s.sinks);
 }
 
-// ---- the loading warp -------------------------------------------------------------------
+// ---- the loading warps, one for keys and one for values ---------------------------------------
 template <int D>
-__device__ __forceinline__ void load_tiles(const PagedArgs &a, const Shape &s, const CUtensorMap *kmap,
-                                           const CUtensorMap *vmap, Barriers &bar, Notes &notes,
-                                           volatile int *gave_up, uint32_t base) {
+__device__ __forceinline__ void load_tiles(const PagedArgs &a, const Shape &s, const CUtensorMap *map,
+                                           Barriers &bar, Notes &notes, volatile int *gave_up, uint32_t base,
+                                           bool values) {
     using C = Cfg<D>;
+    constexpr int N = C::NK;
+    static_assert(C::NK == C::NV, "");
+    uint64_t *const landed = values ? bar.v_land : bar.k_full, *const empty = values ? bar.v_empty : bar.k_empty;
+    const uint32_t slots = base + (values ? C::V : C::K);
     const int lane = threadIdx.x % 32;
     int jt = 0;                       // tile of the CTA
     // Where a wait ran out: what is under way lands before the CTA leaves.
-    auto settle = [&](int nk, int nv) {
-        for (int i = max(0, nk - C::NK); i < nk; ++i) ptx::mbar_wait(&bar.k_full[i % C::NK], (i / C::NK) & 1);
-        for (int i = max(0, nv - C::NV); i < nv; ++i) ptx::mbar_wait(&bar.v_land[i % C::NV], (i / C::NV) & 1);
+    auto settle = [&]() {
+        for (int i = max(0, jt - N); i < jt; ++i) ptx::mbar_wait(&landed[i % N], (i / N) & 1);
     };
 #pragma unroll 1
     for (int x = blockIdx.x; x < s.items; x += gridDim.x) {
         const Item it = item_of(s, x);
 #pragma unroll 1
         for (int t = 0; t < it.ntiles; ++t, ++jt) {
-            const int ks = jt % C::NK, vs = jt % C::NV;
+            const int st = jt % N;
             const int v = t * kTile + lane * kBox, pos = pos_of(it, v);
             const int p = pos / a.c.ps, at = pos - p * a.c.ps;
             const int boxes = min(kTile / kBox, (it.total - t * kTile + kBox - 1) / kBox);
@@ -222,65 +220,31 @@ __device__ __forceinline__ void load_tiles(const PagedArgs &a, const Shape &s, c
             const bool ok = page >= 0 && page < a.c.pages;
             const uint32_t there = __ballot_sync(~0u, ok);
             if (!ok) page = a.c.pages;        // outside: zeros
-            if (jt >= C::NK && !wait_warp(&bar.k_empty[ks], (jt / C::NK - 1) & 1, gave_up)) return settle(jt, jt);
+            if (jt >= N && !wait_warp(&empty[st], (jt / N - 1) & 1, gave_up)) return settle();
             if (lane == 0) {
-                notes.there[jt & 3] = there;
-                ptx::mbar_arrive_expect_tx(&bar.k_full[ks], boxes * C::BOX);
+                if (!values) notes.there[jt & 3] = there;
+                ptx::mbar_arrive_expect_tx(&landed[st], boxes * C::BOX);
             }
             __syncwarp();
             if (lane < boxes) {
 #pragma unroll
                 for (int h = 0; h < D / 64; ++h)
-                    load_box(base + C::K + ks * C::OPERAND + h * C::HALF + lane * kBox * 128, kmap,
-                             &bar.k_full[ks], 64 * h, at, it.hk, page);
-            }
-            if (jt >= C::NV && !wait_warp(&bar.v_empty[vs], (jt / C::NV - 1) & 1, gave_up)) return settle(jt + 1, jt);
-            if (lane == 0) ptx::mbar_arrive_expect_tx(&bar.v_land[vs], boxes * C::BOX);
-            __syncwarp();
-            if (lane < boxes) {
-#pragma unroll
-                for (int h = 0; h < D / 64; ++h)
-                    load_box(base + C::V + vs * C::OPERAND + h * C::HALF + lane * kBox * 128, vmap,
-                             &bar.v_land[vs], 64 * h, at, it.hk, page);
+                    load_box(slots + st * C::OPERAND + h * C::HALF + lane * kBox * 128, map, &landed[st], 64 * h,
+                             at, it.hk, page);
             }
         }
     }
-    if (*gave_up) settle(jt, jt);
+    if (*gave_up) settle();
 }
 
-// ---- the checking warps -----------------------------------------------------------------
-//
-// They load the queries, a warp a block of rows, when the scores of the item before are made, and
-// look through the values.
+// ---- the checking warp ------------------------------------------------------------------
 //
 // A probability of 0 would make NaN of an infinity or NaN that a row does not see: where some row
-// of the item does not see all of a tile, those of its values become zeros here, and the rows'
-// threads add them to the rows that see them.  Other tiles pass as they are.
+// of the item does not see all of a tile, those of its values become zeros here, and at the item's
+// end the rows' threads add them to the rows that see them.  Other tiles pass as they are.
 template <int D>
-__device__ __forceinline__ void load_queries(const PagedArgs &a, const Shape &s, const Item &it, int blk,
-                                             uint32_t dst) {
-    using C = Cfg<D>;
-    const int lane = threadIdx.x % 32;
-#pragma unroll 1
-    for (int k = 0; k < kRows / 32; ++k) {
-        const int r = min(it.rb * kItemRows + blk * kRows + k * 32 + lane, s.rows - 1), t = r / s.G;
-        const int64_t off = it.b * a.q_sb + t * a.q_st + (it.hk * s.G + r - t * s.G) * a.q_sh;
-#pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += C::RPI) {
-            const int row = r0 + lane / C::LPR;
-            const int64_t o = __shfl_sync(~0u, off, row) + (lane % C::LPR) * 8;
-            const bool ok = SSD_IDX_OK(a.err, o + 7, a.q_n);
-            copy16(dst + chunk_at<D>(k * 32 + row, lane % C::LPR),
-                   static_cast<const __nv_bfloat16 *>(a.q) + (ok ? o : 0), ok);
-        }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
-}
-template <int D>
-__device__ __forceinline__ void check_values(const PagedArgs &a, const Shape &s, Barriers &bar, Notes &notes,
-                                             volatile int *gave_up, uint32_t base, int warp) {
+__device__ __forceinline__ void check_values(const Shape &s, Barriers &bar, Notes &notes,
+                                             volatile int *gave_up, uint32_t base) {
     using C = Cfg<D>;
     const int lane = threadIdx.x % 32;
     int jt = 0, nitem = 0;
@@ -288,10 +252,6 @@ __device__ __forceinline__ void check_values(const PagedArgs &a, const Shape &s,
     for (int x = blockIdx.x; x < s.items; x += gridDim.x) {
         const Item it = item_of(s, x);
         if (it.ntiles == 0) continue;
-        if (nitem > 0 && !wait_warp(&bar.q_empty[warp], (nitem - 1) & 1, gave_up)) return;
-        load_queries<D>(a, s, it, warp, base + C::Q + warp * C::OPERAND);
-        if (lane == 0) ptx::mbar_arrive(&bar.q_full[warp]);
-        ++nitem;
 #pragma unroll 1
         for (int t = 0; t < it.ntiles; ++t, ++jt) {
             const int vs = jt % C::NV;
@@ -299,31 +259,36 @@ __device__ __forceinline__ void check_values(const PagedArgs &a, const Shape &s,
             if (!all_see(s, it, t * kTile)) {
                 const int rows = min(kTile, (it.total - t * kTile + kBox - 1) / kBox * kBox);
                 const uint32_t slot = base + C::V + vs * C::OPERAND;
-                bool foul = false;
-#pragma unroll 4
-                for (int r0 = warp * C::RPI; r0 < rows; r0 += kCheckWarps * C::RPI) {
-                    const uint32_t at = slot + chunk_at<D>(r0 + lane / C::LPR, lane % C::LPR);
-                    const uint4 u = lds16(at);
-                    uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                    bool mine = false;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u, mine = true;
-                        if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu, mine = true;
-                    }
-                    if (mine) sts16(at, make_uint4(w[0], w[1], w[2], w[3]));
-                    foul |= mine;
+                // the largest magnitude of each lane's values, as 16-bit integers
+                uint32_t most = 0;
+#pragma unroll 8
+                for (int r0 = 0; r0 < rows; r0 += C::RPI) {
+                    const uint4 u = lds16(slot + chunk_at<D>(r0 + lane / C::LPR, lane % C::LPR));
+                    most = __vmaxu2(__vmaxu2(most, u.x & 0x7fff7fffu), u.y & 0x7fff7fffu);
+                    most = __vmaxu2(__vmaxu2(most, u.z & 0x7fff7fffu), u.w & 0x7fff7fffu);
                 }
-                if (__any_sync(~0u, foul) && lane == 0) notes.foul[jt & 3] = jt + 1;
+                if (__any_sync(~0u, __vcmpgeu2(most, 0x7f807f80u) != 0)) {
+#pragma unroll 1
+                    for (int r0 = 0; r0 < rows; r0 += C::RPI) {
+                        const uint32_t at = slot + chunk_at<D>(r0 + lane / C::LPR, lane % C::LPR);
+                        const uint4 u = lds16(at);
+                        uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[i] &= ~__vcmpgeu2(w[i] & 0x7fff7fffu, 0x7f807f80u);
+                        sts16(at, make_uint4(w[0], w[1], w[2], w[3]));
+                    }
+                    if (lane == 0) notes.foul[nitem & 3] = nitem + 1;
+                }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
             }
             if (lane == 0) ptx::mbar_arrive(&bar.v_full[vs]);
         }
+        ++nitem;
     }
 }
 
-// ---- the issuing thread -------------------------------------------------------------------
+// ---- the issuing thread -----------------------------------------------------------------------
 template <int D>
 __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile int *gave_up, uint32_t base,
                                       uint32_t tmem) {
@@ -331,7 +296,7 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
     constexpr uint32_t kIdS = ptx::idesc_bf16_f32(kRows, 0, false, false);
     constexpr uint32_t kIdO = ptx::idesc_bf16_f32(kRows, D, false, true);
     int x = blockIdx.x, t = 0, jt = 0, nitem = 0;
-    // this item's positions and tiles, and the next one's (found while rows are worked on; what
+    // this item's positions and tiles, and the next one's (found while rows are worked on: what
     // this thread waits for, the tensor core waits for)
     int total = 0, ntiles = 0, next_total = 0, next_tiles = 0;
     auto find_next = [&]() {
@@ -346,16 +311,15 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
         total = next_total;
         ntiles = next_tiles;
     };
-    // scores of tile t of the item, tile jt of the CTA
+    // a block's scores of tile t of the item, tile jt of the CTA
     auto scores = [&](int blk) {
         const int ks = jt % C::NK;
         const uint32_t id = kIdS | uint32_t(min(kTile, (total - t * kTile + 31) & ~31) >> 3) << 17;
         const uint64_t q = ptx::sdesc(base + C::Q + blk * C::OPERAND, 16, 1024);
         const uint64_t k = ptx::sdesc(base + C::K + ks * C::OPERAND, 16, 1024);
-        if (t == 0) {
-            if (!wait_one(&bar.q_full[blk], nitem & 1, gave_up)) return false;
-            ptx::tc_fence_after();
-        }
+        if (blk == 0 && !wait_one(&bar.k_full[ks], (jt / C::NK) & 1, gave_up)) return false;
+        if (t == 0 && !wait_one(&bar.q_full[blk], nitem & 1, gave_up)) return false;
+        ptx::tc_fence_after();
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
             const uint64_t o = uint64_t((i / 4) * C::HALF + (i % 4) * 32) >> 4;
@@ -363,13 +327,11 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
         }
         ptx::mma_commit(&bar.s_full[blk]);
         if (blk == 1) ptx::mma_commit(&bar.k_empty[ks]);
-        if (t + 1 == ntiles) ptx::mma_commit(&bar.q_empty[blk]);
         return true;
     };
-    auto keys_there = [&]() { return wait_one(&bar.k_full[jt % C::NK], (jt / C::NK) & 1, gave_up); };
     find_next();
     take_next();
-    if (ntiles == 0 || !keys_there() || !scores(0) || !scores(1)) return;
+    if (ntiles == 0 || !scores(0) || !scores(1)) return;
     for (;;) {
         const int vs = jt % C::NV, at = jt;
         const int steps = min(kTile / 16, (total - t * kTile + 15) / 16);
@@ -385,25 +347,22 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
             ++t;
         }
         ++jt;
-        if (!wait_one(&bar.v_full[vs], (at / C::NV) & 1, gave_up) || (more && !keys_there())) return;
         const uint64_t v = ptx::sdesc(base + C::V + vs * C::OPERAND, C::HALF, 1024);
 #pragma unroll 1
         for (int blk = 0; blk < 2; ++blk) {
+            if (blk == 0 && !wait_one(&bar.v_full[vs], (at / C::NV) & 1, gave_up)) return;
+            const uint32_t scores_at = tmem + kS + 128 * blk, outputs_at = tmem + kO + 128 * blk;
             // the first 64 positions while the rows' threads work on the others
             if (!wait_one(&bar.p_half[blk], at & 1, gave_up)) return;
             ptx::tc_fence_after();
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (i < steps)
-                    ptx::mma_bf16_ts(tmem + kO + 128 * blk, tmem + kS + 128 * blk + 8 * i, v + uint64_t(i * 128),
-                                     kIdO, 1);
+                if (i < steps) ptx::mma_bf16_ts(outputs_at, scores_at + 8 * i, v + uint64_t(i * 128), kIdO, 1);
             if (!wait_one(&bar.p_full[blk], at & 1, gave_up)) return;
             ptx::tc_fence_after();
 #pragma unroll
             for (int i = 4; i < 8; ++i)
-                if (i < steps)
-                    ptx::mma_bf16_ts(tmem + kO + 128 * blk, tmem + kS + 128 * blk + 8 * i, v + uint64_t(i * 128),
-                                     kIdO, 1);
+                if (i < steps) ptx::mma_bf16_ts(outputs_at, scores_at + 8 * i, v + uint64_t(i * 128), kIdO, 1);
             if (last) ptx::mma_commit(&bar.o_full[blk]);
             if (blk == 1) ptx::mma_commit(&bar.v_empty[vs]);
             if (more && !scores(blk)) return;
@@ -432,11 +391,12 @@ struct RowThread {
         for (int c = 0; c < D; c += 32) ptx::tmem_st32(to + c, z);
         ptx::tmem_st_wait();
     }
-    // Infinities and NaN of a tile's values, added to the rows that see them (zeros stand in their
-    // place; a probability makes no difference to them).
-    __device__ __forceinline__ void add_foul(const Item &it, int t, int own) {
+    // Infinities and NaN of an item's values, added to the rows that see them where zeros stand in
+    // their place (a probability makes no difference to them).
+    __device__ __forceinline__ void add_foul(const Item &it, int own) {
 #pragma unroll 1
-        for (int v = t * kTile; v < min(it.total, (t + 1) * kTile); ++v) {
+        for (int v = 0; v < it.total; ++v) {
+            if (all_see(s, it, v / kTile * kTile)) continue;
             const int pos = pos_of(it, v), p = pos / a.c.ps;
             const int page = SSD_IDX_OK(a.err, it.b * a.tb + p, a.t_n) ? a.table[it.b * a.tb + p] : -1;
             if (page < 0 || page >= a.c.pages) continue;
@@ -456,12 +416,116 @@ struct RowThread {
         }
     }
 
+    // This warp's 32 rows of an item's queries to shared memory (the products that read the ones
+    // before them are done); and their arrival.
+    __device__ __forceinline__ void load_queries(const Item &it) {
+        const int r = min(it.rb * kItemRows + blk * kRows + warp * 32 + lane, s.rows - 1), t = r / s.G;
+        const int64_t off = it.b * a.q_sb + t * a.q_st + (it.hk * s.G + r - t * s.G) * a.q_sh;
+        const uint32_t dst = base + C::Q + blk * C::OPERAND;
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += C::RPI) {
+            const int row = r0 + lane / C::LPR;
+            const int64_t o = __shfl_sync(~0u, off, row) + (lane % C::LPR) * 8;
+            const bool ok = SSD_IDX_OK(a.err, o + 7, a.q_n);
+            copy16(dst + chunk_at<D>(warp * 32 + row, lane % C::LPR),
+                   static_cast<const __nv_bfloat16 *>(a.q) + (ok ? o : 0), ok);
+        }
+    }
+    __device__ __forceinline__ void queries_loaded() {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(&bar.q_full[blk]);
+    }
+
+    // Tile t of an item for this thread's row, which sees [va, vb) of its run, and below vb what lies
+    // below `sinks` too: scores to weights, with the row's reference m and sum l.  kWhole: all rows of
+    // the warp see 128 positions.
+    template <bool kWhole>
+    __device__ __forceinline__ void tile(int t, int va, int vb, uint32_t there, float qs, float &m,
+                                         float &l) {
+        const int v0 = t * kTile;
+        uint32_t raw[4][32];
+        // (of a narrower tile too: what its products have not written is not seen)
+        ptx::tmem_ld32(ts, raw[0]);
+        ptx::tmem_ld32(ts + 32, raw[1]);
+        float mx = -INFINITY;
+        auto look = [&](int c) {
+            if constexpr (!kWhole) {
+                const int b = v0 + 32 * c;
+                auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
+                uint32_t vis = (there >> (2 * c) & 1 ? 0xffffu : 0u) | (there >> (2 * c + 1) & 1 ? 0xffff0000u : 0u);
+                vis &= below(vb - b) & (~below(va - b) | below(s.sinks - b));
+#pragma unroll
+                for (int i = 0; i < 32; ++i) raw[c][i] = vis & (1u << i) ? raw[c][i] : 0xff800000u;
+            }
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    top[k] = max3(top[k], __uint_as_float(raw[c][i + 2 * k]), __uint_as_float(raw[c][i + 2 * k + 1]));
+            mx = max3(mx, top[0], top[1]);
+        };
+        ptx::tmem_ld_wait();
+        ptx::tmem_ld32(ts + 64, raw[2]);
+        ptx::tmem_ld32(ts + 96, raw[3]);
+        look(0);
+        look(1);
+        ptx::tmem_ld_wait();
+        look(2);
+        look(3);
+        if (__any_sync(~0u, (mx - m) * qs > kSlack || (m == -INFINITY && mx != m))) {
+            const float to_m = fmaxf(m, mx);
+            const float f = m == -INFINITY ? 1.f : ex2((m - to_m) * qs);
+            m = to_m;
+            l *= f;
+            if (t > 0) {              // (the outputs so far are complete: the scores came after them)
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+                    ptx::tmem_ld16(to + c, o);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    ptx::tmem_st16(to + c, o);
+                }
+                ptx::tmem_st_wait();
+            }
+        }
+        const float minus = m == -INFINITY ? 0.f : -m;
+        const F2 mm = f2(minus, minus), qq = f2(qs, qs);
+        F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+        auto weights = [&](int c) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float2 e = parts(mul(add(f2(__uint_as_float(raw[c][2 * i]),
+                                                  __uint_as_float(raw[c][2 * i + 1])), mm), qq));
+                const float x0 = ex2(e.x), x1 = ex2(e.y);
+                sum[i & 1] = add(sum[i & 1], f2(x0, x1));
+                p[i] = pack_bf16(x0, x1);
+            }
+            ptx::tmem_st16(ts + 16 * c, p);
+        };
+        auto half_done = [&](uint64_t *b) {
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(b);
+        };
+        weights(0);
+        weights(1);
+        half_done(&bar.p_half[blk]);
+        weights(2);
+        weights(3);
+        half_done(&bar.p_full[blk]);
+        const float2 s0 = parts(add(sum[0], sum[1]));
+        l += s0.x + s0.y;
+    }
+
     __device__ __forceinline__ bool run() {
-        // (a scale of 0 makes scores of 0, or NaN, before anything is hidden)
-        const bool flat = a.scale == 0.f;
-        const float qs = flat ? 1.f : fabsf(a.scale) * kLog2e;
+        const float qs = a.scale * kLog2e;
         int jt = 0, nitem = 0;
-        const uint32_t sign = a.scale < 0.f ? 0x80000000u : 0u;
+        bool loaded = false;          // this item's queries
         Item it = item_of(s, blockIdx.x), next = it;
 #pragma unroll 1
         for (int x = blockIdx.x; x < s.items; x += gridDim.x, it = next) {
@@ -472,106 +536,38 @@ struct RowThread {
             const int vb = own < it.lo ? min(own + 1, it.ns) : it.ns + own - it.lo + 1;
             const int va = s.window > 0 ? it.ns + max(own - s.window + 1 - it.lo, 0) : 0;
             float m = -INFINITY, l = 0.f;
-            if (it.ntiles) zero_outputs();
+            if (it.ntiles) {
+                if (!loaded) {
+                    load_queries(it);
+                    queries_loaded();
+                }
+                loaded = false;
+                zero_outputs();
+            }
 #pragma unroll 1
             for (int t = 0; t < it.ntiles; ++t, ++jt) {
                 if (!wait_warp(&bar.s_full[blk], jt & 1, gave_up)) return false;
                 ptx::tc_fence_after();
-                const int v0 = t * kTile, width = width_of(it, t);
-                uint32_t raw[4][32];
-                ptx::tmem_ld32(ts, raw[0]);
-                if (32 < width) ptx::tmem_ld32(ts + 32, raw[1]);
-                // every row of the warp sees the whole tile?
+                const int v0 = t * kTile;
                 const uint32_t there = notes.there[jt & 3];
-                const bool all = __all_sync(~0u, v0 + kTile <= vb && (va <= v0 || v0 + kTile <= s.sinks) &&
-                                                     there == (1u << kTile / kBox) - 1);
-                float mx = -INFINITY;
-                auto look = [&](int c) {
-                    if (sign | flat) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            raw[c][i] = __float_as_uint(__uint_as_float(raw[c][i] ^ sign) * (flat ? 0.f : 1.f));
-                    }
-                    if (!all) {
-                        const int b = v0 + 32 * c;
-                        auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
-                        uint32_t vis = (there >> (2 * c) & 1 ? 0xffffu : 0u) | (there >> (2 * c + 1) & 1 ? 0xffff0000u : 0u);
-                        vis &= below(vb - b) & (~below(va - b) | below(s.sinks - b));
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) raw[c][i] = vis & (1u << i) ? raw[c][i] : 0xff800000u;
-                    }
-                    float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            top[k] = max3(top[k], __uint_as_float(raw[c][i + 2 * k]), __uint_as_float(raw[c][i + 2 * k + 1]));
-                    mx = max3(mx, top[0], top[1]);
-                };
-                ptx::tmem_ld_wait();
-                if (64 < width) ptx::tmem_ld32(ts + 64, raw[2]);
-                if (96 < width) ptx::tmem_ld32(ts + 96, raw[3]);
-                look(0);
-                if (32 < width) look(1);
-                ptx::tmem_ld_wait();
-                if (64 < width) look(2);
-                if (96 < width) look(3);
-                if (__any_sync(~0u, (mx - m) * qs > kSlack || (m == -INFINITY && mx != m))) {
-                    const float to_m = fmaxf(m, mx);
-                    const float f = m == -INFINITY ? 1.f : ex2((m - to_m) * qs);
-                    m = to_m;
-                    l *= f;
-                    if (t > 0) {
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
-                            uint32_t o[16];
-                            ptx::tmem_ld16(to + c, o);
-                            ptx::tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            ptx::tmem_st16(to + c, o);
-                        }
-                        ptx::tmem_st_wait();
-                    }
-                }
-                // (also where all of this warp's rows see what another's don't)
-                if (!all_see(s, it, v0)) {
-                    if (!wait_warp(&bar.v_full[jt % C::NV], (jt / C::NV) & 1, gave_up)) return false;
-                    if (notes.foul[jt & 3] == jt + 1) add_foul(it, t, own);
-                }
-                const float minus = m == -INFINITY ? 0.f : -m;
-                const F2 mm = f2(minus, minus), qq = f2(qs, qs);
-                F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-                auto weights = [&](int c) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 e = parts(mul(add(f2(__uint_as_float(raw[c][2 * i]),
-                                                          __uint_as_float(raw[c][2 * i + 1])), mm), qq));
-                        const float x0 = ex2(e.x), x1 = ex2(e.y);
-                        sum[i & 1] = add(sum[i & 1], f2(x0, x1));
-                        p[i] = pack_bf16(x0, x1);
-                    }
-                    ptx::tmem_st16(ts + 16 * c, p);
-                };
-                auto half_done = [&](uint64_t *b) {
-                    ptx::tmem_st_wait();
-                    ptx::tc_fence_before();
-                    ptx::mbar_arrive(b);
-                };
-                weights(0);
-                if (32 < width) weights(1);
-                half_done(&bar.p_half[blk]);
-                if (64 < width) weights(2);
-                if (96 < width) weights(3);
-                half_done(&bar.p_full[blk]);
-                const float2 s0 = parts(add(sum[0], sum[1]));
-                l += s0.x + s0.y;
+                if (__all_sync(~0u, v0 + kTile <= vb && (va <= v0 || v0 + kTile <= s.sinks) &&
+                                        there == (1u << kTile / kBox) - 1))
+                    tile<true>(t, va, vb, there, qs, m, l);
+                else
+                    tile<false>(t, va, vb, there, qs, m, l);
             }
+            // The scores of this item are done with: the next one's queries.
+            next.ntiles = 0;
             if (x + gridDim.x < s.items) next = item_of(s, x + gridDim.x);
+            if (it.ntiles && next.ntiles) {
+                load_queries(next);
+                queries_loaded();
+                loaded = true;
+            }
             if (it.ntiles) {
                 if (!wait_warp(&bar.o_full[blk], nitem & 1, gave_up)) return false;
                 ptx::tc_fence_after();
+                if (notes.foul[nitem & 3] == nitem + 1) add_foul(it, own);
                 ++nitem;
             }
             // Rows of 64 places go through shared memory, so that stores are whole lines (a row a
@@ -580,29 +576,27 @@ struct RowThread {
             const int64_t off = r < s.rows ? it.b * a.o_sb + tk * a.o_st + h * a.o_sh : -1;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const uint32_t stage = base + C::OUT + (blk * 4 + warp) * 32 * 128;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 64) {
-                uint32_t out[2][32];
+            uint32_t out[D / 32][32];
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
                 if (it.ntiles) {
-                    ptx::tmem_ld32(to + c, out[0]);
-                    ptx::tmem_ld32(to + c + 32, out[1]);
-                    ptx::tmem_ld_wait();
+                    ptx::tmem_ld32(to + 32 * k, out[k]);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) out[0][i] = out[1][i] = 0;
+                    for (int i = 0; i < 32; ++i) out[k][i] = 0;
                 }
+            }
+            ptx::tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t(&o)[32] = out[k];
+            for (int c = 0; c < D; c += 64) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t w[4];
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t *const o = &out[c / 32 + k / 4][8 * (k % 4)];
+                    uint32_t w[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            w[j] = pack_bf16(__uint_as_float(o[8 * i + 2 * j]) * inv,
-                                             __uint_as_float(o[8 * i + 2 * j + 1]) * inv);
-                        sts16(stage + lane * 128 + (((4 * k + i) ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        w[j] = pack_bf16(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                    sts16(stage + lane * 128 + ((k ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
                 }
                 __syncwarp();
 #pragma unroll
@@ -637,23 +631,22 @@ k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     const uint32_t base = (ptx::smem_u32(smem_raw) + 1023) & ~1023u;
     if (threadIdx.x == 0) {
         gave_up = 0;
+        ptx::mbar_init(&bar.done, 1);
         notes.foul[0] = notes.foul[1] = notes.foul[2] = notes.foul[3] = 0;
         for (int i = 0; i < 3; ++i) {
             ptx::mbar_init(&bar.k_full[i], 1);
             ptx::mbar_init(&bar.v_land[i], 1);
-            ptx::mbar_init(&bar.v_full[i], kCheckWarps);
+            ptx::mbar_init(&bar.v_full[i], 1);
             ptx::mbar_init(&bar.k_empty[i], 1);
             ptx::mbar_init(&bar.v_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&bar.q_full[i], 1);
-            ptx::mbar_init(&bar.q_empty[i], 1);
+            ptx::mbar_init(&bar.q_full[i], kRows);
             ptx::mbar_init(&bar.p_half[i], kRows);
             ptx::mbar_init(&bar.p_full[i], kRows);
             ptx::mbar_init(&bar.s_full[i], 1);
             ptx::mbar_init(&bar.o_full[i], 1);
         }
-        ptx::mbar_init(&bar.done, 1);
         ptx::fence_mbar_init();
     }
     if (warp == 8) {
@@ -681,10 +674,10 @@ k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 ptx::mbar_wait(&bar.done, 0);
             }
             __syncwarp();
-        } else if (warp == 9) {
-            load_tiles<D>(a, s, &kmap, &vmap, bar, notes, &gave_up, base);
+        } else if (warp < 11) {
+            load_tiles<D>(a, s, warp == 9 ? &kmap : &vmap, bar, notes, &gave_up, base, warp == 10);
         } else {
-            check_values<D>(a, s, bar, notes, &gave_up, base, warp - 10);
+            check_values<D>(s, bar, notes, &gave_up, base);
         }
     }
     ptx::tc_fence_before();
@@ -727,7 +720,8 @@ int64_t items_of(const PagedArgs &a) {
 
 bool prompt_fits(const PagedArgs &a) {
     const int64_t rows = int64_t(a.T) * (a.Hq / a.c.Hkv), items = items_of(a);
-    return a.c.dt == DT_BF16 && a.c.ps % kBox == 0 && a.c.pages > 0 && rows >= kItemRows / 2 && items * 4 >= device_sm_count() && items < (1 << 30);
+    return a.c.dt == DT_BF16 && a.scale > 0.f && a.c.ps % kBox == 0 && a.c.pages > 0 && rows >= kItemRows / 2 &&
+           items * 4 >= device_sm_count() && items < (1 << 30);
 }
 
 cudaError_t launch_paged_prompt(const PagedArgs &a, cudaStream_t stream) {
