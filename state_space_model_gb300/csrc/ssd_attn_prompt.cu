@@ -170,8 +170,9 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, uin
 }
 
 struct Barriers {
-    uint64_t k_full[3], k_empty[3], v_land[3], v_full[3], v_empty[3];
-    uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2];
+    uint64_t k_land[3], v_land[3];
+    uint64_t ready[3];                // a tile's values, looked through, and the next tile's keys
+    uint64_t q_full[2], s_full[2][3], p_full[2], o_full[2];
     uint64_t done;
 };
 // What is known of the last four tiles (a tile's loads begin when the products of scores of the
@@ -198,7 +199,7 @@ __device__ __forceinline__ void load_tiles(const PagedArgs &a, const Shape &s, c
     using C = Cfg<D>;
     constexpr int N = C::NK;
     static_assert(C::NK == C::NV, "");
-    uint64_t *const landed = values ? bar.v_land : bar.k_full, *const empty = values ? bar.v_empty : bar.k_empty;
+    uint64_t *const landed = values ? bar.v_land : bar.k_land;
     const uint32_t slots = base + (values ? C::V : C::K);
     const int lane = threadIdx.x % 32;
     int jt = 0;                       // tile of the CTA
@@ -220,7 +221,10 @@ __device__ __forceinline__ void load_tiles(const PagedArgs &a, const Shape &s, c
             const bool ok = page >= 0 && page < a.c.pages;
             const uint32_t there = __ballot_sync(~0u, ok);
             if (!ok) page = a.c.pages;        // outside: zeros
-            if (jt >= N && !wait_warp(&empty[st], (jt / N - 1) & 1, gave_up)) return settle();
+            // Block 1's scores of tile j are made: the keys of tile j have been read, and (its products are
+            // made in order) the values of tile j - 1.
+            const int j = jt - N + (values ? 1 : 0);
+            if (jt >= N && !wait_warp(&bar.s_full[1][j % N], (j / N) & 1, gave_up)) return settle();
             if (lane == 0) {
                 if (!values) notes.there[jt & 3] = there;
                 ptx::mbar_arrive_expect_tx(&landed[st], boxes * C::BOX);
@@ -252,6 +256,8 @@ __device__ __forceinline__ void check_values(const Shape &s, Barriers &bar, Note
     for (int x = blockIdx.x; x < s.items; x += gridDim.x) {
         const Item it = item_of(s, x);
         if (it.ntiles == 0) continue;
+        bool more = false;            // another item with tiles follows
+        for (int y = x + gridDim.x; y < s.items && !more; y += gridDim.x) more = item_of(s, y).ntiles > 0;
 #pragma unroll 1
         for (int t = 0; t < it.ntiles; ++t, ++jt) {
             const int vs = jt % C::NV;
@@ -282,7 +288,10 @@ __device__ __forceinline__ void check_values(const Shape &s, Barriers &bar, Note
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
             }
-            if (lane == 0) ptx::mbar_arrive(&bar.v_full[vs]);
+            // the next tile's keys too, so that the issuing thread waits once
+            if ((t + 1 < it.ntiles || more) && !wait_warp(&bar.k_land[(jt + 1) % C::NK], ((jt + 1) / C::NK) & 1, gave_up))
+                return;
+            if (lane == 0) ptx::mbar_arrive(&bar.ready[vs]);
         }
         ++nitem;
     }
@@ -317,7 +326,7 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
         const uint32_t id = kIdS | uint32_t(min(kTile, (total - t * kTile + 31) & ~31) >> 3) << 17;
         const uint64_t q = ptx::sdesc(base + C::Q + blk * C::OPERAND, 16, 1024);
         const uint64_t k = ptx::sdesc(base + C::K + ks * C::OPERAND, 16, 1024);
-        if (blk == 0 && !wait_one(&bar.k_full[ks], (jt / C::NK) & 1, gave_up)) return false;
+        if (jt == 0 && !wait_one(&bar.k_land[0], 0, gave_up)) return false;
         if (t == 0 && !wait_one(&bar.q_full[blk], nitem & 1, gave_up)) return false;
         ptx::tc_fence_after();
 #pragma unroll
@@ -325,8 +334,7 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
             const uint64_t o = uint64_t((i / 4) * C::HALF + (i % 4) * 32) >> 4;
             ptx::mma_bf16_ss(tmem + kS + 128 * blk, q + o, k + o, id, i != 0);
         }
-        ptx::mma_commit(&bar.s_full[blk]);
-        if (blk == 1) ptx::mma_commit(&bar.k_empty[ks]);
+        ptx::mma_commit(&bar.s_full[blk][ks]);
         return true;
     };
     find_next();
@@ -350,21 +358,14 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
         const uint64_t v = ptx::sdesc(base + C::V + vs * C::OPERAND, C::HALF, 1024);
 #pragma unroll 1
         for (int blk = 0; blk < 2; ++blk) {
-            if (blk == 0 && !wait_one(&bar.v_full[vs], (at / C::NV) & 1, gave_up)) return;
-            const uint32_t scores_at = tmem + kS + 128 * blk, outputs_at = tmem + kO + 128 * blk;
-            // the first 64 positions while the rows' threads work on the others
-            if (!wait_one(&bar.p_half[blk], at & 1, gave_up)) return;
-            ptx::tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < steps) ptx::mma_bf16_ts(outputs_at, scores_at + 8 * i, v + uint64_t(i * 128), kIdO, 1);
+            if (blk == 0 && !wait_one(&bar.ready[vs], (at / C::NV) & 1, gave_up)) return;
             if (!wait_one(&bar.p_full[blk], at & 1, gave_up)) return;
             ptx::tc_fence_after();
+            const uint32_t scores_at = tmem + kS + 128 * blk, outputs_at = tmem + kO + 128 * blk;
 #pragma unroll
-            for (int i = 4; i < 8; ++i)
+            for (int i = 0; i < 8; ++i)
                 if (i < steps) ptx::mma_bf16_ts(outputs_at, scores_at + 8 * i, v + uint64_t(i * 128), kIdO, 1);
             if (last) ptx::mma_commit(&bar.o_full[blk]);
-            if (blk == 1) ptx::mma_commit(&bar.v_empty[vs]);
             if (more && !scores(blk)) return;
         }
         if (!more) return;
@@ -507,17 +508,13 @@ struct RowThread {
             }
             ptx::tmem_st16(ts + 16 * c, p);
         };
-        auto half_done = [&](uint64_t *b) {
-            ptx::tmem_st_wait();
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(b);
-        };
         weights(0);
         weights(1);
-        half_done(&bar.p_half[blk]);
         weights(2);
         weights(3);
-        half_done(&bar.p_full[blk]);
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&bar.p_full[blk]);
         const float2 s0 = parts(add(sum[0], sum[1]));
         l += s0.x + s0.y;
     }
@@ -546,7 +543,7 @@ struct RowThread {
             }
 #pragma unroll 1
             for (int t = 0; t < it.ntiles; ++t, ++jt) {
-                if (!wait_warp(&bar.s_full[blk], jt & 1, gave_up)) return false;
+                if (!wait_warp(&bar.s_full[blk][jt % C::NK], (jt / C::NK) & 1, gave_up)) return false;
                 ptx::tc_fence_after();
                 const int v0 = t * kTile;
                 const uint32_t there = notes.there[jt & 3];
@@ -634,19 +631,17 @@ k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         ptx::mbar_init(&bar.done, 1);
         notes.foul[0] = notes.foul[1] = notes.foul[2] = notes.foul[3] = 0;
         for (int i = 0; i < 3; ++i) {
-            ptx::mbar_init(&bar.k_full[i], 1);
+            ptx::mbar_init(&bar.k_land[i], 1);
             ptx::mbar_init(&bar.v_land[i], 1);
-            ptx::mbar_init(&bar.v_full[i], 1);
-            ptx::mbar_init(&bar.k_empty[i], 1);
-            ptx::mbar_init(&bar.v_empty[i], 1);
+            ptx::mbar_init(&bar.ready[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&bar.q_full[i], kRows);
-            ptx::mbar_init(&bar.p_half[i], kRows);
             ptx::mbar_init(&bar.p_full[i], kRows);
-            ptx::mbar_init(&bar.s_full[i], 1);
             ptx::mbar_init(&bar.o_full[i], 1);
+            for (int k = 0; k < 3; ++k) ptx::mbar_init(&bar.s_full[i][k], 1);
         }
+        ptx::mbar_init(&bar.done, 1);
         ptx::fence_mbar_init();
     }
     if (warp == 8) {
