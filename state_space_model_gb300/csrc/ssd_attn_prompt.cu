@@ -21,7 +21,7 @@
 // through as one run in boxes of 16 of a page (so pages are multiples of 16; others take the
 // kernels of ssd_attn.cuh), so that a tile holds little that nobody needs wherever the window
 // begins.  (Copies by three warps, 16 bytes a lane, took any page size and four times as long: 253
-// us where the loads make 4096 tokens under a window of 1024 take 123.)
+// us where the loads make 4096 tokens under a window of 1024 take 85.)
 #include "ptx_sm100.cuh"
 #include "ssd_attn.h"
 #include "ssd_block_math.cuh"
@@ -66,9 +66,21 @@ static_assert(Cfg<128>::SMEM + 1024 <= 227 * 1024, "a CTA fits an SM");
 // Tensor memory: scores of the two blocks (P over them), outputs.
 constexpr uint32_t kS = 0, kO = 256;
 
+// Division of 0 <= n < 2^31 by a number known at the launch (T. Granlund and P. Montgomery, 1994): an item's
+// place takes several, one after another, where nothing else goes on.
+struct Divisor {
+    uint32_t d = 1, m = 0, shift = 0;
+    __host__ Divisor(uint32_t n = 1) : d(n) {
+        while ((uint64_t(1) << shift) < d) ++shift;
+        m = uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << shift) - d)) / d + 1);
+    }
+    __device__ __forceinline__ int of(int n) const { return int((__umulhi(m, uint32_t(n)) + uint32_t(n)) >> shift); }
+};
+
 struct Shape {
     const int32_t *lens;
-    int B, T, Hkv, G, cap, window, sinks, rows, nrb, items;
+    int B, T, Hkv, cap, window, sinks, rows, nrb, items;
+    Divisor heads, per_b, G, ps;      // by B Hkv, by Hkv, by the query heads of a key/value head, by the page
 };
 
 // Row block rb of sequence b and head hk.  Index v < total of the run of positions that some row
@@ -82,14 +94,14 @@ struct Item {
 // Item number x: the last rows come first, which see most where there is no window.
 __device__ __forceinline__ Item item_of(const Shape &s, int x) {
     Item it;
-    const int heads = s.B * s.Hkv, y = x / heads, bh = x - y * heads;
+    const int y = s.heads.of(x), bh = x - y * int(s.heads.d);
     it.rb = s.nrb - 1 - y;
-    it.b = bh / s.Hkv;
+    it.b = s.per_b.of(bh);
     it.hk = bh - it.b * s.Hkv;
     it.len = max(s.lens[it.b], 0);
     const int r0 = it.rb * kItemRows, r1 = min(r0 + kItemRows, s.rows) - 1;
-    it.emin = it.len - s.T + r0 / s.G;
-    it.emax = it.len - s.T + r1 / s.G;
+    it.emin = it.len - s.T + s.G.of(r0);
+    it.emax = it.len - s.T + s.G.of(r1);
     const int hi = min(it.emax + 1, s.cap);
     it.lo = s.window > 0 ? min(max(0, it.emin + 1 - s.window), s.cap) / kBox * kBox : 0;
     it.ns = s.sinks < it.lo ? (s.sinks + kBox - 1) / kBox * kBox : it.lo;
@@ -214,7 +226,7 @@ __device__ __forceinline__ void load_tiles(const PagedArgs &a, const Shape &s, c
         for (int t = 0; t < it.ntiles; ++t, ++jt) {
             const int st = jt % N;
             const int v = t * kTile + lane * kBox, pos = pos_of(it, v);
-            const int p = pos / a.c.ps, at = pos - p * a.c.ps;
+            const int p = s.ps.of(pos), at = pos - p * a.c.ps;
             const int boxes = min(kTile / kBox, (it.total - t * kTile + kBox - 1) / kBox);
             int page = -1;
             if (lane < boxes && SSD_IDX_OK(a.err, it.b * a.tb + p, a.t_n)) page = a.table[it.b * a.tb + p];
@@ -343,9 +355,9 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
     for (;;) {
         const int vs = jt % C::NV, at = jt;
         const int steps = min(kTile / 16, (total - t * kTile + 15) / 16);
-        const bool last = t + 1 == ntiles;
+        const bool first = t == 0, last = t + 1 == ntiles;
         bool more = true;
-        if (t == 0) find_next();
+        if (first) find_next();
         if (last) {
             t = 0;
             ++nitem;
@@ -364,7 +376,8 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
             const uint32_t scores_at = tmem + kS + 128 * blk, outputs_at = tmem + kO + 128 * blk;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (i < steps) ptx::mma_bf16_ts(outputs_at, scores_at + 8 * i, v + uint64_t(i * 128), kIdO, 1);
+                if (i < steps)
+                    ptx::mma_bf16_ts(outputs_at, scores_at + 8 * i, v + uint64_t(i * 128), kIdO, !first || i > 0);
             if (last) ptx::mma_commit(&bar.o_full[blk]);
             if (more && !scores(blk)) return;
         }
@@ -384,21 +397,13 @@ struct RowThread {
     uint32_t base, ts, to;            // shared memory; this warp's lanes of S and O
     int blk, lane, warp;              // warp: 0 to 3 of its block
 
-    __device__ __forceinline__ void zero_outputs() {
-        uint32_t z[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) z[i] = 0;
-#pragma unroll
-        for (int c = 0; c < D; c += 32) ptx::tmem_st32(to + c, z);
-        ptx::tmem_st_wait();
-    }
     // Infinities and NaN of an item's values, added to the rows that see them where zeros stand in
     // their place (a probability makes no difference to them).
     __device__ __forceinline__ void add_foul(const Item &it, int own) {
 #pragma unroll 1
         for (int v = 0; v < it.total; ++v) {
             if (all_see(s, it, v / kTile * kTile)) continue;
-            const int pos = pos_of(it, v), p = pos / a.c.ps;
+            const int pos = pos_of(it, v), p = s.ps.of(pos);
             const int page = SSD_IDX_OK(a.err, it.b * a.tb + p, a.t_n) ? a.table[it.b * a.tb + p] : -1;
             if (page < 0 || page >= a.c.pages) continue;
             const int64_t off = page * a.c.sp + it.hk * a.c.sh + (pos - p * a.c.ps) * a.c.st;
@@ -419,9 +424,11 @@ struct RowThread {
 
     // This warp's 32 rows of an item's queries to shared memory (the products that read the ones
     // before them are done); and their arrival.
-    __device__ __forceinline__ void load_queries(const Item &it) {
-        const int r = min(it.rb * kItemRows + blk * kRows + warp * 32 + lane, s.rows - 1), t = r / s.G;
-        const int64_t off = it.b * a.q_sb + t * a.q_st + (it.hk * s.G + r - t * s.G) * a.q_sh;
+    __device__ __forceinline__ int64_t query_of(const Item &it) const {     // the lane's row of them
+        const int r = min(it.rb * kItemRows + blk * kRows + warp * 32 + lane, s.rows - 1), t = s.G.of(r), G = int(s.G.d);
+        return it.b * a.q_sb + t * a.q_st + (it.hk * G + r - t * G) * a.q_sh;
+    }
+    __device__ __forceinline__ void load_queries(int64_t off) {
         const uint32_t dst = base + C::Q + blk * C::OPERAND;
 #pragma unroll
         for (int r0 = 0; r0 < 32; r0 += C::RPI) {
@@ -523,11 +530,11 @@ struct RowThread {
         const float qs = a.scale * kLog2e;
         int jt = 0, nitem = 0;
         bool loaded = false;          // this item's queries
-        Item it = item_of(s, blockIdx.x), next = it;
 #pragma unroll 1
-        for (int x = blockIdx.x; x < s.items; x += gridDim.x, it = next) {
+        for (int x = blockIdx.x; x < s.items; x += gridDim.x) {
+            const Item it = item_of(s, x);
             const int r = it.rb * kItemRows + blk * kRows + warp * 32 + lane, rr = min(r, s.rows - 1);
-            const int own = it.len - s.T + rr / s.G;
+            const int tk = s.G.of(rr), own = it.len - s.T + tk;
             // what it sees of the item's run: [va, vb), and below vb what lies below `sinks` too (where
             // ns < sinks it is lo, and the run has no gap)
             const int vb = own < it.lo ? min(own + 1, it.ns) : it.ns + own - it.lo + 1;
@@ -535,16 +542,25 @@ struct RowThread {
             float m = -INFINITY, l = 0.f;
             if (it.ntiles) {
                 if (!loaded) {
-                    load_queries(it);
+                    load_queries(query_of(it));
                     queries_loaded();
                 }
                 loaded = false;
-                zero_outputs();
             }
+            // the next item's queries, loaded when the last scores of this one are made
+            int64_t next = -1;
 #pragma unroll 1
             for (int t = 0; t < it.ntiles; ++t, ++jt) {
                 if (!wait_warp(&bar.s_full[blk][jt % C::NK], (jt / C::NK) & 1, gave_up)) return false;
                 ptx::tc_fence_after();
+                if (t == it.ntiles / 2 && x + gridDim.x < s.items) {
+                    const Item after = item_of(s, x + gridDim.x);
+                    if (after.ntiles) next = query_of(after);
+                }
+                if (t + 1 == it.ntiles && next >= 0) {
+                    load_queries(next);
+                    loaded = true;
+                }
                 const int v0 = t * kTile;
                 const uint32_t there = notes.there[jt & 3];
                 if (__all_sync(~0u, v0 + kTile <= vb && (va <= v0 || v0 + kTile <= s.sinks) &&
@@ -553,14 +569,7 @@ struct RowThread {
                 else
                     tile<false>(t, va, vb, there, qs, m, l);
             }
-            // The scores of this item are done with: the next one's queries.
-            next.ntiles = 0;
-            if (x + gridDim.x < s.items) next = item_of(s, x + gridDim.x);
-            if (it.ntiles && next.ntiles) {
-                load_queries(next);
-                queries_loaded();
-                loaded = true;
-            }
+            if (loaded) queries_loaded();
             if (it.ntiles) {
                 if (!wait_warp(&bar.o_full[blk], nitem & 1, gave_up)) return false;
                 ptx::tc_fence_after();
@@ -569,7 +578,7 @@ struct RowThread {
             }
             // Rows of 64 places go through shared memory, so that stores are whole lines (a row a
             // thread, 16 bytes at a time, took 3800 cycles an item).
-            const int tk = rr / s.G, h = it.hk * s.G + rr - tk * s.G;
+            const int h = it.hk * int(s.G.d) + rr - tk * int(s.G.d);
             const int64_t off = r < s.rows ? it.b * a.o_sb + tk * a.o_st + h * a.o_sh : -1;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const uint32_t stage = base + C::OUT + (blk * 4 + warp) * 32 * 128;
@@ -706,17 +715,24 @@ cudaError_t launch_d(const PagedArgs &a, const Shape &s, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-int64_t items_of(const PagedArgs &a) {
+int64_t items_of(const PagedArgs &a, int block) {       // row blocks of a size
     const int64_t rows = int64_t(a.T) * (a.Hq / a.c.Hkv);
-    return int64_t(a.B) * a.c.Hkv * ((rows + kItemRows - 1) / kItemRows);
+    return int64_t(a.B) * a.c.Hkv * ((rows + block - 1) / block);
 }
 
 }  // namespace
 
+// An item's time goes by its positions alone, 1.75 us for 128 of them (D = 64: 1.55), with all of its
+// rows there or not; the kernels of ssd_attn.cuh split a sequence's positions over the SMs and take
+// 0.0154 us (0.0106) for 128 positions and a block of 64 rows.  So this kernel takes over at 114 (146)
+// such blocks.  Measured, here / there: 128 blocks (8 sequences of 32 tokens over 8192 positions, 32
+// over 8 heads) 121 / 140 us, D = 64 105 / 99; 256 blocks (512 tokens over 8192) 119 / 261, 105 /
+// 184; 8192 tokens 458 / 2170, 398 / 1499.  (A scale below 0 would have to turn the scores' signs,
+// which no model asks for.)
 bool prompt_fits(const PagedArgs &a) {
-    const int64_t rows = int64_t(a.T) * (a.Hq / a.c.Hkv), items = items_of(a);
-    return a.c.dt == DT_BF16 && a.scale > 0.f && a.c.ps % kBox == 0 && a.c.pages > 0 && rows >= kItemRows / 2 &&
-           items * 4 >= device_sm_count() && items < (1 << 30);
+    const int64_t blocks = items_of(a, 64), sms = device_sm_count();
+    return a.c.dt == DT_BF16 && a.scale > 0.f && a.c.ps % kBox == 0 && a.c.pages > 0 &&
+           (a.c.D == 128 ? 4 * blocks >= 3 * sms : blocks >= sms) && items_of(a, kItemRows) < (1 << 30);
 }
 
 cudaError_t launch_paged_prompt(const PagedArgs &a, cudaStream_t stream) {
@@ -725,13 +741,16 @@ cudaError_t launch_paged_prompt(const PagedArgs &a, cudaStream_t stream) {
     s.B = a.B;
     s.T = a.T;
     s.Hkv = a.c.Hkv;
-    s.G = a.Hq / a.c.Hkv;
     s.cap = a.M * a.c.ps;
     s.window = int(a.window);
     s.sinks = int(a.sinks);
-    s.rows = a.T * s.G;
+    s.heads = Divisor(uint32_t(a.B * a.c.Hkv));
+    s.per_b = Divisor(uint32_t(a.c.Hkv));
+    s.G = Divisor(uint32_t(a.Hq / a.c.Hkv));
+    s.ps = Divisor(uint32_t(a.c.ps));
+    s.rows = a.T * (a.Hq / a.c.Hkv);
     s.nrb = (s.rows + kItemRows - 1) / kItemRows;
-    s.items = int(items_of(a));
+    s.items = int(items_of(a, kItemRows));
     return a.c.D == 64 ? launch_d<64>(a, s, stream) : launch_d<128>(a, s, stream);
 }
 
