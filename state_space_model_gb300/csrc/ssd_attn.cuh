@@ -62,12 +62,11 @@ constexpr int kWarps = 4;                 // of a CTA that compute
 constexpr int kCopyWarps = 4;             // and that copy
 constexpr int kThreads = 32 * (kWarps + kCopyWarps);
 constexpr int kCtasPerSm = 2;
-// Registers of a thread: 128 at the launch (two CTAs of 256 threads fill an SM's file),
-// shared out again as 208 and 48, 128 x (208 + 48) = 256 x 128.
-constexpr int kComputeRegs = 208, kCopyRegs = 48;
 constexpr int kF32Warps = 6;              // of a CTA of the fp32 kernel
 // What the tensor-core kernel's pools hold: bf16, or codes of 8 or 4 bits.
 enum : int { kBf16 = 0, kEight = 1, kFour = 2 };
+// CTAs of the tensor-core kernel on an SM, by the rows of a block.
+constexpr int ctas_of(int format, int rows) { return format == kFour && rows == 8 ? 3 : kCtasPerSm; }
 
 // ---- the schedule -----------------------------------------------------------------
 //
@@ -349,6 +348,12 @@ __device__ __forceinline__ void copy_few(uint32_t dst, const void *src, bool ok)
                  "l"(__cvta_generic_to_global(src)), "r"(ok ? N : 0), "n"(N)
                  : "memory");
 }
+// n bytes (of 16) in one piece, counted at bar.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t n, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(__cvta_generic_to_global(src)), "r"(n), "r"(smem_addr(bar))
+                 : "memory");
+}
 // An arrival at bar once this thread's copies so far have landed.
 __device__ __forceinline__ void copies_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
@@ -503,18 +508,24 @@ struct Cfg {
     static constexpr int OUTS = kWarps * 8 * NQ * D * 4;
     static constexpr bool APART = OUTS > STAGE;
     // tiles that a CTA has room for
-    static constexpr int STAGES = !F4 ? 3 : D == 64 ? 8 : APART ? 4 : 5;
+    static constexpr int CTAS = ctas_of(FMT, RB);           // of an SM
+    static constexpr int STAGES = !F4 ? 3 : CTAS == 3 ? (D == 64 ? 6 : 3) : D == 64 ? 8 : 4;
+    // registers of a thread: as many as the SM has at the launch, shared out again
+    static constexpr int REGS = 65536 / (CTAS * kThreads) / 8 * 8;
+    static constexpr int COPY_REGS = 48, COMPUTE_REGS = 2 * REGS - COPY_REGS;
     static constexpr int SMEM = STAGES * (STAGE + AUX) + (APART ? OUTS : 0);
     static_assert(F4 || !APART, "the outputs fit a stage");
-    static_assert(kCtasPerSm * (SMEM + 2048) <= 228 * 1024, "CTAs fit an SM");
+    static_assert(CTAS * (SMEM + 2048) <= 228 * 1024, "CTAs fit an SM");
 };
 
 // Byte offset of 16-byte chunk c of row r: chunks are exchanged so that the
 // eight rows of a matrix fragment, and the rows and chunks that eight
 // neighbouring lanes read, lie in different banks.
-template <int ROW>
+// (Rows of 4-bit codes lie as in a page, so that whole runs are copied at once: the values' reads meet in
+// pairs, which costs less than the instructions of copying row by row.)
+template <int ROW, bool LINEAR>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
-    if constexpr (ROW == 32) return r * 32 + (c << 4);
+    if constexpr (LINEAR) return r * ROW + (c << 4);
     if constexpr (ROW == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
     return r * ROW + ((c ^ (r & 7)) << 4);
 }
@@ -569,7 +580,7 @@ __device__ __forceinline__ void value_tiles(uint32_t vsm, uint32_t vgr, int j, U
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt) {
             uint32_t f[4];
-            ldsm4_trans(f, vsm + chunk_at<ROW>(16 * j + (lane & 7) + ((lane >> 4) << 3),
+            ldsm4_trans(f, vsm + chunk_at<ROW, C::F4>(16 * j + (lane & 7) + ((lane >> 4) << 3),
                                                2 * mt + ((lane >> 3) & 1)));
             use(mt, f);
         }
@@ -582,11 +593,11 @@ __device__ __forceinline__ void value_tiles(uint32_t vsm, uint32_t vgr, int j, U
         for (int x = 0; x < 4; ++x) {
             const int r = 16 * j + code_pos<ROW>(x >> 1, 2 * c + (x & 1));
             if constexpr (D == 128) {
-                const uint2 u = lds8(vsm + chunk_at<ROW>(r, g >> 1) + (g & 1) * 8);
+                const uint2 u = lds8(vsm + chunk_at<ROW, C::F4>(r, g >> 1) + (g & 1) * 8);
                 v[x][0] = u.x, v[x][1] = u.y;
                 s[x] = lds1(vgr + r * C::GROUPS + g);
             } else {
-                v[x][0] = lds4(vsm + chunk_at<ROW>(r, g >> 2) + (g & 3) * 4);
+                v[x][0] = lds4(vsm + chunk_at<ROW, C::F4>(r, g >> 2) + (g & 3) * 4);
                 s[x] = lds1(vgr + r * C::GROUPS + (g >> 1));
             }
         }
@@ -615,10 +626,10 @@ __device__ __forceinline__ void value_tiles(uint32_t vsm, uint32_t vgr, int j, U
         for (int x = 0; x < 4; ++x) {
             const int r = 16 * j + code_pos<ROW>(x >> 1, 2 * c + (x & 1));
             if constexpr (D == 128) {
-                const uint4 u = lds16(vsm + chunk_at<ROW>(r, g));
+                const uint4 u = lds16(vsm + chunk_at<ROW, C::F4>(r, g));
                 v[x][0] = u.x, v[x][1] = u.y, v[x][2] = u.z, v[x][3] = u.w;
             } else {
-                const uint2 u = lds8(vsm + chunk_at<ROW>(r, g >> 1) + (g & 1) * 8);
+                const uint2 u = lds8(vsm + chunk_at<ROW, C::F4>(r, g >> 1) + (g & 1) * 8);
                 v[x][0] = u.x, v[x][1] = u.y;
             }
         }
@@ -706,6 +717,11 @@ __device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, c
     // RUN positions of one page after another in memory: no addresses from other lanes
     // (96 ragged sequences over fp8 77.0 us, without this way 79.0; bf16 alike)
     const bool runs = a.c.ps % RUN == 0 && a.c.st == ROW / ES;
+    // 4-bit codes: such runs, the scales' among them, are copied whole, a lane a run of one kind
+    // (16 bytes a lane took 65 us for the copies of 64 sequences of 4096 alone)
+    const bool whole = C::F4 && a.c.whole;
+    const int run = a.c.ps % 32 == 0 ? 32 : 16, kind = lane % 6, part = lane / 6 * run;
+    bool mixed = false;
     const char *const kpool = static_cast<const char *>(a.c.k);
     const char *const vpool = static_cast<const char *>(a.c.v);
 
@@ -729,13 +745,44 @@ __device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, c
         const uint32_t mask = __ballot_sync(~0u, ok);
         const int64_t off = ok ? page * a.c.sp + it.hk * a.c.sh + at * a.c.st : 0;
         const uint32_t kdst = room.keys(st) + first * ROW, vdst = room.values(st) + first * ROW;
-        if (__all_sync(~0u, runs && mask == kAll)) {
+        bool bulk = false;
+        if constexpr (C::F4) {
+            bulk = __all_sync(~0u, whole && mask == kAll);
+            if (bulk) {
+                // kinds: codes, groups' scales, scales; keys, then values
+                const int from = min(part, KW - 1);
+                const int64_t r = __shfl_sync(~0u, off, from);
+                const int64_t pg = __shfl_sync(~0u, page, from), po = __shfl_sync(~0u, at, from);
+                const int64_t go = pg * a.c.sgp + it.hk * a.c.sgh + po * GROUPS, so = pg * a.c.ssp + it.hk * a.c.ssh + po;
+                const bool value = kind & 1;
+                const char *const src =
+                    kind < 2 ? (value ? vpool : kpool) + r
+                    : kind < 4 ? reinterpret_cast<const char *>(value ? a.c.vg : a.c.kg) + go
+                               : reinterpret_cast<const char *>((value ? a.c.vs : a.c.ks) + so);
+                const uint32_t each = kind < 2 ? ROW : kind < 4 ? GROUPS : 4;
+                const uint32_t dst = (kind < 2 ? room.keys(st) : kind < 4 ? room.groups(st) : smem_addr(room.scales(st))) +
+                                     (value ? KS * each : 0) + (first + part) * each;
+                const bool in = part < KW && SSD_IDX_OK(a.err, r + run * ROW - 1, a.c.n) &&
+                                SSD_IDX_OK(a.err, go + run * GROUPS - 1, a.c.ng) && SSD_IDX_OK(a.err, so + run - 1, a.c.ns);
+                const uint32_t bytes = __reduce_add_sync(~0u, in ? run * each : 0);
+                if (lane == 0) {
+                    room.masks(st)[first / KW] = mask;
+                    ptx::mbar_arrive_expect_tx(&full[st], bytes);
+                }
+                __syncwarp();
+                if (mixed) ptx::fence_proxy_async_smem();    // after copies of the other kind
+                if (in) bulk_load(dst, src, run * each, &full[st]);
+            }
+        }
+        mixed = mixed || !bulk;
+        if (bulk) {
+        } else if (__all_sync(~0u, runs && mask == kAll)) {
 #pragma unroll
             for (int h = 0; h < KW / RUN; ++h) {
                 const int64_t mine = __shfl_sync(~0u, off, h * RUN) * ES + lrow * ROW + lch * 16;
 #pragma unroll
                 for (int j = 0; j < RUN / RPI; ++j) {
-                    const uint32_t d = chunk_at<ROW>(h * RUN + j * RPI + lrow, lch);
+                    const uint32_t d = chunk_at<ROW, C::F4>(h * RUN + j * RPI + lrow, lch);
                     const bool in = SSD_IDX_OK(a.err, mine + j * RPI * ROW + 15, a.c.n * ES);
                     copy16(kdst + d, kpool + mine + j * RPI * ROW, in);
                     copy16(vdst + d, vpool + mine + j * RPI * ROW, in);
@@ -748,26 +795,26 @@ __device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, c
                 const int r = r0 + lrow;
                 const int64_t o = __shfl_sync(~0u, off, r) * ES + lch * 16;
                 const bool in = (mask >> r) & 1 && SSD_IDX_OK(a.err, o + 15, a.c.n * ES);
-                copy16(kdst + chunk_at<ROW>(r, lch), kpool + o, in);
-                copy16(vdst + chunk_at<ROW>(r, lch), vpool + o, in);
+                copy16(kdst + chunk_at<ROW, C::F4>(r, lch), kpool + o, in);
+                copy16(vdst + chunk_at<ROW, C::F4>(r, lch), vpool + o, in);
             }
         }
-        if constexpr (C::F8) {
+        if (C::F8 && !bulk) {
             const int64_t so = ok ? page * a.c.ssp + it.hk * a.c.ssh + at : 0;
             const uint32_t d = smem_addr(room.scales(st)) + (first + lane) * 4;
             const bool in = ok && SSD_IDX_OK(a.err, so, a.c.ns);
             copy_few<4>(d, a.c.ks + so, in);
             copy_few<4>(d + KS * 4, a.c.vs + so, in);
         }
-        if constexpr (C::F4) {
+        if (C::F4 && !bulk) {
             const int64_t go = ok ? page * a.c.sgp + it.hk * a.c.sgh + at * a.c.sgt : 0;
             const uint32_t d = room.groups(st) + (first + lane) * GROUPS;
             const bool in = ok && SSD_IDX_OK(a.err, go + GROUPS - 1, a.c.ng);
-            copy_few<GROUPS>(d, a.c.kg + go, in);
-            copy_few<GROUPS>(d + KS * GROUPS, a.c.vg + go, in);
+            copy_few<C::F4 ? GROUPS : 4>(d, a.c.kg + go, in);
+            copy_few<C::F4 ? GROUPS : 4>(d + KS * GROUPS, a.c.vg + go, in);
         }
         copies_arrive(&full[st]);
-        if (lane == 0) {
+        if (lane == 0 && !bulk) {
             room.masks(st)[first / KW] = mask;
             ptx::mbar_arrive(&full[st]);
         }
@@ -784,7 +831,7 @@ __device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, c
 }
 
 template <int D, int FMT, int NQ, int WR>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, (Cfg<D, FMT, NQ, WR>::CTAS))
 k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
     using C = Cfg<D, FMT, NQ, WR>;
     constexpr bool F8 = C::F8, F4 = C::F4;
@@ -816,16 +863,20 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     int64_t left = span.left - max(0, kItemCost - span.unit);
     if (span.left <= 0 || left <= 0) return;
     const Room<C> room{smem};
-    static_assert(kCopyWarps == kWarps && 128 * (kComputeRegs + kCopyRegs) <= kThreads * 128, "");
+    static_assert(kCopyWarps == kWarps, "two warpgroups");
     if (warp >= kWarps) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::COPY_REGS));
         if (!copy_tiles<C>(a, s, room, full, empty, &gave_up, it, tile, left, (warp - kWarps) * KW)) {
             copies_wait();
+            if constexpr (F4) {       // pieces under way land in microseconds
+                const uint64_t t0 = ptx::globaltimer_ns();
+                while (ptx::globaltimer_ns() - t0 < 1000000ull) {}
+            }
             if (lane == 0) atomicOr(a.err, kErrTimeout);
         }
         return;
     }
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::COMPUTE_REGS));
     const int kg = warp / WR, wr = warp % WR;     // key group, row warp
     const int g = lane >> 2, c = lane & 3;        // fragment row and column pair
 
@@ -964,7 +1015,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
 #pragma unroll
                     for (int j = 0; j < KT; ++j) {
                         uint32_t f[4];
-                        ldsm4(f, ksm + chunk_at<ROW>(16 * j + (lane & 15), 2 * k + (lane >> 4)));
+                        ldsm4(f, ksm + chunk_at<ROW, C::F4>(16 * j + (lane & 15), 2 * k + (lane >> 4)));
 #pragma unroll
                         for (int b = 0; b < NQ; ++b)
                             mma<false>(sc[j][b], f, qf[b][k][0], qf[b][k][1]);
@@ -980,13 +1031,13 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                     for (int i = 0; i < 2; ++i) {
                         const int r = pos_of(j, i);
                         if constexpr (D == 128) {
-                            const uint4 v = lds16(ksm + chunk_at<ROW>(r, c));
+                            const uint4 v = lds16(ksm + chunk_at<ROW, C::F4>(r, c));
                             u[i][0] = v.x, u[i][1] = v.y, u[i][2] = v.z, u[i][3] = v.w;
                             const uint32_t w = widen2(lds2(kgr + r * C::GROUPS + 2 * c));
                             gs[i][0] = __byte_perm(w, w, 0x1010);
                             gs[i][1] = __byte_perm(w, w, 0x3232);
                         } else {
-                            const uint2 v = lds8(ksm + chunk_at<ROW>(r, c >> 1) + (c & 1) * 8);
+                            const uint2 v = lds8(ksm + chunk_at<ROW, C::F4>(r, c >> 1) + (c & 1) * 8);
                             u[i][0] = v.x, u[i][1] = v.y;
                             const uint32_t w = widen2(lds1(kgr + r * C::GROUPS + c));
                             gs[i][0] = gs[i][1] = __byte_perm(w, w, 0x1010);
@@ -1014,8 +1065,8 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
 #pragma unroll
                     for (int j = 0; j < KT; ++j) {
                         // 16 places of two positions: four steps of the product
-                        const uint4 u = lds16(ksm + chunk_at<ROW>(pos_of(j, 0), 4 * h + c));
-                        const uint4 v = lds16(ksm + chunk_at<ROW>(pos_of(j, 1), 4 * h + c));
+                        const uint4 u = lds16(ksm + chunk_at<ROW, C::F4>(pos_of(j, 0), 4 * h + c));
+                        const uint4 v = lds16(ksm + chunk_at<ROW, C::F4>(pos_of(j, 1), 4 * h + c));
                         const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -1239,7 +1290,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                 for (int y = 0; y < KP * (D / 32); ++y) {
                     const int x = y / (D / 32), mine = 32 * (y % (D / 32)) + lane;   // position, place
                     const uint32_t at = F4 ? vgr + x * C::GROUPS + mine / kGroup
-                                           : vsm + chunk_at<ROW>(x, mine * (F8 ? 1 : 2) / 16) +
+                                           : vsm + chunk_at<ROW, C::F4>(x, mine * (F8 ? 1 : 2) / 16) +
                                                  mine * (F8 ? 1 : 2) % 16;
                     float v;
                     if constexpr (F8) v = (lds1(at) & 0x7f) == 0x7f ? NAN : 0.f;
@@ -1383,6 +1434,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                 }
             }
         }
+        if constexpr (F4 && !C::APART) ptx::fence_proxy_async_smem();    // outputs, then copies in pieces
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&empty[st]);
         if (item_end) first_item = false;
@@ -1717,8 +1769,11 @@ cudaError_t launch_join(const PagedArgs &a, const Shape &s, cudaStream_t stream)
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
-    // about 8 CTAs for an item: one wave of them all
-    const int per = s.RB <= 8 ? 4 : s.RB <= 16 ? 2 : 1, at_once = 4 / per;
+    // Items of few parts, which a warp loads at once: a warp a row.  Else about 8 CTAs for an item, one
+    // wave of them all.
+    const int64_t items = int64_t(s.B) * s.Hkv * s.nrb;
+    const bool few = s.ncta <= items * (kJoinAhead - 1);
+    const int per = few || s.RB > 16 ? 1 : s.RB <= 8 ? 4 : 2, at_once = 4 / per;
     cfg.gridDim = dim3(unsigned(s.ncta), unsigned(min(8, (min(s.RB, a.T * s.G) + at_once - 1) / at_once)));
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
@@ -1768,7 +1823,7 @@ inline Shape make_shape(const PagedArgs &a) {
     else
         s.RB = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     s.nrb = int((rows + s.RB - 1) / s.RB);
-    s.ncta = device_sm_count() * kCtasPerSm;
+    s.ncta = device_sm_count() * (a.c.dt == DT_F4E2M1X2 ? ctas_of(kFour, s.RB) : kCtasPerSm);
     return s;
 }
 

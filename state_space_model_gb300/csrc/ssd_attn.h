@@ -27,6 +27,8 @@ struct KvPools {
     int64_t sp = 0, sh = 0, st = 0;           // page, head, token stride of the pools
     int64_t ssp = 0, ssh = 0;                 // page, head stride of the scales
     int64_t sgp = 0, sgh = 0, sgt = 0;        // page, head, token stride of the group scales
+    int whole = 0;                            // 4-bit: 16 tokens of a page and head, with their scales, can
+                                              // be copied in pieces of 16 bytes
     int64_t n = 0, ns = 0, ng = 0;            // extents (largest index + 1), debug build
 };
 

@@ -68,6 +68,11 @@ ssd_status check_groups(const Pools &t, bool out, ssd::KvPools *p) {
     p->sgh = t.kg->stride[1];
     p->sgt = t.kg->stride[2];
     p->ng = extent(t.kg);
+    auto sixteenth = [](const ssd_tensor *x) { return reinterpret_cast<uintptr_t>(x->data) % 16 == 0; };
+    auto apart = [](int64_t shape, int64_t stride, int64_t unit) { return shape <= 1 || stride % unit == 0; };
+    p->whole = p->ps % 16 == 0 && p->st == p->D / 2 && p->sgt == n && sixteenth(t.kg) && sixteenth(t.vg) &&
+               sixteenth(t.ks) && sixteenth(t.vs) && apart(p->pages, p->sgp, 16) && apart(p->Hkv, p->sgh, 16) &&
+               apart(p->pages, p->ssp, 4) && apart(p->Hkv, p->ssh, 4);
     return SSD_OK;
 }
 
