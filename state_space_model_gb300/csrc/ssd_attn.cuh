@@ -717,11 +717,6 @@ __device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, c
     // RUN positions of one page after another in memory: no addresses from other lanes
     // (96 ragged sequences over fp8 77.0 us, without this way 79.0; bf16 alike)
     const bool runs = a.c.ps % RUN == 0 && a.c.st == ROW / ES;
-    // 4-bit codes: such runs, the scales' among them, are copied whole, a lane a run of one kind
-    // (16 bytes a lane took 65 us for the copies of 64 sequences of 4096 alone)
-    const bool whole = C::F4 && a.c.whole;
-    const int run = a.c.ps % 32 == 0 ? 32 : 16, kind = lane % 6, part = lane / 6 * run;
-    bool mixed = false;
     const char *const kpool = static_cast<const char *>(a.c.k);
     const char *const vpool = static_cast<const char *>(a.c.v);
 
@@ -745,38 +740,7 @@ __device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, c
         const uint32_t mask = __ballot_sync(~0u, ok);
         const int64_t off = ok ? page * a.c.sp + it.hk * a.c.sh + at * a.c.st : 0;
         const uint32_t kdst = room.keys(st) + first * ROW, vdst = room.values(st) + first * ROW;
-        bool bulk = false;
-        if constexpr (C::F4) {
-            bulk = __all_sync(~0u, whole && mask == kAll);
-            if (bulk) {
-                // kinds: codes, groups' scales, scales; keys, then values
-                const int from = min(part, KW - 1);
-                const int64_t r = __shfl_sync(~0u, off, from);
-                const int64_t pg = __shfl_sync(~0u, page, from), po = __shfl_sync(~0u, at, from);
-                const int64_t go = pg * a.c.sgp + it.hk * a.c.sgh + po * GROUPS, so = pg * a.c.ssp + it.hk * a.c.ssh + po;
-                const bool value = kind & 1;
-                const char *const src =
-                    kind < 2 ? (value ? vpool : kpool) + r
-                    : kind < 4 ? reinterpret_cast<const char *>(value ? a.c.vg : a.c.kg) + go
-                               : reinterpret_cast<const char *>((value ? a.c.vs : a.c.ks) + so);
-                const uint32_t each = kind < 2 ? ROW : kind < 4 ? GROUPS : 4;
-                const uint32_t dst = (kind < 2 ? room.keys(st) : kind < 4 ? room.groups(st) : smem_addr(room.scales(st))) +
-                                     (value ? KS * each : 0) + (first + part) * each;
-                const bool in = part < KW && SSD_IDX_OK(a.err, r + run * ROW - 1, a.c.n) &&
-                                SSD_IDX_OK(a.err, go + run * GROUPS - 1, a.c.ng) && SSD_IDX_OK(a.err, so + run - 1, a.c.ns);
-                const uint32_t bytes = __reduce_add_sync(~0u, in ? run * each : 0);
-                if (lane == 0) {
-                    room.masks(st)[first / KW] = mask;
-                    ptx::mbar_arrive_expect_tx(&full[st], bytes);
-                }
-                __syncwarp();
-                if (mixed) ptx::fence_proxy_async_smem();    // after copies of the other kind
-                if (in) bulk_load(dst, src, run * each, &full[st]);
-            }
-        }
-        mixed = mixed || !bulk;
-        if (bulk) {
-        } else if (__all_sync(~0u, runs && mask == kAll)) {
+        if (__all_sync(~0u, runs && mask == kAll)) {
 #pragma unroll
             for (int h = 0; h < KW / RUN; ++h) {
                 const int64_t mine = __shfl_sync(~0u, off, h * RUN) * ES + lrow * ROW + lch * 16;
@@ -799,14 +763,14 @@ __device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, c
                 copy16(vdst + chunk_at<ROW, C::F4>(r, lch), vpool + o, in);
             }
         }
-        if (C::F8 && !bulk) {
+        if constexpr (C::F8) {
             const int64_t so = ok ? page * a.c.ssp + it.hk * a.c.ssh + at : 0;
             const uint32_t d = smem_addr(room.scales(st)) + (first + lane) * 4;
             const bool in = ok && SSD_IDX_OK(a.err, so, a.c.ns);
             copy_few<4>(d, a.c.ks + so, in);
             copy_few<4>(d + KS * 4, a.c.vs + so, in);
         }
-        if (C::F4 && !bulk) {
+        if constexpr (C::F4) {
             const int64_t go = ok ? page * a.c.sgp + it.hk * a.c.sgh + at * a.c.sgt : 0;
             const uint32_t d = room.groups(st) + (first + lane) * GROUPS;
             const bool in = ok && SSD_IDX_OK(a.err, go + GROUPS - 1, a.c.ng);
@@ -814,7 +778,7 @@ __device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, c
             copy_few<C::F4 ? GROUPS : 4>(d + KS * GROUPS, a.c.vg + go, in);
         }
         copies_arrive(&full[st]);
-        if (lane == 0 && !bulk) {
+        if (lane == 0) {
             room.masks(st)[first / KW] = mask;
             ptx::mbar_arrive(&full[st]);
         }
@@ -826,6 +790,111 @@ __device__ __forceinline__ bool copy_tiles(const PagedArgs &a, const Shape &s, c
             len = a.lens[min(it.b + 1, a.B - 1)];
         }
         look_up();
+    }
+    return true;
+}
+
+// The same for 4-bit codes whose runs of 16 or 32 positions of a page lie in one piece, their scales
+// too: a lane copies a run of one kind (codes, groups' scales or scales, of keys or values).  Tiles
+// are half the bytes of 8-bit ones while a tile's instructions stay, and copying and computing warps
+// share the SM's: a run found and copied takes a third of those of 16 bytes a lane.  Where some
+// position is not there, the part is filled a position a lane, with zeros.
+template <typename C>
+__device__ __forceinline__ bool copy_runs(const PagedArgs &a, const Shape &s, const Room<C> room,
+                                          uint64_t *full, uint64_t *empty, volatile int *gave_up,
+                                          Item it, int tile, int64_t left, int first) {
+    constexpr int KS = C::KS, KW = C::KW, ROW = C::ROW, GROUPS = C::GROUPS, STAGES = C::STAGES;
+    constexpr int LPR = ROW / 16, RPI = 32 / LPR;
+    static_assert(KW == 32, "");
+    const int lane = threadIdx.x % 32;
+    const int shift = (a.c.ps & (a.c.ps - 1)) ? -1 : __ffs(a.c.ps) - 1;
+    const int run = a.c.ps % 32 == 0 ? 32 : 16, kind = lane % 6, part = lane / 6 * run;
+    const bool value = kind & 1, mine = part < KW;
+    // in bytes: a kind's page, head and token strides, and its place in a stage
+    const char *const base = kind < 2   ? static_cast<const char *>(value ? a.c.v : a.c.k)
+                             : kind < 4 ? reinterpret_cast<const char *>(value ? a.c.vg : a.c.kg)
+                                        : reinterpret_cast<const char *>(value ? a.c.vs : a.c.ks);
+    const int64_t per_page = kind < 2 ? a.c.sp : kind < 4 ? a.c.sgp : a.c.ssp * 4;
+    const int64_t per_head = kind < 2 ? a.c.sh : kind < 4 ? a.c.sgh : a.c.ssh * 4;
+    const int each = kind < 2 ? ROW : kind < 4 ? GROUPS : 4;
+    [[maybe_unused]] const int64_t extent = kind < 2 ? a.c.n : kind < 4 ? a.c.ng : a.c.ns * 4;
+    const uint32_t place = (kind < 2 ? room.keys(0) : kind < 4 ? room.groups(0) : smem_addr(room.scales(0))) +
+                           (value ? KS * each : 0) + (first + part) * each;
+    const uint32_t per_stage = kind < 2 ? C::STAGE : C::AUX;
+
+    int page, at;
+    int len = a.lens[min(it.b + 1, a.B - 1)];
+    auto page_of = [&](int pos) { return shift >= 0 ? pos >> shift : pos / a.c.ps; };
+    auto look_up = [&]() {            // this lane's run of the next tile
+        page = -1;
+        const int pos = tile_at<KS>(it, tile) + first + part, p = page_of(pos);
+        at = pos - p * a.c.ps;
+        if (left > 0 && mine && pos + run <= it.hi && (pos >= it.lo || (kSinks && pos + run <= s.sinks)) &&
+            SSD_IDX_OK(a.err, it.b * a.tb + p, a.t_n))
+            page = a.table[it.b * a.tb + p];
+    };
+    look_up();
+    bool mixed = false;
+    uint32_t phase = 1;
+#pragma unroll 1
+    for (int n = 0, st = 0; left > 0; ++n) {
+        if (n >= STAGES && !wait_for(&empty[st], phase, gave_up)) return false;
+        const bool ok = page >= 0 && page < a.c.pages;
+        if (__all_sync(~0u, ok || !mine)) {
+            const int64_t off = page * per_page + it.hk * per_head + at * each;
+            const bool in = mine && SSD_IDX_OK(a.err, off + run * each - 1, extent);
+            if (lane == 0) {
+                room.masks(st)[first / KW] = 0xffffffffu;
+                ptx::mbar_arrive_expect_tx(&full[st], 2 * KW * (ROW + GROUPS + 4));
+            }
+            __syncwarp();
+            if (mixed) ptx::fence_proxy_async_smem();    // after copies of the other kind
+            if (in) bulk_load(place + st * per_stage, base + off, run * each, &full[st]);
+        } else {
+            mixed = true;
+            const int pos = tile_at<KS>(it, tile) + first + lane, p = page_of(pos), from = pos - p * a.c.ps;
+            int pg = -1;
+            if (in_range(s, it, pos) && SSD_IDX_OK(a.err, it.b * a.tb + p, a.t_n)) pg = a.table[it.b * a.tb + p];
+            const bool there = pg >= 0 && pg < a.c.pages;
+            const uint32_t mask = __ballot_sync(~0u, there);
+            const int64_t off = there ? pg * a.c.sp + it.hk * a.c.sh + from * a.c.st : 0;
+            const uint32_t kdst = room.keys(st) + first * ROW, vdst = room.values(st) + first * ROW;
+#pragma unroll 1
+            for (int r0 = 0; r0 < KW; r0 += RPI) {
+                const int r = r0 + lane / LPR;
+                const int64_t o = __shfl_sync(~0u, off, r) + lane % LPR * 16;
+                const bool in = (mask >> r) & 1 && SSD_IDX_OK(a.err, o + 15, a.c.n);
+                copy16(kdst + chunk_at<ROW, true>(r, lane % LPR), static_cast<const char *>(a.c.k) + o, in);
+                copy16(vdst + chunk_at<ROW, true>(r, lane % LPR), static_cast<const char *>(a.c.v) + o, in);
+            }
+            const int64_t so = there ? pg * a.c.ssp + it.hk * a.c.ssh + from : 0;
+            const uint32_t d = smem_addr(room.scales(st)) + (first + lane) * 4;
+            bool in = there && SSD_IDX_OK(a.err, so, a.c.ns);
+            copy_few<4>(d, a.c.ks + so, in);
+            copy_few<4>(d + KS * 4, a.c.vs + so, in);
+            const int64_t go = there ? pg * a.c.sgp + it.hk * a.c.sgh + from * a.c.sgt : 0;
+            const uint32_t e = room.groups(st) + (first + lane) * GROUPS;
+            in = there && SSD_IDX_OK(a.err, go + GROUPS - 1, a.c.ng);
+            copy_few<GROUPS>(e, a.c.kg + go, in);
+            copy_few<GROUPS>(e + KS * GROUPS, a.c.vg + go, in);
+            if (lane == 0) {
+                room.masks(st)[first / KW] = mask;
+                ptx::mbar_arrive(&full[st]);
+            }
+        }
+        copies_arrive(&full[st]);
+        --left;
+        if (++tile == it.ntiles) {
+            tile = 0;
+            left -= kItemCost;
+            it = next_item<KS>(s, it, len);
+            len = a.lens[min(it.b + 1, a.B - 1)];
+        }
+        look_up();
+        if (++st == STAGES) {
+            st = 0;
+            phase ^= 1;
+        }
     }
     return true;
 }
@@ -866,7 +935,13 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     static_assert(kCopyWarps == kWarps, "two warpgroups");
     if (warp >= kWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::COPY_REGS));
-        if (!copy_tiles<C>(a, s, room, full, empty, &gave_up, it, tile, left, (warp - kWarps) * KW)) {
+        bool done;
+        if constexpr (F4)
+            done = a.c.whole ? copy_runs<C>(a, s, room, full, empty, &gave_up, it, tile, left, (warp - kWarps) * KW)
+                             : copy_tiles<C>(a, s, room, full, empty, &gave_up, it, tile, left, (warp - kWarps) * KW);
+        else
+            done = copy_tiles<C>(a, s, room, full, empty, &gave_up, it, tile, left, (warp - kWarps) * KW);
+        if (!done) {
             copies_wait();
             if constexpr (F4) {       // pieces under way land in microseconds
                 const uint64_t t0 = ptx::globaltimer_ns();
@@ -924,7 +999,14 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
     const int tile_first = tile;          // of the first item; later ones begin at 0
     bool first_item = true;
 
-    for (int n = 0, st = 0; left > 0; ++n, st = st + 1 == STAGES ? 0 : st + 1) {
+    uint32_t phase = 0;
+    auto next_stage = [&](int &st) {
+        if (++st == STAGES) {
+            st = 0;
+            phase ^= 1;
+        }
+    };
+    for (int st = 0; left > 0; next_stage(st)) {
         if (fresh) {
             fresh = false;
 #pragma unroll
@@ -979,7 +1061,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
         // A warp whose wait ran out goes on without waiting, over whatever the stages hold:
         // others may have seen the same copies land, and would wait for it at the barriers
         // below for ever.
-        if (!wait_for(&full[st], (n / STAGES) & 1, &gave_up) && lane == 0) atomicOr(a.err, kErrTimeout);
+        if (!wait_for(&full[st], phase, &gave_up) && lane == 0) atomicOr(a.err, kErrTimeout);
         const int kbase = tile_at<KS>(it, tile) + kg * WR * KW;
 #pragma unroll 1
         for (int sub = 0; sub < KW * WR / KP; ++sub) {
@@ -1127,14 +1209,20 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
             float vs[KT][2], f[NQ][2];       // codes: value scales; what the outputs are multiplied by
             if constexpr (F8) {
                 float lv[KT][2], most = -INFINITY;
+                auto log_scale = [](float v) { return fminf(fmaxf(lg2(fabsf(v)), kLeastLog), kMostLog) - kLift; };
 #pragma unroll
                 for (int j = 0; j < KT; ++j)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         vs[j][i] = vsc[pos_of(j, i)];
-                        lv[j][i] = fminf(fmaxf(lg2(fabsf(vs[j][i])), kLeastLog), kMostLog) - kLift;
-                        most = fmaxf(most, lv[j][i]);
+                        if constexpr (F4) {           // the largest first, its log then
+                            most = fmaxf(most, fabsf(vs[j][i]));
+                        } else {
+                            lv[j][i] = log_scale(vs[j][i]);
+                            most = fmaxf(most, lv[j][i]);
+                        }
                     }
+                if constexpr (F4) most = log_scale(most);
                 // the largest score with the largest scale: mostly no weight is ahead of that bound
 #pragma unroll
                 for (int b = 0; b < NQ; ++b)
@@ -1143,6 +1231,12 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                         moved = moved || fmaf(mn[b][p] - m[b][p], qs[b][p], most) > k[b][p] + kAhead;
                 moved = __any_sync(~0u, moved);
                 if (moved) {
+                    if constexpr (F4) {
+#pragma unroll
+                        for (int j = 0; j < KT; ++j)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) lv[j][i] = log_scale(vs[j][i]);
+                    }
 #pragma unroll
                     for (int b = 0; b < NQ; ++b)
 #pragma unroll
