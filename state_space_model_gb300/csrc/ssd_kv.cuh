@@ -517,7 +517,7 @@ cudaError_t append_codes(const KvAppendArgs &a, cudaStream_t s) {
 constexpr int kReadTokens = 32;      // most tokens of a CTA
 constexpr int kNearLens = 512;       // sequences whose cu_lens a CTA keeps near
 template <typename T, typename P, int D>
-__global__ void __launch_bounds__(256, 4) k_kv_read(const __grid_constant__ KvReadArgs a, int TB) {
+__global__ void __launch_bounds__(256, std::is_same_v<P, Nibbles> ? 5 : 4) k_kv_read(const __grid_constant__ KvReadArgs a, int TB) {
     constexpr int NV = D / 8;
     constexpr bool kFours = std::is_same_v<P, Nibbles>;
     constexpr bool kCodes = sizeof(P) == 1;
@@ -643,7 +643,9 @@ template <typename T, typename P, int D>
 cudaError_t read_t(const KvReadArgs &a, cudaStream_t s) {
     // tokens of a CTA: 1024 vectors' worth, fewer where that leaves SMs without one (the
     // kernel alone, 300 tokens of 4 heads of 64: 4.4 us, with 32 a CTA 4.7)
-    int TB = 1024 / (a.c.Hkv * (D / 8));
+    // (4-bit codes, whose vectors are half the bytes: 2048, and five CTAs an SM; 32768 tokens of 8 heads of 128
+    // 36.6 us with 1024 and four, 32.8 so, 78% of the copy rate; 262144 of them 258 and 225, 91%)
+    int TB = (std::is_same_v<P, Nibbles> ? 2048 : 1024) / (a.c.Hkv * (D / 8));
     TB = TB < 1 ? 1 : TB > kReadTokens ? kReadTokens : TB;
     while (TB > 1 && (a.T + TB - 1) / TB < kSms) TB /= 2;
     const int64_t blocks = (a.T + TB - 1) / TB;
