@@ -220,8 +220,9 @@ constexpr int kAppendWarps = 4;
 // kWhole: every row is turned whole (R = D).  Elsewhere places that are not turned keep what
 // they hold, by a choice of results: a factor of 0 would bring infinities and NaN over from
 // their neighbours.  (The choice in every lane of the 8192 tokens: 36.2 us.)
-// kAxes: positions of several axes; each lane loads the angles of the axes that its columns
-// belong to, a vector at a time, and keeps those that are theirs.
+// kAxes: positions of several axes; a warp collects the angles of its token's columns, each from its
+// axis's row of the table, in shared memory (4999 tokens of 28 + 2 x 4 heads: 22.6 us; a lane that
+// loads every axis's vectors and keeps what is its own, 23.2).
 template <typename T, int D, int kCodes, bool kWhole, bool kAxes, int U>
 __global__ void __launch_bounds__(32 * kAppendWarps, 6)
 k_kv_append(const __grid_constant__ KvAppendArgs a, int warps) {
@@ -274,26 +275,24 @@ k_kv_append(const __grid_constant__ KvAppendArgs a, int warps) {
         [[maybe_unused]] const int64_t last = a.interleaved ? 4 * v1 + 3 : 8 * l + 7;
         turn = SSD_IDX_OK(a.err, pos * a.cs_st + last, a.cs_n) && SSD_IDX_OK(a.err, pos * a.sn_st + last, a.sn_n);
     }
-    if (kAxes && turn) {
-        // columns c0 .. c0 + 3 of both vectors (interleaved), or 8 l .. 8 l + 7, as two fours
+    if constexpr (kAxes) {
+        // column by column, each from its axis's row, for all rows of the warp
+        __shared__ __align__(16) float angles[kAppendWarps][2][D / 2];
+        float(&held)[2][D / 2] = angles[threadIdx.x / 32];
+        for (int c = lane; c < a.R / 2; c += 32) {
+            const int axis = a.axis_of[c / 16] >> (2 * (c % 16)) & 3;
+            const int64_t p = axis == 0 ? pos : axis == 1 ? more[0] : axis == 2 ? more[1] : more[2];
+            if (SSD_IDX_OK(a.err, p * a.cs_st + c, a.cs_n)) held[0][c] = a.cos[p * a.cs_st + c];
+            if (SSD_IDX_OK(a.err, p * a.sn_st + c, a.sn_n)) held[1][c] = a.sin[p * a.sn_st + c];
+        }
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int c0 = a.interleaved ? 4 * (i ? v1 : v0) : 8 * l + 4 * i;
-            const uint32_t of = a.axis_of[c0 / 16] >> (2 * (c0 % 16));
 #pragma unroll
-            for (int j = 0; j < kMaxAxes; ++j) {
-                const uint32_t other = of ^ (0x55u * j);       // 0 in the fields of axis j
-                const uint32_t hits = ~(other | other >> 1) & 0x55u;
-                const int64_t p = j ? more[j - 1] : pos;
-                if (!hits || !SSD_IDX_OK(a.err, p * a.cs_st + c0 + 3, a.cs_n) ||
-                    !SSD_IDX_OK(a.err, p * a.sn_st + c0 + 3, a.sn_n))
-                    continue;
-                const float4 c = *reinterpret_cast<const float4 *>(a.cos + p * a.cs_st + c0);
-                const float4 s = *reinterpret_cast<const float4 *>(a.sin + p * a.sn_st + c0);
-                const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (hits >> (2 * k) & 1) cs[4 * i + k] = cc[k], sn[4 * i + k] = ss[k];
+            for (int k = 0; k < 4; ++k) {
+                cs[4 * i + k] = turn ? held[0][c0 + k] : 1.f;
+                sn[4 * i + k] = turn ? held[1][c0 + k] : 0.f;
             }
         }
     } else if (turn) {
