@@ -127,16 +127,16 @@ bool count(Py_ssize_t n, Py_ssize_t want) {
 // A sequence of integers (None: empty), false with an exception set otherwise.
 bool integers(PyObject *o, const char *name, std::vector<int32_t> &out) {
     if (o == Py_None) return true;
-    PyObject *s = PySequence_Fast(o, name);
-    if (!s) return false;
-    const Py_ssize_t n = PySequence_Fast_GET_SIZE(s);
-    for (Py_ssize_t i = 0; i < n; ++i) {
-        const long v = PyLong_AsLong(PySequence_Fast_GET_ITEM(s, i));
+    PyObject *s = PySequence_Check(o) ? PySequence_Tuple(o) : nullptr;   // its items stay as they are
+    for (Py_ssize_t i = 0; s && i < PyTuple_GET_SIZE(s); ++i) {
+        const long v = PyLong_AsLong(PyTuple_GET_ITEM(s, i));
         if (v == -1 && PyErr_Occurred()) break;
         out.push_back(int32_t(std::max(std::min(v, long(INT32_MAX)), long(INT32_MIN))));
     }
-    Py_DECREF(s);
-    return !PyErr_Occurred();
+    const bool bad = !s || PyErr_Occurred();
+    Py_XDECREF(s);
+    if (bad) PyErr_Format(PyExc_TypeError, "%s: a sequence of integers expected", name);
+    return !bad;
 }
 
 // (q, k, v, slots, positions, cos, sin, q_weight, k_weight, eps, interleaved,
@@ -149,7 +149,7 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int inter = PyObject_IsTrue(a[10]);
         if (PyErr_Occurred()) return nullptr;
         std::vector<int32_t> sections;
-        if (!integers(a[17], "sections: a sequence of integers expected", sections)) return nullptr;
+        if (!integers(a[17], "sections", sections)) return nullptr;
         if (a[17] != Py_None && sections.empty()) {
             PyErr_SetString(PyExc_ValueError, "sections: empty");
             return nullptr;

@@ -106,7 +106,7 @@ ssd_status check_tensor(const ssd_tensor *t, const char *name, int ndim,
     if (t->stride[ndim - 1] != 1 && shape[ndim - 1] > 1)
         return fail(SSD_ERR_INVALID_ARG, "%s: innermost stride %lld, must be 1", name,
                     (long long)t->stride[ndim - 1]);
-    if (contiguous) {
+    if (contiguous && numel > 0) {
         int64_t want = 1;
         for (int i = ndim - 1; i >= 0; --i) {
             if (shape[i] > 1 && t->stride[i] != want)
