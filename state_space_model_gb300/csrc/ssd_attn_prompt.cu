@@ -446,16 +446,19 @@ struct RowThread {
     }
 
     // Tile t of an item for this thread's row, which sees [va, vb) of its run, and below vb what lies
-    // below `sinks` too: scores to weights, with the row's reference m and sum l.  kWhole: all rows of
+    // below `sinks` too: scores to weights, with the row's reference m and sum l.  large: the
+    // warp's scores are.  kWhole: all rows of
     // the warp see 128 positions.
     template <bool kWhole>
     __device__ __forceinline__ void tile(int t, int va, int vb, uint32_t there, float qs, float &m,
-                                         float &l) {
+                                         float &l, float &minus, bool &large) {
         const int v0 = t * kTile;
         uint32_t raw[4][32];
         // (of a narrower tile too: what its products have not written is not seen)
         ptx::tmem_ld32(ts, raw[0]);
         ptx::tmem_ld32(ts + 32, raw[1]);
+        ptx::tmem_ld32(ts + 64, raw[2]);
+        ptx::tmem_ld32(ts + 96, raw[3]);
         float mx = -INFINITY;
         auto look = [&](int c) {
             if constexpr (!kWhole) {
@@ -475,14 +478,11 @@ struct RowThread {
             mx = max3(mx, top[0], top[1]);
         };
         ptx::tmem_ld_wait();
-        ptx::tmem_ld32(ts + 64, raw[2]);
-        ptx::tmem_ld32(ts + 96, raw[3]);
         look(0);
         look(1);
-        ptx::tmem_ld_wait();
         look(2);
         look(3);
-        if (__any_sync(~0u, (mx - m) * qs > kSlack || (m == -INFINITY && mx != m))) {
+        if (__any_sync(~0u, (mx - m) * qs > kSlack || (m == -INFINITY && mx != m)) || large) {
             const float to_m = fmaxf(m, mx);
             const float f = m == -INFINITY ? 1.f : ex2((m - to_m) * qs);
             m = to_m;
@@ -499,16 +499,26 @@ struct RowThread {
                 }
                 ptx::tmem_st_wait();
             }
+            // 2^(qs s - qs m) is one operation below: qs m rounded is off by 2^-15 at most below 1024, the
+            // same for all of a row's weights.  For larger scores the difference first.
+            const float ref = m == -INFINITY ? 0.f : m;
+            minus = -(ref * qs);
+            large = __any_sync(~0u, !(fabsf(minus) < 1024.f));
+            if (large) {
+                minus = 0.f;
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    raw[i / 32][i % 32] = __float_as_uint(__uint_as_float(raw[i / 32][i % 32]) - ref);
+            }
         }
-        const float minus = m == -INFINITY ? 0.f : -m;
         const F2 mm = f2(minus, minus), qq = f2(qs, qs);
         F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
         auto weights = [&](int c) {
             uint32_t p[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float2 e = parts(mul(add(f2(__uint_as_float(raw[c][2 * i]),
-                                                  __uint_as_float(raw[c][2 * i + 1])), mm), qq));
+                const float2 e = parts(fma(f2(__uint_as_float(raw[c][2 * i]), __uint_as_float(raw[c][2 * i + 1])),
+                                           qq, mm));
                 const float x0 = ex2(e.x), x1 = ex2(e.y);
                 sum[i & 1] = add(sum[i & 1], f2(x0, x1));
                 p[i] = pack_bf16(x0, x1);
@@ -539,7 +549,8 @@ struct RowThread {
             // ns < sinks it is lo, and the run has no gap)
             const int vb = own < it.lo ? min(own + 1, it.ns) : it.ns + own - it.lo + 1;
             const int va = s.window > 0 ? it.ns + max(own - s.window + 1 - it.lo, 0) : 0;
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f, minus = 0.f;   // minus: -qs m where that is small
+            bool large = false;
             if (it.ntiles) {
                 if (!loaded) {
                     load_queries(query_of(it));
@@ -565,9 +576,9 @@ struct RowThread {
                 const uint32_t there = notes.there[jt & 3];
                 if (__all_sync(~0u, v0 + kTile <= vb && (va <= v0 || v0 + kTile <= s.sinks) &&
                                         there == (1u << kTile / kBox) - 1))
-                    tile<true>(t, va, vb, there, qs, m, l);
+                    tile<true>(t, va, vb, there, qs, m, l, minus, large);
                 else
-                    tile<false>(t, va, vb, there, qs, m, l);
+                    tile<false>(t, va, vb, there, qs, m, l, minus, large);
             }
             if (loaded) queries_loaded();
             if (it.ntiles) {
@@ -637,7 +648,6 @@ k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     const uint32_t base = (ptx::smem_u32(smem_raw) + 1023) & ~1023u;
     if (threadIdx.x == 0) {
         gave_up = 0;
-        ptx::mbar_init(&bar.done, 1);
         notes.foul[0] = notes.foul[1] = notes.foul[2] = notes.foul[3] = 0;
         for (int i = 0; i < 3; ++i) {
             ptx::mbar_init(&bar.k_land[i], 1);
@@ -729,10 +739,11 @@ int64_t items_of(const PagedArgs &a, int block) {       // row blocks of a size
 // over 8 heads) 121 / 140 us, D = 64 105 / 99; 256 blocks (512 tokens over 8192) 119 / 261, 105 /
 // 184; 8192 tokens 458 / 2170, 398 / 1499.  (A scale below 0 would have to turn the scores' signs,
 // which no model asks for.  Fewer rows than a block of a sequence and head take the others too: 96
-// sequences, 4 rows, a window of 1024: 93 us here, 47 there.)
+// sequences, 4 rows, a window of 1024: 93 us here, 47 there.  Pools with a stride of 0 have no tensor map.)
 bool prompt_fits(const PagedArgs &a) {
     const int64_t blocks = items_of(a, 64), sms = device_sm_count();
-    return a.c.dt == DT_BF16 && a.T * (a.Hq / a.c.Hkv) >= kRows && a.scale > 0.f && a.c.ps % kBox == 0 && a.c.pages > 0 &&
+    const bool apart = a.c.st > 0 && (a.c.Hkv == 1 || a.c.sh > 0) && (a.c.pages == 1 || a.c.sp > 0);
+    return apart && a.c.dt == DT_BF16 && a.T * (a.Hq / a.c.Hkv) >= kRows && a.scale > 0.f && a.c.ps % kBox == 0 && a.c.pages > 0 &&
            (a.c.D == 128 ? 4 * blocks >= 3 * sms : blocks >= sms) && items_of(a, kItemRows) < (1 << 30);
 }
 

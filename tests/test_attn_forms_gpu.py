@@ -432,3 +432,47 @@ def test_pieces_of_prompts_views(attn):
     got = attn.paged_attention(wide[:, :, 2:18, :64], *pools.pools, table, lens, window=500, sinks=4,
                                out=outw[:, :300, :, :64])
     assert torch.equal(got, want) and (outw[:, 300] == 0).all() and (outw[..., 64:] == 0).all()
+
+
+@pytest.mark.parametrize("size", [1e2, 1e4, 1e10, 1e17])
+@pytest.mark.parametrize("D", [64, 128])
+def test_pieces_of_prompts_huge_scores_are_one_hot(attn, size, D):
+    """Finite scores so large that one position has all the weight: the output is its value (rounded to
+    16 bits at most twice, as a weight and as the result), whatever the size.  Rows of keys that are
+    powers of two apart, so that a row's largest score is its next one's double."""
+    T, Hq, Hkv, n = 1300, 32, 8, 1500
+    q, pools, table, lens = problem(1, T, Hq, Hkv, D, 16, [n], BF, 61)
+    k = raw(pools.pools[0])
+    g = torch.Generator(device="cuda").manual_seed(3)
+    # position j's key: +-2^(j % 12) in one place, the same place as the queries' only one
+    flat = table[0].long()
+    j = torch.arange(n, device="cuda")
+    order = torch.rand(n, generator=g, device="cuda")
+    keys = torch.zeros(n, D, device="cuda", dtype=BF)
+    keys[:, 3] = torch.exp2(j % 12).to(BF) * torch.where(order < 0.5, -1.0, 1.0).to(BF)
+    k[flat[j // 16], :, j % 16] = keys[:, None]
+    q.zero_()
+    q[..., 3] = size
+    out, lse = attn.paged_attention(q, *pools.pools, table, lens, scale=1.0, window=200, sinks=7, return_lse=True)
+    own = n - T + torch.arange(T, device="cuda")
+    see = (j <= own[:, None]) & ((j > own[:, None] - 200) | (j < 7))
+    score = torch.where(see, keys[:, 3].double(), -torch.inf)
+    top = score.amax(1, keepdim=True)
+    weight = (score == top).double()
+    weight = weight / weight.sum(1, keepdim=True)
+    v = pools.rows(1, flat[j // 16], j % 16)                       # [n, Hkv, D]
+    want = torch.einsum("tj,jhd->thd", weight, v).repeat_interleave(Hq // Hkv, 1)
+    assert ((out[0].double() - want).abs() <= 2.0 ** -7 * torch.einsum("tj,jhd->thd", weight, v.abs()).repeat_interleave(
+        Hq // Hkv, 1) + 1e-30).all()
+    ref = top * float(torch.tensor(size).to(BF)) + torch.log((score == top).double().sum(1, keepdim=True))
+    assert ((lse[0].double() - ref).abs() <= 2.0 ** -20 * (1 + ref.abs())).all()
+
+
+def test_pieces_of_prompts_of_shared_pools(attn):
+    """Heads that share memory (a stride of 0)."""
+    q, pools, table, lens = problem(1, 1300, 32, 1, 128, 16, [1400], BF, 62)
+    wide = [x.expand(-1, 8, -1, -1) for x in pools.pools]
+    got = attn.paged_attention(q, *wide, table, lens)
+    want = attn.paged_attention(q, *[x.contiguous() for x in wide], table, lens)
+    top = want.float().abs().amax()
+    assert ((got - want).float().abs() <= 2.0 ** -6 * top).all()
