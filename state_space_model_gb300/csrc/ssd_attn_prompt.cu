@@ -79,34 +79,39 @@ struct Divisor {
 
 struct Shape {
     const int32_t *lens;
-    int B, T, Hkv, cap, window, sinks, rows, nrb, items;
+    int B, T, Hkv, cap, window, sinks, rows, nrb;
+    int items, whole;                 // items with halves counted; those that are not halves
     Divisor heads, per_b, G, ps;      // by B Hkv, by Hkv, by the query heads of a key/value head, by the page
 };
 
-// Row block rb of sequence b and head hk.  Index v < total of the run of positions that some row
+// Rows r0 on of sequence b and head hk, for one block of a half item.  Index v < total of the run of positions that some row
 // sees: position v below ns, then lo + v - ns; ns and lo are multiples of a box.
 struct Item {
-    int b, hk, rb;
+    int b, hk, r0;
+    bool half;
     int len, emin, emax;
     int lo, ns, total, ntiles;
 };
 
-// Item number x: the last rows come first, which see most where there is no window.
+// Item number x: the last rows come first, which see most where there is no window.  From s.whole
+// on two numbers share an item, a block of rows each.
 __device__ __forceinline__ Item item_of(const Shape &s, int x) {
     Item it;
-    const int y = s.heads.of(x), bh = x - y * int(s.heads.d);
-    it.rb = s.nrb - 1 - y;
+    it.half = x >= s.whole;
+    const int i = it.half ? s.whole + (x - s.whole) / 2 : x;
+    const int y = s.heads.of(i), bh = i - y * int(s.heads.d);
+    it.r0 = (s.nrb - 1 - y) * kItemRows + (it.half ? (x - s.whole) % 2 * kRows : 0);
     it.b = s.per_b.of(bh);
     it.hk = bh - it.b * s.Hkv;
     it.len = max(s.lens[it.b], 0);
-    const int r0 = it.rb * kItemRows, r1 = min(r0 + kItemRows, s.rows) - 1;
-    it.emin = it.len - s.T + s.G.of(r0);
+    const int r1 = min(it.r0 + (it.half ? kRows : kItemRows), s.rows) - 1;
+    it.emin = it.len - s.T + s.G.of(it.r0);
     it.emax = it.len - s.T + s.G.of(r1);
     const int hi = min(it.emax + 1, s.cap);
     it.lo = s.window > 0 ? min(max(0, it.emin + 1 - s.window), s.cap) / kBox * kBox : 0;
     it.ns = s.sinks < it.lo ? (s.sinks + kBox - 1) / kBox * kBox : it.lo;
     if (s.sinks == 0 || hi <= 0) it.ns = 0;
-    it.total = it.ns + max(0, hi - it.lo);
+    it.total = it.r0 < s.rows ? it.ns + max(0, hi - it.lo) : 0;
     it.ntiles = (it.total + kTile - 1) / kTile;
     return it;
 }
@@ -320,17 +325,20 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
     // this item's positions and tiles, and the next one's (found while rows are worked on: what
     // this thread waits for, the tensor core waits for)
     int total = 0, ntiles = 0, next_total = 0, next_tiles = 0;
+    bool half = false, next_half = false;
     auto find_next = [&]() {
         next_tiles = 0;
         for (; x < s.items && next_tiles == 0; x += gridDim.x) {
             const Item it = item_of(s, x);
-            next_total = it.total;
-            next_tiles = it.ntiles;
+            next_total = __shfl_sync(~0u, it.total, 0);
+            next_tiles = __shfl_sync(~0u, it.ntiles, 0);
+            next_half = it.half;
         }
     };
     auto take_next = [&]() {
         total = next_total;
         ntiles = next_tiles;
+        half = next_half;
     };
     // a block's scores of tile t of the item, tile jt of the CTA
     auto scores = [&](int blk) {
@@ -338,15 +346,20 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
         const uint32_t id = kIdS | uint32_t(min(kTile, (total - t * kTile + 31) & ~31) >> 3) << 17;
         const uint64_t q = ptx::sdesc(base + C::Q + blk * C::OPERAND, 16, 1024);
         const uint64_t k = ptx::sdesc(base + C::K + ks * C::OPERAND, 16, 1024);
-        if (jt == 0 && !wait_one(&bar.k_land[0], 0, gave_up)) return false;
-        if (t == 0 && !wait_one(&bar.q_full[blk], nitem & 1, gave_up)) return false;
-        ptx::tc_fence_after();
+        if (jt == 0 && !wait_warp(&bar.k_land[0], 0, gave_up)) return false;
+        if (t == 0 && !wait_warp(&bar.q_full[blk], nitem & 1, gave_up)) return false;
+        if (ptx::elect_one()) {
+            ptx::tc_fence_after();
+            if (blk == 0 || !half) {  // (the second block of a half item only counts along)
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            const uint64_t o = uint64_t((i / 4) * C::HALF + (i % 4) * 32) >> 4;
-            ptx::mma_bf16_ss(tmem + kS + 128 * blk, q + o, k + o, id, i != 0);
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint64_t o = uint64_t((i / 4) * C::HALF + (i % 4) * 32) >> 4;
+                    ptx::mma_bf16_ss(tmem + kS + 128 * blk, q + o, k + o, id, i != 0);
+                }
+            }
+            ptx::mma_commit(&bar.s_full[blk][ks]);
         }
-        ptx::mma_commit(&bar.s_full[blk][ks]);
+        __syncwarp();
         return true;
     };
     find_next();
@@ -355,7 +368,7 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
     for (;;) {
         const int vs = jt % C::NV, at = jt;
         const int steps = min(kTile / 16, (total - t * kTile + 15) / 16);
-        const bool first = t == 0, last = t + 1 == ntiles;
+        const bool first = t == 0, last = t + 1 == ntiles, one = half;
         bool more = true;
         if (first) find_next();
         if (last) {
@@ -368,17 +381,22 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
         }
         ++jt;
         const uint64_t v = ptx::sdesc(base + C::V + vs * C::OPERAND, C::HALF, 1024);
-#pragma unroll 1
-        for (int blk = 0; blk < 2; ++blk) {
-            if (blk == 0 && !wait_one(&bar.ready[vs], (at / C::NV) & 1, gave_up)) return;
-            if (!wait_one(&bar.p_full[blk], at & 1, gave_up)) return;
-            ptx::tc_fence_after();
-            const uint32_t scores_at = tmem + kS + 128 * blk, outputs_at = tmem + kO + 128 * blk;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < steps)
-                    ptx::mma_bf16_ts(outputs_at, scores_at + 8 * i, v + uint64_t(i * 128), kIdO, !first || i > 0);
-            if (last) ptx::mma_commit(&bar.o_full[blk]);
+        for (int blk = 0; blk < 2; ++blk) {
+            if (blk == 0 && !wait_warp(&bar.ready[vs], (at / C::NV) & 1, gave_up)) return;
+            if (!wait_warp(&bar.p_full[blk], at & 1, gave_up)) return;
+            if (ptx::elect_one()) {
+                ptx::tc_fence_after();
+                const uint32_t scores_at = tmem + kS + 128 * blk, outputs_at = tmem + kO + 128 * blk;
+                if (blk == 0 || !one) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < steps)
+                            ptx::mma_bf16_ts(outputs_at, scores_at + 8 * i, v + uint64_t(i * 128), kIdO, !first || i > 0);
+                }
+                if (last) ptx::mma_commit(&bar.o_full[blk]);
+            }
+            __syncwarp();
             if (more && !scores(blk)) return;
         }
         if (!more) return;
@@ -425,7 +443,7 @@ struct RowThread {
     // This warp's 32 rows of an item's queries to shared memory (the products that read the ones
     // before them are done); and their arrival.
     __device__ __forceinline__ int64_t query_of(const Item &it) const {     // the lane's row of them
-        const int r = min(it.rb * kItemRows + blk * kRows + warp * 32 + lane, s.rows - 1), t = s.G.of(r), G = int(s.G.d);
+        const int r = min(it.r0 + blk * kRows + warp * 32 + lane, s.rows - 1), t = s.G.of(r), G = int(s.G.d);
         return it.b * a.q_sb + t * a.q_st + (it.hk * G + r - t * G) * a.q_sh;
     }
     __device__ __forceinline__ void load_queries(int64_t off) {
@@ -543,7 +561,8 @@ struct RowThread {
 #pragma unroll 1
         for (int x = blockIdx.x; x < s.items; x += gridDim.x) {
             const Item it = item_of(s, x);
-            const int r = it.rb * kItemRows + blk * kRows + warp * 32 + lane, rr = min(r, s.rows - 1);
+            const bool mine = blk == 0 || !it.half;
+            const int r = mine ? it.r0 + blk * kRows + warp * 32 + lane : s.rows, rr = min(r, s.rows - 1);
             const int tk = s.G.of(rr), own = it.len - s.T + tk;
             // what it sees of the item's run: [va, vb), and below vb what lies below `sinks` too (where
             // ns < sinks it is lo, and the run has no gap)
@@ -553,24 +572,30 @@ struct RowThread {
             bool large = false;
             if (it.ntiles) {
                 if (!loaded) {
-                    load_queries(query_of(it));
+                    if (mine) load_queries(query_of(it));
                     queries_loaded();
                 }
                 loaded = false;
             }
             // the next item's queries, loaded when the last scores of this one are made
-            int64_t next = -1;
+            int64_t next = -1;        // where the lane's row of them is
+            bool follow = false;
 #pragma unroll 1
             for (int t = 0; t < it.ntiles; ++t, ++jt) {
                 if (!wait_warp(&bar.s_full[blk][jt % C::NK], (jt / C::NK) & 1, gave_up)) return false;
                 ptx::tc_fence_after();
                 if (t == it.ntiles / 2 && x + gridDim.x < s.items) {
                     const Item after = item_of(s, x + gridDim.x);
-                    if (after.ntiles) next = query_of(after);
+                    follow = after.ntiles > 0;
+                    if (follow && (blk == 0 || !after.half)) next = query_of(after);
                 }
-                if (t + 1 == it.ntiles && next >= 0) {
-                    load_queries(next);
+                if (t + 1 == it.ntiles && follow) {
+                    if (next >= 0) load_queries(next);
                     loaded = true;
+                }
+                if (!mine) {
+                    ptx::mbar_arrive(&bar.p_full[blk]);
+                    continue;
                 }
                 const int v0 = t * kTile;
                 const uint32_t there = notes.there[jt & 3];
@@ -584,9 +609,10 @@ struct RowThread {
             if (it.ntiles) {
                 if (!wait_warp(&bar.o_full[blk], nitem & 1, gave_up)) return false;
                 ptx::tc_fence_after();
-                if (notes.foul[nitem & 3] == nitem + 1) add_foul(it, own);
+                if (mine && notes.foul[nitem & 3] == nitem + 1) add_foul(it, own);
                 ++nitem;
             }
+            if (!mine) continue;
             // Rows of 64 places go through shared memory, so that stores are whole lines (a row a
             // thread, 16 bytes at a time, took 3800 cycles an item).
             const int h = it.hk * int(s.G.d) + rr - tk * int(s.G.d);
@@ -670,7 +696,7 @@ k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = tmem_at;
+    const uint32_t tmem = __shfl_sync(~0u, tmem_at, 0);
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
         const int blk = warp / 4;
@@ -681,9 +707,9 @@ k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 8) {
-            if (lane == 0) {
-                issue<D>(s, bar, &gave_up, base, tmem);
-                // nothing is under way when tensor memory is given back
+            issue<D>(s, bar, &gave_up, base, tmem);
+            // nothing is under way when tensor memory is given back
+            if (ptx::elect_one()) {
                 ptx::mma_commit(&bar.done);
                 ptx::mbar_wait(&bar.done, 0);
             }
@@ -762,7 +788,11 @@ cudaError_t launch_paged_prompt(const PagedArgs &a, cudaStream_t stream) {
     s.ps = Divisor(uint32_t(a.c.ps));
     s.rows = a.T * (a.Hq / a.c.Hkv);
     s.nrb = (s.rows + kItemRows - 1) / kItemRows;
-    s.items = int(items_of(a, kItemRows));
+    // Where the items do not go up in whole rounds of the SMs, and half of them are free in the last one,
+    // that round's items are halved.
+    const int n = int(items_of(a, kItemRows)), sms = device_sm_count(), over = n % sms;
+    s.whole = 2 * over <= sms ? n - over : n;
+    s.items = 2 * n - s.whole;
     return a.c.D == 64 ? launch_d<64>(a, s, stream) : launch_d<128>(a, s, stream);
 }
 
