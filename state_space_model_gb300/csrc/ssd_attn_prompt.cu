@@ -34,6 +34,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #define SSD_DBG_FILE 9u   // kDbgPrompt
 
@@ -42,7 +43,7 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kRows = 128, kItemRows = 2 * kRows;   // rows of a block, of an item
-constexpr int kTile = 128;                          // positions of a tile
+constexpr int kTile = 128, kPart = kTile / 2;       // positions of a tile, of it for a block of a half item
 constexpr int kBox = 16;                             // positions of a load
 constexpr int kThreads = 2 * kRows + 32 * 4;         // and a warp that issues, two that load, one that checks
 // Registers of a thread: 168 at the launch (65536 / 384), shared out as 208 for the rows'
@@ -84,7 +85,7 @@ struct Shape {
     Divisor heads, per_b, G, ps;      // by B Hkv, by Hkv, by the query heads of a key/value head, by the page
 };
 
-// Rows r0 on of sequence b and head hk, for one block of a half item.  Index v < total of the run of positions that some row
+// Rows r0 on of sequence b and head hk.  Index v < total of the run of positions that some row
 // sees: position v below ns, then lo + v - ns; ns and lo are multiples of a box.
 struct Item {
     int b, hk, r0;
@@ -94,7 +95,8 @@ struct Item {
 };
 
 // Item number x: the last rows come first, which see most where there is no window.  From s.whole
-// on two numbers share an item, a block of rows each.
+// on two numbers share an item, a block of rows each, of which the CTA's two blocks of threads see
+// half of every tile each and join their sums at the end.
 __device__ __forceinline__ Item item_of(const Shape &s, int x) {
     Item it;
     it.half = x >= s.whole;
@@ -190,6 +192,7 @@ struct Barriers {
     uint64_t k_land[3], v_land[3];
     uint64_t ready[3];                // a tile's values, looked through, and the next tile's keys
     uint64_t q_full[2], s_full[2][3], p_full[2], o_full[2];
+    uint64_t parted, joined;          // a half item's second sums are written, and read
     uint64_t done;
 };
 // What is known of the last four tiles (a tile's loads begin when the products of scores of the
@@ -198,6 +201,7 @@ struct Notes {
     uint32_t there[4];                // bit i: box i's page exists
     int foul[4];                      // of the last four items: the item's number + 1 if a value that was
                                       // looked at is infinite or NaN
+    float2 sums[kRows];               // a half item's second maxima and sums
 };
 
 // The rows of an item: from where on some do not see all that is there (v >= least), and below
@@ -343,20 +347,24 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
     // a block's scores of tile t of the item, tile jt of the CTA
     auto scores = [&](int blk) {
         const int ks = jt % C::NK;
-        const uint32_t id = kIdS | uint32_t(min(kTile, (total - t * kTile + 31) & ~31) >> 3) << 17;
-        const uint64_t q = ptx::sdesc(base + C::Q + blk * C::OPERAND, 16, 1024);
-        const uint64_t k = ptx::sdesc(base + C::K + ks * C::OPERAND, 16, 1024);
         if (jt == 0 && !wait_warp(&bar.k_land[0], 0, gave_up)) return false;
         if (t == 0 && !wait_warp(&bar.q_full[blk], nitem & 1, gave_up)) return false;
+        auto multiply = [&](int n, uint32_t q_at, uint32_t k_at) {
+            const uint32_t id = kIdS | uint32_t((n + 31) & ~31) >> 3 << 17;
+            const uint64_t q = ptx::sdesc(q_at, 16, 1024), k = ptx::sdesc(k_at, 16, 1024);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const uint64_t o = uint64_t((i / 4) * C::HALF + (i % 4) * 32) >> 4;
+                ptx::mma_bf16_ss(tmem + kS + 128 * blk, q + o, k + o, id, i != 0);
+            }
+        };
         if (ptx::elect_one()) {
             ptx::tc_fence_after();
-            if (blk == 0 || !half) {  // (the second block of a half item only counts along)
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint64_t o = uint64_t((i / 4) * C::HALF + (i % 4) * 32) >> 4;
-                    ptx::mma_bf16_ss(tmem + kS + 128 * blk, q + o, k + o, id, i != 0);
-                }
-            }
+            const int left = total - t * kTile, behind = left - blk * kPart;
+            if (!half)
+                multiply(min(kTile, left), base + C::Q + blk * C::OPERAND, base + C::K + ks * C::OPERAND);
+            else if (behind > 0)      // a part of the tile each, for the same queries
+                multiply(min(kPart, behind), base + C::Q, base + C::K + ks * C::OPERAND + blk * kPart * 128);
             ptx::mma_commit(&bar.s_full[blk][ks]);
         }
         __syncwarp();
@@ -367,8 +375,8 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
     if (ntiles == 0 || !scores(0) || !scores(1)) return;
     for (;;) {
         const int vs = jt % C::NV, at = jt;
-        const int steps = min(kTile / 16, (total - t * kTile + 15) / 16);
-        const bool first = t == 0, last = t + 1 == ntiles, one = half;
+        const int left = total - t * kTile;
+        const bool first = t == 0, last = t + 1 == ntiles, halved = half;
         bool more = true;
         if (first) find_next();
         if (last) {
@@ -388,12 +396,18 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
             if (ptx::elect_one()) {
                 ptx::tc_fence_after();
                 const uint32_t scores_at = tmem + kS + 128 * blk, outputs_at = tmem + kO + 128 * blk;
-                if (blk == 0 || !one) {
+                auto add_up = [&](int n, int chunk, auto most) {
+                    const int steps = (n + 15) / 16;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
+                    for (int i = 0; i < decltype(most)::value; ++i)
                         if (i < steps)
-                            ptx::mma_bf16_ts(outputs_at, scores_at + 8 * i, v + uint64_t(i * 128), kIdO, !first || i > 0);
-                }
+                            ptx::mma_bf16_ts(outputs_at, scores_at + 8 * i, v + uint64_t((chunk + i) * 128), kIdO,
+                                             !first || i > 0);
+                };
+                if (!halved)
+                    add_up(left, 0, std::integral_constant<int, kTile / 16>());
+                else
+                    add_up(left - blk * kPart, blk * kPart / 16, std::integral_constant<int, kPart / 16>());
                 if (last) ptx::mma_commit(&bar.o_full[blk]);
             }
             __syncwarp();
@@ -440,10 +454,13 @@ struct RowThread {
         }
     }
 
+    __device__ __forceinline__ int row_of(const Item &it) const {
+        return it.r0 + (it.half ? 0 : blk * kRows) + warp * 32 + lane;
+    }
     // This warp's 32 rows of an item's queries to shared memory (the products that read the ones
     // before them are done); and their arrival.
     __device__ __forceinline__ int64_t query_of(const Item &it) const {     // the lane's row of them
-        const int r = min(it.r0 + blk * kRows + warp * 32 + lane, s.rows - 1), t = s.G.of(r), G = int(s.G.d);
+        const int r = min(row_of(it), s.rows - 1), t = s.G.of(r), G = int(s.G.d);
         return it.b * a.q_sb + t * a.q_st + (it.hk * G + r - t * G) * a.q_sh;
     }
     __device__ __forceinline__ void load_queries(int64_t off) {
@@ -466,17 +483,14 @@ struct RowThread {
     // Tile t of an item for this thread's row, which sees [va, vb) of its run, and below vb what lies
     // below `sinks` too: scores to weights, with the row's reference m and sum l.  large: the
     // warp's scores are.  kWhole: all rows of
-    // the warp see 128 positions.
-    template <bool kWhole>
-    __device__ __forceinline__ void tile(int t, int va, int vb, uint32_t there, float qs, float &m,
+    // the warp see all positions.  W: 128, or 64 of a half item, from v0 on.
+    template <bool kWhole, int W>
+    __device__ __forceinline__ void tile(int t, int v0, int va, int vb, uint32_t there, float qs, float &m,
                                          float &l, float &minus, bool &large) {
-        const int v0 = t * kTile;
-        uint32_t raw[4][32];
+        uint32_t raw[W / 32][32];
         // (of a narrower tile too: what its products have not written is not seen)
-        ptx::tmem_ld32(ts, raw[0]);
-        ptx::tmem_ld32(ts + 32, raw[1]);
-        ptx::tmem_ld32(ts + 64, raw[2]);
-        ptx::tmem_ld32(ts + 96, raw[3]);
+#pragma unroll
+        for (int c = 0; c < W / 32; ++c) ptx::tmem_ld32(ts + 32 * c, raw[c]);
         float mx = -INFINITY;
         auto look = [&](int c) {
             if constexpr (!kWhole) {
@@ -496,10 +510,8 @@ struct RowThread {
             mx = max3(mx, top[0], top[1]);
         };
         ptx::tmem_ld_wait();
-        look(0);
-        look(1);
-        look(2);
-        look(3);
+#pragma unroll
+        for (int c = 0; c < W / 32; ++c) look(c);
         if (__any_sync(~0u, (mx - m) * qs > kSlack || (m == -INFINITY && mx != m)) || large) {
             const float to_m = fmaxf(m, mx);
             const float f = m == -INFINITY ? 1.f : ex2((m - to_m) * qs);
@@ -525,7 +537,7 @@ struct RowThread {
             if (large) {
                 minus = 0.f;
 #pragma unroll
-                for (int i = 0; i < 128; ++i)
+                for (int i = 0; i < W; ++i)
                     raw[i / 32][i % 32] = __float_as_uint(__uint_as_float(raw[i / 32][i % 32]) - ref);
             }
         }
@@ -543,10 +555,8 @@ struct RowThread {
             }
             ptx::tmem_st16(ts + 16 * c, p);
         };
-        weights(0);
-        weights(1);
-        weights(2);
-        weights(3);
+#pragma unroll
+        for (int c = 0; c < W / 32; ++c) weights(c);
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bar.p_full[blk]);
@@ -554,22 +564,57 @@ struct RowThread {
         l += s0.x + s0.y;
     }
 
+    // An item's tiles.  loaded: the next one's queries are on their way.
+    template <bool kHalf>
+    __device__ __forceinline__ bool tiles(const Item &it, int x, int va, int vb, float qs, int &jt, bool &loaded,
+                                          float &m, float &l) {
+        constexpr int W = kHalf ? kPart : kTile;
+        float minus = 0.f;            // -qs m where that is small
+        bool large = false;
+        // the next item's queries, loaded when the last scores of this one are made
+        int64_t next = -1;            // where the lane's row of them is
+        bool follow = false;
+#pragma unroll 1
+        for (int t = 0; t < it.ntiles; ++t, ++jt) {
+            if (!wait_warp(&bar.s_full[blk][jt % C::NK], (jt / C::NK) & 1, gave_up)) return false;
+            ptx::tc_fence_after();
+            if (t == it.ntiles / 2 && x + gridDim.x < s.items) {
+                const Item after = item_of(s, x + gridDim.x);
+                follow = after.ntiles > 0;
+                if (follow && (blk == 0 || !after.half)) next = query_of(after);
+            }
+            if (t + 1 == it.ntiles && follow) {
+                // (a half item's other scores are made of the same queries)
+                if (kHalf && blk == 0 && !wait_warp(&bar.s_full[1][jt % C::NK], (jt / C::NK) & 1, gave_up)) return false;
+                if (next >= 0) load_queries(next);
+                loaded = true;
+            }
+            const int v0 = t * kTile + (kHalf ? blk * W : 0);
+            constexpr uint32_t kAll = (1u << W / kBox) - 1;
+            const uint32_t there = notes.there[jt & 3] >> (kHalf ? blk * (W / kBox) : 0) & kAll;
+            if (__all_sync(~0u, v0 + W <= vb && (va <= v0 || v0 + W <= s.sinks) && there == kAll))
+                tile<true, W>(t, v0, va, vb, there, qs, m, l, minus, large);
+            else
+                tile<false, W>(t, v0, va, vb, there, qs, m, l, minus, large);
+        }
+        return true;
+    }
+
     __device__ __forceinline__ bool run() {
         const float qs = a.scale * kLog2e;
-        int jt = 0, nitem = 0;
+        int jt = 0, nitem = 0, nhalf = 0;
         bool loaded = false;          // this item's queries
 #pragma unroll 1
         for (int x = blockIdx.x; x < s.items; x += gridDim.x) {
             const Item it = item_of(s, x);
-            const bool mine = blk == 0 || !it.half;
-            const int r = mine ? it.r0 + blk * kRows + warp * 32 + lane : s.rows, rr = min(r, s.rows - 1);
+            const bool mine = blk == 0 || !it.half;    // (of a half item the first block's threads write)
+            const int r = row_of(it), rr = min(r, s.rows - 1);
             const int tk = s.G.of(rr), own = it.len - s.T + tk;
             // what it sees of the item's run: [va, vb), and below vb what lies below `sinks` too (where
             // ns < sinks it is lo, and the run has no gap)
             const int vb = own < it.lo ? min(own + 1, it.ns) : it.ns + own - it.lo + 1;
             const int va = s.window > 0 ? it.ns + max(own - s.window + 1 - it.lo, 0) : 0;
-            float m = -INFINITY, l = 0.f, minus = 0.f;   // minus: -qs m where that is small
-            bool large = false;
+            float m = -INFINITY, l = 0.f;
             if (it.ntiles) {
                 if (!loaded) {
                     if (mine) load_queries(query_of(it));
@@ -577,42 +622,55 @@ struct RowThread {
                 }
                 loaded = false;
             }
-            // the next item's queries, loaded when the last scores of this one are made
-            int64_t next = -1;        // where the lane's row of them is
-            bool follow = false;
-#pragma unroll 1
-            for (int t = 0; t < it.ntiles; ++t, ++jt) {
-                if (!wait_warp(&bar.s_full[blk][jt % C::NK], (jt / C::NK) & 1, gave_up)) return false;
-                ptx::tc_fence_after();
-                if (t == it.ntiles / 2 && x + gridDim.x < s.items) {
-                    const Item after = item_of(s, x + gridDim.x);
-                    follow = after.ntiles > 0;
-                    if (follow && (blk == 0 || !after.half)) next = query_of(after);
-                }
-                if (t + 1 == it.ntiles && follow) {
-                    if (next >= 0) load_queries(next);
-                    loaded = true;
-                }
-                if (!mine) {
-                    ptx::mbar_arrive(&bar.p_full[blk]);
-                    continue;
-                }
-                const int v0 = t * kTile;
-                const uint32_t there = notes.there[jt & 3];
-                if (__all_sync(~0u, v0 + kTile <= vb && (va <= v0 || v0 + kTile <= s.sinks) &&
-                                        there == (1u << kTile / kBox) - 1))
-                    tile<true>(t, va, vb, there, qs, m, l, minus, large);
-                else
-                    tile<false>(t, va, vb, there, qs, m, l, minus, large);
-            }
+            if (!(it.half ? tiles<true>(it, x, va, vb, qs, jt, loaded, m, l) : tiles<false>(it, x, va, vb, qs, jt, loaded, m, l)))
+                return false;
             if (loaded) queries_loaded();
+            float f0 = 1.f, f1 = 0.f;             // the two sums' factors
+            bool two = false;                     // there is something in the second
             if (it.ntiles) {
                 if (!wait_warp(&bar.o_full[blk], nitem & 1, gave_up)) return false;
+                if (it.half) {
+                    if (blk == 1) {
+                        notes.sums[warp * 32 + lane] = make_float2(m, l);
+                        ptx::mbar_arrive(&bar.parted);
+                        if (!wait_warp(&bar.joined, nhalf & 1, gave_up)) return false;
+                    } else {
+                        if (!wait_warp(&bar.o_full[1], nitem & 1, gave_up) ||
+                            !wait_warp(&bar.parted, nhalf & 1, gave_up))
+                            return false;
+                        const float2 other = notes.sums[warp * 32 + lane];
+                        const float to_m = fmaxf(m, other.x);
+                        f0 = m == -INFINITY ? 0.f : ex2((m - to_m) * qs);
+                        two = other.x != -INFINITY;
+                        f1 = two ? ex2((other.x - to_m) * qs) : 0.f;
+                        l = l * f0 + other.y * f1;
+                        m = to_m;
+                    }
+                    ++nhalf;
+                }
                 ptx::tc_fence_after();
-                if (mine && notes.foul[nitem & 3] == nitem + 1) add_foul(it, own);
-                ++nitem;
             }
+            const bool joins = it.half && it.ntiles && blk == 0, foul = it.ntiles && notes.foul[nitem & 3] == nitem + 1;
+            nitem += it.ntiles > 0;
             if (!mine) continue;
+            if (joins) {              // O = f0 O + f1 O of the other block, back where it was
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16], p[16];
+                    ptx::tmem_ld16(to + c, o);
+                    ptx::tmem_ld16(to + kRows + c, p);
+                    ptx::tmem_ld_wait();
+                    // (what was never written may be anything)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        o[i] = __float_as_uint(__uint_as_float(o[i]) * f0 + (two ? __uint_as_float(p[i]) * f1 : 0.f));
+                    ptx::tmem_st16(to + c, o);
+                }
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&bar.joined);
+            }
+            if (foul) add_foul(it, own);
             // Rows of 64 places go through shared memory, so that stores are whole lines (a row a
             // thread, 16 bytes at a time, took 3800 cycles an item).
             const int h = it.hk * int(s.G.d) + rr - tk * int(s.G.d);
@@ -686,6 +744,8 @@ k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             ptx::mbar_init(&bar.o_full[i], 1);
             for (int k = 0; k < 3; ++k) ptx::mbar_init(&bar.s_full[i][k], 1);
         }
+        ptx::mbar_init(&bar.parted, kRows);
+        ptx::mbar_init(&bar.joined, kRows);
         ptx::mbar_init(&bar.done, 1);
         ptx::fence_mbar_init();
     }
