@@ -10,18 +10,24 @@
 //                   back over S
 //   O += P V        tcgen05, P from tensor memory, O in tensor memory (fp32)
 //
-// What bounds it is the products, 4 D flops a row and position: with 256 rows to a tile the
-// reads from L2 are 64 KB for 2 x 4.2 Mflop of them each.  So one thread issues nothing but
-// products, in the order S0, S1, then for every tile O0, S0 (next), O1, S1 (next): while a
-// block's exponentials run, the tensor core has the other's products.  Two warps load (TMA),
-// tiles ahead and across items, and the CTA goes from item to item (sequence, head, 256 rows)
-// with the next one's queries and keys already there.
+// What bounds it is the products, 4 D flops a row and position, and the way from one to the next: a
+// block's scores, its exponentials and its outputs follow one another, 2700 cycles a tile, 1024 of them
+// products.  So a warp issues nothing but products, in the order S0, S1, then for every tile O0, S0
+// (next), O1, S1 (next): while a block's exponentials run, the tensor core has the other's products.
+// (All of that warp goes through the loop and one lane issues, so that descriptors stay uniform: a single
+// thread's branch took 100 cycles a product instead of 25, 444 us instead of 418 for 8192 tokens of 32
+// over 8 heads; outputs and the next scores issued together, 407: 1350 TFLOP/s.)  With 256 rows to a
+// tile the reads from L2 are 64 KB for 2 x 4.2 Mflop of them each.  Two warps load (TMA), tiles ahead
+// and across items, and the CTA goes from item to item (sequence, head, 256 rows) with the next one's
+// queries and keys already there.  Where most SMs would have no item in the last round, an item is
+// halved: 128 rows, for which the two blocks take half of every tile each and join their sums at the end
+// (512 tokens over 8192: 64 items 104 us, 128 halves 82).
 //
 // The positions that some row of an item sees, sinks first and then the window's, are counted
 // through as one run in boxes of 16 of a page (so pages are multiples of 16; others take the
 // kernels of ssd_attn.cuh), so that a tile holds little that nobody needs wherever the window
-// begins.  (Copies by three warps, 16 bytes a lane, took any page size and four times as long: 253
-// us where the loads make 4096 tokens under a window of 1024 take 85.)
+// begins.  (Copies by three warps, 16 bytes a lane, took any page size and three times as
+// long: 253 us for 4096 tokens under a window of 1024 where the loads take 78.)
 #include "ptx_sm100.cuh"
 #include "ssd_attn.h"
 #include "ssd_block_math.cuh"
@@ -344,11 +350,9 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
         ntiles = next_tiles;
         half = next_half;
     };
-    // a block's scores of tile t of the item, tile jt of the CTA
+    // a block's scores of tile t of the item, tile jt of the CTA (one lane's)
     auto scores = [&](int blk) {
-        const int ks = jt % C::NK;
-        if (jt == 0 && !wait_warp(&bar.k_land[0], 0, gave_up)) return false;
-        if (t == 0 && !wait_warp(&bar.q_full[blk], nitem & 1, gave_up)) return false;
+        const int ks = jt % C::NK, left = total - t * kTile;
         auto multiply = [&](int n, uint32_t q_at, uint32_t k_at) {
             const uint32_t id = kIdS | uint32_t((n + 31) & ~31) >> 3 << 17;
             const uint64_t q = ptx::sdesc(q_at, 16, 1024), k = ptx::sdesc(k_at, 16, 1024);
@@ -358,24 +362,28 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
                 ptx::mma_bf16_ss(tmem + kS + 128 * blk, q + o, k + o, id, i != 0);
             }
         };
+        if (!half)
+            multiply(min(kTile, left), base + C::Q + blk * C::OPERAND, base + C::K + ks * C::OPERAND);
+        else if (left > blk * kPart)  // a part of the tile each, for the same queries
+            multiply(min(kPart, left - blk * kPart), base + C::Q, base + C::K + ks * C::OPERAND + blk * kPart * 128);
+        ptx::mma_commit(&bar.s_full[blk][ks]);
+    };
+    // the first ones of an item
+    auto first_scores = [&](int blk) {
+        if (jt == 0 && !wait_warp(&bar.k_land[0], 0, gave_up)) return false;
+        if (!wait_warp(&bar.q_full[blk], nitem & 1, gave_up)) return false;
         if (ptx::elect_one()) {
             ptx::tc_fence_after();
-            const int left = total - t * kTile, behind = left - blk * kPart;
-            if (!half)
-                multiply(min(kTile, left), base + C::Q + blk * C::OPERAND, base + C::K + ks * C::OPERAND);
-            else if (behind > 0)      // a part of the tile each, for the same queries
-                multiply(min(kPart, behind), base + C::Q, base + C::K + ks * C::OPERAND + blk * kPart * 128);
-            ptx::mma_commit(&bar.s_full[blk][ks]);
+            scores(blk);
         }
         __syncwarp();
         return true;
     };
     find_next();
     take_next();
-    if (ntiles == 0 || !scores(0) || !scores(1)) return;
+    if (ntiles == 0 || !first_scores(0) || !first_scores(1)) return;
     for (;;) {
-        const int vs = jt % C::NV, at = jt;
-        const int left = total - t * kTile;
+        const int vs = jt % C::NV, at = jt, left = total - t * kTile;
         const bool first = t == 0, last = t + 1 == ntiles, halved = half;
         bool more = true;
         if (first) find_next();
@@ -395,23 +403,25 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
             if (!wait_warp(&bar.p_full[blk], at & 1, gave_up)) return;
             if (ptx::elect_one()) {
                 ptx::tc_fence_after();
-                const uint32_t scores_at = tmem + kS + 128 * blk, outputs_at = tmem + kO + 128 * blk;
                 auto add_up = [&](int n, int chunk, auto most) {
                     const int steps = (n + 15) / 16;
 #pragma unroll
                     for (int i = 0; i < decltype(most)::value; ++i)
                         if (i < steps)
-                            ptx::mma_bf16_ts(outputs_at, scores_at + 8 * i, v + uint64_t((chunk + i) * 128), kIdO,
-                                             !first || i > 0);
+                            ptx::mma_bf16_ts(tmem + kO + 128 * blk, tmem + kS + 128 * blk + 8 * i,
+                                             v + uint64_t((chunk + i) * 128), kIdO, !first || i > 0);
                 };
                 if (!halved)
                     add_up(left, 0, std::integral_constant<int, kTile / 16>());
                 else
                     add_up(left - blk * kPart, blk * kPart / 16, std::integral_constant<int, kPart / 16>());
-                if (last) ptx::mma_commit(&bar.o_full[blk]);
+                if (last)
+                    ptx::mma_commit(&bar.o_full[blk]);
+                else
+                    scores(blk);
             }
             __syncwarp();
-            if (more && !scores(blk)) return;
+            if (last && more && !first_scores(blk)) return;
         }
         if (!more) return;
     }
@@ -818,19 +828,20 @@ int64_t items_of(const PagedArgs &a, int block) {       // row blocks of a size
 
 }  // namespace
 
-// An item's time goes by its positions alone, 1.75 us for 128 of them (D = 64: 1.55), with all of its
-// rows there or not; the kernels of ssd_attn.cuh split a sequence's positions over the SMs and take
-// 0.0154 us (0.0106) for 128 positions and a block of 64 rows.  So this kernel takes over at 114 (146)
-// such blocks.  Measured, here / there: 128 blocks (8 sequences of 32 tokens over 8192 positions, 32
-// over 8 heads) 121 / 140 us, D = 64 105 / 99; 256 blocks (512 tokens over 8192) 119 / 261, 105 /
-// 184; 8192 tokens 458 / 2170, 398 / 1499.  (A scale below 0 would have to turn the scores' signs,
-// which no model asks for.  Fewer rows than a block of a sequence and head take the others too: 96
-// sequences, 4 rows, a window of 1024: 93 us here, 47 there.  Pools with a stride of 0 have no tensor map.)
+// An item's time goes by its positions alone, 1.57 us for 128 of them (D = 64: 1.39), a half item's 1.28
+// (1.12), with all of its rows there or not; the kernels of ssd_attn.cuh split a sequence's positions
+// over the SMs and take 0.0154 us (0.0106) for 128 positions and a block of 64 rows.  So this kernel takes
+// over at 83 (106) such blocks.  Measured, here / there: 88 blocks
+// (176 tokens of 32 over 8 heads over 8192) 81 / 102 us; 112 blocks, D = 64, 72 / 91; 256 blocks (512 tokens over 8192) 82 /
+// 261 us, D = 64 72 / 184; 8192 tokens 407 / 2167, 354 / 1500.  (A scale below 0 would have to turn the
+// scores' signs, which no model asks for.  Fewer rows than a block of a sequence and head take the others
+// too: 96 sequences, 4 rows, a window of 1024: 93 us here, 47 there.  Pools with a stride of 0 have no
+// tensor map.)
 bool prompt_fits(const PagedArgs &a) {
     const int64_t blocks = items_of(a, 64), sms = device_sm_count();
     const bool apart = a.c.st > 0 && (a.c.Hkv == 1 || a.c.sh > 0) && (a.c.pages == 1 || a.c.sp > 0);
     return apart && a.c.dt == DT_BF16 && a.T * (a.Hq / a.c.Hkv) >= kRows && a.scale > 0.f && a.c.ps % kBox == 0 && a.c.pages > 0 &&
-           (a.c.D == 128 ? 4 * blocks >= 3 * sms : blocks >= sms) && items_of(a, kItemRows) < (1 << 30);
+           20 * blocks >= (a.c.D == 128 ? 11 : 14) * sms && items_of(a, kItemRows) < (1 << 30);
 }
 
 cudaError_t launch_paged_prompt(const PagedArgs &a, cudaStream_t stream) {

@@ -346,6 +346,12 @@ PROMPTS = [
     (128, 8, 8, 128, 128, [128, 5000, 1, 127, 200], 1, 1),
     (257, 6, 6, 64, 100, [257, 1300, 256, 255, 30, 4000, 1], 1000, 64),
     (90, 33, 11, 128, 32, [90, 3000, 91, 0], 500, 10000),
+    # a whole round of items and halved ones behind it; a half without rows; 16 positions in all
+    (1400, 32, 8, 128, 16, [1411], 0, 0),
+    (1400, 32, 8, 64, 16, [3000], 400, 20),
+    (90, 8, 8, 128, 16, [300] * 12, 0, 0),
+    (300, 32, 8, 128, 16, [16], 0, 0),
+    (300, 32, 8, 64, 32, [70, 64, 1], 33, 7),
 ]
 
 
