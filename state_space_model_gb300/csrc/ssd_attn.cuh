@@ -484,12 +484,15 @@ __device__ __forceinline__ void let_next_start() {
 // copies are under way while two tiles are worked on.
 //
 // Measured (GB300, of the rate of a large copy, 6765 GB/s): 64 sequences of 4096, 64
-// query heads over 8 of 128, bf16: 170 us, 93%; the same in fp8 95 us, 86%; one
-// sequence of 131072, 32 over 8: 86 us, 92%; 96 of 17 to 16384 over fp8: 77 us, 82%.
+// query heads over 8 of 128, bf16: 167 us, 95%; the same in fp8 95 us, 86%; in 4 bits
+// 80 us, 59%; one sequence of 131072, 32 over 8: 86 us, 92%; 96 of 17 to 16384 over fp8:
+// 77 us, 82%.
 // Query rows cost little up to 32 a key/value head in bf16 (177 us) and 16 in fp8
 // (105 us); at 64 in bf16 (265 us) and 32 in fp8 (168 us) the products take longer than
-// the reads.  Pieces of prompts are blocks of 64 rows: 8192 tokens of 32 over 8 heads
-// take 2.1 ms in bf16, 258 TFLOP/s.
+// the reads.  In 4 bits they do from 8 rows on (16 rows 104 us, 32 179): a conversion and a
+// product with the group's scale for every four codes share the issue slots, the latter
+// the tensor cores' pipe too.  Pieces of prompts are blocks of 64 rows (8192 tokens of 32 over
+// 8 heads: 2.4 ms in fp8); over bf16 pools ssd_attn_prompt.cu takes them.
 template <int D_, int FMT_, int NQ_, int WR_>
 struct Cfg {
     static constexpr int D = D_, FMT = FMT_, NQ = NQ_, WR = WR_, WK = kWarps / WR_;
@@ -1898,7 +1901,7 @@ cudaError_t launch_f32(const PagedArgs &a, const Shape &s, cudaStream_t stream) 
 // the rest of the four along the positions).  More rows than 64 are several row
 // blocks, each of which reads the cache.  64 sequences of 4096 over 8 key/value heads of
 // 128, microseconds for bf16 / fp8 with blocks of half the rows, this rule's, twice:
-//   8 rows              -  170 /  95  170 /  99
+//   8 rows              -  167 /  95  170 /  99
 //   16 rows     327 / 176  174 / 105  171 / 163
 //   32 rows     334 / 191  177 / 168  252 / 290
 inline Shape make_shape(const PagedArgs &a) {

@@ -11,7 +11,7 @@
 //   O += P V        tcgen05, P from tensor memory, O in tensor memory (fp32)
 //
 // What bounds it is the products, 4 D flops a row and position, and the way from one to the next: a
-// block's scores, its exponentials and its outputs follow one another, 2700 cycles a tile, 1024 of them
+// block's scores, its exponentials and its outputs follow one another, 2950 cycles a tile, 1024 of them
 // products.  So a warp issues nothing but products, in the order S0, S1, then for every tile O0, S0
 // (next), O1, S1 (next): while a block's exponentials run, the tensor core has the other's products.
 // (All of that warp goes through the loop and one lane issues, so that descriptors stay uniform: a single
