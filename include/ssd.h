@@ -530,8 +530,9 @@ ssd_status ssd_paged_attention_workspace_size(int64_t batch, int64_t tokens, int
  * SSD_I32, innermost stride 1; lens [B] SSD_I32; lse [B, T, Hq] f32
  * contiguous, may be NULL; workspace as above, 256-byte aligned, contents
  * ignored.  T (Hq / Hkv) at most 2^24.  Two launches (many rows over bf16 pools whose
- * pages are multiples of 16 tokens: one, which does not use the workspace); scores, sums
- * and partial results in f32, the probabilities rounded to 16 bits for the product with bf16
+ * pages are multiples of 16 tokens: one; rows that are many in a batch only: three, of
+ * which the lengths let one kernel or the other work); scores, sums and partial results in
+ * f32, the probabilities rounded to 16 bits for the product with bf16
  * values or 8-bit codes.  Scales may be any finite numbers; a row's probability times a
  * value's scale is held in 11 bits down to 2^-22 of the row's largest such weight, and
  * value scales below 2^-114 in fewer (ssd_kv_append writes none below 2^-105). */

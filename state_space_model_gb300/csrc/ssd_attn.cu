@@ -13,7 +13,12 @@ cudaError_t launch_paged(const PagedArgs &in, cudaStream_t s) {
     PagedArgs a = in;
     cudaError_t e = device_error_word(&a.err);
     if (e != cudaSuccess) return e;
-    if (prompt_fits(a)) return launch_paged_prompt(a, s);
+    const Prompt many = prompt_fits(a);
+    if (many == Prompt::kAsk) a.ask = device_sm_count();
+    if (many != Prompt::kNo) {
+        e = launch_paged_prompt(a, s);
+        if (e != cudaSuccess || many == Prompt::kYes) return e;
+    }
     const bool sinks = a.sinks > 0;
     switch (a.c.dt) {
     case DT_F8E4M3: return sinks ? launch_paged_sinks_f8(a, s) : launch_paged_f8(a, s);

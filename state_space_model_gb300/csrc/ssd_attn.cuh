@@ -27,6 +27,7 @@
 
 #include "ptx_sm100.cuh"
 #include "ssd_attn.h"
+#include "ssd_attn_choice.cuh"
 #include "ssd_block_math.cuh"
 #include "ssd_debug.cuh"
 #include "ssd_f32x2.cuh"
@@ -926,6 +927,10 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
         ptx::mbar_init(&empty[threadIdx.x], kWarps);
     }
     __syncthreads();
+    if (FMT == kBf16 && a.ask && prompt_pays(a, a.ask)) {
+        if (threadIdx.x == 0 && cut_ok(a, s, blockIdx.x)) reinterpret_cast<Cut *>(a.ws)[blockIdx.x].parts = 0;
+        return;
+    }
     const Stretch span = find<KS, kThreads / 32>(s, blockIdx.x, &finder);
     if (threadIdx.x == 0 && cut_ok(a, s, blockIdx.x)) reinterpret_cast<Cut *>(a.ws)[blockIdx.x].parts = 0;
     // A cursor: an item, a tile of it, and the units left; the tiles of an item come

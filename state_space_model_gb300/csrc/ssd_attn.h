@@ -83,12 +83,14 @@ struct PagedArgs {
     char *ws = nullptr;
     int64_t q_n = 0, o_n = 0, t_n = 0, ws_n = 0;      // extents (ws_n: bytes), debug build
     unsigned int *err = nullptr;
+    int ask = 0;          // the SMs, where two kernels are launched and the lengths tell which works
 };
 // Workspace for this problem (c.dt, c.Hkv, c.D, B, T, Hq set).
 size_t paged_workspace(const PagedArgs &a);
 cudaError_t launch_paged(const PagedArgs &a, cudaStream_t s);
 // its parts: many rows, pools of codes, calls with sinks
-bool prompt_fits(const PagedArgs &a);
+enum class Prompt { kNo, kYes, kAsk };   // kAsk: by the lengths, which the kernels look at
+Prompt prompt_fits(const PagedArgs &a);
 cudaError_t launch_paged_prompt(const PagedArgs &a, cudaStream_t s);
 cudaError_t launch_paged_f8(const PagedArgs &a, cudaStream_t s);
 cudaError_t launch_paged_f4(const PagedArgs &a, cudaStream_t s);

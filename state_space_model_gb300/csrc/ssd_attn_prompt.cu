@@ -30,6 +30,7 @@
 // long: 253 us for 4096 tokens under a window of 1024 where the loads take 78.)
 #include "ptx_sm100.cuh"
 #include "ssd_attn.h"
+#include "ssd_attn_choice.cuh"
 #include "ssd_block_math.cuh"
 #include "ssd_debug.cuh"
 #include "ssd_f32x2.cuh"
@@ -728,7 +729,8 @@ struct RowThread {
     }
 };
 
-template <int D>
+// kAsk: the lengths tell whether this kernel works.
+template <int D, bool kAsk>
 __global__ void __launch_bounds__(kThreads, 1)
 k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
@@ -740,6 +742,7 @@ k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     __shared__ uint32_t tmem_at;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const uint32_t base = (ptx::smem_u32(smem_raw) + 1023) & ~1023u;
+    if (kAsk && !prompt_pays(a, a.ask)) return;
     if (threadIdx.x == 0) {
         gave_up = 0;
         notes.foul[0] = notes.foul[1] = notes.foul[2] = notes.foul[3] = 0;
@@ -796,14 +799,14 @@ k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     if (warp == 8) ptx::tmem_dealloc(tmem, 512);
 }
 
-template <int D>
+template <int D, bool kAsk>
 cudaError_t launch_d(const PagedArgs &a, const Shape &s, cudaStream_t stream) {
     static std::atomic<uint64_t> done[4];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 256 || !((done[dev / 64].load(std::memory_order_acquire) >> (dev % 64)) & 1)) {
-        e = cudaFuncSetAttribute(k_paged_prompt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+        e = cudaFuncSetAttribute(k_paged_prompt<D, kAsk>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
         if (e != cudaSuccess) return e;
         if (dev < 256) done[dev / 64].fetch_or(uint64_t(1) << (dev % 64));
     }
@@ -817,7 +820,7 @@ cudaError_t launch_d(const PagedArgs &a, const Shape &s, cudaStream_t stream) {
         if ((e = make_tmap_bf16(&map[i], i ? a.c.v : a.c.k, 4, dims, strides, box)) != cudaSuccess) return e;
     }
     const int grid = s.items < device_sm_count() ? s.items : device_sm_count();
-    k_paged_prompt<D><<<grid, kThreads, Cfg<D>::SMEM, stream>>>(map[0], map[1], a, s);
+    k_paged_prompt<D, kAsk><<<grid, kThreads, Cfg<D>::SMEM, stream>>>(map[0], map[1], a, s);
     return cudaGetLastError();
 }
 
@@ -836,12 +839,16 @@ int64_t items_of(const PagedArgs &a, int block) {       // row blocks of a size
 // 261 us, D = 64 72 / 184; 8192 tokens 407 / 2167, 354 / 1500.  (A scale below 0 would have to turn the
 // scores' signs, which no model asks for.  Fewer rows than a block of a sequence and head take the others
 // too: 96 sequences, 4 rows, a window of 1024: 93 us here, 47 there.  Pools with a stride of 0 have no
-// tensor map.)
-bool prompt_fits(const PagedArgs &a) {
+// tensor map.)  Where a single sequence has so many blocks (what whole items need: 102, D = 64 131) no
+// lengths make this the slower one; where it takes all of a batch's, the lengths tell (prompt_pays).
+Prompt prompt_fits(const PagedArgs &a) {
     const int64_t blocks = items_of(a, 64), sms = device_sm_count();
     const bool apart = a.c.st > 0 && (a.c.Hkv == 1 || a.c.sh > 0) && (a.c.pages == 1 || a.c.sp > 0);
-    return apart && a.c.dt == DT_BF16 && a.T * (a.Hq / a.c.Hkv) >= kRows && a.scale > 0.f && a.c.ps % kBox == 0 && a.c.pages > 0 &&
-           20 * blocks >= (a.c.D == 128 ? 11 : 14) * sms && items_of(a, kItemRows) < (1 << 30);
+    const bool wide = a.c.D == 128;
+    if (!apart || a.c.dt != DT_BF16 || a.T * (a.Hq / a.c.Hkv) < kRows || !(a.scale > 0.f) || a.c.ps % kBox ||
+        a.c.pages <= 0 || 20 * blocks < (wide ? 11 : 14) * sms || items_of(a, kItemRows) >= (1 << 30))
+        return Prompt::kNo;
+    return a.B == 1 || 20 * blocks >= int64_t(a.B) * (wide ? 14 : 18) * sms ? Prompt::kYes : Prompt::kAsk;
 }
 
 cudaError_t launch_paged_prompt(const PagedArgs &a, cudaStream_t stream) {
@@ -864,7 +871,8 @@ cudaError_t launch_paged_prompt(const PagedArgs &a, cudaStream_t stream) {
     const int n = int(items_of(a, kItemRows)), sms = device_sm_count(), over = n % sms;
     s.whole = 2 * over <= sms ? n - over : n;
     s.items = 2 * n - s.whole;
-    return a.c.D == 64 ? launch_d<64>(a, s, stream) : launch_d<128>(a, s, stream);
+    if (a.ask) return a.c.D == 64 ? launch_d<64, true>(a, s, stream) : launch_d<128, true>(a, s, stream);
+    return a.c.D == 64 ? launch_d<64, false>(a, s, stream) : launch_d<128, false>(a, s, stream);
 }
 
 }  // namespace ssd

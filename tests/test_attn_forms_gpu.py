@@ -482,3 +482,33 @@ def test_pieces_of_prompts_of_shared_pools(attn):
     want = attn.paged_attention(q, *[x.contiguous() for x in wide], table, lens)
     top = want.float().abs().amax()
     assert ((got - want).float().abs() <= 2.0 ** -6 * top).all()
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 5)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows_of_batches_of_any_lengths(attn, D, window, sinks):
+    """The lengths, which only the device has, tell which kernel takes the call: a batch of equal ones,
+    one long one among short ones, empty ones; one captured graph serves them all."""
+    B, T, Hq, Hkv = 14, 32, 32, 8
+    longest = 9000
+    q, pools, table, lens = problem(B, T, Hq, Hkv, D, 16, [longest] + [1500] * (B - 1), BF, 70)
+    cases = [[1500] * B, [longest] + [40] * (B - 1), [33] * B, [0] * B, [longest] + [1500] * (B - 1),
+             [31, 32, 33, 1, 0] + [1000] * (B - 5)]
+    out = torch.empty_like(q)
+    ws = torch.empty(max(attn.paged_attention_workspace_size(B, T, Hq, Hkv, D), 1), dtype=torch.uint8, device="cuda")
+    call = lambda: attn.paged_attention(q, *pools.pools, table, lens, window=window, sinks=sinks, out=out, workspace=ws)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for n in cases:
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        out.fill_(7.0)
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        assert torch.equal(call(), got)
+        check(attn, (q, pools, table, lens), window, sinks)
+        assert torch.equal(attn.paged_attention(q, *pools.pools, table, lens, window=window, sinks=sinks), got)
