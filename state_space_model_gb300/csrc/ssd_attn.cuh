@@ -903,7 +903,9 @@ __device__ __forceinline__ bool copy_runs(const PagedArgs &a, const Shape &s, co
     return true;
 }
 
-template <int D, int FMT, int NQ, int WR>
+// ASK: the lengths tell whether this kernel works (compiled apart: as a
+// choice at run time it cost the calls that are not asked 4 to 7%).
+template <int D, int FMT, int NQ, int WR, bool ASK>
 __global__ void __launch_bounds__(kThreads, (Cfg<D, FMT, NQ, WR>::CTAS))
 k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
     using C = Cfg<D, FMT, NQ, WR>;
@@ -927,7 +929,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
         ptx::mbar_init(&empty[threadIdx.x], kWarps);
     }
     __syncthreads();
-    if (FMT == kBf16 && a.ask && prompt_pays(a, a.ask)) {
+    if (ASK && prompt_pays(a, a.ask)) {
         if (threadIdx.x == 0 && cut_ok(a, s, blockIdx.x)) reinterpret_cast<Cut *>(a.ws)[blockIdx.x].parts = 0;
         return;
     }
@@ -1884,13 +1886,13 @@ cudaError_t launch_join(const PagedArgs &a, const Shape &s, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, k_paged_join<T, D, F8>, a, s, per);
 }
 
-template <int D, int FMT, int NQ, int WR>
+template <int D, int FMT, int NQ, int WR, bool ASK = false>
 cudaError_t launch_mma(const PagedArgs &a, const Shape &s, cudaStream_t stream) {
     using C = Cfg<D, FMT, NQ, WR>;
     static std::atomic<uint64_t> done[4];
-    cudaError_t e = allow_smem(k_paged_mma<D, FMT, NQ, WR>, C::SMEM, done);
+    cudaError_t e = allow_smem(k_paged_mma<D, FMT, NQ, WR, ASK>, C::SMEM, done);
     if (e != cudaSuccess) return e;
-    k_paged_mma<D, FMT, NQ, WR><<<s.ncta, kThreads, C::SMEM, stream>>>(a, s);
+    k_paged_mma<D, FMT, NQ, WR, ASK><<<s.ncta, kThreads, C::SMEM, stream>>>(a, s);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return launch_join<__nv_bfloat16, D, C::F8>(a, s, stream);
 }
@@ -1940,6 +1942,8 @@ cudaError_t launch_f32_rows(const PagedArgs &a, cudaStream_t stream) {
 template <int D, int FMT>
 cudaError_t launch_rows(const PagedArgs &a, cudaStream_t stream) {
     const Shape s = make_shape(a);
+    if constexpr (FMT == kBf16)       // (blocks of 64 rows)
+        if (a.ask) return launch_mma<D, FMT, 2, 4, true>(a, s, stream);
     switch (s.RB) {
     case 8: return launch_mma<D, FMT, 1, 1>(a, s, stream);
     case 16: return launch_mma<D, FMT, 2, 1>(a, s, stream);

@@ -40,6 +40,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -840,7 +841,9 @@ int64_t items_of(const PagedArgs &a, int block) {       // row blocks of a size
 // scores' signs, which no model asks for.  Fewer rows than a block of a sequence and head take the others
 // too: 96 sequences, 4 rows, a window of 1024: 93 us here, 47 there.  Pools with a stride of 0 have no
 // tensor map.)  Where a single sequence has so many blocks (what whole items need: 102, D = 64 131) no
-// lengths make this the slower one; where it takes all of a batch's, the lengths tell (prompt_pays).
+// lengths make this the slower one, and as little where no row can see more than 1536 positions (one
+// of so many among 13 of 33: 27 / 32 us, D = 64 23 / 25);
+// where it takes all of a batch's blocks, the lengths tell (prompt_pays).
 Prompt prompt_fits(const PagedArgs &a) {
     const int64_t blocks = items_of(a, 64), sms = device_sm_count();
     const bool apart = a.c.st > 0 && (a.c.Hkv == 1 || a.c.sh > 0) && (a.c.pages == 1 || a.c.sp > 0);
@@ -848,7 +851,10 @@ Prompt prompt_fits(const PagedArgs &a) {
     if (!apart || a.c.dt != DT_BF16 || a.T * (a.Hq / a.c.Hkv) < kRows || !(a.scale > 0.f) || a.c.ps % kBox ||
         a.c.pages <= 0 || 20 * blocks < (wide ? 11 : 14) * sms || items_of(a, kItemRows) >= (1 << 30))
         return Prompt::kNo;
-    return a.B == 1 || 20 * blocks >= int64_t(a.B) * (wide ? 14 : 18) * sms ? Prompt::kYes : Prompt::kAsk;
+    int64_t most = int64_t(a.M) * a.c.ps;
+    if (a.window > 0) most = std::min(most, a.window + a.sinks + kItemRows / (a.Hq / a.c.Hkv));
+    const bool any = a.B == 1 || most <= 1536 || 20 * blocks >= int64_t(a.B) * (wide ? 14 : 18) * sms;
+    return any ? Prompt::kYes : Prompt::kAsk;
 }
 
 cudaError_t launch_paged_prompt(const PagedArgs &a, cudaStream_t stream) {
