@@ -6,13 +6,13 @@ batch of prompts and then generates hidden states token by token:
 * the state-space layer with ``ssd.mixer_prologue`` + ``ssd.chunked_fwd`` for the
   prompt and ``ssd.mixer_prologue`` + ``ssd.state_update`` for single tokens;
 * the attention layer with ``attn.kv_append`` (norm, rotation and the write into an
-  8-bit paged cache in one pass) + ``attn.paged_attention`` for both.
+  8-bit or 4-bit paged cache in one pass) + ``attn.paged_attention`` for both.
 
 At the end it reads the cache back (``attn.kv_read``) and checks the last token's
 attention against a plain softmax over those rows, and the whole decoding against one
 prompt of the full length.  Run it from the repository's root on a GPU:
 
-    python examples/hybrid_decode.py [--cache bf16]
+    python examples/hybrid_decode.py [--cache bf16 | fp4]
 """
 import argparse
 import math
@@ -75,10 +75,17 @@ class AttentionLayer:
         order = torch.randperm(batch * per, generator=g, device="cuda")
         self.table = order.view(batch, per).to(torch.int32)
         shape = (batch * per, HKV, PAGE, D)
-        kind = torch.float8_e4m3fn if cache == "fp8" else BF
-        self.k = torch.zeros(shape, device="cuda").to(kind)
-        self.v = torch.zeros(shape, device="cuda").to(kind)
-        self.ks, self.vs = (torch.ones(shape[:3], device="cuda") if cache == "fp8" else None for _ in range(2))
+        def pool(bits, kind):
+            """Codes of so many bits; torch has few operations for these types."""
+            return torch.zeros(*shape[:3], int(D * bits) // 8, dtype=torch.uint8, device="cuda").view(kind)
+
+        kind = {"fp4": torch.float4_e2m1fn_x2, "fp8": torch.float8_e4m3fn, "bf16": BF}[cache]
+        self.k, self.v = (pool({"fp4": 4, "fp8": 8, "bf16": 16}[cache], kind) for _ in range(2))
+        self.scales = {}
+        if cache != "bf16":
+            self.scales = {n: torch.ones(shape[:3], device="cuda") for n in ("k_scale", "v_scale")}
+        if cache == "fp4":       # a byte for each 16 places
+            self.scales.update({n: pool(0.5, torch.float8_e4m3fn) for n in ("k_group_scale", "v_group_scale")})
         self.lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
 
     def __call__(self, hidden):
@@ -88,11 +95,11 @@ class AttentionLayer:
         pos = self.lens[:, None] + torch.arange(n, device="cuda", dtype=torch.int32)
         slots = self.table.gather(1, (pos // PAGE).long()) * PAGE + pos % PAGE
         self.lens += n
-        self.q = attn.kv_append(q, k, v, slots.flatten().contiguous(), self.k, self.v, k_scale=self.ks,
-                                v_scale=self.vs, positions=pos.flatten().contiguous(), cos=self.cos,
-                                sin=self.sin, q_weight=self.q_weight, k_weight=self.k_weight)
+        self.q = attn.kv_append(q, k, v, slots.flatten().contiguous(), self.k, self.v,
+                                positions=pos.flatten().contiguous(), cos=self.cos, sin=self.sin,
+                                q_weight=self.q_weight, k_weight=self.k_weight, **self.scales)
         out = attn.paged_attention(self.q.view(batch, n, HQ, D), self.k, self.v, self.table, self.lens,
-                                   k_scale=self.ks, v_scale=self.vs)
+                                   **self.scales)
         self.out = out
         return hidden + out.flatten(-2) @ self.w_out
 
@@ -110,8 +117,8 @@ def check_last_token(layer):
     """The last token's attention against a softmax over the rows read back: largest error."""
     lens = layer.lens.tolist()
     cu = torch.tensor([sum(lens[:i]) for i in range(len(lens) + 1)], dtype=torch.int32, device="cuda")
-    keys, values = attn.kv_read(layer.k, layer.v, layer.table, cu, sum(lens), k_scale=layer.ks, v_scale=layer.vs,
-                                dtype=torch.float32 if layer.ks is not None else None)
+    keys, values = attn.kv_read(layer.k, layer.v, layer.table, cu, sum(lens), **layer.scales,
+                                dtype=torch.float32 if layer.scales else None)
     worst = 0.0
     for b, n in enumerate(lens):
         rows = slice(int(cu[b]), int(cu[b]) + n)
@@ -139,7 +146,7 @@ def main(cache="fp8", batch=3, prompt=300, tokens=12, seed=7):
 
 if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
-    ap.add_argument("--cache", choices=["fp8", "bf16"], default="fp8")
+    ap.add_argument("--cache", choices=["fp8", "bf16", "fp4"], default="fp8")
     last, apart = main(ap.parse_args().cache)
     print(f"last token's attention against a softmax over the cache read back: {last:.2e}")
     print(f"decoding token by token against one prompt of the full length:    {apart:.2e}")

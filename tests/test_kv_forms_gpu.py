@@ -414,6 +414,21 @@ def test_prompts_in_a_graph(attn):
         assert torch.equal(call(), got)
 
 
+def test_example_over_a_4_bit_cache(attn):
+    """The hybrid example's checks (test_attn_gpu.py runs it over the other caches).  Decoding against one
+    prompt of the full length: keys and values differ by a layer's bf16 roundings before they are coded,
+    so that a code near a halfway point may be its neighbour, a third of its group's largest away at
+    most, with its position's weight."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "hybrid_decode.py")
+    spec = importlib.util.spec_from_file_location("hybrid_decode", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    last, apart = mod.main("fp4")
+    assert last < 2e-2 and apart < 5e-2
+
+
 DEBUG_CHILD = r"""
 import ctypes, json, sys
 sys.path[:0] = [sys.argv[1], sys.argv[1] + "/tests"]
