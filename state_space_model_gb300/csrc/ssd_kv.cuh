@@ -221,10 +221,12 @@ constexpr int kAppendWarps = 4;
 // they hold, by a choice of results: a factor of 0 would bring infinities and NaN over from
 // their neighbours.  (The choice in every lane of the 8192 tokens: 36.2 us.)
 // kAxes: positions of several axes; a warp collects the angles of its token's columns, each from its
-// axis's row of the table, in shared memory (4999 tokens of 28 + 2 x 4 heads: 22.6 us; a lane that
-// loads every axis's vectors and keeps what is its own, 23.2).
+// axis's row of the table, in shared memory (4999 tokens of 28 + 2 x 4 heads: 20.5 us; a lane that
+// loads every axis's vectors and keeps what is its own, 0.7 more).  CTAs an SM: as many as a warp's passes
+// leave registers for (that case with six 22.6 us; 8192 tokens of 16 + 2 x 8 heads in fp32, two passes,
+// 48 us with eight, 53 with six; four passes with seven spill and are no faster).
 template <typename T, int D, int kCodes, bool kWhole, bool kAxes, int U>
-__global__ void __launch_bounds__(32 * kAppendWarps, 6)
+__global__ void __launch_bounds__(32 * kAppendWarps, (U == 4 ? 6 : U == 3 ? 7 : 8))
 k_kv_append(const __grid_constant__ KvAppendArgs a, int warps) {
     constexpr int LR = D / 16, RPP = 32 / LR;
     const int64_t id = int64_t(blockIdx.x) * kAppendWarps + threadIdx.x / 32;
@@ -480,14 +482,15 @@ cudaError_t append_u(const KvAppendArgs &a, cudaStream_t s) {
 }
 
 // As few warps a token as take at most four passes each (fp32: two, for their
-// registers), the passes spread evenly over them, where that still fills the GPU with
+// registers; 4-bit heads of 64 too: 5000 tokens of 24 + 2 x 4 14.4 us, with up to four
+// 16.4), the passes spread evenly over them, where that still fills the GPU with
 // warps: one load of the angles for a warp's passes, all their loads in flight (4999
 // tokens of 24 + 2 x 4 heads 12.3 us, with a warp a pass 14.4).  Else a warp a pass, so
 // that a few tokens spread over as many SMs as they can (the kernel alone, 64 tokens of
 // 64 + 2 x 8 heads in fp8 4.1 us, with four passes a warp 5.5; one token 3.7 and 5.8).
 template <typename T, int D, int kCodes, bool kAxes>
 cudaError_t append_t(const KvAppendArgs &a, cudaStream_t s) {
-    constexpr int RPP = 512 / D, kMost = sizeof(T) == 4 ? 2 : 4;
+    constexpr int RPP = 512 / D, kMost = sizeof(T) == 4 || (kCodes == kFour && D == 64) ? 2 : 4;
     const int passes = (a.Hq + RPP - 1) / RPP + 2 * ((a.c.Hkv + RPP - 1) / RPP);
     const int warps = (passes + kMost - 1) / kMost;
     if (a.T * warps < kFillWarps) return append_u<T, D, kCodes, kAxes, 1>(a, s);
