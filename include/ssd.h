@@ -468,7 +468,7 @@ ssd_status ssd_kv_append(const ssd_tensor *q, const ssd_tensor *k, const ssd_ten
  * the pairs out in turn.)  With nsections = 0 positions is [T].
  *
  * Pools of 4-bit codes: k_group_scale, v_group_scale, with SSD_F4E2M1X2 pools only.  In f32,
- *   scale = max(amax, 2^-96) / 2688 over the head's row (2688 = 6 * 448),
+ *   scale = max(amax, 2^-96) * (1 / 2688) over the head's row (2688 = 6 * 448),
  *   group scale = gmax / (6 * scale) over 16 places, rounded to nearest even to e4m3 (at
  *       most 448),
  *   code = u / (group scale * scale) rounded to nearest even, saturated at 6; 0 where the

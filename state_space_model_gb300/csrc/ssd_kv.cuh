@@ -410,7 +410,7 @@ k_kv_append(const __grid_constant__ KvAppendArgs a, int warps) {
             float amax = max_nan(kAmaxFloor, max_nan(m[0], m[1]));
 #pragma unroll
             for (int o = LR / 2; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(~0u, amax, o));
-            const float scale = amax / (kFourMax * kCodeMax), six = kFourMax * scale;
+            const float scale = amax * (1.f / (kFourMax * kCodeMax)), six = kFourMax * scale;
             const int64_t goff = page * a.c.sgp + h * a.c.sgh + at * a.c.sgt;
             uint8_t *const rows = static_cast<uint8_t *>(kind == 2 ? a.c.v : a.c.k) + off;
             float own[2], step[2];

@@ -91,7 +91,7 @@ def divided(a, b):
 def f4_reference(rows):
     """(elements' codes, group scales, scales) of float32 rows, each operation rounded."""
     n = rows.abs()
-    scale = divided(n.amax(-1).clamp(min=2.0 ** -96), 2688.0)
+    scale = n.amax(-1).clamp(min=2.0 ** -96) * float(divided(torch.ones(1), 2688.0))
     group = divided(n.unflatten(-1, (-1, 16)).amax(-1), 6 * scale[..., None]).clamp(max=448).to(F8)
     step = (group.float() * scale[..., None]).repeat_interleave(16, -1)
     x = torch.where(step == 0, torch.zeros_like(rows), divided(rows, step)).double()
