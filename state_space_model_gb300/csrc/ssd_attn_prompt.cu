@@ -352,8 +352,8 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
         ntiles = next_tiles;
         half = next_half;
     };
-    // a block's scores of tile t of the item, tile jt of the CTA (one lane's)
-    auto scores = [&](int blk) {
+    // a block's scores of tile t of the item, tile jt of the CTA (one lane's); halved: of a half item
+    auto scores = [&](int blk, auto halved) {
         const int ks = jt % C::NK, left = total - t * kTile;
         auto multiply = [&](int n, uint32_t q_at, uint32_t k_at) {
             const uint32_t id = kIdS | uint32_t((n + 31) & ~31) >> 3 << 17;
@@ -364,7 +364,7 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
                 ptx::mma_bf16_ss(tmem + kS + 128 * blk, q + o, k + o, id, i != 0);
             }
         };
-        if (!half)
+        if constexpr (!decltype(halved)::value)
             multiply(min(kTile, left), base + C::Q + blk * C::OPERAND, base + C::K + ks * C::OPERAND);
         else if (left > blk * kPart)  // a part of the tile each, for the same queries
             multiply(min(kPart, left - blk * kPart), base + C::Q, base + C::K + ks * C::OPERAND + blk * kPart * 128);
@@ -376,57 +376,63 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
         if (!wait_warp(&bar.q_full[blk], nitem & 1, gave_up)) return false;
         if (ptx::elect_one()) {
             ptx::tc_fence_after();
-            scores(blk);
+            if (half)
+                scores(blk, std::true_type());
+            else
+                scores(blk, std::false_type());
         }
         __syncwarp();
         return true;
     };
+    // The items of a kind (half ones come last; a loop for each keeps its instructions together): false
+    // where the CTA has no more.
+    auto items = [&](auto halved) {
+        constexpr bool kHalf = decltype(halved)::value;
+        constexpr int kSteps = (kHalf ? kPart : kTile) / 16;
+        for (;;) {
+            const int vs = jt % C::NV, at = jt, left = total - t * kTile;
+            const bool first = t == 0, last = t + 1 == ntiles;
+            bool more = true;
+            if (first) find_next();
+            if (last) {
+                t = 0;
+                ++nitem;
+                take_next();
+                more = ntiles > 0;
+            } else {
+                ++t;
+            }
+            ++jt;
+            const uint64_t v = ptx::sdesc(base + C::V + vs * C::OPERAND, C::HALF, 1024);
+#pragma unroll(kHalf ? 2 : 1)
+            for (int blk = 0; blk < 2; ++blk) {
+                if (blk == 0 && !wait_warp(&bar.ready[vs], (at / C::NV) & 1, gave_up)) return false;
+                if (!wait_warp(&bar.p_full[blk], at & 1, gave_up)) return false;
+                if (ptx::elect_one()) {
+                    ptx::tc_fence_after();
+                    const int behind = kHalf ? blk * kPart : 0, steps = (left - behind + 15) / 16;
+#pragma unroll
+                    for (int i = 0; i < kSteps; ++i)
+                        if (i < steps)
+                            ptx::mma_bf16_ts(tmem + kO + 128 * blk, tmem + kS + 128 * blk + 8 * i,
+                                             v + uint64_t((behind / 16 + i) * 128), kIdO, !first || i > 0);
+                    if (last)
+                        ptx::mma_commit(&bar.o_full[blk]);
+                    else
+                        scores(blk, halved);
+                }
+                __syncwarp();
+                if (last && more && !first_scores(blk)) return false;
+            }
+            if (!more) return false;
+            if (half != kHalf) return true;
+        }
+    };
     find_next();
     take_next();
     if (ntiles == 0 || !first_scores(0) || !first_scores(1)) return;
-    for (;;) {
-        const int vs = jt % C::NV, at = jt, left = total - t * kTile;
-        const bool first = t == 0, last = t + 1 == ntiles, halved = half;
-        bool more = true;
-        if (first) find_next();
-        if (last) {
-            t = 0;
-            ++nitem;
-            take_next();
-            more = ntiles > 0;
-        } else {
-            ++t;
-        }
-        ++jt;
-        const uint64_t v = ptx::sdesc(base + C::V + vs * C::OPERAND, C::HALF, 1024);
-#pragma unroll
-        for (int blk = 0; blk < 2; ++blk) {
-            if (blk == 0 && !wait_warp(&bar.ready[vs], (at / C::NV) & 1, gave_up)) return;
-            if (!wait_warp(&bar.p_full[blk], at & 1, gave_up)) return;
-            if (ptx::elect_one()) {
-                ptx::tc_fence_after();
-                auto add_up = [&](int n, int chunk, auto most) {
-                    const int steps = (n + 15) / 16;
-#pragma unroll
-                    for (int i = 0; i < decltype(most)::value; ++i)
-                        if (i < steps)
-                            ptx::mma_bf16_ts(tmem + kO + 128 * blk, tmem + kS + 128 * blk + 8 * i,
-                                             v + uint64_t((chunk + i) * 128), kIdO, !first || i > 0);
-                };
-                if (!halved)
-                    add_up(left, 0, std::integral_constant<int, kTile / 16>());
-                else
-                    add_up(left - blk * kPart, blk * kPart / 16, std::integral_constant<int, kPart / 16>());
-                if (last)
-                    ptx::mma_commit(&bar.o_full[blk]);
-                else
-                    scores(blk);
-            }
-            __syncwarp();
-            if (last && more && !first_scores(blk)) return;
-        }
-        if (!more) return;
-    }
+    if (!half && !items(std::false_type())) return;
+    items(std::true_type());
 }
 
 // ---- the rows' threads ----------------------------------------------------------------------
