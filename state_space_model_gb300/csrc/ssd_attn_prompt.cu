@@ -11,23 +11,24 @@
 //   O += P V        tcgen05, P from tensor memory, O in tensor memory (fp32)
 //
 // What bounds it is the products, 4 D flops a row and position, and the way from one to the next: a
-// block's scores, its exponentials and its outputs follow one another, 2950 cycles a tile, 1024 of them
-// products.  So a warp issues nothing but products, in the order S0, S1, then for every tile O0, S0
-// (next), O1, S1 (next): while a block's exponentials run, the tensor core has the other's products.
-// (All of that warp goes through the loop and one lane issues, so that descriptors stay uniform: a single
-// thread's branch took 100 cycles a product instead of 25, 444 us instead of 418 for 8192 tokens of 32
-// over 8 heads; outputs and the next scores issued together, 407: 1350 TFLOP/s.)  With 256 rows to a
-// tile the reads from L2 are 64 KB for 2 x 4.2 Mflop of them each.  Two warps load (TMA), tiles ahead
-// and across items, and the CTA goes from item to item (sequence, head, 256 rows) with the next one's
-// queries and keys already there.  Where most SMs would have no item in the last round, an item is
-// halved: 128 rows, for which the two blocks take half of every tile each and join their sums at the end
-// (512 tokens over 8192: 64 items 104 us, 128 halves 82).
+// block's scores, its exponentials and its outputs follow one another, 2900 cycles a tile, 1024 of
+// them products.  So a warp issues nothing but products, in the order S0, S1, then for every tile O0,
+// S0 (next), O1, S1 (next): while a block's exponentials run, the tensor core has the other's
+// products. (All of that warp goes through the loop and one lane issues, so that descriptors stay
+// uniform: a single thread's branch took 100 cycles a product instead of 25, 444 us instead of 418 for
+// 8192 tokens of 32 over 8 heads; outputs and the next scores issued together, 407; a loop for each
+// kind of item, its blocks' code once, so that it stays in the instruction cache, 399: 1376 TFLOP/s.)
+// With 256 rows to a tile the reads from L2 are 64 KB for 2 x 4.2 Mflop of them each.  Two warps load
+// (TMA), tiles ahead and across items, and the CTA goes from item to item (sequence, head, 256 rows)
+// with the next one's queries and keys already there.  Where most SMs would have no item in the last
+// round, an item is halved: 128 rows, for which the two blocks take half of every tile each and join
+// their sums at the end (512 tokens over 8192: 64 items 104 us, 128 halves 78).
 //
 // The positions that some row of an item sees, sinks first and then the window's, are counted
 // through as one run in boxes of 16 of a page (so pages are multiples of 16; others take the
 // kernels of ssd_attn.cuh), so that a tile holds little that nobody needs wherever the window
 // begins.  (Copies by three warps, 16 bytes a lane, took any page size and three times as
-// long: 253 us for 4096 tokens under a window of 1024 where the loads take 78.)
+// long: 253 us for 4096 tokens under a window of 1024 where the loads take 76.)
 #include "ptx_sm100.cuh"
 #include "ssd_attn.h"
 #include "ssd_attn_choice.cuh"
@@ -640,7 +641,8 @@ struct RowThread {
                 }
                 loaded = false;
             }
-            if (!(it.half ? tiles<true>(it, x, va, vb, qs, jt, loaded, m, l) : tiles<false>(it, x, va, vb, qs, jt, loaded, m, l)))
+            if (!(it.half ? tiles<true>(it, x, va, vb, qs, jt, loaded, m, l)
+                          : tiles<false>(it, x, va, vb, qs, jt, loaded, m, l)))
                 return false;
             if (loaded) queries_loaded();
             float f0 = 1.f, f1 = 0.f;             // the two sums' factors
@@ -838,18 +840,19 @@ int64_t items_of(const PagedArgs &a, int block) {       // row blocks of a size
 
 }  // namespace
 
-// An item's time goes by its positions alone, 1.57 us for 128 of them (D = 64: 1.39), a half item's 1.28
-// (1.12), with all of its rows there or not; the kernels of ssd_attn.cuh split a sequence's positions
-// over the SMs and take 0.0154 us (0.0106) for 128 positions and a block of 64 rows.  So this kernel takes
-// over at 83 (106) such blocks.  Measured, here / there: 88 blocks
-// (176 tokens of 32 over 8 heads over 8192) 81 / 102 us; 112 blocks, D = 64, 72 / 91; 256 blocks (512 tokens over 8192) 82 /
-// 261 us, D = 64 72 / 184; 8192 tokens 407 / 2167, 354 / 1500.  (A scale below 0 would have to turn the
-// scores' signs, which no model asks for.  Fewer rows than a block of a sequence and head take the others
-// too: 96 sequences, 4 rows, a window of 1024: 93 us here, 47 there.  Pools with a stride of 0 have no
-// tensor map.)  Where a single sequence has so many blocks (what whole items need: 102, D = 64 131) no
-// lengths make this the slower one, and as little where no row can see more than 1536 positions (one
-// of so many among 13 of 33: 27 / 32 us, D = 64 23 / 25);
-// where it takes all of a batch's blocks, the lengths tell (prompt_pays).
+// An item's time goes by its positions alone, 1.55 us for 128 of them (D = 64: 1.36), a half item's 1.23
+// (1.11), with all of its rows there or not; the kernels of ssd_attn.cuh split a sequence's positions
+// over the SMs and take 0.0154 us (0.0106) for 128 positions and a block of 64 rows.  So this kernel is
+// the faster one from 80 (105) such blocks on, and taken from 84 (107).  Measured, here / there: 88 blocks
+// (176 tokens of 32 over 8 heads over 8192) 78 / 102 us; 112 blocks, D = 64, 70 / 91; 256 blocks (512
+// tokens over 8192) 78 / 261 us, D = 64 71 / 184; 8192 tokens 399 / 2167, 345 / 1500.  (A scale below 0
+// would have to turn the scores' signs, which no model asks for.  Fewer rows than a block of a sequence
+// and head take the others too: 96 sequences, 4 rows, a window of 1024: 93 us here, 47 there.  Pools with
+// a stride of 0 have no tensor map.)
+// Where a single sequence has so many blocks (what whole items need: 106, D = 64 137) no lengths make
+// this the slower one, and as little where no row can see more than 1536 positions (one of so many among
+// 13 of 33: 27 / 31 us, D = 64 23 / 25); where it takes all of a batch's blocks, the lengths tell
+// (prompt_pays).
 Prompt prompt_fits(const PagedArgs &a) {
     const int64_t blocks = items_of(a, 64), sms = device_sm_count();
     const bool apart = a.c.st > 0 && (a.c.Hkv == 1 || a.c.sh > 0) && (a.c.pages == 1 || a.c.sp > 0);
