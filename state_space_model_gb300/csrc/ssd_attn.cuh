@@ -91,6 +91,7 @@ struct Shape {
     int B, T, Hkv;
     int cap;              // positions that the page table has room for
     int window;
+    int back;             // how far back a row sees: the window, or further than there are positions
     int sinks;            // positions below this are seen beside the window; 0 without one
     int RB;               // rows of a row block (the rows of a sequence and head: T G)
     int nrb;              // row blocks
@@ -110,8 +111,9 @@ struct Item {
 
 // (What runs once for an item or a CTA is kept small, so that the loop over tiles stays
 // near: when a kernel was 120 KB of code, a fifth of the loop's time was spent waiting
-// for instructions.  Calls out of line are no way, they fix the registers of both
-// kinds of warps.)
+// for instructions.  2% more of it on the way of a short call cost that 2 to 7%: 16 sequences of four
+// tokens under a window 20.2 -> 21.2 us, eight of 32 tokens over fp8 18.5 -> 19.9.  Calls out of line are
+// no way, they fix the registers of both kinds of warps.)
 template <int KS>
 __device__ __forceinline__ void item_range(const Shape &s, Item &it) {
     it.emin = it.len - s.T;
@@ -144,7 +146,7 @@ __device__ __forceinline__ bool in_range(const Shape &s, const Item &it, int pos
 }
 // Whether the row at place `own` sees position pos.
 __device__ __forceinline__ bool sees(const Shape &s, int own, int pos) {
-    return pos <= own && (s.window == 0 || pos > own - s.window || (kSinks && pos < s.sinks));
+    return pos <= own && (pos > own - s.back || (kSinks && pos < s.sinks));
 }
 
 // The cost of one key/value head of a sequence.
@@ -1372,8 +1374,9 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                 // (4-bit codes are finite, their groups' scales may be NaN)
                 constexpr int SPAN = KP * (F4 ? C::GROUPS : ROW) / 16;
 #pragma unroll 1
-                for (int x = lane; x < SPAN; x += 32) {
-                    const uint4 u = lds16((F4 ? vgr : vsm) + x * 16);
+                for (int x = 0; x < (SPAN + 31) / 32; ++x) {
+                    if (SPAN % 32 && x * 32 + lane >= SPAN) continue;
+                    const uint4 u = lds16((F4 ? vgr : vsm) + (x * 32 + lane) * 16);
                     const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
@@ -1405,15 +1408,18 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
                         // place d is row dr of output tile dt, in the lanes of group dg
                         const int dg = F8 ? d / (D / 8) : d % 8;
                         const int half = F8 ? d % 2 : d / 8 % 2, dt = F8 ? d % (D / 8) / 2 : d / 16;
+                        bool see[NQ][2];
+#pragma unroll
+                        for (int b = 0; b < NQ; ++b)
+#pragma unroll
+                            for (int p = 0; p < 2; ++p) see[b][p] = g == dg && sees(s, e[b][p], k0 + x);
 #pragma unroll
                         for (int j = 0; j < MT; ++j)
 #pragma unroll
                             for (int b = 0; b < NQ; ++b)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const bool see = sees(s, e[b][i & 1], k0 + x);
-                                    if (j == dt && g == dg && i >> 1 == half && see) o[j][b][i] += add;
-                                }
+                                for (int i = 0; i < 4; ++i)
+                                    if (j == dt && i >> 1 == half && see[b][i & 1]) o[j][b][i] += add;
                     }
                 }
 #pragma unroll
@@ -1919,6 +1925,7 @@ inline Shape make_shape(const PagedArgs &a) {
     s.Hkv = a.c.Hkv;
     s.cap = a.M * a.c.ps;
     s.window = int(a.window);
+    s.back = a.window > 0 ? s.window : 0x7fff0000;    // (rows' places are -65535 and more: no overflow)
     s.sinks = int(a.sinks);
     s.G = a.Hq / a.c.Hkv;
     const int64_t rows = int64_t(a.T) * s.G;
