@@ -9,16 +9,8 @@ size_t paged_workspace(const PagedArgs &a) {
     return s.ncta * (sizeof(Cut) + 2 * part_floats(s.RB, a.c.D) * sizeof(float));
 }
 
-cudaError_t launch_paged(const PagedArgs &in, cudaStream_t s) {
-    PagedArgs a = in;
-    cudaError_t e = device_error_word(&a.err);
-    if (e != cudaSuccess) return e;
-    const Prompt many = prompt_fits(a);
-    if (many == Prompt::kAsk) a.ask = device_sm_count();
-    if (many != Prompt::kNo) {
-        e = launch_paged_prompt(a, s);
-        if (e != cudaSuccess || many == Prompt::kYes) return e;
-    }
+namespace {
+cudaError_t launch_others(const PagedArgs &a, cudaStream_t s) {
     const bool sinks = a.sinks > 0;
     switch (a.c.dt) {
     case DT_F8E4M3: return sinks ? launch_paged_sinks_f8(a, s) : launch_paged_f8(a, s);
@@ -30,6 +22,17 @@ cudaError_t launch_paged(const PagedArgs &in, cudaStream_t s) {
         if (sinks) return launch_paged_sinks(a, s);
         return a.c.D == 64 ? launch_rows<64, kBf16>(a, s) : launch_rows<128, kBf16>(a, s);
     }
+}
+}  // namespace
+
+cudaError_t launch_paged(const PagedArgs &in, cudaStream_t s) {
+    PagedArgs a = in;
+    cudaError_t e = device_error_word(&a.err);
+    if (e != cudaSuccess) return e;
+    const Prompt many = prompt_fits(a);
+    if (many == Prompt::kYes) return launch_paged_prompt(a, s);
+    if (many == Prompt::kAsk) ask_lengths(a);    // (k_paged_mma's launch brings the other)
+    return launch_others(a, s);
 }
 
 }  // namespace ssd

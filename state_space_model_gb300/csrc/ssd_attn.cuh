@@ -467,14 +467,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-// Waits until the kernel before this one on the stream has finished (for a
-// launch that may start early) / lets the next one start early.
-__device__ __forceinline__ void wait_for_previous() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void let_next_start() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 // ---- the tensor-core kernel -----------------------------------------------------------
 //
@@ -905,8 +897,10 @@ __device__ __forceinline__ bool copy_runs(const PagedArgs &a, const Shape &s, co
     return true;
 }
 
-// ASK: the lengths tell whether this kernel works (compiled apart: as a
-// choice at run time it cost the calls that are not asked 4 to 7%).
+// ASK: the lengths tell whether this kernel works or k_paged_prompt, which is launched between this and the
+// join (compiled apart: as a choice at run time it cost the calls that are not asked 4 to 7%).  Where this one
+// works (a batch of one of 32768 positions among seven of 100; 12 of 17 to 16384): 95.4 and 67.9 us, with the
+// other launched first 96.4 and 68.8, behind the join 96.5 and 68.8, not launched at all 92.9 and 65.6.
 template <int D, int FMT, int NQ, int WR, bool ASK>
 __global__ void __launch_bounds__(kThreads, (Cfg<D, FMT, NQ, WR>::CTAS))
 k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s) {
@@ -931,7 +925,7 @@ k_paged_mma(const __grid_constant__ PagedArgs a, const __grid_constant__ Shape s
         ptx::mbar_init(&empty[threadIdx.x], kWarps);
     }
     __syncthreads();
-    if (ASK && prompt_pays(a, a.ask)) {
+    if (ASK && prompt_pays(a)) {
         if (threadIdx.x == 0 && cut_ok(a, s, blockIdx.x)) reinterpret_cast<Cut *>(a.ws)[blockIdx.x].parts = 0;
         return;
     }
@@ -1900,6 +1894,9 @@ cudaError_t launch_mma(const PagedArgs &a, const Shape &s, cudaStream_t stream) 
     if (e != cudaSuccess) return e;
     k_paged_mma<D, FMT, NQ, WR, ASK><<<s.ncta, kThreads, C::SMEM, stream>>>(a, s);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if constexpr (ASK) {
+        if ((e = launch_paged_prompt(a, stream)) != cudaSuccess) return e;
+    }
     return launch_join<__nv_bfloat16, D, C::F8>(a, s, stream);
 }
 
@@ -1950,7 +1947,7 @@ template <int D, int FMT>
 cudaError_t launch_rows(const PagedArgs &a, cudaStream_t stream) {
     const Shape s = make_shape(a);
     if constexpr (FMT == kBf16)       // (blocks of 64 rows)
-        if (a.ask) return launch_mma<D, FMT, 2, 4, true>(a, s, stream);
+        if (a.ask.on) return launch_mma<D, FMT, 2, 4, true>(a, s, stream);
     switch (s.RB) {
     case 8: return launch_mma<D, FMT, 1, 1>(a, s, stream);
     case 16: return launch_mma<D, FMT, 2, 1>(a, s, stream);

@@ -83,7 +83,13 @@ struct PagedArgs {
     char *ws = nullptr;
     int64_t q_n = 0, o_n = 0, t_n = 0, ws_n = 0;      // extents (ws_n: bytes), debug build
     unsigned int *err = nullptr;
-    int ask = 0;          // the SMs, where two kernels are launched and the lengths tell which works
+    // Where two kernels are launched and the lengths tell which works: costs for each 128 positions
+    // (units of 0.1 ns times the SMs) of the longest sequence, of all where items are dealt out in turn, and of
+    // all for the other kernel; no row sees more positions than `most`.
+    struct Ask {
+        int on = 0, most = 0;
+        uint64_t one = 0, share = 0, line = 0;
+    } ask;
 };
 // Workspace for this problem (c.dt, c.Hkv, c.D, B, T, Hq set).
 size_t paged_workspace(const PagedArgs &a);
@@ -91,6 +97,7 @@ cudaError_t launch_paged(const PagedArgs &a, cudaStream_t s);
 // its parts: many rows, pools of codes, calls with sinks
 enum class Prompt { kNo, kYes, kAsk };   // kAsk: by the lengths, which the kernels look at
 Prompt prompt_fits(const PagedArgs &a);
+void ask_lengths(PagedArgs &a);          // kAsk: sets a.ask
 cudaError_t launch_paged_prompt(const PagedArgs &a, cudaStream_t s);
 cudaError_t launch_paged_f8(const PagedArgs &a, cudaStream_t s);
 cudaError_t launch_paged_f4(const PagedArgs &a, cudaStream_t s);

@@ -738,7 +738,8 @@ struct RowThread {
     }
 };
 
-// kAsk: the lengths tell whether this kernel works.
+// kAsk: the lengths tell whether this kernel works or k_paged_mma, which is launched before it.  It may start
+// while that one's CTAs leave: it reads nothing that they write, and is not done before they are.
 template <int D, bool kAsk>
 __global__ void __launch_bounds__(kThreads, 1)
 k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -751,7 +752,10 @@ k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     __shared__ uint32_t tmem_at;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const uint32_t base = (ptx::smem_u32(smem_raw) + 1023) & ~1023u;
-    if (kAsk && !prompt_pays(a, a.ask)) return;
+    if constexpr (kAsk) {
+        let_next_start();
+        if (!prompt_pays(a)) return wait_for_previous();
+    }
     if (threadIdx.x == 0) {
         gave_up = 0;
         notes.foul[0] = notes.foul[1] = notes.foul[2] = notes.foul[3] = 0;
@@ -806,6 +810,7 @@ k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     __syncthreads();
     if (threadIdx.x == 0 && gave_up) atomicOr(a.err, kErrTimeout);
     if (warp == 8) ptx::tmem_dealloc(tmem, 512);
+    if constexpr (kAsk) wait_for_previous();
 }
 
 template <int D, bool kAsk>
@@ -829,8 +834,17 @@ cudaError_t launch_d(const PagedArgs &a, const Shape &s, cudaStream_t stream) {
         if ((e = make_tmap_bf16(&map[i], i ? a.c.v : a.c.k, 4, dims, strides, box)) != cudaSuccess) return e;
     }
     const int grid = s.items < device_sm_count() ? s.items : device_sm_count();
-    k_paged_prompt<D, kAsk><<<grid, kThreads, Cfg<D>::SMEM, stream>>>(map[0], map[1], a, s);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<D>::SMEM;
+    cfg.stream = stream;
+    cfg.attrs = &at;
+    cfg.numAttrs = kAsk ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k_paged_prompt<D, kAsk>, map[0], map[1], a, s);
 }
 
 int64_t items_of(const PagedArgs &a, int block) {       // row blocks of a size
@@ -866,6 +880,21 @@ Prompt prompt_fits(const PagedArgs &a) {
     return any ? Prompt::kYes : Prompt::kAsk;
 }
 
+// The costs that prompt_fits' comment gives; of less than half a round of items all are halved.
+void ask_lengths(PagedArgs &a) {
+    const bool wide = a.c.D == 128;
+    const int G = a.Hq / a.c.Hkv;
+    const uint64_t sms = device_sm_count(), items = items_of(a, kItemRows), per = items / a.B;
+    int64_t most = int64_t(a.M) * a.c.ps;
+    if (a.window > 0) most = std::min(most, a.window + a.sinks + kItemRows / G);
+    const uint64_t whole = wide ? 15500 : 13600, part = wide ? 12300 : 11100;
+    a.ask.on = 1;
+    a.ask.most = int(most);
+    a.ask.one = (2 * items <= sms ? part : whole) * sms;
+    a.ask.share = items <= sms ? 0 : per * whole;
+    a.ask.line = items_of(a, 64) / a.B * (wide ? 154 : 106) * sms;
+}
+
 cudaError_t launch_paged_prompt(const PagedArgs &a, cudaStream_t stream) {
     Shape s{};
     s.lens = a.lens;
@@ -886,7 +915,7 @@ cudaError_t launch_paged_prompt(const PagedArgs &a, cudaStream_t stream) {
     const int n = int(items_of(a, kItemRows)), sms = device_sm_count(), over = n % sms;
     s.whole = 2 * over <= sms ? n - over : n;
     s.items = 2 * n - s.whole;
-    if (a.ask) return a.c.D == 64 ? launch_d<64, true>(a, s, stream) : launch_d<128, true>(a, s, stream);
+    if (a.ask.on) return a.c.D == 64 ? launch_d<64, true>(a, s, stream) : launch_d<128, true>(a, s, stream);
     return a.c.D == 64 ? launch_d<64, false>(a, s, stream) : launch_d<128, false>(a, s, stream);
 }
 
