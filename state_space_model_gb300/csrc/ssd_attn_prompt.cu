@@ -105,7 +105,8 @@ struct Item {
 
 // Item number x: the last rows come first, which see most where there is no window.  From s.whole
 // on two numbers share an item, a block of rows each, of which the CTA's two blocks of threads see
-// half of every tile each and join their sums at the end.
+// half of every tile each and join their sums at the end.  A CTA has one of those at most, its last
+// item: they begin with a round of the SMs and are no more than these (launch_paged_prompt).
 __device__ __forceinline__ Item item_of(const Shape &s, int x) {
     Item it;
     it.half = x >= s.whole;
@@ -201,7 +202,7 @@ struct Barriers {
     uint64_t k_land[3], v_land[3];
     uint64_t ready[3];                // a tile's values, looked through, and the next tile's keys
     uint64_t q_full[2], s_full[2][3], p_full[2], o_full[2];
-    uint64_t parted, joined;          // a half item's second sums are written, and read
+    uint64_t parted;                  // a half item's second sums are written
     uint64_t done;
 };
 // What is known of the last four tiles (a tile's loads begin when the products of scores of the
@@ -385,8 +386,7 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
         __syncwarp();
         return true;
     };
-    // The items of a kind (half ones come last; a loop for each keeps its instructions together): false
-    // where the CTA has no more.
+    // The items of a kind (a loop for each keeps its instructions together): false where the CTA has no more.
     auto items = [&](auto halved) {
         constexpr bool kHalf = decltype(halved)::value;
         constexpr int kSteps = (kHalf ? kPart : kTile) / 16;
@@ -394,12 +394,12 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
             const int vs = jt % C::NV, at = jt, left = total - t * kTile;
             const bool first = t == 0, last = t + 1 == ntiles;
             bool more = true;
-            if (first) find_next();
+            if (!kHalf && first) find_next();
             if (last) {
                 t = 0;
                 ++nitem;
-                take_next();
-                more = ntiles > 0;
+                if (!kHalf) take_next();
+                more = !kHalf && ntiles > 0;
             } else {
                 ++t;
             }
@@ -423,7 +423,7 @@ __device__ __forceinline__ void issue(const Shape &s, Barriers &bar, volatile in
                         scores(blk, halved);
                 }
                 __syncwarp();
-                if (last && more && !first_scores(blk)) return false;
+                if (!kHalf && last && more && !first_scores(blk)) return false;
             }
             if (!more) return false;
             if (half != kHalf) return true;
@@ -591,22 +591,22 @@ struct RowThread {
         float minus = 0.f;            // -qs m where that is small
         bool large = false;
         // the next item's queries, loaded when the last scores of this one are made
-        int64_t next = -1;            // where the lane's row of them is
-        bool follow = false;
+        [[maybe_unused]] int64_t next = -1;     // where the lane's row of them is
+        [[maybe_unused]] bool follow = false;
 #pragma unroll 1
         for (int t = 0; t < it.ntiles; ++t, ++jt) {
             if (!wait_warp(&bar.s_full[blk][jt % C::NK], (jt / C::NK) & 1, gave_up)) return false;
             ptx::tc_fence_after();
-            if (t == it.ntiles / 2 && x + gridDim.x < s.items) {
-                const Item after = item_of(s, x + gridDim.x);
-                follow = after.ntiles > 0;
-                if (follow && (blk == 0 || !after.half)) next = query_of(after);
-            }
-            if (t + 1 == it.ntiles && follow) {
-                // (a half item's other scores are made of the same queries)
-                if (kHalf && blk == 0 && !wait_warp(&bar.s_full[1][jt % C::NK], (jt / C::NK) & 1, gave_up)) return false;
-                if (next >= 0) load_queries(next);
-                loaded = true;
+            if constexpr (!kHalf) {
+                if (t == it.ntiles / 2 && x + gridDim.x < s.items) {
+                    const Item after = item_of(s, x + gridDim.x);
+                    follow = after.ntiles > 0;
+                    if (follow && (blk == 0 || !after.half)) next = query_of(after);
+                }
+                if (t + 1 == it.ntiles && follow) {
+                    if (next >= 0) load_queries(next);
+                    loaded = true;
+                }
             }
             const int v0 = t * kTile + (kHalf ? blk * W : 0);
             constexpr uint32_t kAll = (1u << W / kBox) - 1;
@@ -621,7 +621,7 @@ struct RowThread {
 
     __device__ __forceinline__ bool run() {
         const float qs = a.scale * kLog2e;
-        int jt = 0, nitem = 0, nhalf = 0;
+        int jt = 0, nitem = 0;
         bool loaded = false;          // this item's queries
 #pragma unroll 1
         for (int x = blockIdx.x; x < s.items; x += gridDim.x) {
@@ -653,10 +653,9 @@ struct RowThread {
                     if (blk == 1) {
                         notes.sums[warp * 32 + lane] = make_float2(m, l);
                         ptx::mbar_arrive(&bar.parted);
-                        if (!wait_warp(&bar.joined, nhalf & 1, gave_up)) return false;
                     } else {
                         if (!wait_warp(&bar.o_full[1], nitem & 1, gave_up) ||
-                            !wait_warp(&bar.parted, nhalf & 1, gave_up))
+                            !wait_warp(&bar.parted, 0, gave_up))
                             return false;
                         const float2 other = notes.sums[warp * 32 + lane];
                         const float to_m = fmaxf(m, other.x);
@@ -666,7 +665,6 @@ struct RowThread {
                         l = l * f0 + other.y * f1;
                         m = to_m;
                     }
-                    ++nhalf;
                 }
                 ptx::tc_fence_after();
             }
@@ -687,8 +685,6 @@ struct RowThread {
                     ptx::tmem_st16(to + c, o);
                 }
                 ptx::tmem_st_wait();
-                ptx::tc_fence_before();
-                ptx::mbar_arrive(&bar.joined);
             }
             if (foul) add_foul(it, own);
             // Rows of 64 places go through shared memory, so that stores are whole lines (a row a
@@ -771,7 +767,6 @@ k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             for (int k = 0; k < 3; ++k) ptx::mbar_init(&bar.s_full[i][k], 1);
         }
         ptx::mbar_init(&bar.parted, kRows);
-        ptx::mbar_init(&bar.joined, kRows);
         ptx::mbar_init(&bar.done, 1);
         ptx::fence_mbar_init();
     }
