@@ -61,6 +61,9 @@ constexpr int kRowRegs = 208, kOtherRegs = 88;
 // The maximum in use follows the true one when that is ahead by so much (log2 units): moving it
 // means to go over the outputs in tensor memory.
 constexpr float kSlack = 8.f;
+// A row's reference is a whole number (RowThread::tile) below this (log2 units): rounded to fp32, the product
+// that it is next to is off by 2^-5 at most.
+constexpr float kFar = 1048576.f;
 
 template <int D>
 struct Cfg {
@@ -211,7 +214,7 @@ struct Notes {
     uint32_t there[4];                // bit i: box i's page exists
     int foul[4];                      // of the last four items: the item's number + 1 if a value that was
                                       // looked at is infinite or NaN
-    float2 sums[kRows];               // a half item's second maxima and sums
+    float3 sums[kRows];               // a half item's second maxima, references (RowThread::tile) and sums
 };
 
 // The rows of an item: from where on some do not see all that is there (v >= least), and below
@@ -500,10 +503,13 @@ struct RowThread {
     }
 
     // Tile t of an item for this thread's row, which sees [va, vb) of its run, and below vb what lies
-    // below `sinks` too: scores to weights, with the row's reference m and sum l.  large: the
-    // warp's scores are.  kWhole: all rows of
-    // the warp see all positions.  W: 128, or 64 of a half item, from v0 on.
-    template <bool kWhole, int W>
+    // below `sinks` too: scores to weights 2^(qs s - r), with the row's sum l.  r = -minus follows qs m, m
+    // the largest score when it was set, as the nearest whole number: qs s - r is one operation, rounded
+    // once, all weights of a row stand to one another as their scores do, and a change of r is a power of
+    // two.  large: for scores from 2^20 on the nearest number may be far off, and the warp's weights are
+    // 2^(qs (s - m)).  (r = qs m rounded took as long, and moved by up to 2^-14 from tile to tile.)
+    // kAll: all rows of the warp see all positions.  W: 128, or 64 of a half item, from v0 on.
+    template <bool kAll, int W>
     __device__ __forceinline__ void tile(int t, int v0, int va, int vb, uint32_t there, float qs, float &m,
                                          float &l, float &minus, bool &large) {
         uint32_t raw[W / 32][32];
@@ -512,7 +518,7 @@ struct RowThread {
         for (int c = 0; c < W / 32; ++c) ptx::tmem_ld32(ts + 32 * c, raw[c]);
         float mx = -INFINITY;
         auto look = [&](int c) {
-            if constexpr (!kWhole) {
+            if constexpr (!kAll) {
                 const int b = v0 + 32 * c;
                 auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
                 uint32_t vis = (there >> (2 * c) & 1 ? 0xffffu : 0u) | (there >> (2 * c + 1) & 1 ? 0xffff0000u : 0u);
@@ -532,9 +538,17 @@ struct RowThread {
 #pragma unroll
         for (int c = 0; c < W / 32; ++c) look(c);
         if (__any_sync(~0u, (mx - m) * qs > kSlack || (m == -INFINITY && mx != m)) || large) {
-            const float to_m = fmaxf(m, mx);
-            const float f = m == -INFINITY ? 1.f : ex2((m - to_m) * qs);
+            const float to_m = fmaxf(m, mx), whole = rintf(to_m * qs);
+            const bool none = to_m == -INFINITY, far = __any_sync(~0u, !none && !(fabsf(whole) < kFar));
+            const float next = none || far ? 0.f : -whole;
+            const float f = m == -INFINITY ? 1.f
+                                           : ex2(large && far ? (m - to_m) * qs
+                                                 : large      ? fmaf(m, qs, next)
+                                                 : far        ? fmaf(-to_m, qs, -minus)
+                                                              : next - minus);
             m = to_m;
+            minus = next;
+            large = far;
             l *= f;
             if (t > 0) {              // (the outputs so far are complete: the scores came after them)
 #pragma unroll 1
@@ -548,13 +562,8 @@ struct RowThread {
                 }
                 ptx::tmem_st_wait();
             }
-            // 2^(qs s - qs m) is one operation below: qs m rounded is off by 2^-15 at most below 1024, the
-            // same for all of a row's weights.  For larger scores the difference first.
-            const float ref = m == -INFINITY ? 0.f : m;
-            minus = -(ref * qs);
-            large = __any_sync(~0u, !(fabsf(minus) < 1024.f));
             if (large) {
-                minus = 0.f;
+                const float ref = none ? 0.f : m;
 #pragma unroll
                 for (int i = 0; i < W; ++i)
                     raw[i / 32][i % 32] = __float_as_uint(__uint_as_float(raw[i / 32][i % 32]) - ref);
@@ -586,10 +595,8 @@ struct RowThread {
     // An item's tiles.  loaded: the next one's queries are on their way.
     template <bool kHalf>
     __device__ __forceinline__ bool tiles(const Item &it, int x, int va, int vb, float qs, int &jt, bool &loaded,
-                                          float &m, float &l) {
+                                          float &m, float &l, float &minus, bool &large) {
         constexpr int W = kHalf ? kPart : kTile;
-        float minus = 0.f;            // -qs m where that is small
-        bool large = false;
         // the next item's queries, loaded when the last scores of this one are made
         [[maybe_unused]] int64_t next = -1;     // where the lane's row of them is
         [[maybe_unused]] bool follow = false;
@@ -633,7 +640,8 @@ struct RowThread {
             // ns < sinks it is lo, and the run has no gap)
             const int vb = own < it.lo ? min(own + 1, it.ns) : it.ns + own - it.lo + 1;
             const int va = s.window > 0 ? it.ns + max(own - s.window + 1 - it.lo, 0) : 0;
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f, minus = 0.f;
+            bool large = false;
             if (it.ntiles) {
                 if (!loaded) {
                     if (mine) load_queries(query_of(it));
@@ -641,8 +649,8 @@ struct RowThread {
                 }
                 loaded = false;
             }
-            if (!(it.half ? tiles<true>(it, x, va, vb, qs, jt, loaded, m, l)
-                          : tiles<false>(it, x, va, vb, qs, jt, loaded, m, l)))
+            if (!(it.half ? tiles<true>(it, x, va, vb, qs, jt, loaded, m, l, minus, large)
+                          : tiles<false>(it, x, va, vb, qs, jt, loaded, m, l, minus, large)))
                 return false;
             if (loaded) queries_loaded();
             float f0 = 1.f, f1 = 0.f;             // the two sums' factors
@@ -651,18 +659,28 @@ struct RowThread {
                 if (!wait_warp(&bar.o_full[blk], nitem & 1, gave_up)) return false;
                 if (it.half) {
                     if (blk == 1) {
-                        notes.sums[warp * 32 + lane] = make_float2(m, l);
+                        notes.sums[warp * 32 + lane] = make_float3(m, large ? NAN : minus, l);
                         ptx::mbar_arrive(&bar.parted);
                     } else {
                         if (!wait_warp(&bar.o_full[1], nitem & 1, gave_up) ||
                             !wait_warp(&bar.parted, 0, gave_up))
                             return false;
-                        const float2 other = notes.sums[warp * 32 + lane];
+                        const float3 other = notes.sums[warp * 32 + lane];
                         const float to_m = fmaxf(m, other.x);
-                        f0 = m == -INFINITY ? 0.f : ex2((m - to_m) * qs);
+                        const bool one = m != -INFINITY;
                         two = other.x != -INFINITY;
-                        f1 = two ? ex2((other.x - to_m) * qs) : 0.f;
-                        l = l * f0 + other.y * f1;
+                        const bool far = isnan(other.y);
+                        if (large || far) {   // the weights' own references in terms of the maxima
+                            f0 = one ? ex2((m - to_m) * qs - (large ? 0.f : fmaf(m, qs, minus))) : 0.f;
+                            f1 = two ? ex2((other.x - to_m) * qs - (far ? 0.f : fmaf(other.x, qs, other.y))) : 0.f;
+                            large = true;
+                        } else {
+                            const float both = fminf(one ? minus : INFINITY, two ? other.y : INFINITY);
+                            f0 = one ? ex2(both - minus) : 0.f;
+                            f1 = two ? ex2(both - other.y) : 0.f;
+                            minus = both;
+                        }
+                        l = l * f0 + other.z * f1;
                         m = to_m;
                     }
                 }
@@ -728,7 +746,7 @@ struct RowThread {
             }
             const int64_t at = (int64_t(it.b) * s.T + tk) * a.Hq + h;
             if (a.lse && r < s.rows && SSD_IDX_OK(a.err, at, int64_t(s.B) * s.T * a.Hq))
-                a.lse[at] = l == 0.f ? -INFINITY : (m * qs + log2f(l)) * kLn2;
+                a.lse[at] = l == 0.f ? -INFINITY : ((large ? m * qs : -minus) + log2f(l)) * kLn2;
         }
         return true;
     }

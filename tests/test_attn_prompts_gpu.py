@@ -36,3 +36,70 @@ def test_calls_whose_lengths_tell_follow_one_another(attn, D):
     torch.cuda.synchronize()
     for i, x in enumerate(got):
         assert torch.equal(x, want[i % len(sets)]), i
+
+
+@pytest.mark.parametrize("T,n", [(1300, 1400), (300, 1400)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_log_sums_are_rounded_where_they_must_be(attn, D, T, n):
+    """Large scores that rise from tile to tile, a little in most rows and by more than a reference may lag
+    in one of four, so that all rows' references move with each tile.  Scores q0 600 + q1 k1 are exact in
+    f32, and so is scale log2(e) up to f32's log2(e), so what a log sum errs by is
+
+    * 2^-17 of its log2, and the rest: a weight's exponent is below 16 in size where it counts (2^-21), its
+      exponential 2^-22, sums of 50 in turn 50 2^-24, log2 2^-22,
+    * half a step of f32 of the log2 (reference plus log2 of the sum), and of the result."""
+    Hq, Hkv, G, scale = 32, 8, 4, 0.5
+    q, pools, table, lens = problem(1, T, Hq, Hkv, D, 16, [n], BF, 63)
+    q.zero_()
+    row = torch.arange(T, device="cuda")[:, None] * G + torch.arange(G, device="cuda")
+    q0 = 1.25 + (row * 37 % 96) / 128
+    q1 = torch.where(row % G == 0, 128.0, 1.0)
+    j = torch.arange(n, device="cuda")
+    k1 = (j // 128 * 8 + j * 5 % 8) / 64
+    q[0, :, :, 0], q[0, :, :, 1] = q0.repeat(1, Hkv).to(BF), q1.repeat(1, Hkv).to(BF)
+    keys = torch.zeros(n, D, device="cuda")
+    keys[:, 0], keys[:, 1] = 600, k1
+    pools.pools[0][table[0].long()[j // 16], :, j % 16] = keys[:, None].to(BF)
+    assert torch.equal(keys.to(BF).float(), keys) and torch.equal(q0.to(BF).double(), q0.double())
+    _, lse = attn.paged_attention(q, *pools.pools, table, lens, scale=scale, return_lse=True)
+    log2e = float(torch.tensor(1.4426950408889634, dtype=torch.float32))
+    for t0 in range(0, T, 100):
+        t = slice(t0, t0 + 100)
+        s = (600 * q0[t].double()[..., None] + q1[t].double()[..., None] * k1.double()) * (scale * log2e)
+        own = n - T + torch.arange(T, device="cuda")[t]
+        s = s.masked_fill(j > own[:, None, None], float("-inf"))
+        top = s.amax(-1)
+        log2 = top + torch.log2(torch.exp2(s - top[..., None]).sum(-1))
+        ref = log2 * 0.6931471805599453
+        half = lambda v: torch.exp2(torch.floor(torch.log2(v.abs())) - 24)
+        bound = 0.6931471805599453 * (half(log2) + 2.0 ** -17) + half(ref) + 2.0 ** -19
+        for h in range(Hkv):
+            assert ((lse[0, t, h * G: (h + 1) * G].double() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("T", [1300, 300])
+@pytest.mark.parametrize("D", [64, 128])
+def test_references_of_any_size_follow_one_another(attn, D, T):
+    """Scores from -2^24 over -2^12 and 2^12 to 2^21, a size for 64 positions: a row's weight is that of the last
+    size that it sees, shared by its positions.  Nothing but roundings to 16 bits (weight, result) and, in the
+    log sums, of the factor of the scores."""
+    Hq, Hkv, n = 32, 8, 1400
+    q, pools, table, lens = problem(1, T, Hq, Hkv, D, 16, [n], BF, 64)
+    j = torch.arange(n, device="cuda")
+    size = j // 64
+    key = torch.where(size < 13, -torch.exp2((12 - size).double()), torch.exp2((size - 13).double()))
+    keys = torch.zeros(n, D, device="cuda", dtype=BF)
+    keys[:, 5] = key.to(BF)
+    pools.pools[0][table[0].long()[j // 16], :, j % 16] = keys[:, None]
+    q.zero_()
+    q[..., 5] = 2.0 ** 12
+    out, lse = attn.paged_attention(q, *pools.pools, table, lens, scale=1.0, return_lse=True)
+    own = n - T + torch.arange(T, device="cuda")
+    score = torch.where(j <= own[:, None], key * 2.0 ** 12, -torch.inf)
+    top = score.amax(1, keepdim=True)
+    weight = (score == top).double()
+    count = weight.sum(1, keepdim=True)
+    v = pools.rows(1, table[0].long()[j // 16], j % 16)
+    want, most = (torch.einsum("tj,jhd->thd", weight / count, x).repeat_interleave(Hq // Hkv, 1) for x in (v, v.abs()))
+    assert ((out[0].double() - want).abs() <= 2.0 ** -7 * most + 1e-30).all()
+    assert ((lse[0].double() - top - torch.log(count)).abs() <= 2.0 ** -20 * (1 + top.abs())).all()
