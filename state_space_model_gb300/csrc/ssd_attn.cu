@@ -29,7 +29,10 @@ cudaError_t launch_paged(const PagedArgs &in, cudaStream_t s) {
     PagedArgs a = in;
     cudaError_t e = device_error_word(&a.err);
     if (e != cudaSuccess) return e;
-    const Prompt many = prompt_fits(a);
+    Prompt many = prompt_fits(a);
+    PromptMaps maps;
+    if (many != Prompt::kNo && !make_prompt_maps(a, &maps)) many = Prompt::kNo;
+    a.maps = &maps;
     if (many == Prompt::kYes) return launch_paged_prompt(a, s);
     if (many == Prompt::kAsk) ask_lengths(a);    // (k_paged_mma's launch brings the other)
     return launch_others(a, s);

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "ssd_common.h"
+#include "ssd_tmap.h"
 
 #include <stddef.h>
 
@@ -69,6 +70,12 @@ struct KvReadArgs {
 cudaError_t launch_kv_read(const KvReadArgs &a, cudaStream_t s);
 cudaError_t launch_kv_read_ex(const KvReadArgs &a, cudaStream_t s);       // its 4-bit pools
 
+// The pools' tensor maps for k_paged_prompt: 64 places, then tokens, heads and pages, by their strides.
+struct PromptMaps {
+    CUtensorMap k, v;
+    int token = 1, head = 2, page = 3;        // the maps' dimensions
+};
+
 struct PagedArgs {
     KvPools c;
     int B = 0, T = 1, Hq = 1, M = 0;
@@ -90,6 +97,7 @@ struct PagedArgs {
         int on = 0, most = 0;
         uint64_t one = 0, share = 0, line = 0;
     } ask;
+    const PromptMaps *maps = nullptr;         // host memory, for the launch
 };
 // Workspace for this problem (c.dt, c.Hkv, c.D, B, T, Hq set).
 size_t paged_workspace(const PagedArgs &a);
@@ -97,6 +105,7 @@ cudaError_t launch_paged(const PagedArgs &a, cudaStream_t s);
 // its parts: many rows, pools of codes, calls with sinks
 enum class Prompt { kNo, kYes, kAsk };   // kAsk: by the lengths, which the kernels look at
 Prompt prompt_fits(const PagedArgs &a);
+bool make_prompt_maps(const PagedArgs &a, PromptMaps *m);     // false: there are none for these pools
 void ask_lengths(PagedArgs &a);          // kAsk: sets a.ask
 cudaError_t launch_paged_prompt(const PagedArgs &a, cudaStream_t s);
 cudaError_t launch_paged_f8(const PagedArgs &a, cudaStream_t s);

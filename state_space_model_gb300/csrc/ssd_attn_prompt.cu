@@ -93,6 +93,7 @@ struct Divisor {
 struct Shape {
     const int32_t *lens;
     int B, T, Hkv, cap, window, sinks, rows, nrb;
+    int token, head, page;            // dimensions of the tensor maps
     int items, whole;                 // items with halves counted; those that are not halves
     Divisor heads, per_b, G, ps;      // by B Hkv, by Hkv, by the query heads of a key/value head, by the page
 };
@@ -255,6 +256,8 @@ __device__ __forceinline__ void load_tiles(const PagedArgs &a, const Shape &s, c
             const bool ok = page >= 0 && page < a.c.pages;
             const uint32_t there = __ballot_sync(~0u, ok);
             if (!ok) page = a.c.pages;        // outside: zeros
+            auto place = [&](int dim) { return dim == s.token ? at : dim == s.head ? it.hk : page; };
+            const int c1 = place(1), c2 = place(2), c3 = place(3);
             // Block 1's scores of tile j are made: the keys of tile j have been read, and (its products are
             // made in order) the values of tile j - 1.
             const int j = jt - N + (values ? 1 : 0);
@@ -268,7 +271,7 @@ __device__ __forceinline__ void load_tiles(const PagedArgs &a, const Shape &s, c
 #pragma unroll
                 for (int h = 0; h < D / 64; ++h)
                     load_box(slots + st * C::OPERAND + h * C::HALF + lane * kBox * 128, map, &landed[st], 64 * h,
-                             at, it.hk, page);
+                             c1, c2, c3);
             }
         }
     }
@@ -837,15 +840,6 @@ cudaError_t launch_d(const PagedArgs &a, const Shape &s, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         if (dev < 256) done[dev / 64].fetch_or(uint64_t(1) << (dev % 64));
     }
-    CUtensorMap map[2];
-    for (int i = 0; i < 2; ++i) {
-        // (a stride of a dimension of one is whatever the caller's tensor has: any will do)
-        auto stride = [](int64_t n, int64_t elements) { return uint64_t(n > 1 ? elements * 2 : 16); };
-        const uint64_t dims[4] = {uint64_t(D), uint64_t(a.c.ps), uint64_t(a.c.Hkv), uint64_t(a.c.pages)};
-        const uint64_t strides[3] = {stride(a.c.ps, a.c.st), stride(a.c.Hkv, a.c.sh), stride(a.c.pages, a.c.sp)};
-        const uint32_t box[4] = {64, kBox, 1, 1};
-        if ((e = make_tmap_bf16(&map[i], i ? a.c.v : a.c.k, 4, dims, strides, box)) != cudaSuccess) return e;
-    }
     const int grid = s.items < device_sm_count() ? s.items : device_sm_count();
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at{};
@@ -857,7 +851,7 @@ cudaError_t launch_d(const PagedArgs &a, const Shape &s, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = &at;
     cfg.numAttrs = kAsk ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_paged_prompt<D, kAsk>, map[0], map[1], a, s);
+    return cudaLaunchKernelEx(&cfg, k_paged_prompt<D, kAsk>, a.maps->k, a.maps->v, a, s);
 }
 
 int64_t items_of(const PagedArgs &a, int block) {       // row blocks of a size
@@ -874,23 +868,49 @@ int64_t items_of(const PagedArgs &a, int block) {       // row blocks of a size
 // (176 tokens of 32 over 8 heads over 8192) 78 / 102 us; 112 blocks, D = 64, 70 / 91; 256 blocks (512
 // tokens over 8192) 78 / 261 us, D = 64 71 / 184; 8192 tokens 399 / 2167, 345 / 1500.  (A scale below 0
 // would have to turn the scores' signs, which no model asks for.  Fewer rows than a block of a sequence
-// and head take the others too: 96 sequences, 4 rows, a window of 1024: 93 us here, 47 there.  Pools with
-// a stride of 0 have no tensor map.)
+// and head take the others too: 96 sequences, 4 rows, a window of 1024: 93 us here, 47 there.)
 // Where a single sequence has so many blocks (what whole items need: 106, D = 64 137) no lengths make
 // this the slower one, and as little where no row can see more than 1536 positions (one of so many among
 // 13 of 33: 27 / 31 us, D = 64 23 / 25); where it takes all of a batch's blocks, the lengths tell
 // (prompt_pays).
 Prompt prompt_fits(const PagedArgs &a) {
     const int64_t blocks = items_of(a, 64), sms = device_sm_count();
-    const bool apart = a.c.st > 0 && (a.c.Hkv == 1 || a.c.sh > 0) && (a.c.pages == 1 || a.c.sp > 0);
     const bool wide = a.c.D == 128;
-    if (!apart || a.c.dt != DT_BF16 || a.T * (a.Hq / a.c.Hkv) < kRows || !(a.scale > 0.f) || a.c.ps % kBox ||
+    if (a.c.dt != DT_BF16 || a.T * (a.Hq / a.c.Hkv) < kRows || !(a.scale > 0.f) || a.c.ps % kBox ||
         a.c.pages <= 0 || 20 * blocks < (wide ? 11 : 14) * sms || items_of(a, kItemRows) >= (1 << 30))
         return Prompt::kNo;
     int64_t most = int64_t(a.M) * a.c.ps;
     if (a.window > 0) most = std::min(most, a.window + a.sinks + kItemRows / (a.Hq / a.c.Hkv));
     const bool any = a.B == 1 || most <= 1536 || 20 * blocks >= int64_t(a.B) * (wide ? 14 : 18) * sms;
     return any ? Prompt::kYes : Prompt::kAsk;
+}
+
+// A map's strides grow, each a multiple of the one before and below 2^40 bytes: so the tokens, heads and pages
+// of the pools are its dimensions in the order of their strides, and pools with others (a stride of 0 that heads
+// share, heads apart by some places more than their tokens take) have none.  A dimension of one comes last, with
+// any stride.
+bool make_prompt_maps(const PagedArgs &a, PromptMaps *m) {
+    struct Dim {
+        uint64_t n, stride;
+        int *at;
+    } d[3] = {{uint64_t(a.c.ps), uint64_t(a.c.st) * 2, &m->token},
+              {uint64_t(a.c.Hkv), uint64_t(a.c.sh) * 2, &m->head},
+              {uint64_t(a.c.pages), uint64_t(a.c.sp) * 2, &m->page}};
+    std::stable_sort(d, d + 3, [](const Dim &x, const Dim &y) {
+        return x.n > 1 && (y.n <= 1 || x.stride < y.stride);
+    });
+    uint64_t dims[4] = {uint64_t(a.c.D)}, strides[3], below = uint64_t(a.c.D) * 2;
+    uint32_t box[4] = {64, 1, 1, 1};
+    for (int i = 0; i < 3; ++i) {
+        *d[i].at = i + 1;
+        dims[i + 1] = d[i].n;
+        strides[i] = d[i].n > 1 ? d[i].stride : below;
+        if (strides[i] < below || strides[i] >= uint64_t(1) << 40 || (i && strides[i] % below)) return false;
+        below = strides[i];
+    }
+    box[m->token] = kBox;
+    return make_tmap_bf16(&m->k, a.c.k, 4, dims, strides, box) == cudaSuccess &&
+           make_tmap_bf16(&m->v, a.c.v, 4, dims, strides, box) == cudaSuccess;
 }
 
 // The costs that prompt_fits' comment gives; of less than half a round of items all are halved.
@@ -928,6 +948,9 @@ cudaError_t launch_paged_prompt(const PagedArgs &a, cudaStream_t stream) {
     const int n = int(items_of(a, kItemRows)), sms = device_sm_count(), over = n % sms;
     s.whole = 2 * over <= sms ? n - over : n;
     s.items = 2 * n - s.whole;
+    s.token = a.maps->token;
+    s.head = a.maps->head;
+    s.page = a.maps->page;
     if (a.ask.on) return a.c.D == 64 ? launch_d<64, true>(a, s, stream) : launch_d<128, true>(a, s, stream);
     return a.c.D == 64 ? launch_d<64, false>(a, s, stream) : launch_d<128, false>(a, s, stream);
 }

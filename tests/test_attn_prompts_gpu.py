@@ -1,5 +1,8 @@
 """Pieces of prompts and batches of many rows over bf16 pools: what the kernels carry from one item, one
 launch and one call to the next.  References and bounds are test_attn_forms_gpu.py's."""
+import ctypes
+import itertools
+
 import pytest
 import torch
 
@@ -7,6 +10,30 @@ from test_attn_forms_gpu import BF, check, problem
 from test_attn_gpu import attn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+def launches(attn, prob, **kw):
+    """Kernels that a call launches: 1 where k_paged_prompt takes it, 2 where the others do, 3 where the lengths
+    tell.  (Counted in a captured graph, which is not run.)"""
+    q, pools, table, lens = prob
+    B, T, Hq, D = q.shape
+    need = attn.paged_attention_workspace_size(B, T, Hq, pools.Hkv, D, pools.pdt)
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(q)
+    call = lambda: attn.paged_attention(q, *pools.pools, table, lens, out=out, workspace=ws, **pools.kw, **kw)
+    cuda = ctypes.CDLL("libcuda.so.1")
+    s = torch.cuda.Stream()
+    handle, graph, n = ctypes.c_void_p(s.cuda_stream), ctypes.c_void_p(), ctypes.c_size_t()
+    with torch.cuda.stream(s):
+        call()                                       # (what a first call sets up cannot be captured)
+        s.synchronize()
+        assert cuda.cuStreamBeginCapture_v2(handle, 2) == 0
+        try:
+            call()
+        finally:
+            assert cuda.cuStreamEndCapture(handle, ctypes.byref(graph)) == 0
+    assert cuda.cuGraphGetNodes(graph, None, ctypes.byref(n)) == 0 and cuda.cuGraphDestroy(graph) == 0
+    return n.value
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -103,3 +130,47 @@ def test_references_of_any_size_follow_one_another(attn, D, T):
     want, most = (torch.einsum("tj,jhd->thd", weight / count, x).repeat_interleave(Hq // Hkv, 1) for x in (v, v.abs()))
     assert ((out[0].double() - want).abs() <= 2.0 ** -7 * most + 1e-30).all()
     assert ((lse[0].double() - top - torch.log(count)).abs() <= 2.0 ** -20 * (1 + top.abs())).all()
+
+
+# ---- layouts of the pools ------------------------------------------------------------------------
+
+def in_order(x, order):
+    """The pool x [pages, Hkv, ps, D] with its first three dimensions in memory in another order."""
+    back = [order.index(i) for i in range(3)]
+    return x.permute(*order, 3).contiguous().permute(*back, 3)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("order", list(itertools.permutations(range(3))), ids=str)
+def test_pools_in_any_order_of_memory(attn, D, order):
+    for Hkv in (8, 1):
+        q, pools, table, lens = prob = problem(2, 500 if Hkv == 8 else 3000, 4 * Hkv, Hkv, D, 48, [700, 300], BF, 65)
+        kw = dict(window=300, sinks=4)
+        want, _ = check(attn, prob, **kw) if Hkv == 8 else (attn.paged_attention(q, *pools.pools, table, lens, **kw), 0)
+        assert launches(attn, prob, **kw) == 1
+        pools.pools = [in_order(x, order) for x in pools.pools]
+        assert launches(attn, prob, **kw) == 1
+        assert torch.equal(attn.paged_attention(q, *pools.pools, table, lens, **kw), want)
+
+
+def test_pools_without_a_tensor_map(attn):
+    """Heads that lie some places further apart than their tokens take, or on top of one another: served too."""
+    q, pools, table, lens = prob = problem(1, 1300, 32, 8, 128, 16, [1400], BF, 66)
+    pages = pools.pools[0].shape[0]
+    assert launches(attn, prob) == 1
+    wide = []
+    for x in pools.pools:
+        room = torch.zeros(pages, 8, 16 * 128 + 8, dtype=BF, device="cuda")
+        room[..., : 16 * 128] = x.flatten(2)
+        wide.append(room[..., : 16 * 128].unflatten(2, (16, 128)))
+    pools.pools = wide
+    assert not wide[0].is_contiguous() and launches(attn, prob) == 2
+    check(attn, prob)
+    check(attn, prob, 200, 3)
+    # one page or one head whose stride is whatever it is
+    q, pools, table, lens = prob = problem(1, 1300, 32, 8, 128, 1408, [1400], BF, 67)
+    want, _ = check(attn, prob)
+    pools.pools = [x[int(table[0, 0]):][:1].as_strided((1, 8, 1408, 128), (7, 1408 * 128, 128, 1)) for x in pools.pools]
+    table.zero_()
+    assert launches(attn, prob) == 1
+    assert torch.equal(attn.paged_attention(q, *pools.pools, table, lens), want)
