@@ -805,7 +805,7 @@ k_paged_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         const uint32_t lanes = uint32_t(warp % 4 * 32) << 16;
         RowThread<D> rows{a, s, bar, notes, &gave_up, base, tmem + lanes + kS + 128 * blk,
                           tmem + lanes + kO + 128 * blk, blk, lane, warp % 4};
-        rows.run();
+        if (!rows.run()) asm volatile("cp.async.wait_all;" ::: "memory");    // (given up: queries under way)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 8) {
