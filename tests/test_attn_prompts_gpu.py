@@ -174,3 +174,97 @@ def test_pools_without_a_tensor_map(attn):
     table.zero_()
     assert launches(attn, prob) == 1
     assert torch.equal(attn.paged_attention(q, *pools.pools, table, lens), want)
+
+
+# ---- the path's own cases -----------------------------------------------------------------------
+
+CASES = [
+    # (T, Hq, Hkv, D, ps, lens, window, sinks): pages of 16 n and rows enough for the path
+    (700, 16, 2, 128, 48, [2000], 300, 0),
+    (700, 16, 2, 128, 48, [2000, 650], 300, 5),
+    (300, 40, 8, 64, 16, [1700, 300, 301, 40], 129, 200),              # more sinks than a window
+    (130, 8, 8, 128, 16, [130, 257, 128, 640, 129], 128, 1),           # one row behind a block
+    (128, 8, 8, 128, 128, [128, 5000, 1, 127, 200, 129], 1, 1),        # a row sees itself and the sink
+    (257, 6, 6, 64, 112, [257, 1300, 256, 255, 30, 4000, 1], 1000, 64),
+    (130, 8, 8, 128, 16, [300] * 12, 0, 0),
+    (1300, 32, 8, 128, 16, [3000, 0], 0, 0),                           # items without positions between others
+    (1300, 32, 8, 64, 16, [0, 3000, 0], 900, 20),
+    (700, 32, 8, 128, 32, [2000, 0, 0, 5, 0, 701], 0, 0),
+    (700, 32, 8, 64, 32, [699, 0, 1400], 250, 0),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_cases_that_the_path_takes(attn, case):
+    T, Hq, Hkv, D, ps, lens, window, sinks = case
+    prob = problem(len(lens), T, Hq, Hkv, D, ps, lens, BF, 300 + T)
+    assert launches(attn, prob, window=window, sinks=sinks) == 1
+    check(attn, prob, window, sinks)
+
+
+@pytest.mark.parametrize("ps", [16, 48, 64])
+@pytest.mark.parametrize("D", [64, 128])
+def test_missing_pages(attn, D, ps):
+    """Pages that are no pages, among those that rows see, at the sinks and between sinks and window; a length
+    beyond the table."""
+    q, pools, table, lens = prob = problem(4, 300, 32, 4, D, ps, [1700, 1000, 310, 600], BF, 14, poison=False)
+    M = table.shape[1]
+    table[0, 240 // ps: 640 // ps], table[0, 0], table[1, :] = -1, pools.pools[0].shape[0], -7
+    table[3, 560 // ps], table[2, 1] = -1, 2 ** 31 - 1
+    lens[2] = M * ps + 77
+    for window, sinks in ((0, 0), (100, 50), (100, 1), (0, 9)):
+        assert launches(attn, prob, window=window, sinks=sinks) == 1
+        check(attn, prob, window, sinks)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (200, 0), (200, 9)])
+def test_unseen_values_stay_out_of_half_items(attn, D, bad, window, sinks):
+    """All items are halved: an infinity or NaN in either half of a tile reaches the rows that see it alone."""
+    T, Hq, Hkv, ps, n = 300, 32, 8, 16, 900
+    q, pools, table, lens = prob = problem(1, T, Hq, Hkv, D, ps, [n], BF, 15)
+    kw = dict(window=window, sinks=sinks)
+    assert launches(attn, prob, **kw) == 1
+    call = lambda: attn.paged_attention(q, *pools.pools, table, lens, **kw)
+    good = call()
+    e = n - T + torch.arange(T, device="cuda")
+    G = Hq // Hkv
+    for at in (0, 3, 100, 400, 460, 550, 640, 700, 767, 768, 898, 899):
+        place = (int(table[0, at // ps]), 2, at % ps, 7)
+        was = pools.pools[1][place].clone()
+        pools.pools[1][place] = bad
+        got = call()
+        pools.pools[1][place] = was
+        see = e >= at
+        if window:
+            see &= (at > e - window) | (at < sinks)
+        hit = torch.zeros(got.shape, dtype=torch.bool, device="cuda")
+        hit[0, :, 2 * G: 3 * G, 7] = see[:, None]
+        assert torch.equal(got[~hit], good[~hit])
+        assert not torch.isfinite(got[hit]).any()
+
+
+@pytest.mark.parametrize("B,T,longest", [(1, 1500, 3000), (2, 1300, 2500), (1, 300, 2000)])
+def test_replays_match_the_definition(attn, B, T, longest):
+    """One captured call, replayed with other lengths, each result against the definition."""
+    q, pools, table, lens = prob = problem(B, T, 32, 8, 128, 16, [longest] * B, BF, 68, poison=False)
+    kw = dict(window=700, sinks=9)
+    assert launches(attn, prob, **kw) == 1
+    out = torch.empty_like(q)
+    ws = torch.empty(max(attn.paged_attention_workspace_size(B, T, 32, 8, 128), 1), dtype=torch.uint8, device="cuda")
+    call = lambda: attn.paged_attention(q, *pools.pools, table, lens, out=out, workspace=ws, **kw)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for n in (longest - 1, T + 60, 200, 0, 1, longest):
+        lens.fill_(n)
+        lens[-1] = n if B == 1 else longest - n
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        want, _ = check(attn, prob, 700, 9)
+        assert torch.equal(got, want)
