@@ -222,11 +222,19 @@ constexpr int kAppendWarps = 4;
 // their neighbours.  (The choice in every lane of the 8192 tokens: 36.2 us.)
 // kAxes: positions of several axes; a warp collects the angles of its token's columns, each from its
 // axis's row of the table, in shared memory (4999 tokens of 28 + 2 x 4 heads: 20.5 us; a lane that
-// loads every axis's vectors and keeps what is its own, 0.7 more).  CTAs an SM: as many as a warp's passes
-// leave registers for (that case with six 22.6 us; 8192 tokens of 16 + 2 x 8 heads in fp32, two passes,
-// 48 us with eight, 53 with six; four passes with seven spill and are no faster).
+// loads every axis's vectors and keeps what is its own, 0.7 more).
+// CTAs of an SM, by the passes of a warp: a few spilled words (up to 96 bytes of loads) cost less than a CTA
+// in flight.  8192 tokens, with these / with as many as nothing spills with: bf16, 32 + 2 x 8 heads of 128,
+// four passes 33.6 / 35.6 us, to 4 bits 41.0 / 42.8; 28 + 2 x 4, three axes, three passes 31.9 / 36.4; fp32,
+// 16 + 2 x 8, three axes, two passes to 8 bits 48.2 / 55.6.  Two passes in fp32 with one axis gain nothing from
+// eight (to 8 bits 20.4 us with heads of 64, half turned 24.8; with seven, which spill nothing, 20.3 and 24.0;
+// six 20.9 and 24.5).
+template <typename T, bool kAxes, int U>
+constexpr int append_ctas() {
+    return U == 4 ? 6 : U == 3 || (U == 2 && sizeof(T) == 4 && !kAxes) ? 7 : 8;
+}
 template <typename T, int D, int kCodes, bool kWhole, bool kAxes, int U>
-__global__ void __launch_bounds__(32 * kAppendWarps, (U == 4 ? 6 : U == 3 ? 7 : 8))
+__global__ void __launch_bounds__(32 * kAppendWarps, (append_ctas<T, kAxes, U>()))
 k_kv_append(const __grid_constant__ KvAppendArgs a, int warps) {
     constexpr int LR = D / 16, RPP = 32 / LR;
     const int64_t id = int64_t(blockIdx.x) * kAppendWarps + threadIdx.x / 32;
@@ -646,7 +654,8 @@ cudaError_t read_t(const KvReadArgs &a, cudaStream_t s) {
     // tokens of a CTA: 1024 vectors' worth, fewer where that leaves SMs without one (the
     // kernel alone, 300 tokens of 4 heads of 64: 4.4 us, with 32 a CTA 4.7)
     // (4-bit codes, whose vectors are half the bytes: 2048, and five CTAs an SM; 32768 tokens of 8 heads of 128
-    // 36.6 us with 1024 and four, 32.8 so, 78% of the copy rate; 262144 of them 258 and 225, 91%)
+    // 36.6 us with 1024 and four, 32.8 so, 78% of the copy rate; 262144 of them 258 and 225, 91%; rows of fp32,
+    // where five CTAs spill 36 bytes: 75.8 and 509 us, with four 73.6 and 524)
     int TB = (std::is_same_v<P, Nibbles> ? 2048 : 1024) / (a.c.Hkv * (D / 8));
     TB = TB < 1 ? 1 : TB > kReadTokens ? kReadTokens : TB;
     while (TB > 1 && (a.T + TB - 1) / TB < kSms) TB /= 2;
