@@ -29,8 +29,10 @@ import torch
 from . import _native
 
 _CODES = {torch.float32: _native.SSD_F32, torch.bfloat16: _native.SSD_BF16,
-          torch.float8_e4m3fn: _native.SSD_F8E4M3,
-          torch.float4_e2m1fn_x2: _native.SSD_F4E2M1X2}
+          torch.float8_e4m3fn: _native.SSD_F8E4M3}
+if hasattr(torch, "float4_e2m1fn_x2"):       # torch 2.8; without it there are the other pools
+    _CODES[torch.float4_e2m1fn_x2] = _native.SSD_F4E2M1X2
+_OF_CODES = (_native.SSD_F8E4M3, _native.SSD_F4E2M1X2)
 
 _ext_module = None
 _lock = threading.Lock()
@@ -95,7 +97,7 @@ def kv_read(k_cache, v_cache, page_table, cu_lens, tokens, *, starts=None, k_sca
     else:
         k = v = None
         if dtype is not None and dtype is not k_cache.dtype and (
-                k_cache.dtype not in (torch.float8_e4m3fn, torch.float4_e2m1fn_x2)
+                _CODES.get(k_cache.dtype) not in _OF_CODES
                 or dtype not in (torch.bfloat16, torch.float32)):
             raise ValueError(f"rows of {k_cache.dtype} pools cannot be read as {dtype}")
     r = (_ext_module or _load()).kv_read(k_cache, v_cache, k_scale, v_scale, k_group_scale,

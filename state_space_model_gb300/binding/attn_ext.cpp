@@ -22,9 +22,12 @@
 #include <optional>
 #include <vector>
 
+#include "scalar_types.h"
 #include "ssd.h"
 
 namespace {
+
+bool four_bits(at::ScalarType t) { return FourBits<at::ScalarType>::is(t); }
 
 decltype(&ssd_kv_append_ex) g_append = nullptr;
 decltype(&ssd_kv_read_ex) g_read = nullptr;
@@ -37,8 +40,7 @@ int code_of(at::ScalarType t) {
     case at::kBFloat16: return SSD_BF16;
     case at::kInt: return SSD_I32;
     case at::kFloat8_e4m3fn: return SSD_F8E4M3;
-    case at::kFloat4_e2m1fn_x2: return SSD_F4E2M1X2;
-    default: return 99;      // the library names it
+    default: return four_bits(t) ? int(SSD_F4E2M1X2) : 99;      // the library names it
     }
 }
 
@@ -206,8 +208,8 @@ PyObject *kv_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 return nullptr;
             }
             at::ScalarType dt = pool->scalar_type();
-            const int64_t D = pool->size(3) * (dt == at::kFloat4_e2m1fn_x2 ? 2 : 1);
-            if (dt == at::kFloat8_e4m3fn || dt == at::kFloat4_e2m1fn_x2)
+            const int64_t D = pool->size(3) * (four_bits(dt) ? 2 : 1);
+            if (dt == at::kFloat8_e4m3fn || four_bits(dt))
                 dt = f32 ? at::kFloat : at::kBFloat16;
             kv[i] = make(*pool, {tokens, pool->size(1), D}, dt);
         }

@@ -37,6 +37,7 @@ LIB = os.path.join(PKG, "libssd_gb300.so")
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libssd_gb300_debug.so")
 BINDING_SRC = os.path.join(PKG, "binding", "attn_ext.cpp")
+BINDING_TYPES = os.path.join(PKG, "binding", "scalar_types.h")
 BINDING = os.path.join(PKG, "_attn_ext.so")
 BINDING_STAMP = os.path.join(BUILD, "attn_ext.stamp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -111,7 +112,7 @@ def _binding_up_to_date() -> bool:
             return False
     t = os.path.getmtime(BINDING)
     return all(os.path.getmtime(p) <= t for p in (
-        BINDING_SRC, os.path.join(ROOT, "include", "ssd.h"), os.path.abspath(__file__)))
+        BINDING_SRC, BINDING_TYPES, os.path.join(ROOT, "include", "ssd.h"), os.path.abspath(__file__)))
 
 
 def build_binding() -> str | None:
