@@ -529,13 +529,14 @@ ssd_status ssd_paged_attention_workspace_size(int64_t batch, int64_t tokens, int
  * q, out [B, T, Hq, D] (f32 with f32 pools, else bf16); page_table [B, M]
  * SSD_I32, innermost stride 1; lens [B] SSD_I32; lse [B, T, Hq] f32
  * contiguous, may be NULL; workspace as above, 256-byte aligned, contents
- * ignored.  T (Hq / Hkv) at most 2^24.  Two launches (many rows over bf16 pools whose
+ * ignored (it is asked for whichever kernels take the call: some use none).  T (Hq /
+ * Hkv) at most 2^24.  Two launches (many rows over bf16 pools whose
  * pages are multiples of 16 tokens: one; rows that are many in a batch only: three, of
  * which the lengths let one kernel or the other work); scores, sums and partial results in
  * f32, the probabilities rounded to 16 bits for the product with bf16
- * values or 8-bit codes.  Scales may be any finite numbers; a row's probability times a
+ * values or codes.  Scales may be any finite numbers; a row's probability times a
  * value's scale is held in 11 bits down to 2^-22 of the row's largest such weight, and
- * value scales below 2^-114 in fewer (ssd_kv_append writes none below 2^-105). */
+ * value scales below 2^-114 in fewer (the appends write none below 2^-108). */
 ssd_status ssd_paged_attention(const ssd_tensor *q, const ssd_tensor *k_cache,
                                const ssd_tensor *v_cache, const ssd_tensor *k_scale,
                                const ssd_tensor *v_scale, const ssd_tensor *page_table,

@@ -22,13 +22,13 @@
 // (TMA), tiles ahead and across items, and the CTA goes from item to item (sequence, head, 256 rows)
 // with the next one's queries and keys already there.  Where most SMs would have no item in the last
 // round, an item is halved: 128 rows, for which the two blocks take half of every tile each and join
-// their sums at the end (512 tokens over 8192: 64 items 104 us, 128 halves 78).
+// their sums at the end (512 tokens over 8192: 64 items 104 us, 128 halves 70).
 //
 // The positions that some row of an item sees, sinks first and then the window's, are counted
 // through as one run in boxes of 16 of a page (so pages are multiples of 16; others take the
 // kernels of ssd_attn.cuh), so that a tile holds little that nobody needs wherever the window
 // begins.  (Copies by three warps, 16 bytes a lane, took any page size and three times as
-// long: 253 us for 4096 tokens under a window of 1024 where the loads take 76.)
+// long: 253 us for 4096 tokens under a window of 1024 where the loads take 75.)
 #include "ptx_sm100.cuh"
 #include "ssd_attn.h"
 #include "ssd_attn_choice.cuh"
@@ -75,7 +75,7 @@ struct Cfg {
     static constexpr int LPR = D / 8, RPI = 32 / LPR;      // 16-byte chunks of a row, rows a pass
     static constexpr int BOX = kBox * D * 2;               // bytes of a box
 };
-static_assert(Cfg<128>::SMEM + 1024 <= 227 * 1024, "a CTA fits an SM");
+static_assert(Cfg<128>::SMEM + 2048 <= 227 * 1024, "a CTA fits an SM, with its barriers and notes");
 // Tensor memory: scores of the two blocks (P over them), outputs.
 constexpr uint32_t kS = 0, kO = 256;
 
@@ -861,12 +861,12 @@ int64_t items_of(const PagedArgs &a, int block) {       // row blocks of a size
 
 }  // namespace
 
-// An item's time goes by its positions alone, 1.55 us for 128 of them (D = 64: 1.36), a half item's 1.23
-// (1.11), with all of its rows there or not; the kernels of ssd_attn.cuh split a sequence's positions
+// An item's time goes by its positions alone, 1.55 us for 128 of them (D = 64: 1.36), a half item's 1.10
+// (0.93), with all of its rows there or not; the kernels of ssd_attn.cuh split a sequence's positions
 // over the SMs and take 0.0154 us (0.0106) for 128 positions and a block of 64 rows.  So this kernel is
-// the faster one from 80 (105) such blocks on, and taken from 84 (107).  Measured, here / there: 88 blocks
-// (176 tokens of 32 over 8 heads over 8192) 78 / 102 us; 112 blocks, D = 64, 70 / 91; 256 blocks (512
-// tokens over 8192) 78 / 261 us, D = 64 71 / 184; 8192 tokens 399 / 2167, 345 / 1500.  (A scale below 0
+// the faster one from 72 (88) such blocks on, and taken from 84 (107).  Measured, here / there: 88 blocks
+// (176 tokens of 32 over 8 heads over 8192) 70 / 102 us; 112 blocks, D = 64, 59 / 91; 256 blocks (512
+// tokens over 8192) 70 / 261 us, D = 64 60 / 184; 8192 tokens 399 / 2167, 344 / 1500.  (A scale below 0
 // would have to turn the scores' signs, which no model asks for.  Fewer rows than a block of a sequence
 // and head take the others too: 96 sequences, 4 rows, a window of 1024: 93 us here, 47 there.)
 // Where a single sequence has so many blocks (what whole items need: 106, D = 64 137) no lengths make
@@ -920,7 +920,7 @@ void ask_lengths(PagedArgs &a) {
     const uint64_t sms = device_sm_count(), items = items_of(a, kItemRows), per = items / a.B;
     int64_t most = int64_t(a.M) * a.c.ps;
     if (a.window > 0) most = std::min(most, a.window + a.sinks + kItemRows / G);
-    const uint64_t whole = wide ? 15500 : 13600, part = wide ? 12300 : 11100;
+    const uint64_t whole = wide ? 15500 : 13600, part = wide ? 11000 : 9300;
     a.ask.on = 1;
     a.ask.most = int(most);
     a.ask.one = (2 * items <= sms ? part : whole) * sms;
