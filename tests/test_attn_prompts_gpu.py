@@ -2,6 +2,10 @@
 launch and one call to the next.  References and bounds are test_attn_forms_gpu.py's."""
 import ctypes
 import itertools
+import json
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -268,3 +272,70 @@ def test_replays_match_the_definition(attn, B, T, longest):
         got = out.clone()
         want, _ = check(attn, prob, 700, 9)
         assert torch.equal(got, want)
+
+
+def test_calls_whose_lengths_tell_on_two_streams_and_in_one_graph(attn):
+    """Two such calls at once, each with its own workspace; then both in a graph over one."""
+    B, T, Hq, Hkv = 14, 32, 32, 8
+    probs = [problem(B, T, Hq, Hkv, D, 16, n, BF, 80 + D) for D, n in ((64, [9000] + [40] * 13), (128, [1600] * 14))]
+    for p in probs:
+        assert launches(attn, p) == 3
+    call = lambda p, **kw: attn.paged_attention(p[0], *p[1].pools, p[2], p[3], **kw)
+    want = [call(p) for p in probs]
+    streams = [torch.cuda.Stream() for _ in probs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(call(probs[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+    outs = [torch.empty_like(p[0]) for p in probs]
+    ws = torch.empty(max(attn.paged_attention_workspace_size(B, T, Hq, Hkv, D) for D in (64, 128)), dtype=torch.uint8,
+                     device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(2):
+            for p, out in zip(probs, outs):
+                call(p, out=out, workspace=ws)
+    for _ in range(3):
+        for out in outs:
+            out.fill_(7.0)
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, x) for out, x in zip(outs, want))
+
+
+DEBUG_CHILD = r"""
+import ctypes, json, sys
+sys.path[:0] = [sys.argv[1], sys.argv[1] + "/tests"]
+import test_attn_prompts_gpu as t
+from state_space_model_gb300 import _native, attn
+import torch
+assert _native.LIB_PATH.endswith("libssd_gb300_debug.so"), _native.LIB_PATH
+for case in t.CASES:
+    T, Hq, Hkv, D, ps, lens, window, sinks = case
+    t.check(attn, t.problem(len(lens), T, Hq, Hkv, D, ps, lens, t.BF, 300 + T), window, sinks)
+for D in (64, 128):
+    t.test_calls_whose_lengths_tell_follow_one_another(attn, D)
+    t.test_missing_pages(attn, D, 48)
+    for order in ((0, 2, 1), (1, 2, 0)):
+        t.test_pools_in_any_order_of_memory(attn, D, order)
+lib = _native.load()
+st = lib.ssd_device_status(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+print(json.dumps({"status": st, "detail": lib.ssd_last_error_detail().decode()}))
+"""
+
+
+def test_debug_build_finds_every_index_in_bounds(attn):
+    from state_space_model_gb300 import build
+    build.build(debug_bounds=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", DEBUG_CHILD, root], env=dict(os.environ, SSD_DEBUG_BOUNDS="1"),
+                       cwd=root, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout + r.stderr
+    out = json.loads(r.stdout.strip().splitlines()[-1])
+    assert out["status"] == 0, out["detail"]
